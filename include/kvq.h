@@ -68,7 +68,10 @@ typedef int kvq_status;
 /* Bits that kernels OR into kvq_decode_params.error_flag */
 #define KVQ_DEVERR_WAIT_TIMEOUT 1   /* a pipeline wait gave up (results invalid) */
 #define KVQ_DEVERR_SEQ_CLAMPED 2    /* seq_lens[b] exceeded the cache; clamped */
-#define KVQ_DEVERR_BAD_PAGE 4       /* a block-table entry was out of range; page 0 read */
+#define KVQ_DEVERR_BAD_PAGE 4       /* a block-table entry was out of range; page 0 read
+                                       (kvq_rope_append: the token's rows are not written) */
+#define KVQ_DEVERR_BAD_POSITION 8   /* a position past the rotation table; its rows are
+                                       not written */
 
 /*
  * A paged quantized KV cache.  Caller-owned plain struct; the library only
@@ -215,6 +218,96 @@ kvq_status kvq_amax_bf16(const void* x /* device bf16 [n] */, size_t n,
 kvq_status kvq_quantize_append(const kvq_cache* c, const void* k_new, const void* v_new,
                                const void* kpe_new, const int32_t* start_pos, int batch,
                                int n_tokens, void* stream);
+
+/*
+ * Norm and rotation of queries and keys.  Which the model applies, and with
+ * what, is the same for every call of a layer:
+ *   norm:     n_i = (x_i r) w_i,  r = 1 / sqrt(sum_j x_j^2 / head_dim + eps)
+ *             over each head, where weights are given (q_norm for queries,
+ *             k_norm for keys; each may be NULL on its own);
+ *   rotation: of the head's first rot_dim elements, by the angles of the
+ *             token's position, (a, b) -> (a cos - b sin, b cos + a sin) over
+ *             the pairs (i, i + rot_dim/2) (interleaved = 0) or (2i, 2i + 1)
+ *             (interleaved = 1), i < rot_dim/2; the rest passes unrotated.
+ * All of it runs in fp32 on the bf16 input; a result is rounded once, to its
+ * output type.  A row's sum of squares has to stay in the range of fp32.
+ */
+typedef struct kvq_rotary {
+  const float* cos_sin;      /* (device) [num_positions][rot_dim]: the rot_dim/2
+                                cosines of a position, then its sines; 16-byte
+                                aligned (ignored where rot_dim is 0) */
+  int32_t num_positions;     /* rows of the table */
+  int32_t rot_dim;           /* 0 (no rotation) or a multiple of 32, <= head_dim */
+  int32_t interleaved;       /* 0 or 1 */
+  const float* q_norm;       /* (device, optional) [head_dim], 16-byte aligned */
+  const float* k_norm;       /* (device, optional) [head_dim]; MLA: [512], the latent's */
+  float eps;                 /* finite >= 0 (read where a norm is given) */
+} kvq_rotary;
+
+/*
+ * Rows of heads, such as a slice of a packed projection: head h of token t is
+ * the head_dim elements at data + t * token_stride + h * head_stride.  Strides
+ * count elements (bytes where the rows hold codes), are multiples of 8 in [0,
+ * 2^31) and data is 16-byte aligned.  Rows that a call writes may not overlap
+ * one another.
+ */
+typedef struct kvq_heads {
+  void* data;                /* (device) */
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t num_heads;         /* >= 1 */
+} kvq_heads;
+
+/*
+ * Norm and rotation of queries q and keys k (either may be NULL) in one pass:
+ * token t of num_tokens is at positions[t] (device int32; may be NULL without
+ * a rotation).
+ *   q, k   bf16 rows;  head_dim 64, 128 or 256.
+ *   q_out  bf16 rows, or with q_fp8 = 1 E4M3 codes for an FP8-query decode:
+ *          E4M3(fl32(y / s)), s = q_head_scale[h] (device) where given, else
+ *          q_scale (finite > 0), as kvq_quantize_fp8 rounds.
+ *   k_out  bf16 rows.
+ * bf16 outputs may be the inputs themselves (same data and strides); otherwise
+ * no output may overlap an input.  Tokens at negative positions are skipped
+ * (their output rows stay as they were: the padding of a batch), and so are
+ * tokens at positions past the table, which set KVQ_DEVERR_BAD_POSITION.
+ * num_tokens times the number of heads < 2^31 (else KVQ_ERR_UNSUPPORTED).
+ */
+kvq_status kvq_norm_rope(const kvq_rotary* r, int head_dim, int num_tokens,
+                         const int32_t* positions, const kvq_heads* q, const kvq_heads* q_out,
+                         int q_fp8, float q_scale, const float* q_head_scale, const kvq_heads* k,
+                         const kvq_heads* k_out, int32_t* error_flag, void* stream);
+
+/*
+ * kvq_quantize_append of keys that are normed and rotated on the way, and, in
+ * the same launch, the norm and rotation of the step's queries.
+ *   Token (b, t), t < n_tokens, of the padded batch is row b * n_tokens + t of
+ *   k, v, kpe, q and q_out, and goes to position start_pos[b] + t, which also
+ *   gives its angles.
+ *   new_lens (device int32 [batch], optional): only the first new_lens[b]
+ *   tokens of request b are real; the rest are neither read nor written, and
+ *   their cache rows and q_out rows stay as they were.
+ *   k, v   bf16 rows of num_kv_heads heads;  head_dim 64, 128 or 256.
+ *   q, q_out, q_fp8, q_scale, q_head_scale (q may be NULL): as in
+ *          kvq_norm_rope.  A decode that reads q_out must not use
+ *          fresh_tokens (q is not complete before this call); without q the
+ *          call takes kvq_quantize_append's place in that contract.
+ *   MLA cache (head_dim 512, rope_dim 64): k holds the latents (normed with
+ *          k_norm where given, not rotated), kpe the rope keys (rotated, bf16);
+ *          v and q are NULL, and rot_dim is at most 64.
+ * The quantisers are kvq_quantize_append's on the fp32 values (V: the same
+ * codes).  error_flag (device, optional) gets KVQ_DEVERR_BAD_POSITION for a
+ * position past the rotation table and KVQ_DEVERR_BAD_PAGE for a page index
+ * out of range.  A token at a negative position or past the rotation table is
+ * skipped altogether; one whose page index is out of range, or that lies past
+ * the block table (as in the plain append), gets no cache row, but its q_out
+ * row is written.
+ */
+kvq_status kvq_rope_append(const kvq_cache* c, const kvq_rotary* r, int batch, int n_tokens,
+                           const int32_t* start_pos, const int32_t* new_lens, const kvq_heads* k,
+                           const kvq_heads* v, const kvq_heads* kpe, const kvq_heads* q,
+                           const kvq_heads* q_out, int q_fp8, float q_scale,
+                           const float* q_head_scale, int32_t* error_flag, void* stream);
 
 /*
  * Split-count heuristic (host only, deterministic).  base = batch *

@@ -113,6 +113,64 @@ kvq_status check_params(const kvq_decode_params* p) {
   return KVQ_OK;
 }
 
+// Rows of heads, `tokens` of them: 16-byte loads need the base and the strides
+// aligned; outputs may not overlap themselves.
+kvq_status check_heads(const kvq_heads* h, int dim, long long tokens, bool out) {
+  if (!h || !h->data || !aligned16(h->data) || h->num_heads < 1) return KVQ_ERR_INVALID;
+  const long long ts = h->token_stride, hs = h->head_stride;
+  if (ts < 0 || hs < 0 || ts % 8 != 0 || hs % 8 != 0) return KVQ_ERR_INVALID;
+  if (ts >= (1LL << 31) || hs >= (1LL << 31)) return KVQ_ERR_UNSUPPORTED;
+  if (out) {
+    const bool by_token = (h->num_heads == 1 || hs >= dim) &&
+                          (tokens == 1 || ts >= (h->num_heads - 1) * hs + dim);
+    const bool by_head = (tokens == 1 || ts >= dim) &&
+                         (h->num_heads == 1 || hs >= (tokens - 1) * ts + dim);
+    if (!by_token && !by_head) return KVQ_ERR_INVALID;
+  }
+  return KVQ_OK;
+}
+
+kvq_status check_rotary(const kvq_rotary* r, int dim) {
+  if (!r) return KVQ_ERR_INVALID;
+  if (r->rot_dim < 0 || r->rot_dim > dim || r->rot_dim % 2 != 0) return KVQ_ERR_INVALID;
+  if (r->interleaved != 0 && r->interleaved != 1) return KVQ_ERR_INVALID;
+  if (r->rot_dim > 0 && (!r->cos_sin || !aligned16(r->cos_sin) || r->num_positions < 1))
+    return KVQ_ERR_INVALID;
+  if ((r->q_norm && !aligned16(r->q_norm)) || (r->k_norm && !aligned16(r->k_norm)))
+    return KVQ_ERR_INVALID;
+  if ((r->q_norm || r->k_norm) && !(std::isfinite(r->eps) && r->eps >= 0.f))
+    return KVQ_ERR_INVALID;
+  if (r->rot_dim % 32 != 0) return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+// The query rows of a call: their output rows and E4M3 scale.
+kvq_status check_query_rows(const kvq_heads* q, const kvq_heads* out, int dim, long long tokens,
+                            int q_fp8, float q_scale, const float* q_head_scale) {
+  kvq_status s = check_heads(q, dim, tokens, false);
+  if (s != KVQ_OK) return s;
+  s = check_heads(out, dim, tokens, true);
+  if (s != KVQ_OK) return s;
+  if (out->num_heads != q->num_heads) return KVQ_ERR_INVALID;
+  if (q_fp8 != 0 && q_fp8 != 1) return KVQ_ERR_INVALID;
+  if (q_fp8 && !q_head_scale && !finite_pos(q_scale)) return KVQ_ERR_INVALID;
+  return KVQ_OK;
+}
+
+RopeRows rope_rows(const kvq_heads* h) {
+  if (!h) return RopeRows{nullptr, 0, 0, 0};
+  return RopeRows{static_cast<uint16_t*>(h->data), (long)h->token_stride, (long)h->head_stride,
+                  h->num_heads};
+}
+
+void rotary_args(RopeArgs& a, const kvq_rotary* r) {
+  a.cos_sin = r->cos_sin;
+  a.num_positions = r->num_positions;
+  a.rot = r->rot_dim;
+  a.interleaved = r->interleaved;
+  a.eps = r->eps;
+}
+
 kvq_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
 
 // ---------------------------------------------------------------------------
@@ -284,6 +342,118 @@ kvq_status kvq_quantize_append(const kvq_cache* c, const void* k_new, const void
   a.v_hs = c->v_head_scale;
   a.has_v = is_mla(c) ? 0 : 1;
   return cuda_status(launch_append(a, as_stream(stream)));
+}
+
+kvq_status kvq_norm_rope(const kvq_rotary* r, int head_dim, int num_tokens,
+                         const int32_t* positions, const kvq_heads* q, const kvq_heads* q_out,
+                         int q_fp8, float q_scale, const float* q_head_scale, const kvq_heads* k,
+                         const kvq_heads* k_out, int32_t* error_flag, void* stream) {
+  if (head_dim < 1 || num_tokens < 0) return KVQ_ERR_INVALID;
+  kvq_status s = check_rotary(r, head_dim);
+  if (s != KVQ_OK) return s;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return KVQ_ERR_UNSUPPORTED;
+  if (!q && !k) return KVQ_ERR_INVALID;
+  if (num_tokens == 0) return KVQ_OK;
+  if (q) {
+    s = check_query_rows(q, q_out, head_dim, num_tokens, q_fp8, q_scale, q_head_scale);
+    if (s != KVQ_OK) return s;
+  }
+  if (k) {
+    s = check_heads(k, head_dim, num_tokens, false);
+    if (s == KVQ_OK) s = check_heads(k_out, head_dim, num_tokens, true);
+    if (s != KVQ_OK) return s;
+    if (k_out->num_heads != k->num_heads) return KVQ_ERR_INVALID;
+  }
+  if (r->rot_dim > 0 && !positions) return KVQ_ERR_INVALID;
+  const long long heads = (q ? (long long)q->num_heads : 0) + (k ? (long long)k->num_heads : 0);
+  if (num_tokens * heads >= (1LL << 31)) return KVQ_ERR_UNSUPPORTED;
+  RopeArgs a{};
+  rotary_args(a, r);
+  a.q = rope_rows(q);
+  a.k = rope_rows(k);
+  a.q_out = rope_rows(q ? q_out : nullptr);
+  a.k_out = rope_rows(k ? k_out : nullptr);
+  a.q_norm = q ? r->q_norm : nullptr;
+  a.k_norm = k ? r->k_norm : nullptr;
+  a.rows = (unsigned)(num_tokens * heads);
+  a.positions = positions;
+  a.q_fp8 = q ? q_fp8 : 0;
+  a.q_scale = q_scale;
+  a.q_recip = a.q_fp8 && !q_head_scale ? (float)(1.0 / (double)q_scale) : 0.f;
+  a.q_hs = q_head_scale;
+  a.error_flag = error_flag;
+  return cuda_status(launch_rope(head_dim, false, a, as_stream(stream)));
+}
+
+kvq_status kvq_rope_append(const kvq_cache* c, const kvq_rotary* r, int batch, int n_tokens,
+                           const int32_t* start_pos, const int32_t* new_lens, const kvq_heads* k,
+                           const kvq_heads* v, const kvq_heads* kpe, const kvq_heads* q,
+                           const kvq_heads* q_out, int q_fp8, float q_scale,
+                           const float* q_head_scale, int32_t* error_flag, void* stream) {
+  kvq_status s = check_cache(c);
+  if (s != KVQ_OK) return s;
+  if (batch < 0 || n_tokens < 0) return KVQ_ERR_INVALID;
+  const bool mla = is_mla(c);
+  const int D = c->head_dim;
+  s = check_rotary(r, mla ? c->rope_dim : D);
+  if (s != KVQ_OK) return s;
+  if (mla) {
+    if (v || !kpe) return KVQ_ERR_INVALID;
+    if (D != 512 || c->rope_dim != 64 || q) return KVQ_ERR_UNSUPPORTED;
+  } else {
+    if (!v || kpe) return KVQ_ERR_INVALID;
+    if (D != 64 && D != 128 && D != 256) return KVQ_ERR_UNSUPPORTED;
+  }
+  const long long tokens = (long long)batch * n_tokens;
+  if (tokens == 0) return KVQ_OK;
+  if (!start_pos) return KVQ_ERR_INVALID;
+  s = check_heads(k, D, tokens, false);
+  if (s == KVQ_OK) s = mla ? check_heads(kpe, c->rope_dim, tokens, false)
+                           : check_heads(v, D, tokens, false);
+  if (s != KVQ_OK) return s;
+  if (k->num_heads != c->num_kv_heads || (mla ? kpe : v)->num_heads != c->num_kv_heads)
+    return KVQ_ERR_INVALID;
+  if (q) {
+    s = check_query_rows(q, q_out, D, tokens, q_fp8, q_scale, q_head_scale);
+    if (s != KVQ_OK) return s;
+  }
+  const long long heads = mla ? 1 : 2LL * c->num_kv_heads + (q ? q->num_heads : 0);
+  if (tokens >= (1LL << 31) || tokens * heads >= (1LL << 31)) return KVQ_ERR_UNSUPPORTED;
+  RopeArgs a{};
+  a.fmt = c->fmt;
+  rotary_args(a, r);
+  a.q = rope_rows(q);
+  a.k = rope_rows(k);
+  a.v = rope_rows(mla ? kpe : v);
+  a.q_out = rope_rows(q ? q_out : nullptr);
+  a.q_norm = q ? r->q_norm : nullptr;
+  a.k_norm = r->k_norm;
+  a.rows = (unsigned)(tokens * heads);
+  a.start_pos = start_pos;
+  a.new_lens = new_lens;
+  a.T = n_tokens;
+  a.q_fp8 = q ? q_fp8 : 0;
+  a.q_scale = q_scale;
+  a.q_recip = a.q_fp8 && !q_head_scale ? (float)(1.0 / (double)q_scale) : 0.f;
+  a.q_hs = q_head_scale;
+  a.error_flag = error_flag;
+  a.Hkv = c->num_kv_heads;
+  a.ps = c->page_size;
+  a.max_pages = c->max_pages_per_seq;
+  a.num_pages = c->num_pages;
+  a.block_table = c->block_table;
+  a.k_codes = static_cast<uint8_t*>(c->k_codes);
+  a.v_codes = static_cast<uint8_t*>(c->v_codes);
+  a.k_bscale = static_cast<uint8_t*>(c->k_bscale);
+  a.v_bscale = static_cast<uint8_t*>(c->v_bscale);
+  a.k_pe = static_cast<uint16_t*>(c->k_pe);
+  a.k_scale = c->k_scale;
+  a.v_scale = c->v_scale;
+  a.k_recip = (float)(1.0 / (double)c->k_scale);
+  a.v_recip = mla ? a.k_recip : (float)(1.0 / (double)c->v_scale);
+  a.k_hs = c->k_head_scale;
+  a.v_hs = c->v_head_scale;
+  return cuda_status(launch_rope(D, mla, a, as_stream(stream)));
 }
 
 kvq_status kvq_auto_splits(int num_sms, int batch, int num_kv_heads, int q_per_kv,

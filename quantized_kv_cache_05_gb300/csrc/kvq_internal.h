@@ -86,6 +86,45 @@ struct PartialArgs {
   int cluster_merge;
 };
 
+// Rows of heads: head h of token t starts at data + t * token_stride + h *
+// head_stride (elements; 16-bit ones, or bytes where the rows hold codes).
+struct RopeRows {
+  uint16_t* data;
+  long token_stride, head_stride;
+  int heads;
+};
+
+struct RopeArgs {
+  int fmt;                    // 0: rows out (kvq_norm_rope), else the cache's format
+  RopeRows q, k, v;           // inputs (MLA: k the latent, v the rope keys)
+  RopeRows q_out, k_out;
+  unsigned rows;              // tokens * heads (MLA: tokens)
+  const float* cos_sin;
+  int num_positions, rot, interleaved;
+  const float* q_norm;
+  const float* k_norm;
+  float eps;
+  const int32_t* positions;   // kvq_norm_rope: per token
+  const int32_t* start_pos;   // append: per request
+  const int32_t* new_lens;
+  int T;                      // append: tokens per request
+  int q_fp8;
+  float q_scale, q_recip;
+  const float* q_hs;
+  int32_t* error_flag;
+  // the cache (append)
+  int Hkv, ps, max_pages, num_pages;
+  const int32_t* block_table;
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  uint8_t* k_bscale;
+  uint8_t* v_bscale;
+  uint16_t* k_pe;
+  float k_scale, v_scale, k_recip, v_recip;
+  const float* k_hs;
+  const float* v_hs;
+};
+
 struct CombineArgs {
   const float* part_o;
   const float* part_lse;
@@ -134,6 +173,7 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
 }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t st);
+cudaError_t launch_rope(int D, bool mla, const RopeArgs& a, cudaStream_t st);
 cudaError_t launch_amax_bf16(const uint16_t* x, size_t n, float* out, cudaStream_t st);
 cudaError_t launch_encode(int kind, const float* x, uint8_t* out, size_t n, cudaStream_t st);
 // E4M3(fl32(x / s)) of bf16 x, s per tensor (recip = RN(1/s)) or per head

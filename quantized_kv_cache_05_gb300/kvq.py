@@ -23,9 +23,11 @@ KVQ_OK, KVQ_ERR_INVALID, KVQ_ERR_UNSUPPORTED, KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA = 
 KVQ_FP8_E4M3, KVQ_NVFP4 = 1, 2
 KVQ_OUT_F32, KVQ_OUT_BF16, KVQ_OUT_E4M3 = 0, 1, 2
 KVQ_DEVERR_WAIT_TIMEOUT, KVQ_DEVERR_SEQ_CLAMPED = 1, 2
+KVQ_DEVERR_BAD_PAGE, KVQ_DEVERR_BAD_POSITION = 4, 8
 KVQ_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 _int = ctypes.c_int
 _f = ctypes.c_float
 _P = ctypes.c_void_p
@@ -51,6 +53,19 @@ class kvq_decode_params(ctypes.Structure):
     ]
 
 
+class kvq_rotary(ctypes.Structure):
+    _fields_ = [
+        ("cos_sin", _P), ("num_positions", _i32), ("rot_dim", _i32), ("interleaved", _i32),
+        ("q_norm", _P), ("k_norm", _P), ("eps", _f),
+    ]
+
+
+class kvq_heads(ctypes.Structure):
+    _fields_ = [("data", _P), ("token_stride", _i64), ("head_stride", _i64), ("num_heads", _i32)]
+
+
+_heads_p = ctypes.POINTER(kvq_heads)
+
 # name -> (restype, argtypes); the exported surface of include/kvq.h
 SIGNATURES = {
     "kvq_status_string": (ctypes.c_char_p, [_int]),
@@ -72,6 +87,11 @@ SIGNATURES = {
     "kvq_quantize_fp8": (_int, [_P, _sz, _f, _P, _int, _int, _P, _P]),
     "kvq_prefill": (_int, [ctypes.POINTER(kvq_cache), ctypes.POINTER(kvq_decode_params), _int,
                            _P, _P, _P]),
+    "kvq_norm_rope": (_int, [ctypes.POINTER(kvq_rotary), _int, _int, _P, _heads_p, _heads_p, _int,
+                             _f, _P, _heads_p, _heads_p, _P, _P]),
+    "kvq_rope_append": (_int, [ctypes.POINTER(kvq_cache), ctypes.POINTER(kvq_rotary), _int, _int,
+                               _P, _P, _heads_p, _heads_p, _heads_p, _heads_p, _heads_p, _int, _f,
+                               _P, _P, _P]),
 }
 
 _lock = threading.Lock()
@@ -222,3 +242,24 @@ def kvq_prefill(cache: kvq_cache, params: kvq_decode_params, q_len: int, q, out,
     """Causal prefill attention of q_len new tokens per request (no KV split)."""
     return lib().kvq_prefill(_ref(cache), _ref(params), q_len, _addr(q), _addr(out),
                              _stream(stream))
+
+
+def kvq_norm_rope(rotary: kvq_rotary, head_dim: int, num_tokens: int, positions,
+                  q: Optional[kvq_heads], q_out: Optional[kvq_heads], q_fp8: int, q_scale: float,
+                  q_head_scale, k: Optional[kvq_heads], k_out: Optional[kvq_heads],
+                  error_flag=None, stream=None) -> int:
+    """Per-head norm and position rotation of queries and keys (no cache)."""
+    return lib().kvq_norm_rope(_ref(rotary), head_dim, num_tokens, _addr(positions), _ref(q),
+                               _ref(q_out), q_fp8, q_scale, _addr(q_head_scale), _ref(k),
+                               _ref(k_out), _addr(error_flag), _stream(stream))
+
+
+def kvq_rope_append(cache: kvq_cache, rotary: kvq_rotary, batch: int, n_tokens: int, start_pos,
+                    new_lens, k: Optional[kvq_heads], v: Optional[kvq_heads],
+                    kpe: Optional[kvq_heads], q: Optional[kvq_heads], q_out: Optional[kvq_heads],
+                    q_fp8: int, q_scale: float, q_head_scale, error_flag=None, stream=None) -> int:
+    """Quantize-on-append with the keys' norm and rotation (and the queries')."""
+    return lib().kvq_rope_append(_ref(cache), _ref(rotary), batch, n_tokens, _addr(start_pos),
+                                 _addr(new_lens), _ref(k), _ref(v), _ref(kpe), _ref(q),
+                                 _ref(q_out), q_fp8, q_scale, _addr(q_head_scale),
+                                 _addr(error_flag), _stream(stream))

@@ -18,6 +18,129 @@ OUT = {"f32": kvq.KVQ_OUT_F32, "bf16": kvq.KVQ_OUT_BF16, "e4m3": kvq.KVQ_OUT_E4M
 OUT_TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.uint8}
 
 
+def rope_table(num_positions: int, rot_dim: int, base: float = 10000.0,
+               device: str | torch.device = "cuda") -> torch.Tensor:
+    """Rotation table of ``kvq_rotary`` (fp32 [num_positions][rot_dim]: cosines, then
+    sines) for the angles position * base^(-2i / rot_dim), formed in 64 bits."""
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device)
+    ang = torch.arange(num_positions, dtype=torch.float64, device=device)[:, None] * \
+        base ** (-i / rot_dim)
+    return torch.cat([ang.cos(), ang.sin()], 1).float().contiguous()
+
+
+def _check(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _here(t: torch.Tensor, dtype: torch.dtype, what: str) -> None:
+    """A CUDA tensor of the current device (kernels launch there) and this type."""
+    if t.dtype != dtype or not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: expected {dtype} on cuda:{torch.cuda.current_device()}, got "
+                         f"{t.dtype} on {t.device}")
+
+
+def _index(t: torch.Tensor, n: int, what: str) -> None:
+    """A dense int32 array of n entries."""
+    _here(t, torch.int32, what)
+    _check(t.numel() == n and t.is_contiguous(), f"{what}: expected {n} contiguous entries")
+
+
+class Rotary:
+    """The norm and rotation of a layer's queries and keys (``kvq_rotary``): the
+    table of ``rope_table`` (None: no rotation) and the norms' weights (float32
+    [head_dim] each; None: no norm)."""
+
+    def __init__(self, table: Optional[torch.Tensor], interleaved: bool = False,
+                 q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6):
+        for t, what in ((table, "table"), (q_norm, "q_norm"), (k_norm, "k_norm")):
+            if t is not None:
+                _here(t, torch.float32, what)
+                _check(t.is_contiguous(), f"{what}: expected a contiguous tensor")
+        _check(table is None or table.dim() == 2, "table: expected [positions][rot_dim]")
+        self.table, self.q_norm, self.k_norm = table, q_norm, k_norm
+        r = self._struct = kvq.kvq_rotary()
+        if table is not None:
+            r.cos_sin, r.num_positions, r.rot_dim = table.data_ptr(), *table.shape
+        r.interleaved = 1 if interleaved else 0
+        r.q_norm = q_norm.data_ptr() if q_norm is not None else None
+        r.k_norm = k_norm.data_ptr() if k_norm is not None else None
+        r.eps = eps
+
+    def struct(self) -> kvq.kvq_rotary:
+        return self._struct
+
+    def check_dim(self, q_dim: Optional[int], k_dim: Optional[int]) -> None:
+        """The norms' weights cover the heads given (the kernels read that many)."""
+        for w, dim, what in ((self.q_norm, q_dim, "q_norm"), (self.k_norm, k_dim, "k_norm")):
+            _check(w is None or dim is None or w.numel() == dim, f"{what}: expected {dim} weights")
+
+
+def _heads(t: torch.Tensor, what: str, out_fp8: bool = False) -> kvq.kvq_heads:
+    """Rows of heads [tokens][heads][dim] or [batch][tokens][heads][dim] whose
+    tokens lie at one stride (a slice of a packed projection does)."""
+    _here(t, torch.uint8 if out_fp8 else torch.bfloat16, what)
+    sh, st = t.shape, t.stride()
+    _check(len(sh) in (3, 4) and st[-1] == 1, f"{what}: expected [tokens][heads][dim], dim dense")
+    tok = st[-3]
+    if len(sh) == 4:
+        if sh[1] == 1:
+            tok = st[0]
+        _check(sh[0] == 1 or st[0] == sh[1] * tok, f"{what}: tokens must lie at one stride")
+    return kvq.kvq_heads(t.data_ptr(), tok, st[-2], sh[-2])
+
+
+def _query_out(q: torch.Tensor, out: Optional[torch.Tensor], kind: str) -> torch.Tensor:
+    _check(kind in ("bf16", "e4m3"), "q_out_type: bf16 or e4m3")
+    if out is None:
+        return torch.empty(q.shape, dtype=OUT_TORCH[kind], device=q.device)
+    _check(out.numel() == q.numel() and out.shape[-2:] == q.shape[-2:], "q_out: expected q's shape")
+    return out
+
+
+def _head_scale(t: Optional[torch.Tensor], heads: int) -> Optional[torch.Tensor]:
+    if t is not None:
+        _here(t, torch.float32, "q_head_scale")
+        _check(t.numel() == heads and t.is_contiguous(), "q_head_scale: one scale per query head")
+    return t
+
+
+def norm_rope(rotary: Rotary, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+              positions: Optional[torch.Tensor], q_out: Optional[torch.Tensor] = None,
+              k_out: Optional[torch.Tensor] = None, q_out_type: str = "bf16",
+              q_scale: float = 1.0, q_head_scale: Optional[torch.Tensor] = None,
+              error_flag: Optional[torch.Tensor] = None, stream=None):
+    """Norm and rotation of queries and keys (kvq_norm_rope): q bf16 [T][Hq][D] and k
+    bf16 [T][Hk][D], positions int32 [T].  Returns (q_out, k_out): new tensors, or the
+    given ones (bf16 outputs may be the inputs).  q_out_type "e4m3": uint8 codes."""
+    some = q if q is not None else k
+    _check(some is not None, "norm_rope: q or k is needed")
+    _check(some.dim() == 3, "norm_rope: expected [tokens][heads][dim]")
+    T, D = some.shape[0], some.shape[2]
+    _check(k is None or k.dim() == 3 and (k.shape[0], k.shape[2]) == (T, D),
+           "k: expected q's tokens and dim")
+    rotary.check_dim(None if q is None else D, None if k is None else D)
+    if positions is not None:
+        _index(positions, T, "positions")
+    fp8 = q_out_type == "e4m3"
+    qh = qo = kh = ko = None
+    if q is not None:
+        q_out = _query_out(q, q_out, q_out_type)
+        _head_scale(q_head_scale, q.shape[1])
+        if T:
+            qh, qo = _heads(q, "q"), _heads(q_out, "q_out", fp8)
+    if k is not None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+        _check(k_out.shape == k.shape, "k_out: expected k's shape")
+        if T:
+            kh, ko = _heads(k, "k"), _heads(k_out, "k_out")
+    if T:
+        kvq.check(kvq.kvq_norm_rope(rotary.struct(), D, T, positions, qh, qo, 1 if fp8 else 0, q_scale,
+                                    q_head_scale, kh, ko, error_flag, stream), "kvq_norm_rope")
+    return q_out, k_out
+
+
 class QuantizedKVCache:
     """Paged FP8 / NVFP4 KV cache (layout of ``kvq_cache`` in include/kvq.h).
 
@@ -58,6 +181,44 @@ class QuantizedKVCache:
             return t
         self.k_head_scale, self.v_head_scale = _hs(k_head_scale), _hs(v_head_scale)
 
+    @classmethod
+    def wrap(cls, fmt: str, k_codes: torch.Tensor, v_codes: torch.Tensor,
+             block_table: torch.Tensor, k_scale: float, v_scale: float,
+             k_bscale: Optional[torch.Tensor] = None, v_bscale: Optional[torch.Tensor] = None,
+             k_head_scale: Optional[torch.Tensor] = None,
+             v_head_scale: Optional[torch.Tensor] = None) -> "QuantizedKVCache":
+        """A cache over tensors that the caller holds (K and V in the layout above;
+        not MLA): nothing is allocated or copied."""
+        _check(k_codes.dim() == 4 and k_codes.shape == v_codes.shape,
+               "codes: expected [pages][kv heads][page size][row], K as V")
+        pages, hkv, ps, row = k_codes.shape
+        D = row if fmt == "fp8" else 2 * row
+        arrays = [(k_codes, "k_codes"), (v_codes, "v_codes")]
+        if fmt == "nvfp4":
+            arrays += [(k_bscale, "k_bscale"), (v_bscale, "v_bscale")]
+            for t in (k_bscale, v_bscale):
+                _check(t is not None and t.shape == (pages, hkv, ps, D // 16),
+                       "bscale: expected [pages][kv heads][page size][head_dim / 16]")
+        for t, what in arrays:
+            _here(t, torch.uint8, what)
+            _check(t.is_contiguous(), f"{what}: expected a contiguous tensor")
+        _here(block_table, torch.int32, "block_table")
+        _check(block_table.dim() == 2 and block_table.is_contiguous(),
+               "block_table: expected a contiguous [batch][pages]")
+        for t in (k_head_scale, v_head_scale):
+            if t is not None:
+                _here(t, torch.float32, "head scales")
+                _check(t.numel() == hkv and t.is_contiguous(), "head scales: one per kv head")
+        self = cls.__new__(cls)
+        self.fmt, self.num_pages, self.page_size = fmt, pages, ps
+        self.Hkv, self.D, self.rope = hkv, D, 0
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        self.k_codes, self.v_codes, self.k_pe = k_codes, v_codes, None
+        self.k_bscale, self.v_bscale = k_bscale, v_bscale
+        self.block_table, self.max_pages_per_seq = block_table, block_table.shape[1]
+        self.k_head_scale, self.v_head_scale = k_head_scale, v_head_scale
+        return self
+
     @property
     def mla(self) -> bool:
         return self.rope > 0
@@ -88,6 +249,50 @@ class QuantizedKVCache:
         B, T = k_new.shape[0], k_new.shape[1]
         kvq.check(kvq.kvq_quantize_append(self.struct(), k_new, v_new, kpe_new, start_pos, B, T,
                                           stream), "kvq_quantize_append")
+
+    def append_rope(self, rotary: Rotary, k_new: torch.Tensor, v_new: Optional[torch.Tensor],
+                    start_pos: torch.Tensor, kpe_new: Optional[torch.Tensor] = None,
+                    new_lens: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                    q_out: Optional[torch.Tensor] = None, q_out_type: Optional[str] = None,
+                    q_scale: float = 1.0, q_head_scale: Optional[torch.Tensor] = None,
+                    error_flag: Optional[torch.Tensor] = None,
+                    stream=None) -> Optional[torch.Tensor]:
+        """Append with the keys' norm and rotation, and the queries' in the same launch
+        (kvq_rope_append): k_new/v_new bf16 [B][T][Hkv][D], q bf16 [B][T][Hq][D], all of
+        them strided as a packed projection's slices are; start_pos int32 [B]; new_lens
+        int32 [B] or None (all T).  MLA: k_new the latents [B][T][1][512], kpe_new
+        [B][T][1][64].  Returns q_out (q_out_type "bf16", or "e4m3": uint8 codes; by
+        default q_out's own type, bf16 without one)."""
+        _check(k_new.dim() == 4, "k_new: expected [batch][tokens][kv heads][dim]")
+        B, T = k_new.shape[:2]
+        _check(k_new.shape[2:] == (self.Hkv, self.D), "k_new: expected the cache's heads and dim")
+        _check(self.mla or v_new is not None and v_new.shape == k_new.shape,
+               "v_new: expected k_new's shape")
+        _check(not self.mla or kpe_new is not None and kpe_new.shape == (B, T, 1, self.rope),
+               "kpe_new: expected [batch][tokens][1][rope]")
+        _check(B <= self.block_table.shape[0], "more requests than the block table has")
+        _check(q is None or q.dim() == 4 and q.shape[:2] == (B, T) and q.shape[3] == self.D,
+               "q: expected [batch][tokens][heads][dim]")
+        rotary.check_dim(None if q is None else self.D, self.D)
+        fp8 = False
+        if q is not None:
+            kind = q_out_type or ("e4m3" if q_out is not None and q_out.dtype == torch.uint8 else "bf16")
+            q_out = _query_out(q, q_out, kind)
+            _head_scale(q_head_scale, q.shape[2])
+            fp8 = kind == "e4m3"
+        if B == 0 or T == 0:
+            return q_out
+        _index(start_pos, B, "start_pos")
+        if new_lens is not None:
+            _index(new_lens, B, "new_lens")
+        kvq.check(kvq.kvq_rope_append(
+            self.struct(), rotary.struct(), B, T, start_pos, new_lens, _heads(k_new, "k_new"),
+            None if v_new is None else _heads(v_new, "v_new"),
+            None if kpe_new is None else _heads(kpe_new, "kpe_new"),
+            None if q is None else _heads(q, "q"),
+            None if q is None else _heads(q_out, "q_out", fp8), 1 if fp8 else 0, q_scale,
+            q_head_scale, error_flag, stream), "kvq_rope_append")
+        return q_out
 
 
 @dataclasses.dataclass
