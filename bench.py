@@ -68,7 +68,7 @@ def hbm_peak():
 KERNEL_SOURCES = {
     "decode": ["kvq_decode.cuh", "kvq_decode.cu", "kvq_decode_nvfp4.cu", "kvq_attn.cuh",
                "kvq_device.cuh", "kvq_internal.h"],
-    "mla": ["kvq_mla.cu", "kvq_attn.cuh", "kvq_device.cuh", "kvq_internal.h"],
+    "mla": ["kvq_mla.cu", "kvq_attn.cuh", "kvq_tc.cuh", "kvq_device.cuh", "kvq_internal.h"],
 }
 
 

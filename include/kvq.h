@@ -382,6 +382,51 @@ kvq_status kvq_decode(const kvq_cache* c, const kvq_decode_params* p, const void
                       void* stream);
 
 /*
+ * kvq_decode for a batch whose requests share their first prefix_len tokens,
+ * in the same pages (a system prompt, a document, the common past of sampled
+ * answers): the shared tokens are read once for all requests, and their
+ * scores and values are products of all query rows of a kv head, on the
+ * tensor cores.  The result is kvq_decode's.
+ *   c, p       as for kvq_decode, with each request's whole block table and
+ *              length: tokens prefix_len .. seq_lens[b] - 1 are its own.  A
+ *              request shorter than prefix_len (0 for a padded row) takes no
+ *              part in the sharing and reads its own table only.
+ *   prefix_len (host) a multiple of page_size, at most p->max_kv_len; 0 is
+ *              kvq_decode.
+ *   prefix_table (device int32, optional) [prefix_len / page_size] the shared
+ *              pages; NULL: the first entries of the first row of the block
+ *              table.
+ *   prefix_splits, p->num_splits: chunks of the prefix (at least one 128-token
+ *              tile each: more are lowered) and of each request's own tokens;
+ *              kvq_shared_splits picks both.  Together at most 64.
+ *   part_o, part_lse, counters (device): as for kvq_decode, sized for
+ *              p->num_splits + prefix_splits splits; part_o 32-byte aligned.
+ * FP8 and NVFP4 caches with head_dim 64 or 128, bf16 or FP8 queries, per-head
+ * scales; not MLA, and prob_scale must be 0 (KVQ_ERR_UNSUPPORTED).
+ * fresh_tokens is taken as 0 where prefix_len is positive.  The prefix's
+ * probabilities are rounded to 11 bits for the products with V where the
+ * output is bf16 or E4M3, and kept to 22 for fp32.
+ * Two launches on `stream`; calls that share partials or counters must not
+ * overlap on the GPU.
+ */
+kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int prefix_len,
+                             const int32_t* prefix_table, int prefix_splits, const void* q,
+                             float* part_o, float* part_lse, uint32_t* counters, void* out,
+                             void* stream);
+
+/*
+ * Split counts for kvq_decode_shared (host only, deterministic): own_splits
+ * from kvq_auto_splits of max_own_len (the longest own part), at most 16;
+ * prefix_splits, at most 64 - own_splits and one per 128 tokens, minimizes the
+ * time of the prefix's grid (num_kv_heads x row tiles x splits CTAs, one per
+ * SM, where a row tile is 128 of the batch * q_per_kv rows, or 256 if there
+ * are more).
+ */
+kvq_status kvq_shared_splits(int num_sms, int batch, int num_kv_heads, int q_per_kv,
+                             int prefix_len, int max_own_len, int fmt,
+                             int* prefix_splits /* host */, int* own_splits /* host */);
+
+/*
  * Prefill attention over the cache (Model-Optimizer PR 1832: the prefill
  * kernel of its latency tables, timed against split-KV decode): causal, no
  * KV split.  Request b holds seq_lens[b] = L tokens, the last q_len of them

@@ -491,6 +491,37 @@ kvq_status kvq_auto_splits(int num_sms, int batch, int num_kv_heads, int q_per_k
   return KVQ_OK;
 }
 
+kvq_status kvq_shared_splits(int num_sms, int batch, int num_kv_heads, int q_per_kv,
+                             int prefix_len, int max_own_len, int fmt, int* prefix_splits,
+                             int* own_splits) {
+  if (!prefix_splits || !own_splits || prefix_len < 0 || max_own_len < 0 || q_per_kv < 1)
+    return KVQ_ERR_INVALID;
+  kvq_status s = kvq_auto_splits(num_sms, batch, num_kv_heads, q_per_kv, max_own_len, fmt,
+                                 own_splits);
+  if (s != KVQ_OK) return s;
+  *own_splits = std::min(*own_splits, 16);
+  const long long rows = (long long)batch * q_per_kv;
+  const long long base = num_kv_heads * (rows > 128 ? (rows + 255) / 256 : 1);
+  const long long tiles = ((long long)prefix_len + 127) / 128;
+  const long long most = std::min<long long>(tiles, 64 - *own_splits);
+  // The split count whose waves of one CTA per SM take the fewest tile times:
+  // kFixed for a CTA's start and end, kMerge for each partial that the merge
+  // reads.
+  constexpr double kFixed = 4.0, kMerge = 0.1;
+  double best = 0;
+  int pick = 1;
+  for (long long k = 1; k <= most; ++k) {
+    const double waves = (double)((base * k + num_sms - 1) / num_sms);
+    const double cost = waves * ((double)((tiles + k - 1) / k) + kFixed) + kMerge * (double)k;
+    if (k == 1 || cost < best) {
+      best = cost;
+      pick = (int)k;
+    }
+  }
+  *prefix_splits = pick;
+  return KVQ_OK;
+}
+
 size_t kvq_partial_workspace_bytes(int batch, int num_q_heads, int num_splits, int v_dim) {
   if (batch < 0 || num_q_heads < 0 || num_splits < 0 || v_dim < 0) return 0;
   const size_t rows = (size_t)batch * num_q_heads * num_splits;
@@ -501,10 +532,13 @@ size_t kvq_partial_workspace_bytes(int batch, int num_q_heads, int num_splits, i
 
 namespace {
 
-// Shared body of kvq_decode_partial and kvq_decode (fused when counters).
+// Shared body of kvq_decode_partial and kvq_decode (fused when counters), and
+// of kvq_decode_shared: with prefix_splits > 0 the requests start at token
+// prefix_len, and the merge takes the preceding kernel's prefix_splits
+// partials in too.
 kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const void* q,
                        float* part_o, float* part_lse, uint32_t* counters, void* out,
-                       cudaStream_t stream) {
+                       cudaStream_t stream, int prefix_len = 0, int prefix_splits = 0) {
   kvq_status s = check_cache(c);
   if (s != KVQ_OK) return s;
   s = check_params(p);
@@ -551,6 +585,7 @@ kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const voi
   a.max_pages = c->max_pages_per_seq;
   a.num_pages = c->num_pages;
   a.num_splits = p->num_splits;
+  a.part_splits = p->num_splits;
   a.max_kv_len = p->max_kv_len;
   a.Dv = p->v_dim;
   a.score_floats = (int)score_floats;
@@ -561,6 +596,12 @@ kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const voi
   a.prob_scale = p->prob_scale;
   if (probq) a.prob_fast = prob_reciprocal_ok(p->prob_scale, &a.prob_recip) ? 1 : 0;
   a.fresh = p->fresh_tokens;
+  if (prefix_splits > 0) {
+    a.fresh = 0;
+    a.part_splits = p->num_splits + prefix_splits;
+    a.skip = prefix_len;
+    a.late_merge = 1;
+  }
   a.counters = counters;
   a.out = out;
   a.out_dtype = p->out_dtype;
@@ -612,6 +653,81 @@ kvq_status kvq_decode(const kvq_cache* c, const kvq_decode_params* p, const void
   if (p && p->batch > 0 && (!counters || !out)) return KVQ_ERR_INVALID;
   return decode_impl(c, p, q, part_o, part_lse, counters, out,
                      as_stream(stream));
+}
+
+kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int prefix_len,
+                             const int32_t* prefix_table, int prefix_splits, const void* q,
+                             float* part_o, float* part_lse, uint32_t* counters, void* out,
+                             void* stream) {
+  kvq_status s = check_cache(c);
+  if (s != KVQ_OK) return s;
+  s = check_params(p);
+  if (s != KVQ_OK) return s;
+  if (prefix_len < 0 || prefix_len % c->page_size != 0 || prefix_len > p->max_kv_len)
+    return KVQ_ERR_INVALID;
+  if (prefix_len > 0 && prefix_splits < 1) return KVQ_ERR_INVALID;
+  if (p->batch > 0 && (!q || !aligned16(q) || !part_o || !part_lse || !counters || !out))
+    return KVQ_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(part_o) & 31u) return KVQ_ERR_INVALID;
+  if (p->num_q_heads % c->num_kv_heads != 0) return KVQ_ERR_INVALID;
+  if (is_mla(c) || p->prob_scale > 0.f) return KVQ_ERR_UNSUPPORTED;
+  const int D = c->head_dim;
+  if (p->qk_dim != D || p->v_dim != D) return KVQ_ERR_INVALID;
+  if (D != 64 && D != 128) return KVQ_ERR_UNSUPPORTED;
+  const int G = p->num_q_heads / c->num_kv_heads;
+  if (G > kMaxGroup) return KVQ_ERR_UNSUPPORTED;
+  if ((long long)p->max_kv_len > (long long)c->max_pages_per_seq * c->page_size)
+    return KVQ_ERR_INVALID;
+  if (p->batch == 0) return KVQ_OK;
+  if (prefix_len == 0)
+    return decode_impl(c, p, q, part_o, part_lse, counters, out, as_stream(stream));
+  // a prefix split holds at least one 128-token tile
+  const int tiles = (prefix_len + 127) / 128;
+  if (prefix_splits > tiles) prefix_splits = tiles;
+  if (p->num_splits + prefix_splits > kMaxFusedSplits) return KVQ_ERR_UNSUPPORTED;
+  if ((long long)p->batch * p->num_q_heads * (p->num_splits + prefix_splits) >= (1LL << 31) ||
+      c->num_kv_heads > 65535)
+    return KVQ_ERR_UNSUPPORTED;
+  SharedArgs a{};
+  a.q = q;
+  a.q_fp8 = p->q_fp8;
+  a.q_scale = p->q_scale;
+  a.q_hs = p->q_fp8 ? p->q_head_scale : nullptr;
+  a.k_bscale = static_cast<const uint8_t*>(c->k_bscale);
+  a.v_bscale = static_cast<const uint8_t*>(c->v_bscale);
+  a.prefix_table = prefix_table ? prefix_table : c->block_table;
+  a.seq_lens = p->seq_lens;
+  a.part_o = part_o;
+  a.part_lse = part_lse;
+  a.error_flag = p->error_flag;
+  a.R = p->batch * G;
+  a.G = G;
+  a.Hq = p->num_q_heads;
+  a.Hkv = c->num_kv_heads;
+  a.ps = c->page_size;
+  a.num_pages = c->num_pages;
+  a.prefix = prefix_len;
+  a.splits = prefix_splits;
+  a.box = 16;   // TMA boxes: the largest power of two up to a tile that divides the pages
+  while (a.box < 128 && c->page_size % (2 * a.box) == 0) a.box *= 2;
+  a.split0 = p->num_splits;
+  a.part_splits = p->num_splits + prefix_splits;
+  a.wide_p = p->out_dtype == KVQ_OUT_F32;
+  a.sm_scale = p->sm_scale;
+  a.k_scale = c->k_scale;
+  a.v_scale = c->v_scale;
+  a.k_hs = c->k_head_scale;
+  a.v_hs = c->v_head_scale;
+  const uint64_t rows = (uint64_t)c->num_pages * c->num_kv_heads * c->page_size;
+  const uint64_t row_bytes = c->fmt == KVQ_FP8_E4M3 ? D : D / 2;
+  TensorMaps maps;
+  if (!make_row_map(&maps.k16, c->k_codes, row_bytes, rows, (uint32_t)a.box) ||
+      !make_row_map(&maps.v16, c->v_codes, row_bytes, rows, (uint32_t)a.box))
+    return KVQ_ERR_CUDA;
+  s = cuda_status(launch_shared_prefix(c->fmt, D, maps, a, as_stream(stream)));
+  if (s != KVQ_OK) return s;
+  return decode_impl(c, p, q, part_o, part_lse, counters, out, as_stream(stream), prefix_len,
+                     prefix_splits);
 }
 
 kvq_status kvq_decode_combine(const kvq_decode_params* p, const float* part_o,

@@ -464,7 +464,7 @@ template <int DT>
 __device__ __forceinline__ void merge_staged(const PartialArgs& a, size_t row0, int rows,
                                              const float* staged, const float* w,
                                              const float* winv, bool ok) {
-  const int s = a.num_splits, nq = a.Dv / 4;
+  const int s = a.part_splits, nq = a.Dv / 4;
   const float4* po = reinterpret_cast<const float4*>(staged);
 #pragma unroll 1
   for (int i = threadIdx.x; i < rows * nq; i += blockDim.x) {
@@ -501,7 +501,7 @@ __device__ __forceinline__ void fused_combine_staged(const PartialArgs& a, int b
   }
   __syncthreads();
   if (!is_last) return;
-  const int s = a.num_splits;
+  const int s = a.part_splits;
   float* winv = wbuf + kMaxGroup * kMaxFusedSplits;
   const uint64_t bytes = (uint64_t)rows * s * a.Dv * 4;
   if (bytes > cap) {

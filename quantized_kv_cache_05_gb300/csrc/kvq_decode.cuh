@@ -147,7 +147,10 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
-  if (a.fresh == 0) griddep_wait();
+  // Behind the shared prefix's kernel (a.late_merge) it reads nothing of that
+  // kernel's before the merge, and that kernel let it start only after its
+  // own wait for everything earlier.
+  if (a.fresh == 0 && !a.late_merge) griddep_wait();
 
   // one-page requests: the page index does not depend on the length, so its
   // load overlaps the length's
@@ -161,6 +164,11 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     if (threadIdx.x == 0) record_error(a.error_flag, 2);
     L = L < 0 ? 0 : cap;
   }
+  // a shared prefix is not this kernel's (a.skip is a whole number of pages)
+  if (a.skip > 0 && L >= a.skip) {
+    L -= a.skip;
+    bt += a.skip / a.ps;
+  }
   long c = ((long)L + a.num_splits - 1) / a.num_splits;
   c = (c + 15) / 16 * 16;
   const int cstart = (int)min((long)split * c, (long)L);
@@ -168,7 +176,9 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
   const int nboxes = (cend - cstart + kBoxTokens - 1) / kBoxTokens;
   // first box of the chunk that holds an appended position (overlap mode)
   const int fresh_box = a.fresh == 0 ? 0 : (max(L - a.fresh, cstart) - cstart) / kBoxTokens;
-  bool dep_done = a.fresh == 0;   // this thread has waited for the preceding kernel
+  // this thread has waited for the preceding kernel (no load has to, behind
+  // the shared prefix's)
+  bool dep_done = a.fresh == 0 && !a.late_merge;
   // this warp's boxes: warp, warp + NW, ...
   const int nw = nboxes > warp ? (nboxes - warp + NW - 1) / NW : 0;
   const int total = kSweeps * nw;
@@ -220,7 +230,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
       }
     }
     const long row = ((long)page * a.Hkv + h) * a.ps + off;
-    if (!dep_done && box >= fresh_box) {
+    if (!dep_done && !a.late_merge && box >= fresh_box) {
       griddep_wait();
       dep_done = true;
     }
@@ -627,7 +637,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
                            : ex2(sm.m[w][row] - M) / Ltot * out_mult;
     float lse = (M == -INFINITY || Ltot == 0.f) ? -INFINITY : (M + log2f(Ltot)) * kLn2;
     if (bad) lse = NAN;
-    a.part_lse[(part_row + row) * a.num_splits + split] = lse;
+    a.part_lse[(part_row + row) * a.part_splits + split] = lse;
   }
   __syncthreads();
 
@@ -649,9 +659,9 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     }
     if (bad) acc = make_float4(NAN, NAN, NAN, NAN);
     const int d0 = (D / 8) * (ln >> 2) + 2 * i;
-    float* r0 = a.part_o + ((part_row + h0) * a.num_splits + split) * D + d0;
+    float* r0 = a.part_o + ((part_row + h0) * a.part_splits + split) * D + d0;
     *reinterpret_cast<float2*>(r0) = make_float2(acc.x, acc.z);
-    if (h0 + 1 < a.G) *reinterpret_cast<float2*>(r0 + (size_t)a.num_splits * D) =
+    if (h0 + 1 < a.G) *reinterpret_cast<float2*>(r0 + (size_t)a.part_splits * D) =
         make_float2(acc.y, acc.w);
   }
   // fused combine: the G rows' partials staged at the ring base (the O
@@ -682,7 +692,7 @@ cudaError_t launch_partial_t(const TensorMaps& m, const PartialArgs& a, cudaStre
     // that keeps ctas_per_sm CTAs resident (228 KB per SM, 1 KB reserved per
     // CTA, the static part under 4 KB, the alignment slack)
     constexpr size_t kPerCta = 233472 / ctas_per_sm<FMT, D, PROBQ, NH, NW>() - 1024 - 4096 - 1024;
-    const size_t need = 1024 + (size_t)a.G * a.num_splits * a.Dv * 4 +
+    const size_t need = 1024 + (size_t)a.G * a.part_splits * a.Dv * 4 +
                         (kMaxGroup * kMaxFusedSplits + kMaxGroup) * 4;
     smem = std::max(smem, std::min(need, kPerCta));
   }

@@ -84,6 +84,36 @@ struct PartialArgs {
   // MLA fused decode launched as clusters of the s splits of a request: the
   // partials merge through distributed shared memory (no counters used)
   int cluster_merge;
+  // partials of one row that the merge joins (>= num_splits; this launch
+  // writes 0 .. num_splits - 1 of them)
+  int part_splits;
+  // shared-prefix decode: requests of at least `skip` tokens (whole pages)
+  // start there, and the preceding kernel in the stream writes the partials
+  // num_splits .. part_splits - 1: only the merge waits for it
+  int skip;
+  int late_merge;
+};
+
+// The shared prefix's partials (kvq_shared.cu).
+struct SharedArgs {
+  const void* q;              // as PartialArgs
+  int q_fp8;
+  float q_scale;
+  const float* q_hs;
+  const uint8_t* k_bscale;
+  const uint8_t* v_bscale;
+  const int32_t* prefix_table;
+  const int32_t* seq_lens;
+  float* part_o;
+  float* part_lse;
+  int32_t* error_flag;
+  int R, G, Hq, Hkv, ps, num_pages;   // R = batch * G rows per kv head
+  int prefix, splits, box;            // tokens, splits of this kernel, TMA box rows
+  int split0, part_splits;            // first split's index among a row's partials, their number
+  int wide_p;                         // 1: P as high part and residual (fp32 outputs)
+  float sm_scale, k_scale, v_scale;
+  const float* k_hs;
+  const float* v_hs;
 };
 
 // Rows of heads: head h of token t starts at data + t * token_stride + h *
@@ -196,6 +226,8 @@ cudaError_t launch_mla_partial(const CUtensorMap& tcodes, const CUtensorMap& tpe
                                const CUtensorMap& tcodes64, const CUtensorMap& tpe64,
                                const PartialArgs& a, cudaStream_t st);
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st);
+cudaError_t launch_shared_prefix(int fmt, int D, const TensorMaps& m, const SharedArgs& a,
+                                 cudaStream_t st);
 cudaError_t launch_prefill(int fmt, int D, const TensorMaps& m, const PartialArgs& a,
                            cudaStream_t st);
 

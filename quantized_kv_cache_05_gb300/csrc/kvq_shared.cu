@@ -1,0 +1,578 @@
+// Attention of a whole batch's query rows over a prefix that all requests
+// share, on the 5th-generation tensor cores (sm_103a).
+//
+// All B requests hold the same first tokens, in the same pages.  For one kv
+// head the rows q[b][g] of its B x G query heads are then one matrix Q [R][D],
+// and the prefix's part of the split-KV decode is one attention
+//   S = sm_scale Q K^T,  P = exp(S - max),  O = P V
+// that reads K and V once for every 256 rows instead of once per request.  The
+// kernel writes it as split partials (o normalized, lse) of the shape that the
+// split-KV decode merges; the decode kernel does the requests' own tokens and
+// the merge.  Rows of requests shorter than the prefix take no part (their
+// partial is empty; the decode kernel reads all their tokens).
+//
+// One CTA per SM runs one split for MT x 128 rows, in tiles of 128 tokens:
+//  * a TMA warp brings the tile's codes (boxes of whole 16- to 128-token page
+//    pieces) and block scales into a raw ring;
+//  * four convert warps widen them to f16 (exact: E4M3, and E2M1 times its
+//    block scale, are f16 values) into two K and two V operand tiles in the
+//    128-byte swizzle -- once for all of the CTA's rows.  Rows past the prefix
+//    become zeros, so that nothing a page holds there reaches a result;
+//  * one thread issues tcgen05 MMAs (f16, M = 128): S = Q K^T (K-major K tile)
+//    and O += P V (the V tile read MN-major, P from tensor memory);
+//  * two sets of four softmax warps, one row per thread (so a row's maximum and
+//    sum need no shuffle), turn S into P in place: P's f16 pairs overwrite the
+//    S columns already read.  Their slots alternate on the tensor pipe: two row
+//    tiles with one K/V tile (MT = 2), or even and odd token tiles of one row
+//    tile with accumulators of their own that are joined at the end (MT = 1).
+// The query rows are prescaled by a power of two into f16 (kvq_device.cuh): the
+// bf16 values are exact.  P is scaled by 2^7 against the row's (lazily moving)
+// maximum, which keeps probabilities down to 2^-32 of the largest in f16; its
+// rounding, 2^-12 relative, is under that of bf16 and E4M3 outputs (2^-9,
+// 2^-4).  For fp32 outputs P is an f16 high part plus an f16 residual (two
+// MMAs, 22 bits).  Sums and accumulators are fp32.
+// Every wait is bounded; a timeout sets an error bit and the partials become
+// NaN.
+
+#include "kvq_attn.cuh"
+#include "kvq_tc.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kTok = 128;                 // tokens per tile
+constexpr int kCol = kTok * 128;          // bytes of 64 f16 columns of 128 rows
+constexpr int kConvWarp = 8;              // warps 0-7 softmax (slots 0, 1)
+constexpr int kConvWarps = 4;
+constexpr int kMmaWarp = kConvWarp + kConvWarps, kTmaWarp = kMmaWarp + 1;
+constexpr int kSharedThreads = 32 * (kTmaWarp + 1);
+constexpr float kPShift = 7.0f;           // log2 scale of P
+constexpr int kTmem = 512;                // S0 | S1 | O0 | O1, 128 columns each
+
+template <int FMT, int D, int MT>
+struct SharedGeom {
+  using Gm = Geom<FMT, D>;
+  static constexpr int kCols = D / 64;                  // 64-dim operand columns
+  static constexpr int kTile = kCols * kCol;            // one f16 operand tile
+  static constexpr int kRawCodes = kTok * Gm::kRow;
+  static constexpr int kRaw = (kRawCodes + kTok * Gm::kSRow + 1023) / 1024 * 1024;
+  static constexpr int kOffK = MT * kTile;              // Q tiles, then two K, two V
+  static constexpr int kOffV = kOffK + 2 * kTile;
+  static constexpr int kOffRaw = kOffV + 2 * kTile;
+  // raw ring: as many K and V slots as fit, at most four
+  static constexpr int kRoom = (229376 - kOffRaw) / (2 * kRaw);
+  static constexpr int kSlots = kRoom < 4 ? kRoom : 4;
+  static constexpr int kOffCtl = kOffRaw + 2 * kSlots * kRaw;
+  static_assert(kSlots >= 1, "shared memory");
+};
+
+struct SharedCtl {
+  uint64_t raw_full[2][4], raw_empty[2][4];   // [K, V][slot]
+  uint64_t op_full[2][2], op_empty[2][2];     // [K, V][operand tile]
+  uint64_t s_full[2], p_full[2], o_full[2];   // per softmax slot
+  uint64_t q_full, mma_done;
+  uint32_t tmem;
+  int abort_flag;
+  float m[2][kTok], l[2][kTok];               // MT = 1: the slots' states
+};
+
+__device__ __forceinline__ void st_v8(float* p, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+template <int FMT, int D, int MT, bool P2>
+__global__ void __launch_bounds__(kSharedThreads, 1)
+    shared_prefix_kernel(const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const SharedArgs a) {
+  using Gm = Geom<FMT, D>;
+  using Sg = SharedGeom<FMT, D, MT>;
+  extern __shared__ __align__(1024) uint8_t dyn_smem[];   // the swizzle period
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(dyn_smem);
+  SharedCtl& sm = *reinterpret_cast<SharedCtl*>(dyn_smem + Sg::kOffCtl);
+  volatile int* abort_flag = &sm.abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      for (int k = 0; k < Sg::kSlots; ++k) {
+        mbar_init(smem_u32(&sm.raw_full[i][k]), 1);
+        mbar_init(smem_u32(&sm.raw_empty[i][k]), kConvWarps);
+      }
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(smem_u32(&sm.op_full[i][k]), kConvWarps);
+        mbar_init(smem_u32(&sm.op_empty[i][k]), 1);
+      }
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.p_full[i]), 4);
+      mbar_init(smem_u32(&sm.o_full[i]), 1);
+    }
+    mbar_init(smem_u32(&sm.q_full), 4 * MT);
+    mbar_init(smem_u32(&sm.mma_done), 1);
+    sm.abort_flag = (base & 1023u) != 0;   // (never: the array is aligned)
+    fence_barrier_init();
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&sm.tmem)),
+                 "r"(kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // Every thread waits for the earlier work before any of them lets the decode
+  // kernel start: it reads its inputs without a wait of its own.
+  griddep_wait();
+  griddep_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  const int h = blockIdx.y, split = blockIdx.z;
+  const int row0 = blockIdx.x * (MT * kTok);
+  // tiles [t0, t1) of the prefix
+  const int tiles = (a.prefix + kTok - 1) / kTok;
+  const int t0 = (int)((long)split * tiles / a.splits);
+  const int t1 = (int)((long)(split + 1) * tiles / a.splits);
+  const int nt = t1 - t0;
+  const int units = MT * nt;   // (slot, token tile) pairs in tensor-pipe order
+
+  auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
+    if (wait_or_abort(smem_u32(&bar), parity, abort_flag)) return true;
+    *abort_flag = 1;
+    return false;
+  };
+
+  if (warp == kTmaWarp) {
+    // ================================================================= TMA
+    int issued[2] = {0, 0};
+    for (int j = 0; j < nt; ++j) {
+      const int tok0 = (t0 + j) * kTok;
+      const int nb = (min(kTok, a.prefix - tok0) + a.box - 1) / a.box;
+      // lane i holds the cache row of box i (at most eight boxes)
+      int row = 0;
+      if (lane < nb) {
+        const int tok = tok0 + lane * a.box, pidx = tok / a.ps;
+        int page = __ldg(a.prefix_table + pidx);
+        if (page < 0 || page >= a.num_pages) {
+          record_error(a.error_flag, 4);
+          page = 0;
+        }
+        row = (int)(((long)page * a.Hkv + h) * a.ps + (tok - pidx * a.ps));
+      }
+      const int slot = j % Sg::kSlots;
+      const uint32_t round = (uint32_t)(j / Sg::kSlots);
+      bool ok = true;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (round > 0) ok = ok && wait(sm.raw_empty[kv][slot], (round - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t full = smem_u32(&sm.raw_full[kv][slot]);
+        const uint32_t dst = base + Sg::kOffRaw + (2 * slot + kv) * Sg::kRaw;
+        if (lane == 0) mbar_arrive_expect_tx(full, nb * a.box * (Gm::kRow + Gm::kSRow));
+        __syncwarp();
+        if (lane < nb) {
+          tma_load_2d(dst + lane * a.box * Gm::kRow, kv ? &tmV : &tmK, 0, row, full);
+          if constexpr (FMT == kFmtNvfp4)
+            bulk_load(dst + Sg::kRawCodes + lane * a.box * Gm::kSRow,
+                      (kv ? a.v_bscale : a.k_bscale) + (long)row * Gm::kSRow, a.box * Gm::kSRow,
+                      full);
+        }
+        issued[kv] = j + 1;
+      }
+      if (!ok) break;
+    }
+    // no copy in flight at exit (bounded waits)
+    if (lane == 0)
+      for (int kv = 0; kv < 2; ++kv)
+        for (int j = max(0, issued[kv] - Sg::kSlots); j < issued[kv]; ++j)
+          mbar_wait(smem_u32(&sm.raw_full[kv][j % Sg::kSlots]), (j / Sg::kSlots) & 1);
+  } else if (warp == kMmaWarp) {
+    // ================================================================= MMA
+    if (lane == 0) {
+      constexpr uint32_t kIdS = idesc(0, 0, 0, kTok), kIdO = idesc(0, 0, 1, D);
+      const uint64_t dq = sdesc(base, 16, 1024);
+      const uint64_t dk = sdesc(base + Sg::kOffK, 16, 1024);
+      const uint64_t dv = sdesc(base + Sg::kOffV, kCol, 1024);   // MN-major
+      bool ok = nt == 0 || wait(sm.q_full, 0);
+      // unit u: slot u & 1; token tile u / MT
+      auto issue_s = [&](int u) {
+        const int j = u / MT, slot = u & 1;
+        // the first use of a K tile waits for it
+        if (MT == 1 || slot == 0) ok = ok && wait(sm.op_full[0][j & 1], (j >> 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t q = dq + (uint64_t)((MT == 2 ? slot : 0) * Sg::kTile >> 4);
+        const uint64_t k = dk + (uint64_t)((j & 1) * Sg::kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = (uint64_t)(((kk >> 2) * kCol + (kk & 3) * 32) >> 4);
+          mma(tmem + slot * 128, q + off, k + off, kIdS, kk > 0);
+        }
+        mma_commit(smem_u32(&sm.s_full[slot]));
+        if (MT == 1 || slot == 1) mma_commit(smem_u32(&sm.op_empty[0][j & 1]));
+      };
+      for (int u = 0; u < min(2, units) && ok; ++u) issue_s(u);
+      for (int u = 0; u < units && ok; ++u) {
+        const int j = u / MT, slot = u & 1, i = u >> 1;   // the slot's i-th unit
+        ok = wait(sm.p_full[slot], i & 1);
+        if (ok && (MT == 1 || slot == 0)) ok = wait(sm.op_full[1][j & 1], (j >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t v = dv + (uint64_t)((j & 1) * Sg::kTile >> 4);
+        const uint32_t p = tmem + slot * 128, o = tmem + 256 + slot * 128;
+#pragma unroll
+        for (int kk = 0; kk < kTok / 16; ++kk) {
+          const uint64_t vk = v + (uint64_t)(kk * 2048 >> 4);
+          if constexpr (P2) {   // high parts and residuals in alternating 16-column groups
+            const uint32_t pk = p + 32 * (kk >> 1) + 8 * (kk & 1);
+            mma_ts(o, pk, vk, kIdO, i > 0 || kk > 0);
+            mma_ts(o, pk + 16, vk, kIdO, true);
+          } else {
+            mma_ts(o, p + 8 * kk, vk, kIdO, i > 0 || kk > 0);
+          }
+        }
+        mma_commit(smem_u32(&sm.o_full[slot]));
+        if (MT == 1 || slot == 1) mma_commit(smem_u32(&sm.op_empty[1][j & 1]));
+        if (u + 2 < units) issue_s(u + 2);
+      }
+      // every MMA of this thread has completed at exit (bounded waits)
+      mma_commit(smem_u32(&sm.mma_done));
+      mbar_wait(smem_u32(&sm.mma_done), 0);
+    }
+    __syncwarp();
+  } else if (warp >= kConvWarp) {
+    // ============================================================= convert
+    const int t = threadIdx.x - 32 * kConvWarp;
+    const int p = t & 7, r = t;   // row r of the tile; its atom row p (r = 8 (t >> 3) + p)
+    for (int j = 0; j < nt; ++j) {
+      const int slot = j % Sg::kSlots;
+      const int nvalid = a.prefix - (t0 + j) * kTok;
+      bool ok = true;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t raw = base + Sg::kOffRaw + (2 * slot + kv) * Sg::kRaw;
+        const uint32_t dst = base + (kv ? Sg::kOffV : Sg::kOffK) + (j & 1) * Sg::kTile +
+                             (r >> 3) * 1024 + p * 128;
+        ok = wait(sm.raw_full[kv][slot], (j / Sg::kSlots) & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        constexpr int kChunks = Gm::kRow / 16;
+        uint4 v[kChunks];
+        uint32_t sc[FMT == kFmtNvfp4 ? kChunks : 1];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          v[c] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < nvalid) v[c] = lds128(raw + r * Gm::kRow + (Gm::swz(r, c) << 4));
+        }
+        if constexpr (FMT == kFmtNvfp4) {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            sc[c] = r < nvalid ? lds16(raw + Sg::kRawCodes + r * Gm::kSRow + 2 * c) : 0u;
+        }
+        // the operand tile was last read by the MMAs of tile j - 2
+        if (j >= 2) ok = wait(sm.op_empty[kv][j & 1], ((j >> 1) - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if constexpr (FMT == kFmtFp8) {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {   // 16 dims: two 16-byte pieces
+            uint32_t o[8];
+            e4m3x4_to_f16x2x2(v[c].x, o[0], o[1]);
+            e4m3x4_to_f16x2x2(v[c].y, o[2], o[3]);
+            e4m3x4_to_f16x2x2(v[c].z, o[4], o[5]);
+            e4m3x4_to_f16x2x2(v[c].w, o[6], o[7]);
+            const uint32_t row = dst + (c >> 2) * kCol;
+            const int q = 2 * (c & 3);
+            sts128(row + ((q ^ p) << 4), o[0], o[1], o[2], o[3]);
+            sts128(row + (((q + 1) ^ p) << 4), o[4], o[5], o[6], o[7]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {   // 32 dims, two block scales
+            const uint32_t s2 = e4m3x2_to_f16x2(sc[c]);
+            const uint32_t s_lo = __byte_perm(s2, 0, 0x1010), s_hi = __byte_perm(s2, 0, 0x3232);
+            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+            const uint32_t row = dst + (c >> 1) * kCol;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t e0, e1, e2, e3;
+              e2m1x8_to_f16x2x4(w[k], e0, e1, e2, e3);
+              const uint32_t s = k < 2 ? s_lo : s_hi;
+              const int q = 4 * (c & 1) + k;
+              sts128(row + ((q ^ p) << 4), hmul2(e0, s), hmul2(e1, s), hmul2(e2, s),
+                     hmul2(e3, s));
+            }
+          }
+        }
+        fence_proxy_async_shared();   // generic stores -> operands of the async MMAs
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sm.op_full[kv][j & 1]));
+          mbar_arrive(smem_u32(&sm.raw_empty[kv][slot]));
+        }
+      }
+      if (!__all_sync(0xffffffffu, ok)) break;
+    }
+  } else {
+    // ============================================================= softmax
+    const int slot = warp >> 2;
+    const int r = threadIdx.x & 127;              // row of the slot's tile
+    const int row = row0 + (MT == 2 ? slot * kTok : 0) + r;
+    const bool live = row < a.R;
+    const int b = live ? row / a.G : 0, g = live ? row - b * a.G : 0;
+    const int hq = h * a.G + g;
+    const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t sS = lane_addr + slot * 128, sO = lane_addr + 256 + slot * 128;
+
+    // ---- the row's query, into its operand tile
+    float qsc;   // score scale, log2 domain
+    {
+      const float k_log2 =
+          (a.k_hs ? a.sm_scale * __ldg(a.k_hs + h) : a.sm_scale * a.k_scale) * 1.4426950408889634f;
+      const size_t qrow = (size_t)b * a.Hq + hq;
+      const uint32_t dst = base + (MT == 2 ? slot * Sg::kTile : 0) + (r >> 3) * 1024 + (r & 7) * 128;
+      const bool store = MT == 2 || slot == 0;
+      if (a.q_fp8) {
+        const uint8_t* qp = static_cast<const uint8_t*>(a.q) + qrow * D;
+        qsc = k_log2 * (a.q_hs ? __ldg(a.q_hs + hq) : a.q_scale);
+        if (store) {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            const uint4 v = live ? *reinterpret_cast<const uint4*>(qp + 16 * c)
+                                 : make_uint4(0u, 0u, 0u, 0u);
+            uint32_t o[8];
+            e4m3x4_to_f16x2x2(v.x, o[0], o[1]);
+            e4m3x4_to_f16x2x2(v.y, o[2], o[3]);
+            e4m3x4_to_f16x2x2(v.z, o[4], o[5]);
+            e4m3x4_to_f16x2x2(v.w, o[6], o[7]);
+            const uint32_t at = dst + (c >> 2) * kCol;
+            const int q = 2 * (c & 3);
+            sts128(at + ((q ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+            sts128(at + (((q + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+          }
+        }
+      } else {
+        const uint16_t* qp = static_cast<const uint16_t*>(a.q) + qrow * D;
+        uint4 v[D / 8];
+        uint32_t m2 = 0;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          v[c] = live ? *reinterpret_cast<const uint4*>(qp + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+          m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v[c].x & 0x7FFF7FFFu, v[c].y & 0x7FFF7FFFu),
+                                     __vmaxu2(v[c].z & 0x7FFF7FFFu, v[c].w & 0x7FFF7FFFu)));
+        }
+        const int e = q_prescale_exp(max(m2 & 0xFFFFu, m2 >> 16));
+        const float f = exp2i(e);
+        qsc = scale_pow2(k_log2, -e);
+        if (store) {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              o[k] = pack_f16x2(__uint_as_float(w[k] << 16) * f,
+                                __uint_as_float(w[k] & 0xFFFF0000u) * f);
+            sts128(dst + (c >> 3) * kCol + (((c & 7) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (store && lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+    }
+
+    // ---- the slot's units
+    const int cnt = MT == 2 ? nt : (nt + 1 - slot) / 2;
+    float m = -INFINITY, l = 0.f;   // reference max (log2), sum of 2^(x - m + 7)
+    for (int i = 0; i < cnt; ++i) {
+      const int j = MT == 2 ? i : 2 * i + slot;
+      const int nvalid = a.prefix - (t0 + j) * kTok;
+      if (!__all_sync(0xffffffffu, wait(sm.s_full[slot], i & 1))) break;
+      tc_fence_after();
+      uint32_t s[32];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        tmem_ld32(sS + 32 * c, s);
+        tmem_wait_ld32(s);
+        if (nvalid >= kTok) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(s[k]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (32 * c + k < nvalid) mx = fmaxf(mx, __uint_as_float(s[k]));
+        }
+      }
+      mx *= qsc;
+      const bool move = mx > m + kLazyMax;   // also the first finite tile
+      if (__any_sync(0xffffffffu, move)) {
+        const float alpha = move ? ex2(m - mx) : 1.f;
+        m = move ? mx : m;
+        l *= alpha;
+        // O of the slot's earlier units (complete: this unit's S was committed
+        // after them)
+        if (i > 0) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            tmem_ld32(sO + 32 * c, s);
+            tmem_wait_ld32(s);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * alpha);
+            tmem_st32(sO + 32 * c, s);
+          }
+        }
+      }
+      const float ref = (m == -INFINITY ? 0.f : m) - kPShift;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        tmem_ld32(sS + 32 * c, s);
+        tmem_wait_ld32(s);
+        uint32_t hi[16], lo[16];
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          float p0 = ex2(fmaf(__uint_as_float(s[2 * k]), qsc, -ref));
+          float p1 = ex2(fmaf(__uint_as_float(s[2 * k + 1]), qsc, -ref));
+          if (nvalid < kTok) {
+            if (32 * c + 2 * k >= nvalid) p0 = 0.f;
+            if (32 * c + 2 * k + 1 >= nvalid) p1 = 0.f;
+          }
+          sum += p0 + p1;
+          hi[k] = pack_f16x2(p0, p1);
+          if constexpr (P2) {
+            const float2 f = unpack_f16x2(hi[k]);
+            lo[k] = pack_f16x2(p0 - f.x, p1 - f.y);
+          }
+        }
+        l += sum;
+        tmem_st16(sS + (P2 ? 32 * c : 16 * c), hi);
+        if constexpr (P2) tmem_st16(sS + 32 * c + 16, lo);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[slot]));
+    }
+
+    // ---- the row's partial
+    const float out_mult = a.v_hs ? __ldg(a.v_hs + h) : a.v_scale;
+    const bool share = live && __ldg(a.seq_lens + b) >= a.prefix;
+    const size_t prow = ((size_t)b * a.Hq + hq) * a.part_splits + a.split0 + split;
+    if constexpr (MT == 1) {   // the other slot's state
+      sm.m[slot][r] = m;
+      sm.l[slot][r] = l;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+    }
+    const int cnt1 = nt / 2;   // MT = 1: units of slot 1
+    bool done = true;
+    if (MT == 2) {
+      if (cnt > 0) done = wait(sm.o_full[slot], (cnt - 1) & 1);
+    } else if (nt > 0) {
+      done = wait(sm.o_full[0], (nt - 1 - cnt1) & 1);
+      if (cnt1 > 0) done = wait(sm.o_full[1], (cnt1 - 1) & 1) && done;
+    }
+    const bool bad = __any_sync(0xffffffffu, !done || *abort_flag != 0);
+    tc_fence_after();
+    float f[2] = {0.f, 0.f};   // factors of the slots' accumulators
+    float lse = -INFINITY;
+    {
+      const float m0 = MT == 1 ? sm.m[0][r] : m, l0 = MT == 1 ? sm.l[0][r] : l;
+      const float m1 = MT == 1 ? sm.m[1][r] : -INFINITY, l1 = MT == 1 ? sm.l[1][r] : 0.f;
+      const float M = fmaxf(m0, m1);
+      const float e0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), e1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+      const float L = e0 * l0 + e1 * l1;
+      // l0, l1 may be NaN (a NaN or infinite score): it passes through
+      if (M != -INFINITY && L != 0.f) {
+        f[0] = e0 / L * out_mult;
+        f[1] = e1 / L * out_mult;
+        lse = (M - kPShift + log2f(L)) * kLn2;
+      } else if (!(l0 == 0.f && l1 == 0.f)) {
+        f[0] = f[1] = NAN;
+        lse = NAN;
+      }
+    }
+    if (live && (MT == 2 || slot == 0))
+      a.part_lse[prow] = !share ? -INFINITY : bad ? NAN : lse;
+    // MT = 2: the slot's own O; MT = 1: both, half of the dims per slot
+    constexpr int kChunks = MT == 2 ? D / 32 : D / 64;
+    const int c0 = MT == 2 ? 0 : slot * kChunks;
+    float* po = a.part_o + prow * D;
+#pragma unroll 1
+    for (int c = c0; c < c0 + kChunks; ++c) {
+      uint32_t s[32];
+      float o[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = 0.f;
+      if (nt > 0 && !bad) {
+        tmem_ld32(lane_addr + 256 + (MT == 2 ? slot * 128 : 0) + 32 * c, s);
+        tmem_wait_ld32(s);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(s[k]) * f[0];
+        if (MT == 1 && cnt1 > 0) {
+          tmem_ld32(lane_addr + 256 + 128 + 32 * c, s);
+          tmem_wait_ld32(s);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] += __uint_as_float(s[k]) * f[1];
+        }
+      }
+      if (live) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = !share ? 0.f : bad ? NAN : o[8 * k + e];
+          st_v8(po + 32 * c + 8 * k, v);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) record_error(a.error_flag, 1);
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem)
+                 : "memory");
+  }
+}
+
+template <int FMT, int D, int MT, bool P2>
+cudaError_t launch_shared_t(const TensorMaps& m, const SharedArgs& a, cudaStream_t st) {
+  using Sg = SharedGeom<FMT, D, MT>;
+  constexpr size_t smem = Sg::kOffCtl + sizeof(SharedCtl);
+  static_assert(smem <= 232448, "shared memory of one CTA");
+  auto kern = shared_prefix_kernel<FMT, D, MT, P2>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int tiles = (a.R + MT * kTok - 1) / (MT * kTok);
+  return launch_pdl(kern, dim3(tiles, a.Hkv, a.splits), dim3(kSharedThreads), smem, st, m.k16,
+                    m.v16, a);
+}
+
+template <int FMT, int D>
+cudaError_t dispatch_shared(const TensorMaps& m, const SharedArgs& a, cudaStream_t st) {
+  if (a.R > kTok)
+    return a.wide_p ? launch_shared_t<FMT, D, 2, true>(m, a, st)
+                    : launch_shared_t<FMT, D, 2, false>(m, a, st);
+  return a.wide_p ? launch_shared_t<FMT, D, 1, true>(m, a, st)
+                  : launch_shared_t<FMT, D, 1, false>(m, a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_shared_prefix(int fmt, int D, const TensorMaps& m, const SharedArgs& a,
+                                 cudaStream_t st) {
+  if (fmt == kFmtFp8 && D == 128) return dispatch_shared<kFmtFp8, 128>(m, a, st);
+  if (fmt == kFmtFp8 && D == 64) return dispatch_shared<kFmtFp8, 64>(m, a, st);
+  if (fmt == kFmtNvfp4 && D == 128) return dispatch_shared<kFmtNvfp4, 128>(m, a, st);
+  if (fmt == kFmtNvfp4 && D == 64) return dispatch_shared<kFmtNvfp4, 64>(m, a, st);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace kvq

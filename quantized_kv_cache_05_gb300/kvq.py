@@ -87,6 +87,10 @@ SIGNATURES = {
     "kvq_quantize_fp8": (_int, [_P, _sz, _f, _P, _int, _int, _P, _P]),
     "kvq_prefill": (_int, [ctypes.POINTER(kvq_cache), ctypes.POINTER(kvq_decode_params), _int,
                            _P, _P, _P]),
+    "kvq_decode_shared": (_int, [ctypes.POINTER(kvq_cache), ctypes.POINTER(kvq_decode_params),
+                                 _int, _P, _int, _P, _P, _P, _P, _P, _P]),
+    "kvq_shared_splits": (_int, [_int, _int, _int, _int, _int, _int, _int, ctypes.POINTER(_int),
+                                 ctypes.POINTER(_int)]),
     "kvq_norm_rope": (_int, [ctypes.POINTER(kvq_rotary), _int, _int, _P, _heads_p, _heads_p, _int,
                              _f, _P, _heads_p, _heads_p, _P, _P]),
     "kvq_rope_append": (_int, [ctypes.POINTER(kvq_cache), ctypes.POINTER(kvq_rotary), _int, _int,
@@ -263,3 +267,20 @@ def kvq_rope_append(cache: kvq_cache, rotary: kvq_rotary, batch: int, n_tokens: 
                                  _addr(new_lens), _ref(k), _ref(v), _ref(kpe), _ref(q),
                                  _ref(q_out), q_fp8, q_scale, _addr(q_head_scale),
                                  _addr(error_flag), _stream(stream))
+
+
+def kvq_decode_shared(cache: kvq_cache, params: kvq_decode_params, prefix_len: int, prefix_table,
+                      prefix_splits: int, q, part_o, part_lse, counters, out, stream=None) -> int:
+    """kvq_decode with the batch's shared first prefix_len tokens computed once."""
+    return lib().kvq_decode_shared(_ref(cache), _ref(params), prefix_len, _addr(prefix_table),
+                                   prefix_splits, _addr(q), _addr(part_o), _addr(part_lse),
+                                   _addr(counters), _addr(out), _stream(stream))
+
+
+def kvq_shared_splits(num_sms: int, batch: int, num_kv_heads: int, q_per_kv: int, prefix_len: int,
+                      max_own_len: int, fmt: int) -> tuple[int, int, int]:
+    """(status, prefix splits, own splits) for kvq_decode_shared."""
+    sp, so = _int(0), _int(0)
+    st = lib().kvq_shared_splits(num_sms, batch, num_kv_heads, q_per_kv, prefix_len, max_own_len,
+                                 fmt, ctypes.byref(sp), ctypes.byref(so))
+    return st, int(sp.value), int(so.value)

@@ -399,3 +399,57 @@ def prefill(cache: QuantizedKVCache, q: torch.Tensor, seq_lens: torch.Tensor, cf
     p = cfg.params(seq_lens, error_flag)
     kvq.check(kvq.kvq_prefill(cache.struct(), p, q_len, q, out, stream), "kvq_prefill")
     return out
+
+
+class SharedDecode:
+    """Decode steps of a batch whose requests share their first prefix_len tokens
+    (kvq_decode_shared): the configuration and its scratch, kept between steps.
+    Steps of one object must not overlap on the GPU (they share the scratch)."""
+
+    def __init__(self, cache: QuantizedKVCache, batch: int, num_q_heads: int, prefix_len: int,
+                 max_kv_len: int, sm_scale: float, out: str = "bf16", out_scale: float = 1.0,
+                 q_fp8: bool = False, q_scale: float = 1.0,
+                 q_head_scale: Optional[torch.Tensor] = None,
+                 prefix_table: Optional[torch.Tensor] = None,
+                 splits: Optional[tuple[int, int]] = None):
+        """prefix_table: the shared pages (int32; default: the first row of the cache's
+        block table); splits: (prefix, own) chunks, by default kvq_shared_splits'."""
+        _check(0 <= prefix_len <= max_kv_len, "prefix_len: expected 0 .. max_kv_len")
+        _check(batch <= cache.block_table.shape[0], "more requests than the block table has")
+        _check(num_q_heads % cache.Hkv == 0, "num_q_heads: a multiple of the kv heads")
+        device = cache.k_codes.device
+        if prefix_table is not None:
+            _here(prefix_table, torch.int32, "prefix_table")
+            _check(prefix_table.is_contiguous() and
+                   prefix_table.numel() * cache.page_size >= prefix_len,
+                   "prefix_table: one page per page_size shared tokens")
+        if splits is None:
+            sms = torch.cuda.get_device_properties(device).multi_processor_count
+            st, sp, so = kvq.kvq_shared_splits(sms, max(batch, 1), cache.Hkv,
+                                               num_q_heads // cache.Hkv, prefix_len,
+                                               max_kv_len - prefix_len, FMT[cache.fmt])
+            kvq.check(st, "kvq_shared_splits")
+        else:
+            sp, so = splits
+        self.cache, self.prefix_len, self.prefix_table, self.prefix_splits = (
+            cache, prefix_len, prefix_table, sp)
+        cfg = self.cfg = DecodeConfig(batch, num_q_heads, cache.D, cache.D, so, max_kv_len, sm_scale,
+                                      out=out, out_scale=out_scale, q_fp8=q_fp8, q_scale=q_scale,
+                                      q_head_scale=_head_scale(q_head_scale, num_q_heads))
+        self.ws = FusedWorkspace(dataclasses.replace(cfg, num_splits=so + sp), cache.Hkv, device)
+
+    def __call__(self, q: torch.Tensor, seq_lens: torch.Tensor,
+                 error_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """q bf16 (FP8 query: uint8) [batch][Hq][D], seq_lens int32 [batch] (whole lengths)
+        -> the output buffer [batch][Hq][D], overwritten by the next step."""
+        cfg, ws = self.cfg, self.ws
+        _here(q, torch.uint8 if cfg.q_fp8 else torch.bfloat16, "q")
+        _check(q.shape == (cfg.batch, cfg.num_q_heads, cfg.qk_dim) and q.is_contiguous(),
+               "q: expected a contiguous [batch][heads][dim]")
+        _index(seq_lens, cfg.batch, "seq_lens")
+        if cfg.batch:
+            kvq.check(kvq.kvq_decode_shared(
+                self.cache.struct(), cfg.params(seq_lens, error_flag), self.prefix_len,
+                self.prefix_table, self.prefix_splits, q, ws.part_o, ws.part_lse, ws.counters,
+                ws.out, stream), "kvq_decode_shared")
+        return ws.out

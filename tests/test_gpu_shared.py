@@ -1,0 +1,370 @@
+"""Decode of a batch that shares a prefix (kvq_decode_shared) against softmax
+attention in 64 bits over the dequantized cache.
+
+Bounds.  With A = sum_j softmax_j |v_j| per output: a weight's relative error is
+that of its exponent -- the score's fp32 accumulation, at most (D / 8) 2^-23 of
+sum_d |q_d k_d| sm_scale (16 products per step, each step's sum rounded at worst
+by one unit of 2^-23, twice that for the split accumulators), the exponent's own
+rounding, below 2^-22 of its magnitude (at most 2^5 here), and 2^-22 of the
+exponential -- and, where the output is not fp32, P's rounding to f16, at most
+2^-11.  Numerator and denominator both carry the former.  Sums of up to 2^13
+terms in fp32 add 2^-20 (the partials are short and the errors' signs random).
+The output's own rounding is half a step: bf16 2^-8 of the value; an E4M3 code
+lies between those of the interval's ends.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import rope_ref as R
+from quantized_kv_cache_05_gb300 import build as kbuild
+from quantized_kv_cache_05_gb300 import kvq, runtime
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    kbuild.build()
+    kvq.lib()
+    torch.cuda.init()
+    torch.zeros(1, device=DEV)
+
+
+class Batch:
+    """A cache whose requests share `prefix` tokens; `own` tokens each of their own
+    (None: a padded row of length 0; negative: a request of that many tokens
+    altogether, in pages of its own)."""
+
+    def __init__(self, fmt, D, hq, hkv, ps, prefix, own, seed=1, q_fp8=False, head_scales=False,
+                 q_std=1.0, k_ramp=None):
+        g = self.g = torch.Generator(device=DEV).manual_seed(seed)
+        self.fmt, self.D, self.hq, self.hkv, self.ps, self.prefix, self.B = fmt, D, hq, hkv, ps, prefix, len(own)
+        self.lens = [0 if n is None else -n if n < 0 else prefix + n for n in own]
+        per = max(1, -(-(max([0] + self.lens)) // ps), prefix // ps)
+        pre = prefix // ps
+        pages = pre + self.B * per + 1
+        perm = torch.randperm(pages - 1, generator=g, device=DEV).int() + 1   # page 0 is nobody's
+        bt = torch.zeros(self.B, per, dtype=torch.int32, device=DEV)
+        at = pre
+        for b, n in enumerate(own):
+            need = -(-self.lens[b] // ps)
+            if n is not None and n >= 0:
+                bt[b, :pre] = perm[:pre]
+                bt[b, pre:need] = perm[at:at + need - pre]
+                at += need - pre
+            else:
+                bt[b, :need] = perm[at:at + need]
+                at += need
+        self.shared_pages = perm[:pre].contiguous()
+        self.bt = bt
+        self.cap = per * ps
+        x = [torch.randn(pages, hkv, ps, D, generator=g, device=DEV) for _ in range(2)]
+        if k_ramp is not None:   # scores that grow (or shrink) along the shared tokens
+            for i, page in enumerate(self.shared_pages.tolist()):
+                t = i * ps + torch.arange(ps, device=DEV)
+                x[0][page] *= (k_ramp[0] + (k_ramp[1] - k_ramp[0]) * t / prefix)[None, :, None]
+        hs = [torch.linspace(0.009, 0.02, hkv, device=DEV) * s if head_scales else None for s in (1, 1.3)]
+        sc = (0.0137, 0.0119) if fmt == "fp8" else (0.0023, 0.0029)
+        if fmt == "nvfp4" and head_scales:
+            hs = [h * 0.15 for h in hs]
+        self.codes, self.bscale, self.val = [], [], []
+        for t, h, s in zip(x, hs, sc):
+            scale = h[None, :, None, None] if h is not None else torch.tensor(s, device=DEV)
+            if fmt == "fp8":
+                c = (t / scale).clamp(-448, 448).to(torch.float8_e4m3fn)
+                self.codes.append(c.view(torch.uint8))
+                self.bscale.append(None)
+                self.val.append(c.double() * scale.double())
+            else:
+                blk = t.reshape(pages, hkv, ps, D // 16, 16)
+                bs = (blk.abs().amax(-1) / 6 / scale).clamp(max=448).to(torch.float8_e4m3fn)
+                es = bs.double() * scale.double()
+                grid = torch.tensor(R.E2M1_POS, device=DEV)
+                idx = ((blk.double().abs() / es[..., None])[..., None] - grid).abs().argmin(-1)
+                sign = blk < 0
+                nib = (idx + 8 * sign).to(torch.uint8).reshape(pages, hkv, ps, D // 2, 2)
+                self.codes.append((nib[..., 0] | (nib[..., 1] << 4)).contiguous())
+                self.bscale.append(bs.view(torch.uint8).contiguous())
+                self.val.append((grid[idx] * torch.where(sign, -1.0, 1.0) * es[..., None]).reshape(pages, hkv, ps, D))
+        self.cache = runtime.QuantizedKVCache.wrap(fmt, *self.codes, bt, *sc, *self.bscale, *hs)
+        self.lens_t = torch.tensor(self.lens, device=DEV).int()
+        q = torch.randn(self.B, hq, D, generator=g, device=DEV) * q_std
+        self.q_fp8, self.q_scale = q_fp8, 0.017
+        if q_fp8:
+            c = (q / self.q_scale).clamp(-448, 448).to(torch.float8_e4m3fn)
+            self.q, self.q64 = c.view(torch.uint8), c.double() * float(np.float32(self.q_scale))
+        else:
+            self.q = q.bfloat16()
+            self.q64 = self.q.double()
+        self.sm = 1 / math.sqrt(D)
+
+    def reference(self):
+        """(output, bound on the error before the output's rounding) in 64 bits; the
+        bound without P's rounding."""
+        G = self.hq // self.hkv
+        sm = float(np.float32(self.sm))
+        out = torch.zeros(self.B, self.hq, self.D, dtype=torch.float64, device=DEV)
+        tol, mag = out.clone(), out.clone()
+        for b, n in enumerate(self.lens):
+            if not n:
+                continue
+            pg = self.bt[b, :-(-n // self.ps)].long()
+            for h in range(self.hkv):
+                k, v = (x[pg, h].reshape(-1, self.D)[:n] for x in self.val)
+                q = self.q64[b, h * G:(h + 1) * G]
+                s = q @ k.T * sm
+                p = torch.softmax(s, 1)
+                A = p @ v.abs()
+                eps = (q.abs() @ k.abs().T * sm).amax(1, keepdim=True) * (self.D / 8) * 2.0 ** -23
+                eps = eps + 2.0 ** -17 + 2.0 ** -22
+                hs = slice(h * G, (h + 1) * G)
+                out[b, hs], mag[b, hs] = p @ v, A
+                tol[b, hs] = A * (2 * eps + 2.0 ** -20)
+        return out.cpu().numpy(), tol.cpu().numpy(), mag.cpu().numpy()
+
+    def plan(self, out="bf16", splits=None, **kw):
+        return runtime.SharedDecode(self.cache, self.B, self.hq, self.prefix, self.cap, self.sm, out=out,
+                                    out_scale=0.004, q_fp8=self.q_fp8, q_scale=self.q_scale, splits=splits, **kw)
+
+    def check(self, got, out, ref=None, rows=None, what=""):
+        o, tol, mag = ref or self.reference()
+        if out != "f32":
+            tol = tol + 2.0 ** -11 * mag
+        if rows is not None:
+            o, tol, got = o[rows], tol[rows], got[rows]
+        g = got.double().cpu().numpy() if out != "e4m3" else R.e4m3_values(got.cpu().numpy())
+        if out == "e4m3":
+            s = float(np.float32(0.004))
+            bad = ~((g >= R.round_value((o - tol) / s * (1 + 1e-6 * -np.sign(o - tol)), R.E4M3_POS)) &
+                    (g <= R.round_value((o + tol) / s * (1 + 1e-6 * np.sign(o + tol)), R.E4M3_POS)))
+        else:
+            lim = tol + (np.abs(o) + tol) * (2.0 ** -8 if out == "bf16" else 2.0 ** -23)
+            bad = ~(np.abs(g - o) <= lim)
+        assert not bad.any(), (f"{what}: {bad.sum()} of {bad.size} off, worst "
+                               f"{np.nanmax(np.abs(g - o)) if out != 'e4m3' else 'code'}, at {np.argwhere(bad)[0]}")
+
+
+def run(B, out="bf16", splits=None, **kw):
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    plan = B.plan(out, splits, **kw)
+    o = plan(B.q, B.lens_t, error_flag=flag).clone()
+    torch.cuda.synchronize()
+    assert int(flag) == 0
+    assert int(plan.ws.counters.abs().sum()) == 0
+    return o
+
+
+OWN = [5, 0, 70, 1, 33]
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (3, 3), (14, 2), (16, 1)])
+@pytest.mark.parametrize("ps,prefix", [(16, 16), (16, 400), (48, 768), (128, 1280), (256, 256)])
+def test_few_rows(fmt, D, hq, hkv, ps, prefix):
+    """Up to 128 rows per kv head: one row tile, token tiles in two alternating slots."""
+    B = Batch(fmt, D, hq, hkv, ps, prefix, OWN)
+    ref = B.reference()
+    for splits in (None, (1, 1), (3, 2), (60, 4)):
+        B.check(run(B, "bf16", splits), "bf16", ref, what=f"splits {splits}")
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,hq,hkv", [(16, 8, 1), (43, 6, 2), (70, 4, 1), (130, 4, 1)])
+def test_many_rows(fmt, D, n, hq, hkv):
+    """128 rows exactly, just over, several row tiles with a ragged last one."""
+    own = [(7 * b) % 41 for b in range(n)]
+    B = Batch(fmt, D, hq, hkv, 16, 656, own, seed=n)
+    ref = B.reference()
+    for splits in (None, (1, 1), (5, 1)):
+        B.check(run(B, "bf16", splits), "bf16", ref, what=f"splits {splits}")
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("out", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("q_fp8,head_scales", [(False, False), (True, False), (False, True), (True, True)])
+def test_types(fmt, out, q_fp8, head_scales):
+    for n, D in ((3, 128), (50, 64)):
+        B = Batch(fmt, D, 8, 2, 32, 608, [(11 * b) % 50 for b in range(n)], 3, q_fp8, head_scales)
+        B.check(run(B, out), out)
+
+
+@pytest.mark.parametrize("n", [6, 40])
+def test_idle_and_short_requests(n):
+    """Padded rows give zeros; requests shorter than the prefix read their own pages."""
+    own = [[12, None, -1, 0, -303, None][b % 6] for b in range(n)]
+    B = Batch("fp8", 128, 8, 2, 16, 320, own)
+    for out in ("f32", "bf16"):
+        o = run(B, out, prefix_table=B.shared_pages)
+        B.check(o, out)
+        assert (o[[b for b in range(n) if own[b] is None]] == 0).all()
+    # nobody shares at all
+    B = Batch("fp8", 128, 8, 2, 16, 320, [None, -5] * (n // 2))
+    B.check(run(B, "f32", prefix_table=B.shared_pages), "f32")
+
+
+def test_values_that_nobody_attends_to():
+    """NaN codes after each sequence's end, and in the shared pages for requests that
+    do not share them, reach no output."""
+    own = [9, -40, None, 0]
+    B = Batch("fp8", 128, 8, 2, 16, 160, own)
+    ref = B.reference()
+    for b, n in enumerate(B.lens):
+        if n % 16:
+            page = int(B.bt[b, n // 16])
+            for c in B.codes:
+                c[page, :, n % 16:] = 0x7F
+    B.check(run(B, "f32", prefix_table=B.shared_pages), "f32", ref)
+    for c in B.codes:
+        c[int(B.shared_pages[3]), :, 5] = 0x7F
+    o = B.plan("f32", prefix_table=B.shared_pages)(B.q, B.lens_t)
+    B.check(o, "f32", ref, rows=[1, 2])
+    assert torch.isnan(o[[0, 3]]).all()
+
+
+@pytest.mark.parametrize("ramp", [(0.05, 6.0), (6.0, 0.05), (1.0, 12.0)])
+@pytest.mark.parametrize("n", [3, 40])
+def test_moving_maxima(ramp, n):
+    """Scores that grow by far more than the lazy maximum's headroom, tile by tile."""
+    B = Batch("fp8", 128, 8, 2, 16, 2048, [3] * n, 5, q_std=3.0, k_ramp=ramp)
+    ref = B.reference()
+    # the exponents here reach 2^9: their rounding is 2^-13 of a weight at most
+    ref = (ref[0], ref[1] + 2.0 ** -12 * ref[2], ref[2])
+    for out in ("f32", "bf16"):
+        for splits in ((1, 1), (4, 1)):
+            B.check(run(B, out, splits), out, ref, what=f"{out} {splits}")
+
+
+def test_query_range():
+    """Queries far outside f16: the scores keep their accuracy."""
+    B = Batch("fp8", 64, 4, 2, 16, 512, [4, 20, 0], 2)
+    for e in (-60, 40):
+        B.q64 = (B.q.double() * 2.0 ** e)
+        q = B.q64.bfloat16()
+        assert torch.equal(q.double(), B.q64)
+        old, B.q, sm = B.q, q, B.sm
+        B.sm = sm * 2.0 ** -e
+        B.check(run(B, "f32"), "f32", what=str(e))
+        B.q, B.sm = old, sm
+
+
+def test_is_kvq_decode():
+    """The same call without sharing, and a prefix of length 0."""
+    B = Batch("nvfp4", 128, 8, 2, 16, 480, OWN)
+    cfg = runtime.DecodeConfig(B.B, 8, 128, 128, 3, B.cap, B.sm, out="f32")
+    plain = runtime.decode_fused(B.cache, B.q, B.lens_t, cfg)
+    o = run(B, "f32")
+    tol = 2 * B.reference()[1]
+    assert (np.abs((o - plain).double().cpu().numpy()) <= tol + 1e-9).all()
+    zero = runtime.SharedDecode(B.cache, B.B, 8, 0, B.cap, B.sm, out="f32", splits=(1, 3))
+    assert torch.equal(zero(B.q, B.lens_t), plain)
+
+
+def test_bad_pages_and_lengths():
+    B = Batch("fp8", 64, 4, 2, 16, 160, [4, 20])
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    table = B.shared_pages.clone()
+    for bad in (-1, B.codes[0].shape[0], 2 ** 31 - 1):
+        table[4] = bad
+        flag.zero_()
+        o = B.plan("f32", prefix_table=table)(B.q, B.lens_t, error_flag=flag).clone()
+        assert int(flag) == kvq.KVQ_DEVERR_BAD_PAGE
+        good = B.shared_pages.clone()
+        good[4] = 0      # page 0 is read instead
+        want = B.plan("f32", prefix_table=good)(B.q, B.lens_t)
+        assert torch.equal(o, want)
+    flag.zero_()
+    lens = B.lens_t.clone()
+    lens[0] = B.cap + 1
+    full = B.lens_t.clone()
+    full[0] = B.cap
+    o = B.plan("f32")(B.q, lens, error_flag=flag).clone()
+    assert int(flag) == kvq.KVQ_DEVERR_SEQ_CLAMPED
+    assert torch.equal(o, B.plan("f32")(B.q, full))
+
+
+def test_append_then_decode_in_a_graph():
+    """The step of a serving loop: norm, rotate and append the new tokens, then the
+    shared decode, captured once and replayed with new inputs; two plans of the same
+    cache in one graph keep their scratch apart."""
+    own = [5, 0, 40, 17]
+    B = Batch("fp8", 128, 8, 2, 16, 288, [n + 4 for n in own])
+    G = 4
+    ro = runtime.Rotary(runtime.rope_table(1024, 128), False, 1 + 0.2 * torch.randn(128, device=DEV),
+                        1 + 0.2 * torch.randn(128, device=DEV))
+    x = torch.randn(4, 1, 12 * 128, device=DEV).bfloat16()
+    cut = lambda a, n: x[..., a * 128:(a + n) * 128].unflatten(2, (n, 128))
+    start = torch.tensor([288 + n for n in own], device=DEV).int()
+    lens = start + 1
+    qo = torch.zeros(4, 8, 128, device=DEV).bfloat16()
+    pa, pb = B.plan("f32"), B.plan("bf16")
+
+    def step():
+        B.cache.append_rope(ro, cut(8, 2), cut(10, 2), start, q=cut(0, 8), q_out=qo)
+        return pa(qo, lens), pb(qo, lens)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a, b = step()
+    for k in range(3):
+        x.copy_(torch.randn(x.shape, generator=B.g, device=DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        # the reference from the cache as it stands and the rotated queries
+        B.lens, B.lens_t, B.q, B.q64 = lens.tolist(), lens, qo, qo.double()
+        B.val = [c.view(torch.float8_e4m3fn).double() * float(np.float32(sc))
+                 for c, sc in zip(B.codes, (0.0137, 0.0119))]
+        ref = B.reference()
+        B.check(a, "f32", ref)
+        B.check(b, "bf16", ref)
+        start.add_(1)
+        lens.add_(1)
+
+
+def test_back_to_back_steps_and_streams():
+    """Steps that follow one another without a wait between them, each on new inputs,
+    and two plans on two streams at once."""
+    B = Batch("fp8", 128, 16, 4, 16, 1024, [30] * 20)
+    C = Batch("nvfp4", 64, 8, 1, 16, 512, [10] * 9, seed=9)
+    pb, pc = B.plan("f32"), C.plan("f32")
+    want_b, want_c = pb(B.q, B.lens_t).clone(), pc(C.q, C.lens_t).clone()
+    q2 = B.q.flip(0).contiguous()
+    want2 = pb(q2, B.lens_t).clone()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for k in range(20):
+        with torch.cuda.stream(s1):
+            got.append((pb(B.q if k % 2 else q2, B.lens_t).clone(), want_b if k % 2 else want2))
+        with torch.cuda.stream(s2):
+            got.append((pc(C.q, C.lens_t).clone(), want_c))
+    torch.cuda.synchronize()
+    for g, w in got:
+        assert torch.equal(g, w)
+
+
+def test_runtime_refuses():
+    B = Batch("fp8", 64, 4, 2, 16, 160, [4, 20])
+    for kw in (dict(prefix_len=-16), dict(prefix_len=10 ** 6), dict(batch=3), dict(num_q_heads=5),
+               dict(prefix_table=B.shared_pages[:5]), dict(prefix_table=B.shared_pages.long()),
+               dict(q_head_scale=torch.ones(3, device=DEV))):
+        with pytest.raises(ValueError):
+            runtime.SharedDecode(**{"cache": B.cache, "batch": 2, "num_q_heads": 4, "prefix_len": 160,
+                                    "max_kv_len": B.cap, "sm_scale": 0.1, **kw})
+    plan = B.plan()
+    for args in ((B.q.float(), B.lens_t), (B.q[:1], B.lens_t), (B.q, B.lens_t[:1]), (B.q, B.lens_t.long()),
+                 (B.q.transpose(1, 2), B.lens_t), (B.q.cpu(), B.lens_t)):
+        with pytest.raises(ValueError):
+            plan(*args)
+    with pytest.raises(kvq.KvqError):
+        runtime.SharedDecode(B.cache, 2, 4, 150, B.cap, 0.1)(B.q, B.lens_t)

@@ -1,0 +1,83 @@
+"""kvq_decode_shared and kvq_shared_splits on the host: refusals before any CUDA
+call (the addresses are never touched) and the split rule."""
+import math
+
+import pytest
+
+from quantized_kv_cache_05_gb300 import build as kbuild
+from quantized_kv_cache_05_gb300 import kvq
+
+P = 1 << 20
+OK, INV, UNS = kvq.KVQ_OK, kvq.KVQ_ERR_INVALID, kvq.KVQ_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    kbuild.build()
+    kvq.lib()
+
+
+def cache(**kw):
+    c = kvq.kvq_cache(fmt=kvq.KVQ_FP8_E4M3, num_pages=64, page_size=16, num_kv_heads=2, head_dim=128,
+                      k_codes=P, v_codes=P, k_scale=1.0, v_scale=1.0, block_table=P,
+                      max_pages_per_seq=32)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+def params(**kw):
+    p = kvq.kvq_decode_params(batch=4, num_q_heads=8, qk_dim=128, v_dim=128, num_splits=2, seq_lens=P,
+                              max_kv_len=512, sm_scale=0.1, out_dtype=kvq.KVQ_OUT_BF16, out_scale=1.0)
+    for k, v in kw.items():
+        setattr(p, k, v)
+    return p
+
+
+def call(c=None, p=None, prefix=256, table=None, sp=2, q=P, po=P, pl=P, cn=P, out=P):
+    return kvq.kvq_decode_shared(c or cache(), p or params(), prefix, table, sp, q, po, pl, cn, out, 0)
+
+
+def test_no_batch_is_a_noop():
+    assert call(p=params(batch=0)) == OK
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(prefix=-16), INV), (dict(prefix=250), INV), (dict(prefix=528), INV), (dict(sp=0), INV),
+    (dict(sp=-1), INV), (dict(q=None), INV), (dict(q=P + 8), INV), (dict(po=None), INV),
+    (dict(po=P + 16), INV), (dict(pl=None), INV), (dict(cn=None), INV), (dict(out=None), INV),
+    (dict(p=params(num_splits=0)), INV), (dict(p=params(num_splits=63)), UNS),
+    (dict(p=params(prob_scale=0.1)), UNS), (dict(p=params(num_q_heads=7)), INV),
+    (dict(p=params(num_q_heads=34)), UNS), (dict(p=params(qk_dim=64)), INV),
+    (dict(p=params(v_dim=64)), INV), (dict(p=params(max_kv_len=513)), INV),
+    (dict(p=params(seq_lens=None)), INV), (dict(p=params(sm_scale=math.nan)), INV),
+    (dict(p=params(q_fp8=1, q_scale=0.0)), INV), (dict(p=params(out_dtype=7)), INV),
+    (dict(c=cache(head_dim=256, fmt=kvq.KVQ_NVFP4, k_bscale=P, v_bscale=P),
+          p=params(qk_dim=256, v_dim=256)), UNS),
+    (dict(c=cache(page_size=24)), INV), (dict(c=cache(v_codes=None)), INV),
+    (dict(c=cache(num_kv_heads=70000, num_pages=1), p=params(num_q_heads=70000)), UNS)])
+def test_refused(kw, want):
+    assert call(**kw) == want
+
+
+def test_mla_refused():
+    c = kvq.kvq_cache(fmt=kvq.KVQ_NVFP4, num_pages=8, page_size=16, num_kv_heads=1, head_dim=512,
+                      k_codes=P, k_bscale=P, k_scale=1.0, block_table=P, max_pages_per_seq=32,
+                      rope_dim=64, k_pe=P, v_is_k_latent=1)
+    assert call(c=c, p=params(num_q_heads=16, qk_dim=576, v_dim=512)) == UNS
+
+
+def test_splits():
+    f = kvq.kvq_shared_splits
+    for batch in (1, 4, 31, 64, 200):
+        for hkv, g in ((8, 4), (1, 16), (2, 7), (300, 1)):
+            for prefix in (0, 16, 128, 1040, 32768):
+                for own in (0, 1, 100, 5000):
+                    st, sp, so = f(152, batch, hkv, g, prefix, own, 1)
+                    assert st == OK and 1 <= so <= 16 and 1 <= sp
+                    assert sp <= max(1, (prefix + 127) // 128) and sp + so <= 64
+    # 8 heads x 1 row tile: 19 splits fill the 152 SMs
+    assert f(152, 64, 8, 4, 32768, 1024, 1)[1] == 19
+    assert f(152, 4, 8, 4, 1024, 60, 1)[1] == 8        # one per 128 tokens
+    assert f(0, 4, 8, 4, 1024, 60, 1)[0] == INV and f(152, 4, 8, 0, 1024, 60, 1)[0] == INV
+    assert f(152, 4, 8, 4, -1, 60, 1)[0] == INV and f(152, 4, 8, 4, 16, -1, 1)[0] == INV
