@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 import threading
 from typing import Any, Optional
 
@@ -111,6 +112,8 @@ class KvqError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libkvq.so (built by quantized_kv_cache_05_gb300.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -142,16 +145,23 @@ def _ref(x):
 
 def _stream(s: Any) -> Optional[int]:
     if s is None:
-        try:
-            import torch
-            if torch.cuda.is_available() and torch.cuda.is_initialized():
-                return torch.cuda.current_stream().cuda_stream
-        except Exception:  # pragma: no cover - torch without CUDA
-            pass
-        return None
+        torch = sys.modules.get("torch")
+        if torch is None or not torch.cuda.is_initialized():
+            return None
+        return _raw_stream(torch)
     if isinstance(s, int):
         return s
     return s.cuda_stream
+
+
+def _raw_stream(torch) -> int:
+    """The current stream's handle (the direct query costs a tenth of building the
+    Stream object; the public call serves where a release lacks it)."""
+    c = torch._C
+    try:
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    except AttributeError:  # pragma: no cover - other torch releases
+        return torch.cuda.current_stream().cuda_stream
 
 
 def check(status: int, what: str = "kvq") -> None:

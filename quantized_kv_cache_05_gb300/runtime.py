@@ -35,7 +35,7 @@ def _check(ok: bool, what: str) -> None:
 
 def _here(t: torch.Tensor, dtype: torch.dtype, what: str) -> None:
     """A CUDA tensor of the current device (kernels launch there) and this type."""
-    if t.dtype != dtype or not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.dtype != dtype or not t.is_cuda or t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{what}: expected {dtype} on cuda:{torch.cuda.current_device()}, got "
                          f"{t.dtype} on {t.device}")
 
@@ -43,7 +43,8 @@ def _here(t: torch.Tensor, dtype: torch.dtype, what: str) -> None:
 def _index(t: torch.Tensor, n: int, what: str) -> None:
     """A dense int32 array of n entries."""
     _here(t, torch.int32, what)
-    _check(t.numel() == n and t.is_contiguous(), f"{what}: expected {n} contiguous entries")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous entries")
 
 
 class Rotary:
@@ -82,12 +83,16 @@ def _heads(t: torch.Tensor, what: str, out_fp8: bool = False) -> kvq.kvq_heads:
     tokens lie at one stride (a slice of a packed projection does)."""
     _here(t, torch.uint8 if out_fp8 else torch.bfloat16, what)
     sh, st = t.shape, t.stride()
-    _check(len(sh) in (3, 4) and st[-1] == 1, f"{what}: expected [tokens][heads][dim], dim dense")
-    tok = st[-3]
-    if len(sh) == 4:
-        if sh[1] == 1:
-            tok = st[0]
-        _check(sh[0] == 1 or st[0] == sh[1] * tok, f"{what}: tokens must lie at one stride")
+    n = len(sh)
+    if n == 4:
+        # one token per request: the requests are the tokens
+        tok = st[0] if sh[1] == 1 else st[1]
+        one = sh[0] == 1 or st[0] == sh[1] * tok
+    else:
+        tok, one = st[0], n == 3
+    if not one or st[-1] != 1:
+        raise ValueError(f"{what}: expected [(batch,) tokens][heads][dim] rows, dim dense, the "
+                         "tokens at one stride")
     return kvq.kvq_heads(t.data_ptr(), tok, st[-2], sh[-2])
 
 
