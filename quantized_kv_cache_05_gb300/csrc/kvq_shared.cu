@@ -45,7 +45,11 @@ constexpr int kCol = kTok * 128;          // bytes of 64 f16 columns of 128 rows
 constexpr int kConvWarp = 8;              // warps 0-7 softmax (slots 0, 1)
 constexpr int kConvWarps = 4;
 constexpr int kMmaWarp = kConvWarp + kConvWarps, kTmaWarp = kMmaWarp + 1;
-constexpr int kSharedThreads = 32 * (kTmaWarp + 1);
+constexpr int kSharedThreads = 512;       // four warpgroups: softmax x 2, convert, MMA and TMA
+// Registers per thread of the warpgroups (the launch gives each thread 128, 512
+// for the four): a softmax thread holds its row's 128 scores at once.
+constexpr int kRegSoft = 176, kRegConv = 104, kRegIssue = 56;
+static_assert(2 * kRegSoft + kRegConv + kRegIssue <= 4 * 128, "register pool of the launch");
 constexpr float kPShift = 7.0f;           // log2 scale of P
 constexpr int kTmem = 512;                // S0 | S1 | O0 | O1, 128 columns each
 
@@ -80,6 +84,42 @@ __device__ __forceinline__ void st_v8(float* p, const float (&v)[8]) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
                "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 template <int FMT, int D, int MT, bool P2>
@@ -146,106 +186,110 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     return false;
   };
 
-  if (warp == kTmaWarp) {
-    // ================================================================= TMA
-    int issued[2] = {0, 0};
-    for (int j = 0; j < nt; ++j) {
-      const int tok0 = (t0 + j) * kTok;
-      const int nb = (min(kTok, a.prefix - tok0) + a.box - 1) / a.box;
-      // lane i holds the cache row of box i (at most eight boxes)
-      int row = 0;
-      if (lane < nb) {
-        const int tok = tok0 + lane * a.box, pidx = tok / a.ps;
-        int page = __ldg(a.prefix_table + pidx);
-        if (page < 0 || page >= a.num_pages) {
-          record_error(a.error_flag, 4);
-          page = 0;
-        }
-        row = (int)(((long)page * a.Hkv + h) * a.ps + (tok - pidx * a.ps));
-      }
-      const int slot = j % Sg::kSlots;
-      const uint32_t round = (uint32_t)(j / Sg::kSlots);
-      bool ok = true;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        if (round > 0) ok = ok && wait(sm.raw_empty[kv][slot], (round - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t full = smem_u32(&sm.raw_full[kv][slot]);
-        const uint32_t dst = base + Sg::kOffRaw + (2 * slot + kv) * Sg::kRaw;
-        if (lane == 0) mbar_arrive_expect_tx(full, nb * a.box * (Gm::kRow + Gm::kSRow));
-        __syncwarp();
+  if (warp >= kMmaWarp) {
+  regs_dec<kRegIssue>();
+    if (warp == kTmaWarp) {
+      // ================================================================= TMA
+      int issued[2] = {0, 0};
+      for (int j = 0; j < nt; ++j) {
+        const int tok0 = (t0 + j) * kTok;
+        const int nb = (min(kTok, a.prefix - tok0) + a.box - 1) / a.box;
+        // lane i holds the cache row of box i (at most eight boxes)
+        int row = 0;
         if (lane < nb) {
-          tma_load_2d(dst + lane * a.box * Gm::kRow, kv ? &tmV : &tmK, 0, row, full);
-          if constexpr (FMT == kFmtNvfp4)
-            bulk_load(dst + Sg::kRawCodes + lane * a.box * Gm::kSRow,
-                      (kv ? a.v_bscale : a.k_bscale) + (long)row * Gm::kSRow, a.box * Gm::kSRow,
-                      full);
-        }
-        issued[kv] = j + 1;
-      }
-      if (!ok) break;
-    }
-    // no copy in flight at exit (bounded waits)
-    if (lane == 0)
-      for (int kv = 0; kv < 2; ++kv)
-        for (int j = max(0, issued[kv] - Sg::kSlots); j < issued[kv]; ++j)
-          mbar_wait(smem_u32(&sm.raw_full[kv][j % Sg::kSlots]), (j / Sg::kSlots) & 1);
-  } else if (warp == kMmaWarp) {
-    // ================================================================= MMA
-    if (lane == 0) {
-      constexpr uint32_t kIdS = idesc(0, 0, 0, kTok), kIdO = idesc(0, 0, 1, D);
-      const uint64_t dq = sdesc(base, 16, 1024);
-      const uint64_t dk = sdesc(base + Sg::kOffK, 16, 1024);
-      const uint64_t dv = sdesc(base + Sg::kOffV, kCol, 1024);   // MN-major
-      bool ok = nt == 0 || wait(sm.q_full, 0);
-      // unit u: slot u & 1; token tile u / MT
-      auto issue_s = [&](int u) {
-        const int j = u / MT, slot = u & 1;
-        // the first use of a K tile waits for it
-        if (MT == 1 || slot == 0) ok = ok && wait(sm.op_full[0][j & 1], (j >> 1) & 1);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t q = dq + (uint64_t)((MT == 2 ? slot : 0) * Sg::kTile >> 4);
-        const uint64_t k = dk + (uint64_t)((j & 1) * Sg::kTile >> 4);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t off = (uint64_t)(((kk >> 2) * kCol + (kk & 3) * 32) >> 4);
-          mma(tmem + slot * 128, q + off, k + off, kIdS, kk > 0);
-        }
-        mma_commit(smem_u32(&sm.s_full[slot]));
-        if (MT == 1 || slot == 1) mma_commit(smem_u32(&sm.op_empty[0][j & 1]));
-      };
-      for (int u = 0; u < min(2, units) && ok; ++u) issue_s(u);
-      for (int u = 0; u < units && ok; ++u) {
-        const int j = u / MT, slot = u & 1, i = u >> 1;   // the slot's i-th unit
-        ok = wait(sm.p_full[slot], i & 1);
-        if (ok && (MT == 1 || slot == 0)) ok = wait(sm.op_full[1][j & 1], (j >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t v = dv + (uint64_t)((j & 1) * Sg::kTile >> 4);
-        const uint32_t p = tmem + slot * 128, o = tmem + 256 + slot * 128;
-#pragma unroll
-        for (int kk = 0; kk < kTok / 16; ++kk) {
-          const uint64_t vk = v + (uint64_t)(kk * 2048 >> 4);
-          if constexpr (P2) {   // high parts and residuals in alternating 16-column groups
-            const uint32_t pk = p + 32 * (kk >> 1) + 8 * (kk & 1);
-            mma_ts(o, pk, vk, kIdO, i > 0 || kk > 0);
-            mma_ts(o, pk + 16, vk, kIdO, true);
-          } else {
-            mma_ts(o, p + 8 * kk, vk, kIdO, i > 0 || kk > 0);
+          const int tok = tok0 + lane * a.box, pidx = tok / a.ps;
+          int page = __ldg(a.prefix_table + pidx);
+          if (page < 0 || page >= a.num_pages) {
+            record_error(a.error_flag, 4);
+            page = 0;
           }
+          row = (int)(((long)page * a.Hkv + h) * a.ps + (tok - pidx * a.ps));
         }
-        mma_commit(smem_u32(&sm.o_full[slot]));
-        if (MT == 1 || slot == 1) mma_commit(smem_u32(&sm.op_empty[1][j & 1]));
-        if (u + 2 < units) issue_s(u + 2);
+        const int slot = j % Sg::kSlots;
+        const uint32_t round = (uint32_t)(j / Sg::kSlots);
+        bool ok = true;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          if (round > 0) ok = ok && wait(sm.raw_empty[kv][slot], (round - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t full = smem_u32(&sm.raw_full[kv][slot]);
+          const uint32_t dst = base + Sg::kOffRaw + (2 * slot + kv) * Sg::kRaw;
+          if (lane == 0) mbar_arrive_expect_tx(full, nb * a.box * (Gm::kRow + Gm::kSRow));
+          __syncwarp();
+          if (lane < nb) {
+            tma_load_2d(dst + lane * a.box * Gm::kRow, kv ? &tmV : &tmK, 0, row, full);
+            if constexpr (FMT == kFmtNvfp4)
+              bulk_load(dst + Sg::kRawCodes + lane * a.box * Gm::kSRow,
+                        (kv ? a.v_bscale : a.k_bscale) + (long)row * Gm::kSRow, a.box * Gm::kSRow,
+                        full);
+          }
+          issued[kv] = j + 1;
+        }
+        if (!ok) break;
       }
-      // every MMA of this thread has completed at exit (bounded waits)
-      mma_commit(smem_u32(&sm.mma_done));
-      mbar_wait(smem_u32(&sm.mma_done), 0);
+      // no copy in flight at exit (bounded waits)
+      if (lane == 0)
+        for (int kv = 0; kv < 2; ++kv)
+          for (int j = max(0, issued[kv] - Sg::kSlots); j < issued[kv]; ++j)
+            mbar_wait(smem_u32(&sm.raw_full[kv][j % Sg::kSlots]), (j / Sg::kSlots) & 1);
+    } else if (warp == kMmaWarp) {
+      // ================================================================= MMA
+      if (lane == 0) {
+        constexpr uint32_t kIdS = idesc(0, 0, 0, kTok), kIdO = idesc(0, 0, 1, D);
+        const uint64_t dq = sdesc(base, 16, 1024);
+        const uint64_t dk = sdesc(base + Sg::kOffK, 16, 1024);
+        const uint64_t dv = sdesc(base + Sg::kOffV, kCol, 1024);   // MN-major
+        bool ok = nt == 0 || wait(sm.q_full, 0);
+        // unit u: slot u & 1; token tile u / MT
+        auto issue_s = [&](int u) {
+          const int j = u / MT, slot = u & 1;
+          // the first use of a K tile waits for it
+          if (MT == 1 || slot == 0) ok = ok && wait(sm.op_full[0][j & 1], (j >> 1) & 1);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t q = dq + (uint64_t)((MT == 2 ? slot : 0) * Sg::kTile >> 4);
+          const uint64_t k = dk + (uint64_t)((j & 1) * Sg::kTile >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = (uint64_t)(((kk >> 2) * kCol + (kk & 3) * 32) >> 4);
+            mma(tmem + slot * 128, q + off, k + off, kIdS, kk > 0);
+          }
+          mma_commit(smem_u32(&sm.s_full[slot]));
+          if (MT == 1 || slot == 1) mma_commit(smem_u32(&sm.op_empty[0][j & 1]));
+        };
+        for (int u = 0; u < min(2, units) && ok; ++u) issue_s(u);
+        for (int u = 0; u < units && ok; ++u) {
+          const int j = u / MT, slot = u & 1, i = u >> 1;   // the slot's i-th unit
+          ok = wait(sm.p_full[slot], i & 1);
+          if (ok && (MT == 1 || slot == 0)) ok = wait(sm.op_full[1][j & 1], (j >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t v = dv + (uint64_t)((j & 1) * Sg::kTile >> 4);
+          const uint32_t p = tmem + slot * 128, o = tmem + 256 + slot * 128;
+#pragma unroll
+          for (int kk = 0; kk < kTok / 16; ++kk) {
+            const uint64_t vk = v + (uint64_t)(kk * 2048 >> 4);
+            if constexpr (P2) {   // high parts and residuals in alternating 16-column groups
+              const uint32_t pk = p + 32 * (kk >> 1) + 8 * (kk & 1);
+              mma_ts(o, pk, vk, kIdO, i > 0 || kk > 0);
+              mma_ts(o, pk + 16, vk, kIdO, true);
+            } else {
+              mma_ts(o, p + 8 * kk, vk, kIdO, i > 0 || kk > 0);
+            }
+          }
+          mma_commit(smem_u32(&sm.o_full[slot]));
+          if (MT == 1 || slot == 1) mma_commit(smem_u32(&sm.op_empty[1][j & 1]));
+          if (u + 2 < units) issue_s(u + 2);
+        }
+        // every MMA of this thread has completed at exit (bounded waits)
+        mma_commit(smem_u32(&sm.mma_done));
+        mbar_wait(smem_u32(&sm.mma_done), 0);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else if (warp >= kConvWarp) {
+    regs_dec<kRegConv>();
     // ============================================================= convert
     const int t = threadIdx.x - 32 * kConvWarp;
     const int p = t & 7, r = t;   // row r of the tile; its atom row p (r = 8 (t >> 3) + p)
@@ -317,6 +361,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
     }
   } else {
+    regs_inc<kRegSoft>();
     // ============================================================= softmax
     const int slot = warp >> 2;
     const int r = threadIdx.x & 127;              // row of the slot's tile
@@ -393,22 +438,28 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       const int nvalid = a.prefix - (t0 + j) * kTok;
       if (!__all_sync(0xffffffffu, wait(sm.s_full[slot], i & 1))) break;
       tc_fence_after();
-      uint32_t s[32];
-      float mx = -INFINITY;
+      uint32_t s[4][32];   // the row's scores
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        tmem_ld32(sS + 32 * c, s);
-        tmem_wait_ld32(s);
-        if (nvalid >= kTok) {
+      for (int c = 0; c < 4; ++c) tmem_ld32(sS + 32 * c, s[c]);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(s[k]));
-        } else {
+      for (int c = 0; c < 4; ++c) tmem_wait_ld32(s[c]);
+      if (nvalid < kTok) {   // past the prefix
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            if (32 * c + k < nvalid) mx = fmaxf(mx, __uint_as_float(s[k]));
-        }
+            if (32 * c + k >= nvalid) s[c][k] = 0xFF800000u;   // -inf
       }
-      mx *= qsc;
+      float mx4[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mx4[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+        for (int k = 1; k < 31; k += 2)
+          mx4[c] = max3(mx4[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
+        mx4[c] = fmaxf(mx4[c], __uint_as_float(s[c][31]));
+      }
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * qsc;
       const bool move = mx > m + kLazyMax;   // also the first finite tile
       if (__any_sync(0xffffffffu, move)) {
         const float alpha = move ? ex2(m - mx) : 1.f;
@@ -418,41 +469,39 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         // after them)
         if (i > 0) {
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            tmem_ld32(sO + 32 * c, s);
-            tmem_wait_ld32(s);
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(sO + 16 * c, o);
+            tmem_wait_ld16(o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * alpha);
-            tmem_st32(sO + 32 * c, s);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st16(sO + 16 * c, o);
           }
         }
       }
       const float ref = (m == -INFINITY ? 0.f : m) - kPShift;
+      const uint64_t q2 = pack2(qsc, qsc), r2 = pack2(-ref, -ref);
+      uint64_t sum2 = 0ull;   // two zeros
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        tmem_ld32(sS + 32 * c, s);
-        tmem_wait_ld32(s);
         uint32_t hi[16], lo[16];
-        float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          float p0 = ex2(fmaf(__uint_as_float(s[2 * k]), qsc, -ref));
-          float p1 = ex2(fmaf(__uint_as_float(s[2 * k + 1]), qsc, -ref));
-          if (nvalid < kTok) {
-            if (32 * c + 2 * k >= nvalid) p0 = 0.f;
-            if (32 * c + 2 * k + 1 >= nvalid) p1 = 0.f;
-          }
-          sum += p0 + p1;
+          const float2 x = unpack2(fma2(
+              pack2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), q2, r2));
+          const float p0 = ex2(x.x), p1 = ex2(x.y);
+          sum2 = add2(sum2, pack2(p0, p1));
           hi[k] = pack_f16x2(p0, p1);
           if constexpr (P2) {
             const float2 f = unpack_f16x2(hi[k]);
             lo[k] = pack_f16x2(p0 - f.x, p1 - f.y);
           }
         }
-        l += sum;
         tmem_st16(sS + (P2 ? 32 * c : 16 * c), hi);
         if constexpr (P2) tmem_st16(sS + 32 * c + 16, lo);
       }
+      const float2 sum = unpack2(sum2);
+      l += sum.x + sum.y;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
