@@ -406,7 +406,8 @@ kvq_status kvq_decode(const kvq_cache* c, const kvq_decode_params* p, const void
  * fresh_tokens is taken as 0 where prefix_len is positive.  The prefix's
  * probabilities are rounded to 11 bits for the products with V where the
  * output is bf16 or E4M3, and kept to 22 for fp32.
- * Two launches on `stream`; calls that share partials or counters must not
+ * Two or three launches on `stream` (three where not all own chunks fit on the
+ * SMs beside the prefix); calls that share partials or counters must not
  * overlap on the GPU.
  */
 kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int prefix_len,
@@ -415,12 +416,14 @@ kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int
                              void* stream);
 
 /*
- * Split counts for kvq_decode_shared (host only, deterministic): own_splits
- * from kvq_auto_splits of max_own_len (the longest own part), at most 16;
- * prefix_splits, at most 64 - own_splits and one per 128 tokens, minimizes the
- * time of the prefix's grid (num_kv_heads x row tiles x splits CTAs, one per
- * SM, where a row tile is 128 of the batch * q_per_kv rows, or 256 if there
- * are more).
+ * Split counts for kvq_decode_shared (host only, deterministic): the pair with
+ * the shortest modelled step.  The prefix's grid has num_kv_heads x row tiles x
+ * prefix_splits CTAs, one per SM (a row tile is 128 of the batch * q_per_kv
+ * rows of a kv head, or 256 if there are more); the requests' own chunks
+ * (batch * num_kv_heads * own_splits CTAs, two per SM) run beside it on the
+ * SMs that it leaves free.  own_splits is a power of two up to 16 with at
+ * least 128 tokens of max_own_len, the longest own part, per chunk;
+ * prefix_splits has at least one 128-token tile per chunk; together at most 64.
  */
 kvq_status kvq_shared_splits(int num_sms, int batch, int num_kv_heads, int q_per_kv,
                              int prefix_len, int max_own_len, int fmt,

@@ -171,6 +171,13 @@ void rotary_args(RopeArgs& a, const kvq_rotary* r) {
   a.eps = r->eps;
 }
 
+// Row tiles of a kv head in the shared prefix's kernel: 128 query rows, or 256
+// when there are more.
+long long shared_row_tiles(long long batch, int q_per_kv) {
+  const long long rows = batch * q_per_kv;
+  return rows > 128 ? (rows + 255) / 256 : 1;
+}
+
 kvq_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
 
 // ---------------------------------------------------------------------------
@@ -375,7 +382,7 @@ kvq_status kvq_norm_rope(const kvq_rotary* r, int head_dim, int num_tokens,
   a.k_out = rope_rows(k ? k_out : nullptr);
   a.q_norm = q ? r->q_norm : nullptr;
   a.k_norm = k ? r->k_norm : nullptr;
-  a.rows = (unsigned)(num_tokens * heads);
+  a.tokens = (unsigned)num_tokens;
   a.positions = positions;
   a.q_fp8 = q ? q_fp8 : 0;
   a.q_scale = q_scale;
@@ -428,7 +435,7 @@ kvq_status kvq_rope_append(const kvq_cache* c, const kvq_rotary* r, int batch, i
   a.q_out = rope_rows(q ? q_out : nullptr);
   a.q_norm = q ? r->q_norm : nullptr;
   a.k_norm = r->k_norm;
-  a.rows = (unsigned)(tokens * heads);
+  a.tokens = (unsigned)tokens;
   a.start_pos = start_pos;
   a.new_lens = new_lens;
   a.T = n_tokens;
@@ -496,29 +503,49 @@ kvq_status kvq_shared_splits(int num_sms, int batch, int num_kv_heads, int q_per
                              int* own_splits) {
   if (!prefix_splits || !own_splits || prefix_len < 0 || max_own_len < 0 || q_per_kv < 1)
     return KVQ_ERR_INVALID;
-  kvq_status s = kvq_auto_splits(num_sms, batch, num_kv_heads, q_per_kv, max_own_len, fmt,
-                                 own_splits);
-  if (s != KVQ_OK) return s;
-  *own_splits = std::min(*own_splits, 16);
-  const long long rows = (long long)batch * q_per_kv;
-  const long long base = num_kv_heads * (rows > 128 ? (rows + 255) / 256 : 1);
+  if (num_sms < 1 || batch < 1 || num_kv_heads < 1 ||
+      (fmt != KVQ_FP8_E4M3 && fmt != KVQ_NVFP4))
+    return KVQ_ERR_INVALID;
+  // A model of the step in microseconds, from measurements on GB300 (FP8,
+  // head_dim 128): the prefix's kernel runs one CTA per SM, kTile per token
+  // tile and kFixed around them (256-row tiles; 128-row ones kTile1, kFixed1);
+  // the requests' own chunks take kOwn + kOwnToken per token (half the longest
+  // is taken as the mean), two CTAs on each SM that the prefix leaves free,
+  // and the rest when it is done.  Merging adds kMerge, and a launch of its
+  // own kMergeLaunch where not all own chunks fit beside the prefix.
+  constexpr double kTile = 1.75, kFixed = 8, kTile1 = 1.15, kFixed1 = 4.5;
+  constexpr double kOwn = 5, kOwnToken = 0.01, kMerge = 0.12, kMergeLaunch = 4;
+  const bool wide = (long long)batch * q_per_kv > 128;
+  const long long base = num_kv_heads * shared_row_tiles(batch, q_per_kv);
+  const long long groups = (long long)batch * num_kv_heads;
   const long long tiles = ((long long)prefix_len + 127) / 128;
-  const long long most = std::min<long long>(tiles, 64 - *own_splits);
-  // The split count whose waves of one CTA per SM take the fewest tile times:
-  // kFixed for a CTA's start and end, kMerge for each partial that the merge
-  // reads.
-  constexpr double kFixed = 4.0, kMerge = 0.1;
   double best = 0;
-  int pick = 1;
-  for (long long k = 1; k <= most; ++k) {
-    const double waves = (double)((base * k + num_sms - 1) / num_sms);
-    const double cost = waves * ((double)((tiles + k - 1) / k) + kFixed) + kMerge * (double)k;
-    if (k == 1 || cost < best) {
-      best = cost;
-      pick = (int)k;
+  *prefix_splits = *own_splits = 0;
+  for (int so = 1; so <= 16; so *= 2) {
+    if (so > 1 && max_own_len < 128 * so) break;   // at least 128 tokens per chunk
+    const double own = groups * so;
+    const double t_own = kOwn + kOwnToken * 0.5 * max_own_len / so;
+    for (int sp = 1; sp <= std::max<long long>(1, std::min<long long>(tiles, 64 - so)); ++sp) {
+      const long long ctas = base * sp;
+      const double waves = (double)((ctas + num_sms - 1) / num_sms);
+      const double t_prefix = waves * ((double)((tiles + sp - 1) / sp) * (wide ? kTile : kTile1) +
+                                       (wide ? kFixed : kFixed1));
+      const double room = 2.0 * (double)std::max<long long>(0, num_sms - ctas);
+      double t = t_prefix + kMerge * (sp + so);
+      if (own <= room) {
+        t = std::max(t_prefix, t_own) + kMerge * (sp + so);
+      } else {
+        const double beside = room * std::floor(t_prefix / t_own);
+        t += kMergeLaunch;
+        if (own > beside) t += std::ceil((own - beside) / (2.0 * num_sms)) * t_own;
+      }
+      if (*prefix_splits == 0 || t < best) {
+        best = t;
+        *prefix_splits = sp;
+        *own_splits = so;
+      }
     }
   }
-  *prefix_splits = pick;
   return KVQ_OK;
 }
 
@@ -534,8 +561,8 @@ namespace {
 
 // Shared body of kvq_decode_partial and kvq_decode (fused when counters), and
 // of kvq_decode_shared: with prefix_splits > 0 the requests start at token
-// prefix_len, and the merge takes the preceding kernel's prefix_splits
-// partials in too.
+// prefix_len, and the merge takes the preceding kernel's prefix_splits partials
+// in too.
 kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const void* q,
                        float* part_o, float* part_lse, uint32_t* counters, void* out,
                        cudaStream_t stream, int prefix_len = 0, int prefix_splits = 0) {
@@ -710,14 +737,25 @@ kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int
   a.splits = prefix_splits;
   a.box = 16;   // TMA boxes: the largest power of two up to a tile that divides the pages
   while (a.box < 128 && c->page_size % (2 * a.box) == 0) a.box *= 2;
-  a.split0 = p->num_splits;
-  a.part_splits = p->num_splits + prefix_splits;
   a.wide_p = p->out_dtype == KVQ_OUT_F32;
   a.sm_scale = p->sm_scale;
   a.k_scale = c->k_scale;
   a.v_scale = c->v_scale;
   a.k_hs = c->k_head_scale;
   a.v_hs = c->v_head_scale;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  const long long base = shared_row_tiles(p->batch, G) * c->num_kv_heads;
+  a.split0 = p->num_splits;
+  a.part_splits = p->num_splits + prefix_splits;
+  // The requests' own chunks run beside the prefix on the SMs that it leaves
+  // free.  If those hold all of them at once, each waits there for the prefix
+  // and merges; otherwise they only write their partials, so that waiting ones
+  // keep no others out, and a third launch merges.
+  const long long free_ctas = 2 * (sms - base * prefix_splits);
+  const bool fused = (long long)p->batch * c->num_kv_heads * p->num_splits <= free_ctas;
   const uint64_t rows = (uint64_t)c->num_pages * c->num_kv_heads * c->page_size;
   const uint64_t row_bytes = c->fmt == KVQ_FP8_E4M3 ? D : D / 2;
   TensorMaps maps;
@@ -726,8 +764,19 @@ kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int
     return KVQ_ERR_CUDA;
   s = cuda_status(launch_shared_prefix(c->fmt, D, maps, a, as_stream(stream)));
   if (s != KVQ_OK) return s;
-  return decode_impl(c, p, q, part_o, part_lse, counters, out, as_stream(stream), prefix_len,
-                     prefix_splits);
+  s = decode_impl(c, p, q, part_o, part_lse, fused ? counters : nullptr, out, as_stream(stream),
+                  prefix_len, prefix_splits);
+  if (s != KVQ_OK || fused) return s;
+  CombineArgs m{};
+  m.part_o = part_o;
+  m.part_lse = part_lse;
+  m.out = out;
+  m.rows = p->batch * p->num_q_heads;
+  m.num_splits = a.part_splits;
+  m.Dv = D;
+  m.out_dtype = p->out_dtype;
+  m.out_scale = p->out_scale;
+  return cuda_status(launch_merge_rows(m, as_stream(stream)));
 }
 
 kvq_status kvq_decode_combine(const kvq_decode_params* p, const float* part_o,

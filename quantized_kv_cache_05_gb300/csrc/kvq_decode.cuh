@@ -151,6 +151,8 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
   // kernel's before the merge, and that kernel let it start only after its
   // own wait for everything earlier.
   if (a.fresh == 0 && !a.late_merge) griddep_wait();
+  // partials only: the merging kernel may take its place now, it waits
+  if (a.late_merge && !a.counters) griddep_launch_dependents();
 
   // one-page requests: the page index does not depend on the length, so its
   // load overlaps the length's
@@ -622,8 +624,13 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
       ofrag[((warp * MT + i) * NH + hh) * 32 + lane] =
           make_float4(o[i][hh][0], o[i][hh][1], o[i][hh][2], o[i][hh][3]);
   const size_t part_row = ((size_t)b * a.Hq + (size_t)h * a.G);   // first query head
-  // the grid ends after the preceding kernel in every mode
-  if (!dep_done && threadIdx.x == 0) griddep_wait();
+  // the grid ends after the preceding kernel in every mode; behind the shared
+  // prefix's kernel, with a merge of its own to come, one CTA's wait will do,
+  // so that the others leave their SM to the next ones
+  if (!dep_done && threadIdx.x == 0 &&
+      (!a.late_merge || a.counters ||
+       (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)))
+    griddep_wait();
   if (threadIdx.x < a.G) {
     const int row = threadIdx.x;
     float M = -INFINITY;

@@ -109,7 +109,7 @@ struct SharedArgs {
   int32_t* error_flag;
   int R, G, Hq, Hkv, ps, num_pages;   // R = batch * G rows per kv head
   int prefix, splits, box;            // tokens, splits of this kernel, TMA box rows
-  int split0, part_splits;            // first split's index among a row's partials, their number
+  int split0, part_splits;            // first partial's index among a row's, their number
   int wide_p;                         // 1: P as high part and residual (fp32 outputs)
   float sm_scale, k_scale, v_scale;
   const float* k_hs;
@@ -128,7 +128,7 @@ struct RopeArgs {
   int fmt;                    // 0: rows out (kvq_norm_rope), else the cache's format
   RopeRows q, k, v;           // inputs (MLA: k the latent, v the rope keys)
   RopeRows q_out, k_out;
-  unsigned rows;              // tokens * heads (MLA: tokens)
+  unsigned tokens;
   const float* cos_sin;
   int num_positions, rot, interleaved;
   const float* q_norm;
@@ -226,6 +226,7 @@ cudaError_t launch_mla_partial(const CUtensorMap& tcodes, const CUtensorMap& tpe
                                const CUtensorMap& tcodes64, const CUtensorMap& tpe64,
                                const PartialArgs& a, cudaStream_t st);
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st);
+cudaError_t launch_merge_rows(const CombineArgs& a, cudaStream_t st);
 cudaError_t launch_shared_prefix(int fmt, int D, const TensorMaps& m, const SharedArgs& a,
                                  cudaStream_t st);
 cudaError_t launch_prefill(int fmt, int D, const TensorMaps& m, const PartialArgs& a,

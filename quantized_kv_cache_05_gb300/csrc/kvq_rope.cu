@@ -19,6 +19,8 @@
 // of squares is a butterfly over its lanes, and an NVFP4 block of 16 is the
 // pieces of two neighbouring lanes (rot is a multiple of 32).
 
+#include <algorithm>
+
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
 #include "kvq_quant.cuh"
@@ -27,6 +29,9 @@ namespace kvq {
 namespace {
 
 constexpr int kRopeThreads = 256;
+// From this many lanes (two thousand per SM) on, groups take kRowsEach rows.
+constexpr unsigned long long kManyThreads = 152ull * 2048;
+constexpr int kRowsEach = 6;
 
 // The two pieces (8 elements each) of lane p of a row of D elements, the first
 // `rot` of them rotated.
@@ -51,37 +56,40 @@ __device__ __forceinline__ void load8f(const float* p, float* f) {
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
-// Rotation of a lane's 16 elements; trow: the position's cosines, then sines.
-__device__ __forceinline__ void rotate(float (&f)[16], const float* trow, int half,
-                                       const Pieces& pc, bool interleaved) {
+// The eight angles of a lane's pairs, and the rotation of its 16 elements.
+struct Angles {
   float c[8], s[8];
-  if (!interleaved) {
-    load8f(trow + 8 * pc.c0, c);
-    load8f(trow + half + 8 * pc.c0, s);
+  // trow: the position's cosines, then (half further on) its sines
+  __device__ __forceinline__ void load(const float* trow, int half, const Pieces& pc,
+                                       bool interleaved) {
+    // half-split order: the pairs' members lie at the same place in both
+    // pieces; side by side: pairs 4 c0 .. 4 c0 + 3 in the first, 4 c1 .. in the
+    // second
+    const int i0 = interleaved ? 4 * pc.c0 : 8 * pc.c0, i1 = interleaved ? 4 * pc.c1 : i0 + 4;
+    load4(trow + i0, c);
+    load4(trow + i1, c + 4);
+    load4(trow + half + i0, s);
+    load4(trow + half + i1, s + 4);
+  }
+  static __device__ __forceinline__ void load4(const float* p, float* f) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  }
+  __device__ __forceinline__ void turn(float& x, float& y, int i) const {
+    const float a = x, b = y;
+    x = __fmaf_rn(a, c[i], -__fmul_rn(b, s[i]));
+    y = __fmaf_rn(b, c[i], __fmul_rn(a, s[i]));
+  }
+  __device__ __forceinline__ void apply(float (&f)[16], bool interleaved) const {
+    if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = f[i], b = f[8 + i];
-      f[i] = __fmaf_rn(a, c[i], -__fmul_rn(b, s[i]));
-      f[8 + i] = __fmaf_rn(b, c[i], __fmul_rn(a, s[i]));
-    }
-  } else {
-    // pairs 4 c0 .. 4 c0 + 3 lie in the first piece, 4 c1 .. in the second
-    const float4 ca = __ldg(reinterpret_cast<const float4*>(trow + 4 * pc.c0));
-    const float4 cb = __ldg(reinterpret_cast<const float4*>(trow + 4 * pc.c1));
-    const float4 sa = __ldg(reinterpret_cast<const float4*>(trow + half + 4 * pc.c0));
-    const float4 sb = __ldg(reinterpret_cast<const float4*>(trow + half + 4 * pc.c1));
-    c[0] = ca.x; c[1] = ca.y; c[2] = ca.z; c[3] = ca.w;
-    c[4] = cb.x; c[5] = cb.y; c[6] = cb.z; c[7] = cb.w;
-    s[0] = sa.x; s[1] = sa.y; s[2] = sa.z; s[3] = sa.w;
-    s[4] = sb.x; s[5] = sb.y; s[6] = sb.z; s[7] = sb.w;
+      for (int i = 0; i < 8; ++i) turn(f[2 * i], f[2 * i + 1], i);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = f[2 * i], b = f[2 * i + 1];
-      f[2 * i] = __fmaf_rn(a, c[i], -__fmul_rn(b, s[i]));
-      f[2 * i + 1] = __fmaf_rn(b, c[i], __fmul_rn(a, s[i]));
+      for (int i = 0; i < 8; ++i) turn(f[i], f[8 + i], i);
     }
   }
-}
+};
 
 // 1 / rms of a row spread over LANES lanes (every lane of the warp calls it).
 template <int LANES>
@@ -172,7 +180,7 @@ struct Token {
   long pos;
   bool ok;
 };
-__device__ __forceinline__ Token token_of(const RopeArgs& a, unsigned token, bool first_lane) {
+__device__ __forceinline__ Token token_of(const RopeArgs& a, unsigned token, bool report) {
   Token k;
   k.ok = true;
   k.b = 0;
@@ -187,95 +195,118 @@ __device__ __forceinline__ Token token_of(const RopeArgs& a, unsigned token, boo
   if (k.pos < 0) k.ok = false;
   if (k.ok && a.rot > 0 && k.pos >= a.num_positions) {
     k.ok = false;
-    if (first_lane) record_error(a.error_flag, 8);
+    if (report) record_error(a.error_flag, 8);
   }
   return k;
 }
 
-// Cache row of kv head h at the token's position, or -1 (skipped): past the
-// block table as in the plain append, or a page index out of range.
-__device__ __forceinline__ long rope_cache_row(const RopeArgs& a, const Token& k, int h,
-                                               bool first_lane) {
-  if (!k.ok || k.pos >= (long)a.max_pages * a.ps) return -1;
+// Cache row of kv head 0 at the token's position (head h: + h page_size), or -1
+// (skipped): past the block table as in the plain append, or a page index out
+// of range.
+__device__ __forceinline__ long rope_page(const RopeArgs& a, const Token& k, bool report) {
+  if (k.pos >= (long)a.max_pages * a.ps) return -1;
   const unsigned pos = (unsigned)k.pos, pi = pos / (unsigned)a.ps;
   const int page = __ldg(a.block_table + (size_t)k.b * a.max_pages + pi);
   if (page < 0 || page >= a.num_pages) {
-    if (first_lane) record_error(a.error_flag, 4);
+    if (report) record_error(a.error_flag, 4);
     return -1;
   }
-  return ((long)page * a.Hkv + h) * a.ps + (pos - pi * (unsigned)a.ps);
+  return (long)page * a.Hkv * a.ps + (pos - pi * (unsigned)a.ps);
 }
 
 // FMT 0: bf16 rows out (kvq_norm_rope); otherwise K and V go to the cache.
+// `per_token` lane groups of a block share a token (a power of two), and
+// gridDim.y blocks: a group takes every (per_token gridDim.y)-th of its rows,
+// the next row's loads going out before the present one's arithmetic.
 template <int D, int FMT>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, int per_token) {
   // the append is an ordinary launch (it starts after all earlier work), the
   // other a programmatic one
   if constexpr (FMT == 0) griddep_wait();
   griddep_launch_dependents();
-  constexpr int kLanes = D / 16, kRows = kRopeThreads / kLanes;
-  const int p = threadIdx.x % kLanes;
-  const unsigned row = blockIdx.x * (unsigned)kRows + threadIdx.x / kLanes;
-  const unsigned H = (unsigned)(a.q.heads + a.k.heads + a.v.heads);
-  const bool in = row < a.rows;
-  const unsigned token = in ? row / H : 0;
-  int h = in ? (int)(row - token * H) : 0;
-  const bool isq = h < a.q.heads, isv = h >= a.q.heads + a.k.heads;
-  if (!isq) h -= isv ? a.q.heads + a.k.heads : a.q.heads;
-  const RopeRows& src = isq ? a.q : isv ? a.v : a.k;
-  const Token tk = token_of(a, token, in && p == 0);
+  constexpr int kLanes = D / 16, kGroups = kRopeThreads / kLanes;
+  const int p = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const unsigned token = blockIdx.x * (unsigned)(kGroups / per_token) + group / per_token;
+  const int H = a.q.heads + a.k.heads + a.v.heads;
+  const int first = blockIdx.y * per_token + group % per_token, step = per_token * gridDim.y;
+  const bool in = token < a.tokens;
+  const Token tk = token_of(a, in ? token : 0, in && p == 0 && first == 0);
   const bool ok = in && tk.ok;
 
-  const int rot = isv ? 0 : a.rot;
-  const Pieces pc = pieces<D>(p, rot);
-  float f[16];
-  {
-    const uint16_t* x = src.data + (long)token * src.token_stride + (long)h * src.head_stride;
-    uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-    if (ok) {
-      x0 = *reinterpret_cast<const uint4*>(x + 8 * pc.c0);
-      x1 = *reinterpret_cast<const uint4*>(x + 8 * pc.c1);
-    }
+  // where row i of the token comes from
+  auto source = [&](int i) -> const uint16_t* {
+    const bool isq = i < a.q.heads, isv = i >= a.q.heads + a.k.heads;
+    const RopeRows& src = isq ? a.q : isv ? a.v : a.k;
+    const int h = i - (isq ? 0 : isv ? a.q.heads + a.k.heads : a.q.heads);
+    return src.data + (long)token * src.token_stride + (long)h * src.head_stride;
+  };
+  const Pieces turned = pieces<D>(p, a.rot), plain = pieces<D>(p, 0);
+  auto fetch = [&](int i, uint4& x0, uint4& x1) {
+    x0 = x1 = make_uint4(0, 0, 0, 0);
+    if (!ok || i >= H) return;
+    const Pieces& pc = i < a.q.heads + a.k.heads ? turned : plain;
+    const uint16_t* x = source(i);
+    x0 = *reinterpret_cast<const uint4*>(x + 8 * pc.c0);
+    x1 = *reinterpret_cast<const uint4*>(x + 8 * pc.c1);
+  };
+  uint4 x0, x1;
+  fetch(first, x0, x1);
+  Angles ang;
+  if (turned.turn && ok)
+    ang.load(a.cos_sin + tk.pos * a.rot, a.rot / 2, turned, a.interleaved != 0);
+  // the page is the token's, whatever the head
+  long page_row = -1;
+  if constexpr (FMT != 0) page_row = ok ? rope_page(a, tk, p == 0 && first == 0) : -1;
+
+#pragma unroll 1
+  for (int i0 = 0; i0 < H; i0 += step) {   // the same rounds for every lane of the warp
+    const int i = i0 + first;
+    const bool row = ok && i < H;
+    const bool isq = i < a.q.heads, isv = i >= a.q.heads + a.k.heads;
+    const int h = i - (isq ? 0 : isv ? a.q.heads + a.k.heads : a.q.heads);
+    const Pieces& pc = isv ? plain : turned;
+    float f[16];
     bf16x8_to_f32(x0, f);
     bf16x8_to_f32(x1, f + 8);
-  }
-  // every lane of the warp takes part in the norm's butterfly when any row of
-  // the call has a norm
-  const float* w = isq ? a.q_norm : isv ? nullptr : a.k_norm;
-  if (a.q_norm || a.k_norm) {
-    const float r = inv_rms<kLanes>(f, a.eps);
-    if (w) apply_norm(f, r, w, pc);
-  }
-  if (pc.turn && ok)
-    rotate(f, a.cos_sin + tk.pos * a.rot, a.rot / 2, pc, a.interleaved != 0);
+    if (i0 + step < H) fetch(i + step, x0, x1);
+    // every lane of the warp takes part in the norm's butterfly when any row
+    // of the call has a norm
+    const float* w = isq ? a.q_norm : isv ? nullptr : a.k_norm;
+    if (a.q_norm || a.k_norm) {
+      const float r = inv_rms<kLanes>(f, a.eps);
+      if (w) apply_norm(f, r, w, pc);
+    }
+    if (turned.turn && !isv) ang.apply(f, a.interleaved != 0);
 
-  if (isq || FMT == 0) {
-    const RopeRows& dst = isq ? a.q_out : a.k_out;
-    const long at = (long)token * dst.token_stride + (long)h * dst.head_stride;
-    if (ok) {
-      if (isq && a.q_fp8) {
-        const float s = a.q_hs ? __ldg(a.q_hs + h) : a.q_scale;
-        const float z = a.q_hs ? __frcp_rn(s) : a.q_recip;
-        store_e4m3(f, s, z, reinterpret_cast<uint8_t*>(dst.data) + at, pc);
-      } else {
-        *reinterpret_cast<uint4*>(dst.data + at + 8 * pc.c0) = pack_bf16x8(f);
-        *reinterpret_cast<uint4*>(dst.data + at + 8 * pc.c1) = pack_bf16x8(f + 8);
+    if (isq || FMT == 0) {
+      const RopeRows& dst = isq ? a.q_out : a.k_out;
+      const long at = (long)token * dst.token_stride + (long)h * dst.head_stride;
+      if (row) {
+        if (isq && a.q_fp8) {
+          const float s = a.q_hs ? __ldg(a.q_hs + h) : a.q_scale;
+          const float z = a.q_hs ? __frcp_rn(s) : a.q_recip;
+          store_e4m3(f, s, z, reinterpret_cast<uint8_t*>(dst.data) + at, pc);
+        } else {
+          *reinterpret_cast<uint4*>(dst.data + at + 8 * pc.c0) = pack_bf16x8(f);
+          *reinterpret_cast<uint4*>(dst.data + at + 8 * pc.c1) = pack_bf16x8(f + 8);
+        }
       }
     }
-    if constexpr (FMT != kFmtNvfp4) return;
-  }
-  if constexpr (FMT != 0) {
-    const long crow = (isq || !in) ? -1 : rope_cache_row(a, tk, h, p == 0);
-    const float* hs = isv ? a.v_hs : a.k_hs;
-    const float s = (hs && !isq) ? __ldg(hs + h) : (isv ? a.v_scale : a.k_scale);
-    if constexpr (FMT == kFmtFp8) {
-      if (crow < 0) return;
-      const float z = hs ? __frcp_rn(s) : (isv ? a.v_recip : a.k_recip);
-      store_e4m3(f, s, z, (isv ? a.v_codes : a.k_codes) + crow * D, pc);
-    } else {
-      // lanes without a row stay for their neighbours' shuffles
-      store_nvfp4<D>(f, s, crow >= 0, isv ? a.v_codes : a.k_codes,
-                     isv ? a.v_bscale : a.k_bscale, crow, pc);
+    if constexpr (FMT != 0) {
+      const bool store = row && !isq && page_row >= 0;
+      const long crow = page_row + (long)h * a.ps;
+      const float* hs = isv ? a.v_hs : a.k_hs;
+      const float s = (hs && store) ? __ldg(hs + h) : (isv ? a.v_scale : a.k_scale);
+      if constexpr (FMT == kFmtFp8) {
+        if (store) {
+          const float z = hs ? __frcp_rn(s) : (isv ? a.v_recip : a.k_recip);
+          store_e4m3(f, s, z, (isv ? a.v_codes : a.k_codes) + crow * D, pc);
+        }
+      } else {
+        // lanes without a row stay for their neighbours' shuffles
+        store_nvfp4<D>(f, s, store, isv ? a.v_codes : a.k_codes, isv ? a.v_bscale : a.k_bscale,
+                       crow, pc);
+      }
     }
   }
 }
@@ -287,9 +318,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_mla_kernel(const RopeArgs a
   constexpr int D = 512, kRope = 64;
   const int lane = threadIdx.x & 31;
   const unsigned token = blockIdx.x * (unsigned)(kRopeThreads / 32) + threadIdx.x / 32;
-  if (token >= a.rows) return;   // the whole warp, as below
+  if (token >= a.tokens) return;   // the whole warp, as below
   const Token tk = token_of(a, token, lane == 0);
-  const long crow = tk.ok ? rope_cache_row(a, tk, 0, lane == 0) : -1;
+  const long crow = tk.ok ? rope_page(a, tk, lane == 0) : -1;
   if (crow < 0) return;
 
   const Pieces pc = pieces<D>(lane, 0);
@@ -314,7 +345,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_mla_kernel(const RopeArgs a
   if (lane < kRope / 16) {
     bf16x8_to_f32(e0, f);
     bf16x8_to_f32(e1, f + 8);
-    if (pe.turn) rotate(f, a.cos_sin + tk.pos * a.rot, a.rot / 2, pe, a.interleaved != 0);
+    if (pe.turn) {
+      Angles ang;
+      ang.load(a.cos_sin + tk.pos * a.rot, a.rot / 2, pe, a.interleaved != 0);
+      ang.apply(f, a.interleaved != 0);
+    }
     uint16_t* dst = a.k_pe + crow * kRope;
     *reinterpret_cast<uint4*>(dst + 8 * pe.c0) = pack_bf16x8(f);
     *reinterpret_cast<uint4*>(dst + 8 * pe.c1) = pack_bf16x8(f + 8);
@@ -323,24 +358,37 @@ __global__ void __launch_bounds__(kRopeThreads) rope_mla_kernel(const RopeArgs a
 
 template <int D>
 cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t st) {
-  constexpr unsigned kRows = kRopeThreads / (D / 16);
-  const unsigned blocks = (a.rows + kRows - 1) / kRows;
-  if (a.fmt == 0)
-    return launch_pdl(rope_kernel<D, 0>, dim3(blocks), dim3(kRopeThreads), 0, st, a);
+  constexpr int kGroups = kRopeThreads / (D / 16);
+  const int H = a.q.heads + a.k.heads + a.v.heads;
+  // Few tokens: a group for every row, so that all loads go out at once.  Many:
+  // fewer groups per token, which keep its angles, page and place for several
+  // rows.
+  int per_token = kGroups;
+  while (per_token > 1 && per_token >= 2 * H) per_token /= 2;
+  unsigned y = (unsigned)std::min((H + per_token - 1) / per_token, 65535);
+  const unsigned long long threads = (unsigned long long)a.tokens * (D / 16);
+  if (threads * H >= kManyThreads) {
+    while (per_token > 1 && threads * per_token >= kManyThreads && per_token * kRowsEach > H)
+      per_token /= 2;
+    y = 1;
+  }
+  const unsigned per_block = (unsigned)(kGroups / per_token);
+  const dim3 grid((a.tokens + per_block - 1) / per_block, y), block(kRopeThreads);
+  if (a.fmt == 0) return launch_pdl(rope_kernel<D, 0>, grid, block, 0, st, a, per_token);
   if (a.fmt == kFmtFp8)
-    rope_kernel<D, kFmtFp8><<<blocks, kRopeThreads, 0, st>>>(a);
+    rope_kernel<D, kFmtFp8><<<grid, block, 0, st>>>(a, per_token);
   else
-    rope_kernel<D, kFmtNvfp4><<<blocks, kRopeThreads, 0, st>>>(a);
+    rope_kernel<D, kFmtNvfp4><<<grid, block, 0, st>>>(a, per_token);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_rope(int D, bool mla, const RopeArgs& a, cudaStream_t st) {
-  if (a.rows == 0) return cudaSuccess;
+  if (a.tokens == 0) return cudaSuccess;
   if (mla) {
     const unsigned per = kRopeThreads / 32;
-    rope_mla_kernel<<<(a.rows + per - 1) / per, kRopeThreads, 0, st>>>(a);
+    rope_mla_kernel<<<(a.tokens + per - 1) / per, kRopeThreads, 0, st>>>(a);
     return cudaGetLastError();
   }
   if (D == 64) return launch_rope_t<64>(a, st);

@@ -34,6 +34,8 @@
 // Every wait is bounded; a timeout sets an error bit and the partials become
 // NaN.
 
+#include <type_traits>
+
 #include "kvq_attn.cuh"
 #include "kvq_tc.cuh"
 
@@ -48,7 +50,7 @@ constexpr int kMmaWarp = kConvWarp + kConvWarps, kTmaWarp = kMmaWarp + 1;
 constexpr int kSharedThreads = 512;       // four warpgroups: softmax x 2, convert, MMA and TMA
 // Registers per thread of the warpgroups (the launch gives each thread 128, 512
 // for the four): a softmax thread holds its row's 128 scores at once.
-constexpr int kRegSoft = 176, kRegConv = 104, kRegIssue = 56;
+constexpr int kRegSoft = 176, kRegConv = 96, kRegIssue = 64;
 static_assert(2 * kRegSoft + kRegConv + kRegIssue <= 4 * 128, "register pool of the launch");
 constexpr float kPShift = 7.0f;           // log2 scale of P
 constexpr int kTmem = 512;                // S0 | S1 | O0 | O1, 128 columns each
@@ -73,7 +75,7 @@ struct SharedGeom {
 struct SharedCtl {
   uint64_t raw_full[2][4], raw_empty[2][4];   // [K, V][slot]
   uint64_t op_full[2][2], op_empty[2][2];     // [K, V][operand tile]
-  uint64_t s_full[2], p_full[2], o_full[2];   // per softmax slot
+  uint64_t s_full[2], p_full[2][2], o_full[2];   // per softmax slot (P: per half of the tokens)
   uint64_t q_full, mma_done;
   uint32_t tmem;
   int abort_flag;
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   SharedCtl& sm = *reinterpret_cast<SharedCtl*>(dyn_smem + Sg::kOffCtl);
   volatile int* abort_flag = &sm.abort_flag;
 
-  if (threadIdx.x == 0) {
+  if (warp == kTmaWarp && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       for (int k = 0; k < Sg::kSlots; ++k) {
         mbar_init(smem_u32(&sm.raw_full[i][k]), 1);
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         mbar_init(smem_u32(&sm.op_empty[i][k]), 1);
       }
       mbar_init(smem_u32(&sm.s_full[i]), 1);
-      mbar_init(smem_u32(&sm.p_full[i]), 4);
+      for (int k = 0; k < 2; ++k) mbar_init(smem_u32(&sm.p_full[i][k]), 4);
       mbar_init(smem_u32(&sm.o_full[i]), 1);
     }
     mbar_init(smem_u32(&sm.q_full), 4 * MT);
@@ -166,19 +168,77 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   // kernel start: it reads its inputs without a wait of its own.
   griddep_wait();
   griddep_launch_dependents();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sm.tmem;
 
   const int h = blockIdx.y, split = blockIdx.z;
   const int row0 = blockIdx.x * (MT * kTok);
   // tiles [t0, t1) of the prefix
   const int tiles = (a.prefix + kTok - 1) / kTok;
-  const int t0 = (int)((long)split * tiles / a.splits);
-  const int t1 = (int)((long)(split + 1) * tiles / a.splits);
+  const int t0 = (int)((unsigned)split * (unsigned)tiles / (unsigned)a.splits);   // < 2^30
+  const int t1 = (int)((unsigned)(split + 1) * (unsigned)tiles / (unsigned)a.splits);
   const int nt = t1 - t0;
   const int units = MT * nt;   // (slot, token tile) pairs in tensor-pipe order
+
+  // TMA warp: lane i's cache row of box i (at most eight) of the split's tile j
+  auto box_row = [&](int j) -> int {
+    const int tok = (t0 + j) * kTok + lane * a.box;
+    if (lane * a.box >= kTok || tok >= a.prefix) return 0;
+    const int pidx = tok / a.ps;
+    int page = __ldg(a.prefix_table + pidx);
+    if (page < 0 || page >= a.num_pages) {
+      record_error(a.error_flag, 4);
+      page = 0;
+    }
+    return (int)(((long)page * a.Hkv + h) * a.ps + (tok - pidx * a.ps));
+  };
+  // Softmax thread: its row (slot, r) of the kv head's query rows
+  const int slot = (warp >> 2) & 1, r = threadIdx.x & (kTok - 1);
+  const int row = row0 + (MT == 2 ? slot * kTok : 0) + r;
+  const bool live = warp < kConvWarp && row < a.R;
+  const int b = live ? row / a.G : 0, hq = h * a.G + (live ? row - b * a.G : 0);
+
+  // The copies of tile j (TMA warp): K, then V, of row `row` of each lane's box
+  auto copy_tile = [&](int j, int kv, int row) {
+    const int nb = (min(kTok, a.prefix - (t0 + j) * kTok) + a.box - 1) / a.box;
+    const int rs = j % Sg::kSlots;
+    const uint32_t full = smem_u32(&sm.raw_full[kv][rs]);
+    const uint32_t dst = base + Sg::kOffRaw + (2 * rs + kv) * Sg::kRaw;
+    if (lane == 0) mbar_arrive_expect_tx(full, nb * a.box * (Gm::kRow + Gm::kSRow));
+    __syncwarp();
+    if (lane < nb) {
+      tma_load_2d(dst + lane * a.box * Gm::kRow, kv ? &tmV : &tmK, 0, row, full);
+      if constexpr (FMT == kFmtNvfp4)
+        bulk_load(dst + Sg::kRawCodes + lane * a.box * Gm::kSRow,
+                  (kv ? a.v_bscale : a.k_bscale) + (long)row * Gm::kSRow, a.box * Gm::kSRow,
+                  full);
+    }
+  };
+
+  // The first copies and the query loads go out before the CTA meets: they are
+  // the longest steps to the first MMA.
+  constexpr int kQv = D / 8;       // 16-byte pieces of a bf16 row (FP8: half)
+  uint4 qv[kQv];
+  int len = 0;
+  if (warp == kTmaWarp) {
+    __syncwarp();   // lane 0 has set up the barriers
+    for (int j = 0; j < min(nt, Sg::kSlots); ++j) {
+      const int row = box_row(j);
+      copy_tile(j, 0, row);
+      copy_tile(j, 1, row);
+    }
+  }
+  if (warp < kConvWarp) {
+    const uint4* qp = reinterpret_cast<const uint4*>(
+        static_cast<const uint8_t*>(a.q) + ((size_t)b * a.Hq + hq) * (a.q_fp8 ? D : 2 * D));
+#pragma unroll
+    for (int c = 0; c < kQv; ++c)
+      qv[c] = live && (c < kQv / 2 || !a.q_fp8) ? qp[c] : make_uint4(0u, 0u, 0u, 0u);
+    len = live ? __ldg(a.seq_lens + b) : -1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  if (tmem != 0 && threadIdx.x == 0) *abort_flag = 1;   // (never: see the MMA warp)
 
   auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
     if (wait_or_abort(smem_u32(&bar), parity, abort_flag)) return true;
@@ -187,43 +247,19 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   };
 
   if (warp >= kMmaWarp) {
-  regs_dec<kRegIssue>();
+    regs_dec<kRegIssue>();
     if (warp == kTmaWarp) {
       // ================================================================= TMA
-      int issued[2] = {0, 0};
-      for (int j = 0; j < nt; ++j) {
-        const int tok0 = (t0 + j) * kTok;
-        const int nb = (min(kTok, a.prefix - tok0) + a.box - 1) / a.box;
-        // lane i holds the cache row of box i (at most eight boxes)
-        int row = 0;
-        if (lane < nb) {
-          const int tok = tok0 + lane * a.box, pidx = tok / a.ps;
-          int page = __ldg(a.prefix_table + pidx);
-          if (page < 0 || page >= a.num_pages) {
-            record_error(a.error_flag, 4);
-            page = 0;
-          }
-          row = (int)(((long)page * a.Hkv + h) * a.ps + (tok - pidx * a.ps));
-        }
-        const int slot = j % Sg::kSlots;
-        const uint32_t round = (uint32_t)(j / Sg::kSlots);
+      int issued[2] = {min(nt, Sg::kSlots), min(nt, Sg::kSlots)};
+      for (int j = Sg::kSlots; j < nt; ++j) {
+        const int row = box_row(j);
+        const int rs = j % Sg::kSlots;
         bool ok = true;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          if (round > 0) ok = ok && wait(sm.raw_empty[kv][slot], (round - 1) & 1);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = __all_sync(0xffffffffu, wait(sm.raw_empty[kv][rs], (j / Sg::kSlots - 1) & 1));
           if (!ok) break;
-          const uint32_t full = smem_u32(&sm.raw_full[kv][slot]);
-          const uint32_t dst = base + Sg::kOffRaw + (2 * slot + kv) * Sg::kRaw;
-          if (lane == 0) mbar_arrive_expect_tx(full, nb * a.box * (Gm::kRow + Gm::kSRow));
-          __syncwarp();
-          if (lane < nb) {
-            tma_load_2d(dst + lane * a.box * Gm::kRow, kv ? &tmV : &tmK, 0, row, full);
-            if constexpr (FMT == kFmtNvfp4)
-              bulk_load(dst + Sg::kRawCodes + lane * a.box * Gm::kSRow,
-                        (kv ? a.v_bscale : a.k_bscale) + (long)row * Gm::kSRow, a.box * Gm::kSRow,
-                        full);
-          }
+          copy_tile(j, kv, row);
           issued[kv] = j + 1;
         }
         if (!ok) break;
@@ -235,74 +271,82 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             mbar_wait(smem_u32(&sm.raw_full[kv][j % Sg::kSlots]), (j / Sg::kSlots) & 1);
     } else if (warp == kMmaWarp) {
       // ================================================================= MMA
-      if (lane == 0) {
-        constexpr uint32_t kIdS = idesc(0, 0, 0, kTok), kIdO = idesc(0, 0, 1, D);
-        const uint64_t dq = sdesc(base, 16, 1024);
-        const uint64_t dk = sdesc(base + Sg::kOffK, 16, 1024);
-        const uint64_t dv = sdesc(base + Sg::kOffV, kCol, 1024);   // MN-major
-        bool ok = nt == 0 || wait(sm.q_full, 0);
-        // unit u: slot u & 1; token tile u / MT
-        auto issue_s = [&](int u) {
-          const int j = u / MT, slot = u & 1;
-          // the first use of a K tile waits for it
-          if (MT == 1 || slot == 0) ok = ok && wait(sm.op_full[0][j & 1], (j >> 1) & 1);
-          if (!ok) return;
-          tc_fence_after();
-          const uint64_t q = dq + (uint64_t)((MT == 2 ? slot : 0) * Sg::kTile >> 4);
-          const uint64_t k = dk + (uint64_t)((j & 1) * Sg::kTile >> 4);
+      // The warp stays converged, its elected lane issues; tensor memory
+      // starts at column 0 (all of it is this CTA's).
+      constexpr uint32_t kIdS = idesc(0, 0, 0, kTok), kIdO = idesc(0, 0, 1, D);
+      const uint64_t dq = sdesc(base, 16, 1024);
+      const uint64_t dk = sdesc(base + Sg::kOffK, 16, 1024);
+      const uint64_t dv = sdesc(base + Sg::kOffV, kCol, 1024);   // MN-major
+      auto wait_warp = [&](uint64_t& bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, wait(bar, parity));
+      };
+      bool ok = nt == 0 || wait_warp(sm.q_full, 0);
+      // unit u: slot u & 1; token tile u / MT
+      auto issue_s = [&](int u) {
+        const int j = u / MT, slot = u & 1;
+        // the first use of a K tile waits for it
+        if (MT == 1 || slot == 0) ok = ok && wait_warp(sm.op_full[0][j & 1], (j >> 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t q = dq + (uint64_t)((MT == 2 ? slot : 0) * Sg::kTile >> 4);
+        const uint64_t k = dk + (uint64_t)((j & 1) * Sg::kTile >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = (uint64_t)(((kk >> 2) * kCol + (kk & 3) * 32) >> 4);
-            mma(tmem + slot * 128, q + off, k + off, kIdS, kk > 0);
-          }
-          mma_commit(smem_u32(&sm.s_full[slot]));
-          if (MT == 1 || slot == 1) mma_commit(smem_u32(&sm.op_empty[0][j & 1]));
-        };
-        for (int u = 0; u < min(2, units) && ok; ++u) issue_s(u);
-        for (int u = 0; u < units && ok; ++u) {
-          const int j = u / MT, slot = u & 1, i = u >> 1;   // the slot's i-th unit
-          ok = wait(sm.p_full[slot], i & 1);
-          if (ok && (MT == 1 || slot == 0)) ok = wait(sm.op_full[1][j & 1], (j >> 1) & 1);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = (uint64_t)(((kk >> 2) * kCol + (kk & 3) * 32) >> 4);
+          mma_ss_elect(slot * 128, q + off, k + off, kIdS, kk > 0);
+        }
+        mma_commit_elect(smem_u32(&sm.s_full[slot]));
+        if (MT == 1 || slot == 1) mma_commit_elect(smem_u32(&sm.op_empty[0][j & 1]));
+      };
+      for (int u = 0; u < min(2, units) && ok; ++u) issue_s(u);
+      for (int u = 0; u < units && ok; ++u) {
+        const int j = u / MT, slot = u & 1, i = u >> 1;   // the slot's i-th unit
+        const uint64_t v = dv + (uint64_t)((j & 1) * Sg::kTile >> 4);
+        const uint32_t p = slot * 128, o = 256 + slot * 128;
+        if (MT == 1 || slot == 0) ok = wait_warp(sm.op_full[1][j & 1], (j >> 1) & 1);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {   // the halves of P, as they are written
+          ok = ok && wait_warp(sm.p_full[slot][half], i & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t v = dv + (uint64_t)((j & 1) * Sg::kTile >> 4);
-          const uint32_t p = tmem + slot * 128, o = tmem + 256 + slot * 128;
 #pragma unroll
-          for (int kk = 0; kk < kTok / 16; ++kk) {
+          for (int k4 = 0; k4 < kTok / 32; ++k4) {
+            const int kk = half * (kTok / 32) + k4;
             const uint64_t vk = v + (uint64_t)(kk * 2048 >> 4);
             if constexpr (P2) {   // high parts and residuals in alternating 16-column groups
               const uint32_t pk = p + 32 * (kk >> 1) + 8 * (kk & 1);
-              mma_ts(o, pk, vk, kIdO, i > 0 || kk > 0);
-              mma_ts(o, pk + 16, vk, kIdO, true);
+              mma_ts_elect(o, pk, vk, kIdO, i > 0 || kk > 0);
+              mma_ts_elect(o, pk + 16, vk, kIdO, true);
             } else {
-              mma_ts(o, p + 8 * kk, vk, kIdO, i > 0 || kk > 0);
+              mma_ts_elect(o, p + 8 * kk, vk, kIdO, i > 0 || kk > 0);
             }
           }
-          mma_commit(smem_u32(&sm.o_full[slot]));
-          if (MT == 1 || slot == 1) mma_commit(smem_u32(&sm.op_empty[1][j & 1]));
-          if (u + 2 < units) issue_s(u + 2);
         }
-        // every MMA of this thread has completed at exit (bounded waits)
-        mma_commit(smem_u32(&sm.mma_done));
-        mbar_wait(smem_u32(&sm.mma_done), 0);
+        if (!ok) break;
+        mma_commit_elect(smem_u32(&sm.o_full[slot]));
+        if (MT == 1 || slot == 1) mma_commit_elect(smem_u32(&sm.op_empty[1][j & 1]));
+        if (u + 2 < units) issue_s(u + 2);
       }
+      // every MMA has completed at exit (bounded wait)
+      mma_commit_elect(smem_u32(&sm.mma_done));
+      mbar_wait(smem_u32(&sm.mma_done), 0);
       __syncwarp();
     }
   } else if (warp >= kConvWarp) {
     regs_dec<kRegConv>();
     // ============================================================= convert
     const int t = threadIdx.x - 32 * kConvWarp;
-    const int p = t & 7, r = t;   // row r of the tile; its atom row p (r = 8 (t >> 3) + p)
+    const int p = t & 7, r = t;   // row r of the tile, row p of its 8-row atom
     for (int j = 0; j < nt; ++j) {
-      const int slot = j % Sg::kSlots;
+      const int rs = j % Sg::kSlots;
       const int nvalid = a.prefix - (t0 + j) * kTok;
       bool ok = true;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        const uint32_t raw = base + Sg::kOffRaw + (2 * slot + kv) * Sg::kRaw;
+        const uint32_t raw = base + Sg::kOffRaw + (2 * rs + kv) * Sg::kRaw;
         const uint32_t dst = base + (kv ? Sg::kOffV : Sg::kOffK) + (j & 1) * Sg::kTile +
                              (r >> 3) * 1024 + p * 128;
-        ok = wait(sm.raw_full[kv][slot], (j / Sg::kSlots) & 1);
+        ok = wait(sm.raw_full[kv][rs], (j / Sg::kSlots) & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
         constexpr int kChunks = Gm::kRow / 16;
         uint4 v[kChunks];
@@ -355,7 +399,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&sm.op_full[kv][j & 1]));
-          mbar_arrive(smem_u32(&sm.raw_empty[kv][slot]));
+          mbar_arrive(smem_u32(&sm.raw_empty[kv][rs]));
         }
       }
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -363,12 +407,6 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   } else {
     regs_inc<kRegSoft>();
     // ============================================================= softmax
-    const int slot = warp >> 2;
-    const int r = threadIdx.x & 127;              // row of the slot's tile
-    const int row = row0 + (MT == 2 ? slot * kTok : 0) + r;
-    const bool live = row < a.R;
-    const int b = live ? row / a.G : 0, g = live ? row - b * a.G : 0;
-    const int hq = h * a.G + g;
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t sS = lane_addr + slot * 128, sO = lane_addr + 256 + slot * 128;
 
@@ -377,22 +415,18 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     {
       const float k_log2 =
           (a.k_hs ? a.sm_scale * __ldg(a.k_hs + h) : a.sm_scale * a.k_scale) * 1.4426950408889634f;
-      const size_t qrow = (size_t)b * a.Hq + hq;
       const uint32_t dst = base + (MT == 2 ? slot * Sg::kTile : 0) + (r >> 3) * 1024 + (r & 7) * 128;
       const bool store = MT == 2 || slot == 0;
       if (a.q_fp8) {
-        const uint8_t* qp = static_cast<const uint8_t*>(a.q) + qrow * D;
         qsc = k_log2 * (a.q_hs ? __ldg(a.q_hs + hq) : a.q_scale);
         if (store) {
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
-            const uint4 v = live ? *reinterpret_cast<const uint4*>(qp + 16 * c)
-                                 : make_uint4(0u, 0u, 0u, 0u);
             uint32_t o[8];
-            e4m3x4_to_f16x2x2(v.x, o[0], o[1]);
-            e4m3x4_to_f16x2x2(v.y, o[2], o[3]);
-            e4m3x4_to_f16x2x2(v.z, o[4], o[5]);
-            e4m3x4_to_f16x2x2(v.w, o[6], o[7]);
+            e4m3x4_to_f16x2x2(qv[c].x, o[0], o[1]);
+            e4m3x4_to_f16x2x2(qv[c].y, o[2], o[3]);
+            e4m3x4_to_f16x2x2(qv[c].z, o[4], o[5]);
+            e4m3x4_to_f16x2x2(qv[c].w, o[6], o[7]);
             const uint32_t at = dst + (c >> 2) * kCol;
             const int q = 2 * (c & 3);
             sts128(at + ((q ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
@@ -400,22 +434,18 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           }
         }
       } else {
-        const uint16_t* qp = static_cast<const uint16_t*>(a.q) + qrow * D;
-        uint4 v[D / 8];
         uint32_t m2 = 0;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          v[c] = live ? *reinterpret_cast<const uint4*>(qp + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-          m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v[c].x & 0x7FFF7FFFu, v[c].y & 0x7FFF7FFFu),
-                                     __vmaxu2(v[c].z & 0x7FFF7FFFu, v[c].w & 0x7FFF7FFFu)));
-        }
+        for (int c = 0; c < kQv; ++c)
+          m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(qv[c].x & 0x7FFF7FFFu, qv[c].y & 0x7FFF7FFFu),
+                                     __vmaxu2(qv[c].z & 0x7FFF7FFFu, qv[c].w & 0x7FFF7FFFu)));
         const int e = q_prescale_exp(max(m2 & 0xFFFFu, m2 >> 16));
         const float f = exp2i(e);
         qsc = scale_pow2(k_log2, -e);
         if (store) {
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+          for (int c = 0; c < kQv; ++c) {
+            const uint32_t w[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
             uint32_t o[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -499,18 +529,20 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         }
         tmem_st16(sS + (P2 ? 32 * c : 16 * c), hi);
         if constexpr (P2) tmem_st16(sS + 32 * c + 16, lo);
+        if (c & 1) {   // half of P is written (and O rescaled): its MMAs may go
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[slot][c >> 1]));
+        }
       }
       const float2 sum = unpack2(sum2);
       l += sum.x + sum.y;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[slot]));
     }
 
     // ---- the row's partial
+    const bool share = live && len >= a.prefix;
     const float out_mult = a.v_hs ? __ldg(a.v_hs + h) : a.v_scale;
-    const bool share = live && __ldg(a.seq_lens + b) >= a.prefix;
     const size_t prow = ((size_t)b * a.Hq + hq) * a.part_splits + a.split0 + split;
     if constexpr (MT == 1) {   // the other slot's state
       sm.m[slot][r] = m;
@@ -545,8 +577,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         lse = NAN;
       }
     }
-    if (live && (MT == 2 || slot == 0))
-      a.part_lse[prow] = !share ? -INFINITY : bad ? NAN : lse;
+    lse = !share ? -INFINITY : bad ? NAN : lse;
+    if (live && (MT == 2 || slot == 0)) a.part_lse[prow] = lse;
     // MT = 2: the slot's own O; MT = 1: both, half of the dims per slot
     constexpr int kChunks = MT == 2 ? D / 32 : D / 64;
     const int c0 = MT == 2 ? 0 : slot * kChunks;
@@ -590,38 +622,115 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   }
 }
 
-template <int FMT, int D, int MT, bool P2>
-cudaError_t launch_shared_t(const TensorMaps& m, const SharedArgs& a, cudaStream_t st) {
-  using Sg = SharedGeom<FMT, D, MT>;
-  constexpr size_t smem = Sg::kOffCtl + sizeof(SharedCtl);
-  static_assert(smem <= 232448, "shared memory of one CTA");
-  auto kern = shared_prefix_kernel<FMT, D, MT, P2>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  const int tiles = (a.R + MT * kTok - 1) / (MT * kTok);
-  return launch_pdl(kern, dim3(tiles, a.Hkv, a.splits), dim3(kSharedThreads), smem, st, m.k16,
-                    m.v16, a);
+// Merge of a row's partials (the arithmetic of the split merge: M = max lse,
+// w_j = e^(lse_j - M), O = sum w_j o_j / sum w_j, 0 when all are empty), one
+// warp per row: every partial is one coalesced read, eight in flight per lane.
+constexpr int kMergeWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_rows_kernel(const CombineArgs a) {
+  constexpr int kPer = D / 32;   // dims per lane
+  using Vec = std::conditional_t<kPer == 4, float4, float2>;
+  griddep_wait();
+  const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= a.rows) return;   // the whole warp
+  const int s = a.num_splits;
+  const float* lse = a.part_lse + (size_t)row * s;
+  const Vec* po = reinterpret_cast<const Vec*>(a.part_o + (size_t)row * s * D) + lane;
+  Vec v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k < s) v[k] = __ldcg(po + k * 32);
+  const float l0 = lane < s ? __ldcg(lse + lane) : -INFINITY;
+  const float l1 = lane + 32 < s ? __ldcg(lse + lane + 32) : -INFINITY;
+  float M = fmaxf(l0, l1);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float e0 = l0 == -INFINITY ? 0.f : expf(l0 - M), e1 = l1 == -INFINITY ? 0.f : expf(l1 - M);
+  float sum = e0 + e1;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  float acc[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+#pragma unroll 1
+  for (int j0 = 0; j0 < s; j0 += 8) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int j = j0 + k;
+      const float w = __shfl_sync(0xffffffffu, j < 32 ? e0 : e1, j & 31);
+      if (j < s) {
+        const float* f = reinterpret_cast<const float*>(&v[k]);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[i] += w * f[i];
+        if (j + 8 < s) v[k] = __ldcg(po + (j + 8) * 32);
+      }
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) acc[i] *= inv;
+  const size_t at = (size_t)row * D + lane * kPer;
+  if (a.out_dtype == 0) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) store_out_t<0>(a.out, a.out_scale, at + i, acc[i]);
+  } else if (a.out_dtype == 1) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) store_out_t<1>(a.out, a.out_scale, at + i, acc[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) store_out_t<2>(a.out, a.out_scale, at + i, acc[i]);
+  }
 }
 
-template <int FMT, int D>
-cudaError_t dispatch_shared(const TensorMaps& m, const SharedArgs& a, cudaStream_t st) {
-  if (a.R > kTok)
-    return a.wide_p ? launch_shared_t<FMT, D, 2, true>(m, a, st)
-                    : launch_shared_t<FMT, D, 2, false>(m, a, st);
-  return a.wide_p ? launch_shared_t<FMT, D, 1, true>(m, a, st)
-                  : launch_shared_t<FMT, D, 1, false>(m, a, st);
+// Runs `f` with the kernel of these types and its shared memory.
+template <typename F>
+cudaError_t with_kernel(int fmt, int D, int R, int wide_p, F&& f) {
+  auto pick = [&](auto kfmt, auto kd, auto mt, auto p2) {
+    constexpr int FMT = decltype(kfmt)::value, DD = decltype(kd)::value;
+    constexpr int MT = decltype(mt)::value;
+    using Sg = SharedGeom<FMT, DD, MT>;
+    constexpr size_t smem = Sg::kOffCtl + sizeof(SharedCtl);
+    static_assert(smem <= 232448, "shared memory of one CTA");
+    return f(shared_prefix_kernel<FMT, DD, MT, decltype(p2)::value>, smem, MT);
+  };
+  auto by_p = [&](auto kfmt, auto kd, auto mt) {
+    return wide_p ? pick(kfmt, kd, mt, std::true_type{}) : pick(kfmt, kd, mt, std::false_type{});
+  };
+  auto by_rows = [&](auto kfmt, auto kd) {
+    return R > kTok ? by_p(kfmt, kd, std::integral_constant<int, 2>{})
+                    : by_p(kfmt, kd, std::integral_constant<int, 1>{});
+  };
+  using Fp8 = std::integral_constant<int, kFmtFp8>;
+  using Nvfp4 = std::integral_constant<int, kFmtNvfp4>;
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (fmt == kFmtFp8 && D == 128) return by_rows(Fp8{}, D128{});
+  if (fmt == kFmtFp8 && D == 64) return by_rows(Fp8{}, D64{});
+  if (fmt == kFmtNvfp4 && D == 128) return by_rows(Nvfp4{}, D128{});
+  if (fmt == kFmtNvfp4 && D == 64) return by_rows(Nvfp4{}, D64{});
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
+cudaError_t launch_merge_rows(const CombineArgs& a, cudaStream_t st) {
+  const dim3 grid((a.rows + kMergeWarps - 1) / kMergeWarps), block(32 * kMergeWarps);
+  if (a.num_splits > kMaxFusedSplits) return cudaErrorInvalidValue;
+  if (a.Dv == 128) return launch_pdl(merge_rows_kernel<128>, grid, block, 0, st, a);
+  if (a.Dv == 64) return launch_pdl(merge_rows_kernel<64>, grid, block, 0, st, a);
+  return cudaErrorInvalidValue;
+}
+
 cudaError_t launch_shared_prefix(int fmt, int D, const TensorMaps& m, const SharedArgs& a,
                                  cudaStream_t st) {
-  if (fmt == kFmtFp8 && D == 128) return dispatch_shared<kFmtFp8, 128>(m, a, st);
-  if (fmt == kFmtFp8 && D == 64) return dispatch_shared<kFmtFp8, 64>(m, a, st);
-  if (fmt == kFmtNvfp4 && D == 128) return dispatch_shared<kFmtNvfp4, 128>(m, a, st);
-  if (fmt == kFmtNvfp4 && D == 64) return dispatch_shared<kFmtNvfp4, 64>(m, a, st);
-  return cudaErrorInvalidValue;
+  return with_kernel(fmt, D, a.R, a.wide_p, [&](auto kern, size_t smem, int mt) {
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((a.R + mt * kTok - 1) / (mt * kTok), a.Hkv, a.splits);
+    return launch_pdl(kern, grid, dim3(kSharedThreads), smem, st, m.k16, m.v16, a);
+  });
 }
 
 }  // namespace kvq

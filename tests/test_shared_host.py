@@ -76,8 +76,11 @@ def test_splits():
                     st, sp, so = f(152, batch, hkv, g, prefix, own, 1)
                     assert st == OK and 1 <= so <= 16 and 1 <= sp
                     assert sp <= max(1, (prefix + 127) // 128) and sp + so <= 64
-    # 8 heads x 1 row tile: 19 splits fill the 152 SMs
-    assert f(152, 64, 8, 4, 32768, 1024, 1)[1] == 19
-    assert f(152, 4, 8, 4, 1024, 60, 1)[1] == 8        # one per 128 tokens
+    # few own chunks: they fit beside the prefix (8 heads x splits CTAs, one per SM)
+    sp, so = f(152, 16, 8, 4, 8192, 512, 1)[1:]
+    assert 16 * 8 * so <= 2 * (152 - 8 * sp)
+    assert f(152, 4, 8, 4, 1024, 60, 1)[1:] == (8, 1)      # one tile per split at most
+    # nothing of its own: the prefix takes the whole GPU in one wave
+    assert 8 * f(152, 8, 8, 4, 65536, 0, 1)[1] in range(128, 153)
     assert f(0, 4, 8, 4, 1024, 60, 1)[0] == INV and f(152, 4, 8, 0, 1024, 60, 1)[0] == INV
     assert f(152, 4, 8, 4, -1, 60, 1)[0] == INV and f(152, 4, 8, 4, 16, -1, 1)[0] == INV
