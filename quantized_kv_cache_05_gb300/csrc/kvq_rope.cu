@@ -2,7 +2,7 @@
 // that applies them on the way into the paged cache (sm_103a).
 //
 // For one head x of D elements, all in fp32 from the bf16 input:
-//   n_i = (x_i r) w_i,  r = RN(1 / sqrt(sum x^2 / D + eps))      (optional norm)
+//   n_i = (x_i r) w_i,  r = 1 / sqrt(sum x^2 / D + eps)          (optional norm)
 //   (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin)          (rotation)
 // over the pairs (i, i + rot/2) or (2i, 2i + 1) of the first rot elements, the
 // cosines and sines of the token's position read from the caller's fp32 table;
@@ -29,6 +29,11 @@ namespace kvq {
 namespace {
 
 constexpr int kRopeThreads = 256;
+// Resident blocks per SM: four hide the most latency where rows leave as bf16
+// (chunk of 8192 tokens, 40 heads: 31.3 us against 35.1 with three); the
+// quantisers need more registers than that leaves (4 x 2048 padded tokens, 48
+// heads: 29.7 us with three, 31.3 with four).
+constexpr int rope_ctas(int fmt) { return fmt == 0 ? 4 : 3; }
 // From this many lanes (two thousand per SM) on, groups take kRowsEach rows.
 constexpr unsigned long long kManyThreads = 152ull * 2048;
 constexpr int kRowsEach = 6;
@@ -49,80 +54,100 @@ __device__ __forceinline__ Pieces pieces(int p, int rot) {
   return r;
 }
 
-__device__ __forceinline__ void load8f(const float* p, float* f) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
+// A lane's 16 elements as packed pairs: v[0..3] its first piece, v[4..7] its second.
+struct Row {
+  uint64_t v[8];
 
-// The eight angles of a lane's pairs, and the rotation of its 16 elements.
-struct Angles {
-  float c[8], s[8];
-  // trow: the position's cosines, then (half further on) its sines
-  __device__ __forceinline__ void load(const float* trow, int half, const Pieces& pc,
-                                       bool interleaved) {
-    // half-split order: the pairs' members lie at the same place in both
-    // pieces; side by side: pairs 4 c0 .. 4 c0 + 3 in the first, 4 c1 .. in the
-    // second
-    const int i0 = interleaved ? 4 * pc.c0 : 8 * pc.c0, i1 = interleaved ? 4 * pc.c1 : i0 + 4;
-    load4(trow + i0, c);
-    load4(trow + i1, c + 4);
-    load4(trow + half + i0, s);
-    load4(trow + half + i1, s + 4);
+  static __device__ __forceinline__ uint64_t widen(uint32_t w) {   // two bf16
+    return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
-  static __device__ __forceinline__ void load4(const float* p, float* f) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  __device__ __forceinline__ void from_bf16(uint4 x0, uint4 x1) {
+    v[0] = widen(x0.x); v[1] = widen(x0.y); v[2] = widen(x0.z); v[3] = widen(x0.w);
+    v[4] = widen(x1.x); v[5] = widen(x1.y); v[6] = widen(x1.z); v[7] = widen(x1.w);
   }
-  __device__ __forceinline__ void turn(float& x, float& y, int i) const {
-    const float a = x, b = y;
-    x = __fmaf_rn(a, c[i], -__fmul_rn(b, s[i]));
-    y = __fmaf_rn(b, c[i], __fmul_rn(a, s[i]));
+  static __device__ __forceinline__ uint32_t narrow(uint64_t p) {
+    const float2 f = unpack2(p);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
-  __device__ __forceinline__ void apply(float (&f)[16], bool interleaved) const {
-    if (interleaved) {
+  __device__ __forceinline__ void store_bf16(uint16_t* row, const Pieces& pc) const {
+    *reinterpret_cast<uint4*>(row + 8 * pc.c0) =
+        make_uint4(narrow(v[0]), narrow(v[1]), narrow(v[2]), narrow(v[3]));
+    *reinterpret_cast<uint4*>(row + 8 * pc.c1) =
+        make_uint4(narrow(v[4]), narrow(v[5]), narrow(v[6]), narrow(v[7]));
+  }
+  // RMS norm of a row spread over LANES lanes: r here (every lane of the warp
+  // calls it; the length is a power of two), the weights below.
+  template <int LANES>
+  __device__ __forceinline__ float inv_rms(float eps) const {
+    uint64_t s2 = 0ull;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) turn(f[2 * i], f[2 * i + 1], i);
-    } else {
+    for (int i = 0; i < 8; ++i) s2 = fma2(v[i], v[i], s2);
+    const float2 s = unpack2(s2);
+    float ss = s.x + s.y;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) turn(f[i], f[8 + i], i);
-    }
+    for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    return rsqrtf(ss * (1.0f / (LANES * 16)) + eps);
+  }
+  __device__ __forceinline__ void norm(float r, const float* w, const Pieces& pc) {
+    const uint64_t r2 = pack2(r, r);
+    const float4* w0 = reinterpret_cast<const float4*>(w + 8 * pc.c0);
+    const float4* w1 = reinterpret_cast<const float4*>(w + 8 * pc.c1);
+    const float4 a = __ldg(w0), b = __ldg(w0 + 1), c = __ldg(w1), d = __ldg(w1 + 1);
+    v[0] = mul2(mul2(v[0], r2), pack2(a.x, a.y));
+    v[1] = mul2(mul2(v[1], r2), pack2(a.z, a.w));
+    v[2] = mul2(mul2(v[2], r2), pack2(b.x, b.y));
+    v[3] = mul2(mul2(v[3], r2), pack2(b.z, b.w));
+    v[4] = mul2(mul2(v[4], r2), pack2(c.x, c.y));
+    v[5] = mul2(mul2(v[5], r2), pack2(c.z, c.w));
+    v[6] = mul2(mul2(v[6], r2), pack2(d.x, d.y));
+    v[7] = mul2(mul2(v[7], r2), pack2(d.z, d.w));
   }
 };
 
-// 1 / rms of a row spread over LANES lanes (every lane of the warp calls it).
-template <int LANES>
-__device__ __forceinline__ float inv_rms(const float (&f)[16], float eps) {
-  float ss = 0.f;
+// The angles of a lane's eight pairs, and the rotation of its elements.
+// Half-split order: both members of a pair lie at the same place in the two
+// pieces; side by side (INTER): in the two halves of a packed pair, which takes
+// the cosine (sine) twice.
+template <bool INTER>
+struct Angles {
+  static constexpr int kN = INTER ? 8 : 4;
+  uint64_t c[kN], s[kN], n[INTER ? 1 : kN];   // cos, sin (INTER: (-sin, sin)), -sin
+  // trow: the position's cosines, then (half further on) its sines
+  __device__ __forceinline__ void load(const float* trow, int half, const Pieces& pc) {
+    const int i0 = INTER ? 4 * pc.c0 : 8 * pc.c0, i1 = INTER ? 4 * pc.c1 : 8 * pc.c0 + 4;
+    const float4 ca = __ldg(reinterpret_cast<const float4*>(trow + i0));
+    const float4 cb = __ldg(reinterpret_cast<const float4*>(trow + i1));
+    const float4 sa = __ldg(reinterpret_cast<const float4*>(trow + half + i0));
+    const float4 sb = __ldg(reinterpret_cast<const float4*>(trow + half + i1));
+    const float cs[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+    const float sn[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) ss = __fmaf_rn(f[i], f[i], ss);
-#pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  return __frsqrt_rn(ss * (1.0f / (LANES * 16)) + eps);   // the length is a power of two
-}
-
-__device__ __forceinline__ void apply_norm(float (&f)[16], float r, const float* w,
-                                           const Pieces& pc) {
-  float w0[8], w1[8];
-  load8f(w + 8 * pc.c0, w0);
-  load8f(w + 8 * pc.c1, w1);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f[i] = (f[i] * r) * w0[i];
-    f[8 + i] = (f[8 + i] * r) * w1[i];
+    for (int i = 0; i < kN; ++i) {
+      if constexpr (INTER) {
+        c[i] = pack2(cs[i], cs[i]);
+        s[i] = pack2(-sn[i], sn[i]);
+      } else {
+        c[i] = pack2(cs[2 * i], cs[2 * i + 1]);
+        s[i] = pack2(sn[2 * i], sn[2 * i + 1]);
+        n[i] = pack2(-sn[2 * i], -sn[2 * i + 1]);
+      }
+    }
   }
-}
-
-__device__ __forceinline__ uint4 pack_bf16x8(const float* f) {
-  uint32_t w[4];
+  __device__ __forceinline__ void apply(Row& x) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int i = 0; i < kN; ++i) {
+      if constexpr (INTER) {
+        const float2 f = unpack2(x.v[i]);
+        x.v[i] = fma2(x.v[i], c[i], mul2(pack2(f.y, f.x), s[i]));
+      } else {
+        const uint64_t a = x.v[i], b = x.v[4 + i];
+        x.v[i] = fma2(a, c[i], mul2(b, n[i]));
+        x.v[4 + i] = fma2(b, c[i], mul2(a, s[i]));
+      }
+    }
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
+};
 
 __device__ __forceinline__ uint2 pack_e4m3x8(const float* f) {
   const uint32_t lo = f32x2_to_e4m3x2(f[0], f[1]) | (f32x2_to_e4m3x2(f[2], f[3]) << 16);
@@ -130,39 +155,64 @@ __device__ __forceinline__ uint2 pack_e4m3x8(const float* f) {
   return make_uint2(lo, hi);
 }
 
-// E4M3(fl32(x / s)) of a lane's 16 elements (z = RN(1/s)).
-__device__ __forceinline__ void store_e4m3(float (&f)[16], float s, float z, uint8_t* row,
+// E4M3(fl32(x / s)) of a lane's 16 elements (z = RN(1/s)): the quotients of
+// quotients_for_codes, in packed pairs.
+__device__ __forceinline__ void store_e4m3(const Row& x, float s, float z, uint8_t* row,
                                            const Pieces& pc) {
-  quotients_for_codes<16>(f, s, z, kE4m3Low);
-  *reinterpret_cast<uint2*>(row + 8 * pc.c0) = pack_e4m3x8(f);
-  *reinterpret_cast<uint2*>(row + 8 * pc.c1) = pack_e4m3x8(f + 8);
+  const uint64_t z2 = pack2(z, z), ns2 = pack2(-s, -s);
+  Floats<16> q;
+  uint32_t m = 0xFFFFFFFFu;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t q0 = mul2(x.v[i], z2);
+    const float2 f = unpack2(fma2(fma2(q0, ns2, x.v[i]), z2, q0));
+    q.v[2 * i] = f.x;
+    q.v[2 * i + 1] = f.y;
+    m = min(m, min((__float_as_uint(f.x) + 1u) & kE4m3Low, (__float_as_uint(f.y) + 1u) & kE4m3Low));
+  }
+  if (m <= 2u) {   // some quotient next to a rounding boundary
+    Floats<16> in;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = unpack2(x.v[i]);
+      in.v[2 * i] = f.x;
+      in.v[2 * i + 1] = f.y;
+    }
+    q = ieee_quotients<16>(in, s);
+  }
+  *reinterpret_cast<uint2*>(row + 8 * pc.c0) = pack_e4m3x8(q.v);
+  *reinterpret_cast<uint2*>(row + 8 * pc.c1) = pack_e4m3x8(q.v + 8);
 }
 
 // One NVFP4 half block (8 elements; the neighbouring lane holds the other
 // half): codes in a word, and the block's scale code.  Every lane of the warp
 // calls it.
-__device__ __forceinline__ uint32_t nvfp4_half(const float* x, float g, uint32_t& sc) {
+__device__ __forceinline__ uint32_t nvfp4_half(const uint64_t* v, float g, uint32_t& sc) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack2(v[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
   float bamax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) bamax = fmaxf(bamax, fabsf(x[i]));
+  for (int i = 0; i < 8; ++i) bamax = fmaxf(bamax, fabsf(f[i]));
   bamax = fmaxf(bamax, __shfl_xor_sync(0xffffffffu, bamax, 1));
   const float scf = __fdiv_rn(__fdiv_rn(bamax, 6.0f), g);
   sc = f32x2_to_e4m3x2(scf, 0.f) & 0xFFu;
   const float es = __fmul_rn(unpack_f16x2(e4m3x2_to_f16x2(sc)).x, g);
   if (es == 0.f) return 0u;
-  float f[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = x[i];
   quotients_for_codes<8>(f, es, __frcp_rn(es), kE2m1Low);
   return f32x8_to_e2m1x8(f);
 }
 
 // Both pieces of a lane as NVFP4 codes of cache row `row`; `ok` gates the stores.
 template <int D>
-__device__ __forceinline__ void store_nvfp4(float (&f)[16], float g, bool ok, uint8_t* codes,
+__device__ __forceinline__ void store_nvfp4(const Row& x, float g, bool ok, uint8_t* codes,
                                             uint8_t* scales, long row, const Pieces& pc) {
   uint32_t s0, s1;
-  const uint32_t w0 = nvfp4_half(f, g, s0), w1 = nvfp4_half(f + 8, g, s1);
+  const uint32_t w0 = nvfp4_half(x.v, g, s0), w1 = nvfp4_half(x.v + 4, g, s1);
   if (!ok) return;
   *reinterpret_cast<uint32_t*>(codes + row * (D / 2) + 4 * pc.c0) = w0;
   *reinterpret_cast<uint32_t*>(codes + row * (D / 2) + 4 * pc.c1) = w1;
@@ -216,10 +266,12 @@ __device__ __forceinline__ long rope_page(const RopeArgs& a, const Token& k, boo
 
 // FMT 0: bf16 rows out (kvq_norm_rope); otherwise K and V go to the cache.
 // `per_token` lane groups of a block share a token (a power of two), and
-// gridDim.y blocks: a group takes every (per_token gridDim.y)-th of its rows,
-// the next row's loads going out before the present one's arithmetic.
-template <int D, int FMT>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, int per_token) {
+// gridDim.y blocks: a group takes every (per_token gridDim.y)-th of the token's
+// rows (queries, keys, values in one numbering), the next row's loads going
+// out before the present one's arithmetic.
+template <int D, int FMT, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads, rope_ctas(FMT))
+    rope_kernel(const RopeArgs a, int per_token) {
   // the append is an ordinary launch (it starts after all earlier work), the
   // other a programmatic one
   if constexpr (FMT == 0) griddep_wait();
@@ -227,68 +279,62 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
   constexpr int kLanes = D / 16, kGroups = kRopeThreads / kLanes;
   const int p = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
   const unsigned token = blockIdx.x * (unsigned)(kGroups / per_token) + group / per_token;
-  const int H = a.q.heads + a.k.heads + a.v.heads;
+  const int nq = a.q.heads, nqk = nq + a.k.heads, H = nqk + (FMT == 0 ? 0 : a.v.heads);
   const int first = blockIdx.y * per_token + group % per_token, step = per_token * gridDim.y;
-  const bool in = token < a.tokens;
-  const Token tk = token_of(a, in ? token : 0, in && p == 0 && first == 0);
+  const bool in = token < a.tokens, report = in && p == 0 && first == 0;
+  const Token tk = token_of(a, in ? token : 0, report);
   const bool ok = in && tk.ok;
+  if (!__any_sync(0xffffffffu, ok)) return;   // padding: the whole warp
+  const Pieces turned = pieces<D>(p, a.rot);
 
-  // where row i of the token comes from
-  auto source = [&](int i) -> const uint16_t* {
-    const bool isq = i < a.q.heads, isv = i >= a.q.heads + a.k.heads;
-    const RopeRows& src = isq ? a.q : isv ? a.v : a.k;
-    const int h = i - (isq ? 0 : isv ? a.q.heads + a.k.heads : a.q.heads);
-    return src.data + (long)token * src.token_stride + (long)h * src.head_stride;
-  };
-  const Pieces turned = pieces<D>(p, a.rot), plain = pieces<D>(p, 0);
   auto fetch = [&](int i, uint4& x0, uint4& x1) {
     x0 = x1 = make_uint4(0, 0, 0, 0);
     if (!ok || i >= H) return;
-    const Pieces& pc = i < a.q.heads + a.k.heads ? turned : plain;
-    const uint16_t* x = source(i);
+    const bool isq = i < nq, isv = FMT != 0 && i >= nqk;
+    const RopeRows& src = isq ? a.q : isv ? a.v : a.k;
+    const int h = i - (isq ? 0 : isv ? nqk : nq);
+    const uint16_t* x = src.data + (long)token * src.token_stride + (long)h * src.head_stride;
+    const Pieces pc = isv ? pieces<D>(p, 0) : turned;
     x0 = *reinterpret_cast<const uint4*>(x + 8 * pc.c0);
     x1 = *reinterpret_cast<const uint4*>(x + 8 * pc.c1);
   };
   uint4 x0, x1;
   fetch(first, x0, x1);
-  Angles ang;
-  if (turned.turn && ok)
-    ang.load(a.cos_sin + tk.pos * a.rot, a.rot / 2, turned, a.interleaved != 0);
-  // the page is the token's, whatever the head
+  Angles<INTER> ang;
+  if (turned.turn && ok) ang.load(a.cos_sin + tk.pos * a.rot, a.rot / 2, turned);
+  // cache row of kv head 0: the token's, whatever the head
   long page_row = -1;
-  if constexpr (FMT != 0) page_row = ok ? rope_page(a, tk, p == 0 && first == 0) : -1;
+  if constexpr (FMT != 0) page_row = ok ? rope_page(a, tk, report) : -1;
 
 #pragma unroll 1
   for (int i0 = 0; i0 < H; i0 += step) {   // the same rounds for every lane of the warp
     const int i = i0 + first;
     const bool row = ok && i < H;
-    const bool isq = i < a.q.heads, isv = i >= a.q.heads + a.k.heads;
-    const int h = i - (isq ? 0 : isv ? a.q.heads + a.k.heads : a.q.heads);
-    const Pieces& pc = isv ? plain : turned;
-    float f[16];
-    bf16x8_to_f32(x0, f);
-    bf16x8_to_f32(x1, f + 8);
+    const bool isq = i < nq, isv = FMT != 0 && i >= nqk;
+    const int h = i - (isq ? 0 : isv ? nqk : nq);
+    const Pieces pc = isv ? pieces<D>(p, 0) : turned;
+    Row f;
+    f.from_bf16(x0, x1);
     if (i0 + step < H) fetch(i + step, x0, x1);
     // every lane of the warp takes part in the norm's butterfly when any row
     // of the call has a norm
     const float* w = isq ? a.q_norm : isv ? nullptr : a.k_norm;
     if (a.q_norm || a.k_norm) {
-      const float r = inv_rms<kLanes>(f, a.eps);
-      if (w) apply_norm(f, r, w, pc);
+      const float r = f.template inv_rms<kLanes>(a.eps);
+      if (w) f.norm(r, w, pc);
     }
-    if (turned.turn && !isv) ang.apply(f, a.interleaved != 0);
+    if (turned.turn && !isv) ang.apply(f);
 
     if (isq || FMT == 0) {
-      const RopeRows& dst = isq ? a.q_out : a.k_out;
-      const long at = (long)token * dst.token_stride + (long)h * dst.head_stride;
       if (row) {
+        const RopeRows& dst = isq ? a.q_out : a.k_out;
+        const long at = (long)token * dst.token_stride + (long)h * dst.head_stride;
         if (isq && a.q_fp8) {
           const float s = a.q_hs ? __ldg(a.q_hs + h) : a.q_scale;
-          const float z = a.q_hs ? __frcp_rn(s) : a.q_recip;
-          store_e4m3(f, s, z, reinterpret_cast<uint8_t*>(dst.data) + at, pc);
+          store_e4m3(f, s, a.q_hs ? __frcp_rn(s) : a.q_recip,
+                     reinterpret_cast<uint8_t*>(dst.data) + at, pc);
         } else {
-          *reinterpret_cast<uint4*>(dst.data + at + 8 * pc.c0) = pack_bf16x8(f);
-          *reinterpret_cast<uint4*>(dst.data + at + 8 * pc.c1) = pack_bf16x8(f + 8);
+          f.store_bf16(dst.data + at, pc);
         }
       }
     }
@@ -297,15 +343,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
       const long crow = page_row + (long)h * a.ps;
       const float* hs = isv ? a.v_hs : a.k_hs;
       const float s = (hs && store) ? __ldg(hs + h) : (isv ? a.v_scale : a.k_scale);
+      uint8_t* codes = isv ? a.v_codes : a.k_codes;
       if constexpr (FMT == kFmtFp8) {
-        if (store) {
-          const float z = hs ? __frcp_rn(s) : (isv ? a.v_recip : a.k_recip);
-          store_e4m3(f, s, z, (isv ? a.v_codes : a.k_codes) + crow * D, pc);
-        }
-      } else {
-        // lanes without a row stay for their neighbours' shuffles
-        store_nvfp4<D>(f, s, store, isv ? a.v_codes : a.k_codes, isv ? a.v_bscale : a.k_bscale,
-                       crow, pc);
+        if (store)
+          store_e4m3(f, s, hs ? __frcp_rn(s) : (isv ? a.v_recip : a.k_recip), codes + crow * D, pc);
+      } else {   // lanes without a row stay for their neighbours' shuffles
+        store_nvfp4<D>(f, s, store, codes, isv ? a.v_bscale : a.k_bscale, crow, pc);
       }
     }
   }
@@ -313,6 +356,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
 
 // MLA: one warp per token, the 512-wide latent (normed, then NVFP4) on all
 // lanes, the 64 rope-key elements (rotated, bf16) on the first four.
+template <bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_mla_kernel(const RopeArgs a) {
   griddep_launch_dependents();
   constexpr int D = 512, kRope = 64;
@@ -325,7 +369,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_mla_kernel(const RopeArgs a
 
   const Pieces pc = pieces<D>(lane, 0);
   const uint16_t* x = a.k.data + (long)token * a.k.token_stride;
-  float f[16];
   const uint4 x0 = *reinterpret_cast<const uint4*>(x + 8 * pc.c0);
   const uint4 x1 = *reinterpret_cast<const uint4*>(x + 8 * pc.c1);
   uint4 e0 = make_uint4(0, 0, 0, 0), e1 = e0;
@@ -335,28 +378,22 @@ __global__ void __launch_bounds__(kRopeThreads) rope_mla_kernel(const RopeArgs a
     e0 = *reinterpret_cast<const uint4*>(xe + 8 * pe.c0);
     e1 = *reinterpret_cast<const uint4*>(xe + 8 * pe.c1);
   }
-  bf16x8_to_f32(x0, f);
-  bf16x8_to_f32(x1, f + 8);
-  if (a.k_norm) {
-    const float r = inv_rms<32>(f, a.eps);
-    apply_norm(f, r, a.k_norm, pc);
-  }
+  Row f;
+  f.from_bf16(x0, x1);
+  if (a.k_norm) f.norm(f.inv_rms<32>(a.eps), a.k_norm, pc);
   store_nvfp4<D>(f, a.k_scale, true, a.k_codes, a.k_bscale, crow, pc);
   if (lane < kRope / 16) {
-    bf16x8_to_f32(e0, f);
-    bf16x8_to_f32(e1, f + 8);
+    f.from_bf16(e0, e1);
     if (pe.turn) {
-      Angles ang;
-      ang.load(a.cos_sin + tk.pos * a.rot, a.rot / 2, pe, a.interleaved != 0);
-      ang.apply(f, a.interleaved != 0);
+      Angles<INTER> ang;
+      ang.load(a.cos_sin + tk.pos * a.rot, a.rot / 2, pe);
+      ang.apply(f);
     }
-    uint16_t* dst = a.k_pe + crow * kRope;
-    *reinterpret_cast<uint4*>(dst + 8 * pe.c0) = pack_bf16x8(f);
-    *reinterpret_cast<uint4*>(dst + 8 * pe.c1) = pack_bf16x8(f + 8);
+    f.store_bf16(a.k_pe + crow * kRope, pe);
   }
 }
 
-template <int D>
+template <int D, bool INTER>
 cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t st) {
   constexpr int kGroups = kRopeThreads / (D / 16);
   const int H = a.q.heads + a.k.heads + a.v.heads;
@@ -374,27 +411,32 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t st) {
   }
   const unsigned per_block = (unsigned)(kGroups / per_token);
   const dim3 grid((a.tokens + per_block - 1) / per_block, y), block(kRopeThreads);
-  if (a.fmt == 0) return launch_pdl(rope_kernel<D, 0>, grid, block, 0, st, a, per_token);
+  if (a.fmt == 0) return launch_pdl(rope_kernel<D, 0, INTER>, grid, block, 0, st, a, per_token);
   if (a.fmt == kFmtFp8)
-    rope_kernel<D, kFmtFp8><<<grid, block, 0, st>>>(a, per_token);
+    rope_kernel<D, kFmtFp8, INTER><<<grid, block, 0, st>>>(a, per_token);
   else
-    rope_kernel<D, kFmtNvfp4><<<grid, block, 0, st>>>(a, per_token);
+    rope_kernel<D, kFmtNvfp4, INTER><<<grid, block, 0, st>>>(a, per_token);
   return cudaGetLastError();
+}
+
+template <bool INTER>
+cudaError_t dispatch_rope(int D, bool mla, const RopeArgs& a, cudaStream_t st) {
+  if (mla) {
+    const unsigned per = kRopeThreads / 32;
+    rope_mla_kernel<INTER><<<(a.tokens + per - 1) / per, kRopeThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  if (D == 64) return launch_rope_t<64, INTER>(a, st);
+  if (D == 128) return launch_rope_t<128, INTER>(a, st);
+  if (D == 256) return launch_rope_t<256, INTER>(a, st);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 cudaError_t launch_rope(int D, bool mla, const RopeArgs& a, cudaStream_t st) {
   if (a.tokens == 0) return cudaSuccess;
-  if (mla) {
-    const unsigned per = kRopeThreads / 32;
-    rope_mla_kernel<<<(a.tokens + per - 1) / per, kRopeThreads, 0, st>>>(a);
-    return cudaGetLastError();
-  }
-  if (D == 64) return launch_rope_t<64>(a, st);
-  if (D == 128) return launch_rope_t<128>(a, st);
-  if (D == 256) return launch_rope_t<256>(a, st);
-  return cudaErrorInvalidValue;
+  return a.interleaved ? dispatch_rope<true>(D, mla, a, st) : dispatch_rope<false>(D, mla, a, st);
 }
 
 }  // namespace kvq

@@ -2,12 +2,12 @@
 intervals that the fp32 kernels' results must lie in.
 
 fp32 error of a kernel value y = n_a cos -+ n_b sin, u = 2^-24: the sum of at
-most 512 squares is 16 fused steps per lane and at most 5 butterfly adds, all
-of positive terms: 21 u; the mean's scaling is exact; + eps 1 u; half of that
-through the root, and its rounding 1 u: r within 12 u; n = (x r) w adds 2 u;
-each product of the rotation is rounded once and the sum once: 2 u more.
-Altogether |y' - y| <= 16 u (|n_a cos| + |n_b sin|); 20 u leaves room for the
-second-order terms.
+most 512 squares is 8 fused steps per lane and at most 6 adds, all of positive
+terms: 14 u; the mean's scaling is exact; + eps 1 u; half of that through the
+root, whose own error is at most 2 units in the last place, 4 u: r within 12 u;
+n = (x r) w adds 2 u; each product of the rotation is rounded once and the sum
+once: 2 u more.  Altogether |y' - y| <= 16 u (|n_a cos| + |n_b sin|); 20 u leaves
+room for the second-order terms.
 """
 import numpy as np
 
