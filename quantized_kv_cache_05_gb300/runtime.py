@@ -78,29 +78,31 @@ class Rotary:
             _check(w is None or dim is None or w.numel() == dim, f"{what}: expected {dim} weights")
 
 
-def _heads(t: torch.Tensor, what: str, out_fp8: bool = False) -> kvq.kvq_heads:
+def _heads(t: torch.Tensor, what: str, dtype: torch.dtype = torch.bfloat16) -> kvq.kvq_heads:
     """Rows of heads [tokens][heads][dim] or [batch][tokens][heads][dim] whose
     tokens lie at one stride (a slice of a packed projection does)."""
-    _here(t, torch.uint8 if out_fp8 else torch.bfloat16, what)
+    _here(t, dtype, what)
     sh, st = t.shape, t.stride()
     n = len(sh)
-    if n == 4:
+    if n == 3:
+        if st[2] == 1:
+            return kvq.kvq_heads(t.data_ptr(), st[0], st[1], sh[1])
+    elif n == 4 and st[3] == 1:
         # one token per request: the requests are the tokens
         tok = st[0] if sh[1] == 1 else st[1]
-        one = sh[0] == 1 or st[0] == sh[1] * tok
-    else:
-        tok, one = st[0], n == 3
-    if not one or st[-1] != 1:
-        raise ValueError(f"{what}: expected [(batch,) tokens][heads][dim] rows, dim dense, the "
-                         "tokens at one stride")
-    return kvq.kvq_heads(t.data_ptr(), tok, st[-2], sh[-2])
+        if sh[0] == 1 or st[0] == sh[1] * tok:
+            return kvq.kvq_heads(t.data_ptr(), tok, st[2], sh[2])
+    raise ValueError(f"{what}: expected [(batch,) tokens][heads][dim] rows, dim dense, the tokens at "
+                     "one stride")
 
 
 def _query_out(q: torch.Tensor, out: Optional[torch.Tensor], kind: str) -> torch.Tensor:
-    _check(kind in ("bf16", "e4m3"), "q_out_type: bf16 or e4m3")
+    if kind not in OUT_TORCH or kind == "f32":
+        raise ValueError("q_out_type: bf16 or e4m3")
     if out is None:
-        return torch.empty(q.shape, dtype=OUT_TORCH[kind], device=q.device)
-    _check(out.numel() == q.numel() and out.shape[-2:] == q.shape[-2:], "q_out: expected q's shape")
+        return torch.empty_like(q, dtype=OUT_TORCH[kind], memory_format=torch.contiguous_format)
+    if out.numel() != q.numel() or out.shape[-2:] != q.shape[-2:]:
+        raise ValueError("q_out: expected q's shape")
     return out
 
 
@@ -120,11 +122,11 @@ def norm_rope(rotary: Rotary, q: Optional[torch.Tensor], k: Optional[torch.Tenso
     bf16 [T][Hk][D], positions int32 [T].  Returns (q_out, k_out): new tensors, or the
     given ones (bf16 outputs may be the inputs).  q_out_type "e4m3": uint8 codes."""
     some = q if q is not None else k
-    _check(some is not None, "norm_rope: q or k is needed")
-    _check(some.dim() == 3, "norm_rope: expected [tokens][heads][dim]")
-    T, D = some.shape[0], some.shape[2]
-    _check(k is None or k.dim() == 3 and (k.shape[0], k.shape[2]) == (T, D),
-           "k: expected q's tokens and dim")
+    if some is None or some.dim() != 3:
+        raise ValueError("norm_rope: expected [tokens][heads][dim] in q, k or both")
+    T, _, D = some.shape
+    if k is not None and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != D):
+        raise ValueError("k: expected q's tokens and dim")
     rotary.check_dim(None if q is None else D, None if k is None else D)
     if positions is not None:
         _index(positions, T, "positions")
@@ -134,10 +136,12 @@ def norm_rope(rotary: Rotary, q: Optional[torch.Tensor], k: Optional[torch.Tenso
         q_out = _query_out(q, q_out, q_out_type)
         _head_scale(q_head_scale, q.shape[1])
         if T:
-            qh, qo = _heads(q, "q"), _heads(q_out, "q_out", fp8)
+            qh, qo = _heads(q, "q"), _heads(q_out, "q_out", OUT_TORCH[q_out_type])
     if k is not None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-        _check(k_out.shape == k.shape, "k_out: expected k's shape")
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        elif k_out.shape != k.shape:
+            raise ValueError("k_out: expected k's shape")
         if T:
             kh, ko = _heads(k, "k"), _heads(k_out, "k_out")
     if T:
@@ -229,23 +233,13 @@ class QuantizedKVCache:
         return self.rope > 0
 
     def struct(self) -> kvq.kvq_cache:
-        c = kvq.kvq_cache()
-        c.fmt = FMT[self.fmt]
-        c.num_pages, c.page_size = self.num_pages, self.page_size
-        c.num_kv_heads, c.head_dim = self.Hkv, self.D
-        c.k_codes = self.k_codes.data_ptr()
-        c.v_codes = self.v_codes.data_ptr() if self.v_codes is not None else None
-        c.k_bscale = self.k_bscale.data_ptr() if self.k_bscale is not None else None
-        c.v_bscale = self.v_bscale.data_ptr() if self.v_bscale is not None else None
-        c.k_scale, c.v_scale = self.k_scale, self.v_scale
-        c.block_table = self.block_table.data_ptr()
-        c.max_pages_per_seq = self.max_pages_per_seq
-        c.rope_dim = self.rope
-        c.k_pe = self.k_pe.data_ptr() if self.k_pe is not None else None
-        c.v_is_k_latent = 1 if self.mla else 0
-        c.k_head_scale = self.k_head_scale.data_ptr() if self.k_head_scale is not None else None
-        c.v_head_scale = self.v_head_scale.data_ptr() if self.v_head_scale is not None else None
-        return c
+        # in the order of kvq_cache's fields
+        ptr = lambda t: None if t is None else t.data_ptr()
+        return kvq.kvq_cache(
+            FMT[self.fmt], self.num_pages, self.page_size, self.Hkv, self.D, ptr(self.k_codes),
+            ptr(self.v_codes), ptr(self.k_bscale), ptr(self.v_bscale), self.k_scale, self.v_scale,
+            ptr(self.block_table), self.max_pages_per_seq, self.rope, ptr(self.k_pe),
+            1 if self.mla else 0, ptr(self.k_head_scale), ptr(self.v_head_scale))
 
     def append(self, k_new: torch.Tensor, v_new: Optional[torch.Tensor],
                start_pos: torch.Tensor, kpe_new: Optional[torch.Tensor] = None,
@@ -268,34 +262,37 @@ class QuantizedKVCache:
         int32 [B] or None (all T).  MLA: k_new the latents [B][T][1][512], kpe_new
         [B][T][1][64].  Returns q_out (q_out_type "bf16", or "e4m3": uint8 codes; by
         default q_out's own type, bf16 without one)."""
-        _check(k_new.dim() == 4, "k_new: expected [batch][tokens][kv heads][dim]")
-        B, T = k_new.shape[:2]
-        _check(k_new.shape[2:] == (self.Hkv, self.D), "k_new: expected the cache's heads and dim")
-        _check(self.mla or v_new is not None and v_new.shape == k_new.shape,
-               "v_new: expected k_new's shape")
-        _check(not self.mla or kpe_new is not None and kpe_new.shape == (B, T, 1, self.rope),
-               "kpe_new: expected [batch][tokens][1][rope]")
-        _check(B <= self.block_table.shape[0], "more requests than the block table has")
-        _check(q is None or q.dim() == 4 and q.shape[:2] == (B, T) and q.shape[3] == self.D,
-               "q: expected [batch][tokens][heads][dim]")
-        rotary.check_dim(None if q is None else self.D, self.D)
+        sh = k_new.shape
+        if len(sh) != 4 or sh[2] != self.Hkv or sh[3] != self.D:
+            raise ValueError("k_new: expected [batch][tokens][kv heads][dim] of the cache's")
+        B, T = sh[0], sh[1]
+        if not self.mla and (v_new is None or v_new.shape != sh):
+            raise ValueError("v_new: expected k_new's shape")
+        if self.mla and (kpe_new is None or kpe_new.shape != (B, T, 1, self.rope)):
+            raise ValueError("kpe_new: expected [batch][tokens][1][rope]")
+        if B > self.block_table.shape[0]:
+            raise ValueError("more requests than the block table has")
+        qh = qo = None
         fp8 = False
         if q is not None:
+            if q.dim() != 4 or q.shape[:2] != sh[:2] or q.shape[3] != self.D:
+                raise ValueError("q: expected [batch][tokens][heads][dim]")
             kind = q_out_type or ("e4m3" if q_out is not None and q_out.dtype == torch.uint8 else "bf16")
             q_out = _query_out(q, q_out, kind)
             _head_scale(q_head_scale, q.shape[2])
             fp8 = kind == "e4m3"
+        rotary.check_dim(None if q is None else self.D, self.D)
         if B == 0 or T == 0:
             return q_out
         _index(start_pos, B, "start_pos")
         if new_lens is not None:
             _index(new_lens, B, "new_lens")
+        if q is not None:
+            qh, qo = _heads(q, "q"), _heads(q_out, "q_out", OUT_TORCH[kind])
         kvq.check(kvq.kvq_rope_append(
             self.struct(), rotary.struct(), B, T, start_pos, new_lens, _heads(k_new, "k_new"),
             None if v_new is None else _heads(v_new, "v_new"),
-            None if kpe_new is None else _heads(kpe_new, "kpe_new"),
-            None if q is None else _heads(q, "q"),
-            None if q is None else _heads(q_out, "q_out", fp8), 1 if fp8 else 0, q_scale,
+            None if kpe_new is None else _heads(kpe_new, "kpe_new"), qh, qo, 1 if fp8 else 0, q_scale,
             q_head_scale, error_flag, stream), "kvq_rope_append")
         return q_out
 
@@ -323,19 +320,13 @@ class DecodeConfig:
 
     def params(self, seq_lens: torch.Tensor, error_flag: Optional[torch.Tensor] = None
                ) -> kvq.kvq_decode_params:
-        p = kvq.kvq_decode_params()
-        p.batch, p.num_q_heads = self.batch, self.num_q_heads
-        p.qk_dim, p.v_dim, p.num_splits = self.qk_dim, self.v_dim, self.num_splits
-        p.seq_lens = seq_lens.data_ptr()
-        p.max_kv_len = self.max_kv_len
-        p.sm_scale, p.prob_scale = self.sm_scale, self.prob_scale
-        p.out_dtype, p.out_scale = OUT[self.out], self.out_scale
-        p.error_flag = error_flag.data_ptr() if error_flag is not None else None
-        p.fresh_tokens = self.fresh_tokens
-        p.q_fp8 = 1 if self.q_fp8 else 0
-        p.q_scale = self.q_scale
-        p.q_head_scale = self.q_head_scale.data_ptr() if self.q_head_scale is not None else None
-        return p
+        # in the order of kvq_decode_params' fields
+        ptr = lambda t: None if t is None else t.data_ptr()
+        return kvq.kvq_decode_params(
+            self.batch, self.num_q_heads, self.qk_dim, self.v_dim, self.num_splits,
+            seq_lens.data_ptr(), self.max_kv_len, self.sm_scale, self.prob_scale, OUT[self.out],
+            self.out_scale, ptr(error_flag), self.fresh_tokens, 1 if self.q_fp8 else 0, self.q_scale,
+            ptr(self.q_head_scale))
 
 
 class DecodeWorkspace:
@@ -449,8 +440,8 @@ class SharedDecode:
         -> the output buffer [batch][Hq][D], overwritten by the next step."""
         cfg, ws = self.cfg, self.ws
         _here(q, torch.uint8 if cfg.q_fp8 else torch.bfloat16, "q")
-        _check(q.shape == (cfg.batch, cfg.num_q_heads, cfg.qk_dim) and q.is_contiguous(),
-               "q: expected a contiguous [batch][heads][dim]")
+        if q.shape != (cfg.batch, cfg.num_q_heads, cfg.qk_dim) or not q.is_contiguous():
+            raise ValueError("q: expected a contiguous [batch][heads][dim]")
         _index(seq_lens, cfg.batch, "seq_lens")
         if cfg.batch:
             kvq.check(kvq.kvq_decode_shared(
