@@ -1,10 +1,12 @@
-"""Build the CUDA library libkvq.so in-tree (nvcc, sm_103a only)."""
+"""Build the CUDA library libkvq.so (nvcc, sm_103a only) and the marshalling
+module of the per-step calls (the C compiler, CPython headers) in-tree."""
 from __future__ import annotations
 
 import concurrent.futures
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -12,6 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkvq.so")
+CALL = os.path.join(HERE, "_kvq_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["kvq_api.cu", "kvq_append.cu", "kvq_decode.cu", "kvq_decode_nvfp4.cu", "kvq_mla.cu",
            "kvq_prefill.cu", "kvq_rope.cu",
            "kvq_shared.cu"]
@@ -35,8 +38,24 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def build_call() -> str:
+    """The marshalling module of runtime.py's per-step calls (_kvq_call)."""
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if not cc:
+        raise RuntimeError("no C compiler: it is required to build the _kvq_call module")
+    tmp = CALL + ".tmp"
+    cmd = [cc, "-O2", "-Wall", "-Wextra", "-shared", "-fPIC", "-std=c11", "-I", INCLUDE, "-I",
+           sysconfig.get_paths()["include"], "-o", tmp, os.path.join(CSRC, "kvq_call.c")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed for kvq_call.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL)
+    return CALL
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime()
+                         for f in (LIB, CALL)):
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     cc = nvcc()
@@ -52,8 +71,10 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             print(r.stdout + r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        call = ex.submit(build_call)
         objs = list(ex.map(compile_one, SOURCES))
+        call.result()
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -6,6 +6,7 @@ computation is a libkvq.so kernel.  Nothing here falls back to torch math.
 """
 from __future__ import annotations
 
+import ctypes
 import dataclasses
 from typing import Optional
 
@@ -28,6 +29,26 @@ def rope_table(num_positions: int, rot_dim: int, base: float = 10000.0,
     return torch.cat([ang.cos(), ang.sin()], 1).float().contiguous()
 
 
+_call = None
+
+
+def _calls():
+    """The marshalling module, bound to the loaded library.  A missing one raises."""
+    global _call
+    if _call is None:
+        L = kvq.lib()
+        try:
+            from . import _kvq_call as m
+        except ImportError as e:
+            raise RuntimeError("the _kvq_call module is missing: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        ptr = lambda f: ctypes.cast(f, ctypes.c_void_p).value
+        m.bind(ptr(L.kvq_norm_rope), ptr(L.kvq_rope_append), ptr(L.kvq_decode_shared),
+               torch.bfloat16, torch.uint8, torch.int32, torch.float32)
+        _call = m
+    return _call
+
+
 def _check(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
@@ -38,13 +59,6 @@ def _here(t: torch.Tensor, dtype: torch.dtype, what: str) -> None:
     if t.dtype != dtype or not t.is_cuda or t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{what}: expected {dtype} on cuda:{torch.cuda.current_device()}, got "
                          f"{t.dtype} on {t.device}")
-
-
-def _index(t: torch.Tensor, n: int, what: str) -> None:
-    """A dense int32 array of n entries."""
-    _here(t, torch.int32, what)
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{what}: expected {n} contiguous entries")
 
 
 class Rotary:
@@ -68,32 +82,12 @@ class Rotary:
         r.q_norm = q_norm.data_ptr() if q_norm is not None else None
         r.k_norm = k_norm.data_ptr() if k_norm is not None else None
         r.eps = eps
+        # for the calls: the struct's address, the norms' lengths (-1: none)
+        self.args = (ctypes.addressof(r), -1 if q_norm is None else q_norm.numel(),
+                     -1 if k_norm is None else k_norm.numel())
 
     def struct(self) -> kvq.kvq_rotary:
         return self._struct
-
-    def check_dim(self, q_dim: Optional[int], k_dim: Optional[int]) -> None:
-        """The norms' weights cover the heads given (the kernels read that many)."""
-        for w, dim, what in ((self.q_norm, q_dim, "q_norm"), (self.k_norm, k_dim, "k_norm")):
-            _check(w is None or dim is None or w.numel() == dim, f"{what}: expected {dim} weights")
-
-
-def _heads(t: torch.Tensor, what: str, dtype: torch.dtype = torch.bfloat16) -> kvq.kvq_heads:
-    """Rows of heads [tokens][heads][dim] or [batch][tokens][heads][dim] whose
-    tokens lie at one stride (a slice of a packed projection does)."""
-    _here(t, dtype, what)
-    sh, st = t.shape, t.stride()
-    n = len(sh)
-    if n == 3:
-        if st[2] == 1:
-            return kvq.kvq_heads(t.data_ptr(), st[0], st[1], sh[1])
-    elif n == 4 and st[3] == 1:
-        # one token per request: the requests are the tokens
-        tok = st[0] if sh[1] == 1 else st[1]
-        if sh[0] == 1 or st[0] == sh[1] * tok:
-            return kvq.kvq_heads(t.data_ptr(), tok, st[2], sh[2])
-    raise ValueError(f"{what}: expected [(batch,) tokens][heads][dim] rows, dim dense, the tokens at "
-                     "one stride")
 
 
 def _query_out(q: torch.Tensor, out: Optional[torch.Tensor], kind: str) -> torch.Tensor:
@@ -121,32 +115,16 @@ def norm_rope(rotary: Rotary, q: Optional[torch.Tensor], k: Optional[torch.Tenso
     """Norm and rotation of queries and keys (kvq_norm_rope): q bf16 [T][Hq][D] and k
     bf16 [T][Hk][D], positions int32 [T].  Returns (q_out, k_out): new tensors, or the
     given ones (bf16 outputs may be the inputs).  q_out_type "e4m3": uint8 codes."""
-    some = q if q is not None else k
-    if some is None or some.dim() != 3:
-        raise ValueError("norm_rope: expected [tokens][heads][dim] in q, k or both")
-    T, _, D = some.shape
-    if k is not None and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != D):
-        raise ValueError("k: expected q's tokens and dim")
-    rotary.check_dim(None if q is None else D, None if k is None else D)
-    if positions is not None:
-        _index(positions, T, "positions")
-    fp8 = q_out_type == "e4m3"
-    qh = qo = kh = ko = None
     if q is not None:
         q_out = _query_out(q, q_out, q_out_type)
-        _head_scale(q_head_scale, q.shape[1])
-        if T:
-            qh, qo = _heads(q, "q"), _heads(q_out, "q_out", OUT_TORCH[q_out_type])
-    if k is not None:
-        if k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-        elif k_out.shape != k.shape:
-            raise ValueError("k_out: expected k's shape")
-        if T:
-            kh, ko = _heads(k, "k"), _heads(k_out, "k_out")
-    if T:
-        kvq.check(kvq.kvq_norm_rope(rotary.struct(), D, T, positions, qh, qo, 1 if fp8 else 0, q_scale,
-                                    q_head_scale, kh, ko, error_flag, stream), "kvq_norm_rope")
+    if k is not None and k_out is None:
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+    addr, nq, nk = rotary.args
+    st = (_call or _calls()).norm_rope(torch.cuda.current_device(), kvq._stream(stream), addr, nq, nk,
+                                       q, k, positions, q_out, k_out, q_out_type == "e4m3", q_scale,
+                                       q_head_scale, error_flag)
+    if st:
+        kvq.check(st, "kvq_norm_rope")
     return q_out, k_out
 
 
@@ -262,38 +240,19 @@ class QuantizedKVCache:
         int32 [B] or None (all T).  MLA: k_new the latents [B][T][1][512], kpe_new
         [B][T][1][64].  Returns q_out (q_out_type "bf16", or "e4m3": uint8 codes; by
         default q_out's own type, bf16 without one)."""
-        sh = k_new.shape
-        if len(sh) != 4 or sh[2] != self.Hkv or sh[3] != self.D:
-            raise ValueError("k_new: expected [batch][tokens][kv heads][dim] of the cache's")
-        B, T = sh[0], sh[1]
-        if not self.mla and (v_new is None or v_new.shape != sh):
-            raise ValueError("v_new: expected k_new's shape")
-        if self.mla and (kpe_new is None or kpe_new.shape != (B, T, 1, self.rope)):
-            raise ValueError("kpe_new: expected [batch][tokens][1][rope]")
-        if B > self.block_table.shape[0]:
-            raise ValueError("more requests than the block table has")
-        qh = qo = None
         fp8 = False
         if q is not None:
-            if q.dim() != 4 or q.shape[:2] != sh[:2] or q.shape[3] != self.D:
-                raise ValueError("q: expected [batch][tokens][heads][dim]")
             kind = q_out_type or ("e4m3" if q_out is not None and q_out.dtype == torch.uint8 else "bf16")
             q_out = _query_out(q, q_out, kind)
-            _head_scale(q_head_scale, q.shape[2])
             fp8 = kind == "e4m3"
-        rotary.check_dim(None if q is None else self.D, self.D)
-        if B == 0 or T == 0:
-            return q_out
-        _index(start_pos, B, "start_pos")
-        if new_lens is not None:
-            _index(new_lens, B, "new_lens")
-        if q is not None:
-            qh, qo = _heads(q, "q"), _heads(q_out, "q_out", OUT_TORCH[kind])
-        kvq.check(kvq.kvq_rope_append(
-            self.struct(), rotary.struct(), B, T, start_pos, new_lens, _heads(k_new, "k_new"),
-            None if v_new is None else _heads(v_new, "v_new"),
-            None if kpe_new is None else _heads(kpe_new, "kpe_new"), qh, qo, 1 if fp8 else 0, q_scale,
-            q_head_scale, error_flag, stream), "kvq_rope_append")
+        c = self.struct()
+        addr, nq, nk = rotary.args
+        st = (_call or _calls()).rope_append(
+            torch.cuda.current_device(), kvq._stream(stream), ctypes.addressof(c),
+            self.block_table.shape[0], addr, nq, nk, k_new, v_new, kpe_new, start_pos, new_lens, q,
+            q_out, fp8, q_scale, q_head_scale, error_flag)
+        if st:
+            kvq.check(st, "kvq_rope_append")
         return q_out
 
 
@@ -318,13 +277,13 @@ class DecodeConfig:
     q_scale: float = 1.0
     q_head_scale: Optional[torch.Tensor] = None
 
-    def params(self, seq_lens: torch.Tensor, error_flag: Optional[torch.Tensor] = None
+    def params(self, seq_lens: Optional[torch.Tensor], error_flag: Optional[torch.Tensor] = None
                ) -> kvq.kvq_decode_params:
         # in the order of kvq_decode_params' fields
         ptr = lambda t: None if t is None else t.data_ptr()
         return kvq.kvq_decode_params(
             self.batch, self.num_q_heads, self.qk_dim, self.v_dim, self.num_splits,
-            seq_lens.data_ptr(), self.max_kv_len, self.sm_scale, self.prob_scale, OUT[self.out],
+            ptr(seq_lens), self.max_kv_len, self.sm_scale, self.prob_scale, OUT[self.out],
             self.out_scale, ptr(error_flag), self.fresh_tokens, 1 if self.q_fp8 else 0, self.q_scale,
             ptr(self.q_head_scale))
 
@@ -433,19 +392,18 @@ class SharedDecode:
                                       out=out, out_scale=out_scale, q_fp8=q_fp8, q_scale=q_scale,
                                       q_head_scale=_head_scale(q_head_scale, num_q_heads))
         self.ws = FusedWorkspace(dataclasses.replace(cfg, num_splits=so + sp), cache.Hkv, device)
+        self._params = cfg.params(None)   # the lengths and the flag come with each step
 
     def __call__(self, q: torch.Tensor, seq_lens: torch.Tensor,
                  error_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """q bf16 (FP8 query: uint8) [batch][Hq][D], seq_lens int32 [batch] (whole lengths)
         -> the output buffer [batch][Hq][D], overwritten by the next step."""
-        cfg, ws = self.cfg, self.ws
-        _here(q, torch.uint8 if cfg.q_fp8 else torch.bfloat16, "q")
-        if q.shape != (cfg.batch, cfg.num_q_heads, cfg.qk_dim) or not q.is_contiguous():
-            raise ValueError("q: expected a contiguous [batch][heads][dim]")
-        _index(seq_lens, cfg.batch, "seq_lens")
-        if cfg.batch:
-            kvq.check(kvq.kvq_decode_shared(
-                self.cache.struct(), cfg.params(seq_lens, error_flag), self.prefix_len,
-                self.prefix_table, self.prefix_splits, q, ws.part_o, ws.part_lse, ws.counters,
-                ws.out, stream), "kvq_decode_shared")
+        ws = self.ws
+        c = self.cache.struct()
+        st = (_call or _calls()).decode_shared(
+            torch.cuda.current_device(), kvq._stream(stream), ctypes.addressof(c),
+            ctypes.addressof(self._params), self.prefix_len, self.prefix_table, self.prefix_splits, q,
+            seq_lens, ws.part_o, ws.part_lse, ws.counters, ws.out, error_flag)
+        if st:
+            kvq.check(st, "kvq_decode_shared")
         return ws.out

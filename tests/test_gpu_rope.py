@@ -342,3 +342,17 @@ def test_runtime_refuses():
     assert cache.append_rope(ro, x[:0], x[:0], start[:0]) is None
     empty, _ = runtime.norm_rope(ro, q[:0], None, pos[:0])
     assert empty.shape == (0, 2, 64)
+
+
+def test_single_token_of_odd_stride():
+    """A lone token's stride is never used, whatever torch says it is."""
+    ro = make_rotary(64, 64, False, False)
+    q = rand((1, 3, 64), 1)
+    odd = torch.as_strided(q, (1, 1, 3, 64), (3, 5, 64, 1))
+    pos = torch.tensor([9], device=DEV).int()
+    want, _ = runtime.norm_rope(ro, q, None, pos)
+    cache = make_cache("fp8", 1, 2, 16, 3, 64, 1)
+    got = cache.append_rope(ro, odd, odd, pos, q=odd)
+    assert torch.equal(got[0], want)
+    one = torch.as_strided(q, (1, 1, 64), (7, 5, 1))
+    assert torch.equal(runtime.norm_rope(ro, one, None, pos)[0], want[:, :1])
