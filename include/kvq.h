@@ -405,7 +405,7 @@ kvq_status kvq_decode(const kvq_cache* c, const kvq_decode_params* p, const void
  * scales; not MLA, and prob_scale must be 0 (KVQ_ERR_UNSUPPORTED).
  * fresh_tokens is taken as 0 where prefix_len is positive.  The prefix's
  * probabilities are rounded to 11 bits for the products with V where the
- * output is bf16 or E4M3, and kept to 22 for fp32.
+ * output is bf16 (8 bits itself), and kept to 22 for fp32 and E4M3 outputs.
  * Two or three launches on `stream` (three where not all own chunks fit on the
  * SMs beside the prefix); calls that share partials or counters must not
  * overlap on the GPU.

@@ -737,7 +737,7 @@ kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int
   a.splits = prefix_splits;
   a.box = 16;   // TMA boxes: the largest power of two up to a tile that divides the pages
   while (a.box < 128 && c->page_size % (2 * a.box) == 0) a.box *= 2;
-  a.wide_p = p->out_dtype == KVQ_OUT_F32;
+  a.wide_p = p->out_dtype != KVQ_OUT_BF16;
   a.sm_scale = p->sm_scale;
   a.k_scale = c->k_scale;
   a.v_scale = c->v_scale;

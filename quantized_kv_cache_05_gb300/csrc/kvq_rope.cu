@@ -87,7 +87,12 @@ struct Row {
     float ss = s.x + s.y;
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    return rsqrtf(ss * (1.0f / (LANES * 16)) + eps);
+    // the approximate root and one correction step: within half a unit or so,
+    // where the approximation alone would add most of the row's error (codes
+    // next to a rounding boundary feel it)
+    const float x = ss * (1.0f / (LANES * 16)) + eps, r = rsqrtf(x);
+    const float e = __fmaf_rn(-__fmul_rn(x, r), r, 1.f);
+    return fabsf(e) < 1.f ? __fmaf_rn(0.5f * r, e, r) : r;   // (not at 0, infinity, NaN)
   }
   __device__ __forceinline__ void norm(float r, const float* w, const Pieces& pc) {
     const uint64_t r2 = pack2(r, r);

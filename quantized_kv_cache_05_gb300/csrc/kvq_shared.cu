@@ -27,10 +27,12 @@
 //    tile with accumulators of their own that are joined at the end (MT = 1).
 // The query rows are prescaled by a power of two into f16 (kvq_device.cuh): the
 // bf16 values are exact.  P is scaled by 2^7 against the row's (lazily moving)
-// maximum, which keeps probabilities down to 2^-32 of the largest in f16; its
-// rounding, 2^-12 relative, is under that of bf16 and E4M3 outputs (2^-9,
-// 2^-4).  For fp32 outputs P is an f16 high part plus an f16 residual (two
-// MMAs, 22 bits).  Sums and accumulators are fp32.
+// maximum, which keeps probabilities down to 2^-32 of the largest in f16.  For
+// bf16 outputs P is rounded to f16 once, at most 2^-11 of each weight against
+// the output's own 2^-8; for fp32 outputs, and for E4M3 ones (whose codes are
+// the decode kernel's but where it lies within 2^-20 of a rounding boundary), P
+// is an f16 high part plus an f16 residual, 22 bits, at twice the MMAs of P V.
+// Sums and accumulators are fp32.
 // Every wait is bounded; a timeout sets an error bit and the partials become
 // NaN.
 
@@ -102,6 +104,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+
 template <int FMT, int D, int MT, bool P2>
 __global__ void __launch_bounds__(kSharedThreads, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -193,8 +196,6 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 
   // The first copies and the query loads go out before the CTA meets: they are
   // the longest steps to the first MMA.
-  constexpr int kQv = D / 8;       // 16-byte pieces of a bf16 row (FP8: half)
-  uint4 qv[kQv];
   int len = 0;
   if (warp == kTmaWarp) {
     __syncwarp();   // lane 0 has set up the barriers
@@ -204,12 +205,43 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       copy_tile(j, 1, row);
     }
   }
+  // The queries' 16-byte pieces go straight to the places of the operand tile
+  // that their f16 values take: piece c of a row there, FP8 codes at 2c (they
+  // widen to 2c and 2c + 1).  Consecutive lanes copy consecutive pieces (a
+  // row per thread would touch 32 lines per instruction); rows past the last
+  // are zeros.  (Plain copies: queries may lie in pinned host memory.)
+  const uint32_t qtile = base + (MT == 2 ? slot * Sg::kTile : 0);
+  auto q_at = [&](int trow, int piece) -> uint32_t {
+    return qtile + (piece >> 3) * kCol + (trow >> 3) * 1024 + (trow & 7) * 128 +
+           (((piece ^ trow) & 7) << 4);
+  };
   if (warp < kConvWarp) {
-    const uint4* qp = reinterpret_cast<const uint4*>(
-        static_cast<const uint8_t*>(a.q) + ((size_t)b * a.Hq + hq) * (a.q_fp8 ? D : 2 * D));
-#pragma unroll
-    for (int c = 0; c < kQv; ++c)
-      qv[c] = live && (c < kQv / 2 || !a.q_fp8) ? qp[c] : make_uint4(0u, 0u, 0u, 0u);
+    if (MT == 2 || slot == 0) {
+      const int lp = a.q_fp8 ? D / 16 : D / 8;   // pieces of a row: a power of two
+      const int c = lane & (lp - 1), per = 32 / lp;
+      const int first = row0 + (MT == 2 ? slot * kTok : 0) + 32 * (warp & 3) + lane / lp;
+      // row first + k per: request qb, head qg of the group, without a division each
+      int qb = first / a.G, qg = first - qb * a.G;
+      const int db = per / a.G, dg = per - db * a.G;
+      const long row_bytes = 16 * lp;
+      const uint8_t* q0 = static_cast<const uint8_t*>(a.q) + (long)h * a.G * row_bytes + 16 * c;
+#pragma unroll 4
+      for (int k = 0; k < lp; ++k) {
+        const int trow = 32 * (warp & 3) + lane / lp + k * per;
+        const bool in = first + k * per < a.R;
+        const uint8_t* src = in ? q0 + ((long)qb * a.Hq + qg) * row_bytes : q0;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         q_at(trow, a.q_fp8 ? 2 * c : c)),
+                     "l"(src), "r"(in ? 16 : 0)
+                     : "memory");
+        qb += db;
+        qg += dg;
+        if (qg >= a.G) {
+          qg -= a.G;
+          ++qb;
+        }
+      }
+    }
     len = live ? __ldg(a.seq_lens + b) : -1;
   }
   tc_fence_before();
@@ -393,49 +425,55 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     {
       const float k_log2 =
           (a.k_hs ? a.sm_scale * __ldg(a.k_hs + h) : a.sm_scale * a.k_scale) * 1.4426950408889634f;
-      const uint32_t dst = base + (MT == 2 ? slot * Sg::kTile : 0) + (r >> 3) * 1024 + (r & 7) * 128;
-      const bool store = MT == 2 || slot == 0;
-      if (a.q_fp8) {
-        qsc = k_log2 * (a.q_hs ? __ldg(a.q_hs + hq) : a.q_scale);
-        if (store) {
-#pragma unroll
+      qsc = a.q_fp8 ? k_log2 * (a.q_hs ? __ldg(a.q_hs + hq) : a.q_scale) : 0.f;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();   // the warp's rows are here
+      if (MT == 2 || slot == 0) {
+        if (a.q_fp8) {
+#pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
+            const uint4 v = lds128(q_at(r, 2 * c));
             uint32_t o[8];
-            e4m3x4_to_f16x2x2(qv[c].x, o[0], o[1]);
-            e4m3x4_to_f16x2x2(qv[c].y, o[2], o[3]);
-            e4m3x4_to_f16x2x2(qv[c].z, o[4], o[5]);
-            e4m3x4_to_f16x2x2(qv[c].w, o[6], o[7]);
-            const uint32_t at = dst + (c >> 2) * kCol;
-            const int q = 2 * (c & 3);
-            sts128(at + ((q ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-            sts128(at + (((q + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+            e4m3x4_to_f16x2x2(v.x, o[0], o[1]);
+            e4m3x4_to_f16x2x2(v.y, o[2], o[3]);
+            e4m3x4_to_f16x2x2(v.z, o[4], o[5]);
+            e4m3x4_to_f16x2x2(v.w, o[6], o[7]);
+            sts128(q_at(r, 2 * c), o[0], o[1], o[2], o[3]);
+            sts128(q_at(r, 2 * c + 1), o[4], o[5], o[6], o[7]);
           }
-        }
-      } else {
-        uint32_t m2 = 0;
-#pragma unroll
-        for (int c = 0; c < kQv; ++c)
-          m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(qv[c].x & 0x7FFF7FFFu, qv[c].y & 0x7FFF7FFFu),
-                                     __vmaxu2(qv[c].z & 0x7FFF7FFFu, qv[c].w & 0x7FFF7FFFu)));
-        const int e = q_prescale_exp(max(m2 & 0xFFFFu, m2 >> 16));
-        const float f = exp2i(e);
-        qsc = scale_pow2(k_log2, -e);
-        if (store) {
-#pragma unroll
-          for (int c = 0; c < kQv; ++c) {
-            const uint32_t w[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
+        } else {   // prescaled by a power of two
+          uint32_t m2 = 0;
+#pragma unroll 8
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = lds128(q_at(r, c));
+            m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                       __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+          }
+          const int e = q_prescale_exp(max(m2 & 0xFFFFu, m2 >> 16));
+          const float f = exp2i(e);
+          qsc = scale_pow2(k_log2, -e);
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = lds128(q_at(r, c));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             uint32_t o[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               o[k] = pack_f16x2(__uint_as_float(w[k] << 16) * f,
                                 __uint_as_float(w[k] & 0xFFFF0000u) * f);
-            sts128(dst + (c >> 3) * kCol + (((c & 7) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+            sts128(q_at(r, c), o[0], o[1], o[2], o[3]);
           }
         }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
       }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (store && lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+      if constexpr (MT == 1) {   // slot 1 has the same rows
+        if (slot == 0) sm.m[0][r] = qsc;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        qsc = sm.m[0][r];
+        asm volatile("bar.sync 1, 256;" ::: "memory");   // (m is written again at the end)
+      }
     }
 
     // ---- the slot's units
