@@ -198,28 +198,32 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   // the longest steps to the first MMA.
   int len = 0;
   if (warp == kTmaWarp) {
-    __syncwarp();   // lane 0 has set up the barriers
+    __syncwarp();   // lane 0 has set up the barriers: the others need not wait for more
+    asm volatile("bar.arrive 3, %0;" ::"n"(kSharedThreads) : "memory");
     for (int j = 0; j < min(nt, Sg::kSlots); ++j) {
       const int row = box_row(j);
       copy_tile(j, 0, row);
       copy_tile(j, 1, row);
     }
   }
-  // The queries' 16-byte pieces go straight to the places of the operand tile
-  // that their f16 values take: piece c of a row there, FP8 codes at 2c (they
-  // widen to 2c and 2c + 1).  Consecutive lanes copy consecutive pieces (a
-  // row per thread would touch 32 lines per instruction); rows past the last
-  // are zeros.  (Plain copies: queries may lie in pinned host memory.)
+  // Queries.  Two row tiles: their 16-byte pieces go straight to the places of
+  // the operand tile that their f16 values take, piece c of a row there, FP8
+  // codes at 2c (they widen to 2c and 2c + 1); consecutive lanes copy
+  // consecutive pieces, and rows past the last are zeros (64 requests x 32k
+  // tokens, 256 rows: 57.1 us against 59.0 with a row per thread, whose loads
+  // touch 32 lines each).  One row tile: a row per thread in registers, which
+  // is less code for the few rows (4 requests x 1k: 10.2 us against 10.9
+  // staged).  (Plain copies and loads: queries may lie in pinned host memory.)
   const uint32_t qtile = base + (MT == 2 ? slot * Sg::kTile : 0);
   auto q_at = [&](int trow, int piece) -> uint32_t {
     return qtile + (piece >> 3) * kCol + (trow >> 3) * 1024 + (trow & 7) * 128 +
            (((piece ^ trow) & 7) << 4);
   };
   if (warp < kConvWarp) {
-    if (MT == 2 || slot == 0) {
+    if constexpr (MT == 2) {
       const int lp = a.q_fp8 ? D / 16 : D / 8;   // pieces of a row: a power of two
       const int c = lane & (lp - 1), per = 32 / lp;
-      const int first = row0 + (MT == 2 ? slot * kTok : 0) + 32 * (warp & 3) + lane / lp;
+      const int first = row0 + slot * kTok + 32 * (warp & 3) + lane / lp;
       // row first + k per: request qb, head qg of the group, without a division each
       int qb = first / a.G, qg = first - qb * a.G;
       const int db = per / a.G, dg = per - db * a.G;
@@ -245,10 +249,10 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     len = live ? __ldg(a.seq_lens + b) : -1;
   }
   tc_fence_before();
-  __syncthreads();
+  if (warp != kTmaWarp) asm volatile("bar.sync 3, %0;" ::"n"(kSharedThreads) : "memory");
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  if (tmem != 0 && threadIdx.x == 0) *abort_flag = 1;   // (never: see the MMA warp)
+  if (warp == kMmaWarp && tmem != 0) *abort_flag = 1;   // (never: all of it is ours)
 
   auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
     if (wait_or_abort(smem_u32(&bar), parity, abort_flag)) return true;
@@ -423,56 +427,76 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     // ---- the row's query, into its operand tile
     float qsc;   // score scale, log2 domain
     {
+      // the largest magnitudes of a piece's even and odd bf16 values
+      auto largest = [](const uint4& v) -> uint32_t {
+        return __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                        __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+      };
+      // bf16 piece c, prescaled by a power of two, as f16
+      auto scale_piece = [&](const uint4& v, float f, int c) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[k] = pack_f16x2(__uint_as_float(w[k] << 16) * f,
+                            __uint_as_float(w[k] & 0xFFFF0000u) * f);
+        sts128(q_at(r, c), o[0], o[1], o[2], o[3]);
+      };
+      // 16 FP8 codes as the f16 pieces 2c and 2c + 1
+      auto widen_piece = [&](const uint4& v, int c) {
+        uint32_t o[8];
+        e4m3x4_to_f16x2x2(v.x, o[0], o[1]);
+        e4m3x4_to_f16x2x2(v.y, o[2], o[3]);
+        e4m3x4_to_f16x2x2(v.z, o[4], o[5]);
+        e4m3x4_to_f16x2x2(v.w, o[6], o[7]);
+        sts128(q_at(r, 2 * c), o[0], o[1], o[2], o[3]);
+        sts128(q_at(r, 2 * c + 1), o[4], o[5], o[6], o[7]);
+      };
       const float k_log2 =
           (a.k_hs ? a.sm_scale * __ldg(a.k_hs + h) : a.sm_scale * a.k_scale) * 1.4426950408889634f;
       qsc = a.q_fp8 ? k_log2 * (a.q_hs ? __ldg(a.q_hs + hq) : a.q_scale) : 0.f;
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      __syncwarp();   // the warp's rows are here
-      if (MT == 2 || slot == 0) {
+      if constexpr (MT == 2) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();   // the warp's rows are here
         if (a.q_fp8) {
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            const uint4 v = lds128(q_at(r, 2 * c));
-            uint32_t o[8];
-            e4m3x4_to_f16x2x2(v.x, o[0], o[1]);
-            e4m3x4_to_f16x2x2(v.y, o[2], o[3]);
-            e4m3x4_to_f16x2x2(v.z, o[4], o[5]);
-            e4m3x4_to_f16x2x2(v.w, o[6], o[7]);
-            sts128(q_at(r, 2 * c), o[0], o[1], o[2], o[3]);
-            sts128(q_at(r, 2 * c + 1), o[4], o[5], o[6], o[7]);
-          }
-        } else {   // prescaled by a power of two
+#pragma unroll 2
+          for (int c = 0; c < D / 16; ++c) widen_piece(lds128(q_at(r, 2 * c)), c);
+        } else {
           uint32_t m2 = 0;
 #pragma unroll 8
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = lds128(q_at(r, c));
-            m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                       __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-          }
+          for (int c = 0; c < D / 8; ++c) m2 = __vmaxu2(m2, largest(lds128(q_at(r, c))));
           const int e = q_prescale_exp(max(m2 & 0xFFFFu, m2 >> 16));
-          const float f = exp2i(e);
           qsc = scale_pow2(k_log2, -e);
 #pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = lds128(q_at(r, c));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t o[4];
+          for (int c = 0; c < D / 8; ++c) scale_piece(lds128(q_at(r, c)), exp2i(e), c);
+        }
+      } else {
+        const uint4* qp = reinterpret_cast<const uint4*>(
+            static_cast<const uint8_t*>(a.q) + ((size_t)b * a.Hq + hq) * (a.q_fp8 ? D : 2 * D));
+        uint4 v[D / 8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              o[k] = pack_f16x2(__uint_as_float(w[k] << 16) * f,
-                                __uint_as_float(w[k] & 0xFFFF0000u) * f);
-            sts128(q_at(r, c), o[0], o[1], o[2], o[3]);
+        for (int c = 0; c < D / 8; ++c)
+          v[c] = live && (c < D / 16 || !a.q_fp8) ? qp[c] : make_uint4(0u, 0u, 0u, 0u);
+        if (a.q_fp8) {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+            if (slot == 0) widen_piece(v[c], c);
+        } else {
+          uint32_t m2 = 0;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) m2 = __vmaxu2(m2, largest(v[c]));
+          const int e = q_prescale_exp(max(m2 & 0xFFFFu, m2 >> 16));
+          qsc = scale_pow2(k_log2, -e);
+          if (slot == 0) {   // (both slots have the same rows)
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) scale_piece(v[c], exp2i(e), c);
           }
         }
+      }
+      if (MT == 2 || slot == 0) {
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
-      }
-      if constexpr (MT == 1) {   // slot 1 has the same rows
-        if (slot == 0) sm.m[0][r] = qsc;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        qsc = sm.m[0][r];
-        asm volatile("bar.sync 1, 256;" ::: "memory");   // (m is written again at the end)
       }
     }
 
