@@ -252,7 +252,7 @@ typedef struct kvq_rotary {
  * one another.
  */
 typedef struct kvq_heads {
-  void* data;                /* (device) */
+  void* data;                /* (device, or pinned host memory like the inputs above) */
   int64_t token_stride;
   int64_t head_stride;
   int32_t num_heads;         /* >= 1 */
@@ -285,8 +285,9 @@ kvq_status kvq_norm_rope(const kvq_rotary* r, int head_dim, int num_tokens,
  *   k, v, kpe, q and q_out, and goes to position start_pos[b] + t, which also
  *   gives its angles.
  *   new_lens (device int32 [batch], optional): only the first new_lens[b]
- *   tokens of request b are real; the rest are neither read nor written, and
- *   their cache rows and q_out rows stay as they were.
+ *   tokens of request b are real (all for n_tokens or more, none for 0 or
+ *   less); the rest are neither read nor written, and their cache rows and
+ *   q_out rows stay as they were.  Two real tokens may not share a cache row.
  *   k, v   bf16 rows of num_kv_heads heads;  head_dim 64, 128 or 256.
  *   q, q_out, q_fp8, q_scale, q_head_scale (q may be NULL): as in
  *          kvq_norm_rope.  A decode that reads q_out must not use
@@ -395,14 +396,17 @@ kvq_status kvq_decode(const kvq_cache* c, const kvq_decode_params* p, const void
  *              kvq_decode.
  *   prefix_table (device int32, optional) [prefix_len / page_size] the shared
  *              pages; NULL: the first entries of the first row of the block
- *              table.
+ *              table, whose request then has to be one that shares them.
  *   prefix_splits, p->num_splits: chunks of the prefix (at least one 128-token
  *              tile each: more are lowered) and of each request's own tokens;
  *              kvq_shared_splits picks both.  Together at most 64.
  *   part_o, part_lse, counters (device): as for kvq_decode, sized for
  *              p->num_splits + prefix_splits splits; part_o 32-byte aligned.
  * FP8 and NVFP4 caches with head_dim 64 or 128, bf16 or FP8 queries, per-head
- * scales; not MLA, and prob_scale must be 0 (KVQ_ERR_UNSUPPORTED).
+ * scales; not MLA, and prob_scale must be 0 (KVQ_ERR_UNSUPPORTED).  It pays
+ * from a few requests on: the prefix takes at least one pass of the tensor
+ * cores over 128 rows, and kvq_decode reads a prefix that only one or two
+ * requests share (or that is shorter than what each adds) in less time.
  * fresh_tokens is taken as 0 where prefix_len is positive.  The prefix's
  * probabilities are rounded to 11 bits for the products with V where the
  * output is bf16 (8 bits itself), and kept to 22 for fp32 and E4M3 outputs.

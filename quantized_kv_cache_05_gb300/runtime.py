@@ -61,6 +61,16 @@ def _here(t: torch.Tensor, dtype: torch.dtype, what: str) -> None:
                          f"{t.dtype} on {t.device}")
 
 
+def _launch_device(*held: int) -> int:
+    """The current device, on which the kernels launch: what an object holds (-1:
+    nothing) has to be there."""
+    dev = torch.cuda.current_device()
+    for d in held:
+        if d != dev and d != -1:
+            raise ValueError(f"made on cuda:{d}, called with cuda:{dev} current")
+    return dev
+
+
 class Rotary:
     """The norm and rotation of a layer's queries and keys (``kvq_rotary``): the
     table of ``rope_table`` (None: no rotation) and the norms' weights (float32
@@ -82,9 +92,12 @@ class Rotary:
         r.q_norm = q_norm.data_ptr() if q_norm is not None else None
         r.k_norm = k_norm.data_ptr() if k_norm is not None else None
         r.eps = eps
-        # for the calls: the struct's address, the norms' lengths (-1: none)
+        # for the calls: the struct's address, the norms' lengths (-1: none); the
+        # device that the tensors are on
         self.args = (ctypes.addressof(r), -1 if q_norm is None else q_norm.numel(),
                      -1 if k_norm is None else k_norm.numel())
+        held = [t for t in (table, q_norm, k_norm) if t is not None]
+        self.device = held[0].get_device() if held else -1
 
     def struct(self) -> kvq.kvq_rotary:
         return self._struct
@@ -119,8 +132,9 @@ def norm_rope(rotary: Rotary, q: Optional[torch.Tensor], k: Optional[torch.Tenso
         q_out = _query_out(q, q_out, q_out_type)
     if k is not None and k_out is None:
         k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+    dev = _launch_device(rotary.device)
     addr, nq, nk = rotary.args
-    st = (_call or _calls()).norm_rope(torch.cuda.current_device(), kvq._stream(stream), addr, nq, nk,
+    st = (_call or _calls()).norm_rope(dev, kvq._stream(stream), addr, nq, nk,
                                        q, k, positions, q_out, k_out, q_out_type == "e4m3", q_scale,
                                        q_head_scale, error_flag)
     if st:
@@ -245,10 +259,11 @@ class QuantizedKVCache:
             kind = q_out_type or ("e4m3" if q_out is not None and q_out.dtype == torch.uint8 else "bf16")
             q_out = _query_out(q, q_out, kind)
             fp8 = kind == "e4m3"
+        dev = _launch_device(rotary.device, self.k_codes.get_device())
         c = self.struct()
         addr, nq, nk = rotary.args
         st = (_call or _calls()).rope_append(
-            torch.cuda.current_device(), kvq._stream(stream), ctypes.addressof(c),
+            dev, kvq._stream(stream), ctypes.addressof(c),
             self.block_table.shape[0], addr, nq, nk, k_new, v_new, kpe_new, start_pos, new_lens, q,
             q_out, fp8, q_scale, q_head_scale, error_flag)
         if st:
@@ -399,9 +414,10 @@ class SharedDecode:
         """q bf16 (FP8 query: uint8) [batch][Hq][D], seq_lens int32 [batch] (whole lengths)
         -> the output buffer [batch][Hq][D], overwritten by the next step."""
         ws = self.ws
+        dev = _launch_device(self.cache.k_codes.get_device())
         c = self.cache.struct()
         st = (_call or _calls()).decode_shared(
-            torch.cuda.current_device(), kvq._stream(stream), ctypes.addressof(c),
+            dev, kvq._stream(stream), ctypes.addressof(c),
             ctypes.addressof(self._params), self.prefix_len, self.prefix_table, self.prefix_splits, q,
             seq_lens, ws.part_o, ws.part_lse, ws.counters, ws.out, error_flag)
         if st:

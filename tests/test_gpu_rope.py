@@ -356,3 +356,33 @@ def test_single_token_of_odd_stride():
     assert torch.equal(got[0], want)
     one = torch.as_strided(q, (1, 1, 64), (7, 5, 1))
     assert torch.equal(runtime.norm_rope(ro, one, None, pos)[0], want[:, :1])
+
+
+def test_pinned_host_rows():
+    """New rows read from, and the queries written to, page-locked host memory."""
+    cache, same = (make_cache("fp8", 3, 4, 16, 2, 64, 6) for _ in range(2))
+    ro = make_rotary(64, 64, False, True)
+    x = rand((3, 2, 2, 64), 2)
+    start = torch.tensor([0, 9, 40], device=DEV).int()
+    want = cache.append_rope(ro, x, x, start, q=x)
+    h = x.cpu().pin_memory()
+    out = torch.zeros(x.shape, dtype=torch.bfloat16).pin_memory()
+    rows = lambda t: kvq.kvq_heads(t.data_ptr(), 128, 64, 2)
+    kvq.check(kvq.kvq_rope_append(same.struct(), ro.struct(), 3, 2, start, None, rows(h), rows(h), None, rows(h),
+                                  rows(out), 0, 1.0, None))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want.cpu())
+    assert torch.equal(same.k_codes, cache.k_codes) and torch.equal(same.v_codes, cache.v_codes)
+
+
+def test_new_lens_beyond_the_batch_and_below_zero():
+    cache, full = (make_cache("fp8", 3, 4, 16, 2, 64, 6) for _ in range(2))
+    ro = make_rotary(64, 64, False, False)
+    x = rand((3, 5, 2, 64), 2)
+    start = torch.tensor([3, 0, 20], device=DEV).int()
+    old = cache.k_codes.clone()
+    cache.append_rope(ro, x, x, start, new_lens=torch.tensor([-3, -(2 ** 31), 0], device=DEV).int())
+    assert torch.equal(cache.k_codes, old)
+    cache.append_rope(ro, x, x, start, new_lens=torch.tensor([5, 6, 2 ** 31 - 1], device=DEV).int())
+    full.append_rope(ro, x, x, start)
+    assert torch.equal(cache.k_codes, full.k_codes) and torch.equal(cache.v_codes, full.v_codes)

@@ -353,6 +353,52 @@ def test_back_to_back_steps_and_streams():
         assert torch.equal(g, w)
 
 
+def test_pinned_host_queries_and_output():
+    """Queries read from, and the output written to, page-locked host memory."""
+    for n in (5, 40):      # one row tile, and two; both with few and many own chunks
+        B = Batch("fp8", 128, 8, 2, 16, 320, [(9 * b) % 60 for b in range(n)])
+        for splits in ((2, 1), (3, 4)):
+            plan = B.plan("f32", splits)
+            want = plan(B.q, B.lens_t).clone()
+            q = B.q.cpu().pin_memory()
+            out = torch.full(want.shape, math.nan).pin_memory()
+            ws = plan.ws
+            kvq.check(kvq.kvq_decode_shared(B.cache.struct(), plan.cfg.params(B.lens_t), 320, None, splits[0], q,
+                                            ws.part_o, ws.part_lse, ws.counters, out))
+            torch.cuda.synchronize()
+            assert torch.equal(out, want.cpu())
+
+
+def test_no_requests():
+    B = Batch("fp8", 64, 4, 2, 16, 160, [4, 20])
+    plan = runtime.SharedDecode(B.cache, 0, 4, 160, B.cap, B.sm)
+    assert plan(B.q[:0], B.lens_t[:0]).shape == (0, 4, 64)
+
+
+def test_more_own_chunks_than_fit_beside_the_prefix():
+    """Own chunks in many waves behind a prefix that leaves no SM free, a merge of
+    their own: requests of every kind, in every output type."""
+    own = [None if b % 7 == 3 else -9 if b % 11 == 5 else (37 * b) % 700 for b in range(90)]
+    B = Batch("nvfp4", 64, 16, 8, 16, 2560, own)
+    ref = B.reference()
+    for out in ("f32", "bf16", "e4m3"):
+        for splits in ((19, 4), (20, 1)):
+            B.check(run(B, out, splits, prefix_table=B.shared_pages), out, ref, what=f"{out} {splits}")
+
+
+def test_objects_of_another_device_are_refused():
+    B = Batch("fp8", 64, 4, 2, 16, 160, [4, 20])
+    plan, ro = B.plan(), runtime.Rotary(runtime.rope_table(64, 64))
+    ro.device = 1          # as if made there
+    x = torch.zeros(2, 1, 2, 64, device=DEV).bfloat16()
+    with pytest.raises(ValueError, match="cuda:1"):
+        B.cache.append_rope(ro, x, x, B.lens_t)
+    with pytest.raises(ValueError, match="cuda:1"):
+        runtime.norm_rope(ro, x[:, 0], None, B.lens_t)
+    assert runtime._launch_device(torch.cuda.current_device(), -1) == torch.cuda.current_device()
+    assert plan(B.q, B.lens_t) is plan.ws.out
+
+
 def test_runtime_refuses():
     B = Batch("fp8", 64, 4, 2, 16, 160, [4, 20])
     for kw in (dict(prefix_len=-16), dict(prefix_len=10 ** 6), dict(batch=3), dict(num_q_heads=5),
