@@ -230,7 +230,10 @@ kvq_status kvq_quantize_append(const kvq_cache* c, const void* k_new, const void
  *             the pairs (i, i + rot_dim/2) (interleaved = 0) or (2i, 2i + 1)
  *             (interleaved = 1), i < rot_dim/2; the rest passes unrotated.
  * All of it runs in fp32 on the bf16 input; a result is rounded once, to its
- * output type.  A row's sum of squares has to stay in the range of fp32.
+ * output type.  E4M3 codes whose fp32 quotient lies within 16 steps of a
+ * rounding boundary are decided with 48 bits (values that neither norm nor
+ * rotation changes keep kvq_quantize_fp8's quotient).  A row's sum of squares
+ * has to stay in the range of fp32.
  */
 typedef struct kvq_rotary {
   const float* cos_sin;      /* (device) [num_positions][rot_dim]: the rot_dim/2
@@ -264,8 +267,8 @@ typedef struct kvq_heads {
  * a rotation).
  *   q, k   bf16 rows;  head_dim 64, 128 or 256.
  *   q_out  bf16 rows, or with q_fp8 = 1 E4M3 codes for an FP8-query decode:
- *          E4M3(fl32(y / s)), s = q_head_scale[h] (device) where given, else
- *          q_scale (finite > 0), as kvq_quantize_fp8 rounds.
+ *          E4M3(y / s), s = q_head_scale[h] (device) where given, else q_scale
+ *          (finite > 0), rounded and saturating as kvq_quantize_fp8's.
  *   k_out  bf16 rows.
  * bf16 outputs may be the inputs themselves (same data and strides); otherwise
  * no output may overlap an input.  Tokens at negative positions are skipped

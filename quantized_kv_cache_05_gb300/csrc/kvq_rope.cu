@@ -160,10 +160,112 @@ __device__ __forceinline__ uint2 pack_e4m3x8(const float* f) {
   return make_uint2(lo, hi);
 }
 
+// Sums of two fp32 numbers, hi + lo: some 48 bits from the exact errors of sums
+// (D. Knuth, The Art of Computer Programming 2, 4.2.2) and of fused products.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair two_prod(float a, float b) {
+  const float p = __fmul_rn(a, b);
+  return {p, __fmaf_rn(a, b, -p)};
+}
+__device__ __forceinline__ Pair times(Pair a, Pair b) {
+  Pair p = two_prod(a.hi, b.hi);
+  p.lo += __fmaf_rn(a.hi, b.lo, a.lo * b.hi);
+  return p;
+}
+__device__ __forceinline__ Pair plus(Pair a, Pair b) {
+  Pair s = two_sum(a.hi, b.hi);
+  s.lo += a.lo + b.lo;
+  return s;
+}
+
+// 1 / rms of a row spread over LANES lanes as a pair (every lane of the warp
+// calls it).
+template <int LANES>
+__device__ __forceinline__ Pair inv_rms_pair(const Row& x, float eps) {
+  Pair s = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = unpack2(x.v[i]);
+    // squares of bf16 values are exact
+    Pair t = two_sum(s.hi, __fmul_rn(f.x, f.x));
+    s.lo += t.lo;
+    t = two_sum(t.hi, __fmul_rn(f.y, f.y));
+    s = {t.hi, s.lo + t.lo};
+  }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1)
+    s = plus(s, {__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
+  constexpr float kMean = 1.0f / (LANES * 16);   // a power of two
+  const Pair v = plus({s.hi * kMean, s.lo * kMean}, {eps, 0.f});
+  const float r = rsqrtf(v.hi);
+  const Pair rr = two_prod(r, r);
+  const float e =
+      __fmaf_rn(-v.hi, rr.hi, 1.f) - __fmaf_rn(v.hi, rr.lo, v.lo * rr.hi);   // 1 - v r^2
+  return {r, fabsf(e) < 1.f ? 0.5f * r * e : 0.f};   // (not at 0, infinity, NaN)
+}
+
+// Whether a quotient lies within `near` fp32 steps of an E4M3 rounding boundary
+// (their low 19 fraction bits are zero).
+__device__ __forceinline__ bool near_boundary(float q, uint32_t near) {
+  return ((__float_as_uint(q) + near) & kE4m3Low) <= 2 * near;
+}
+
+// Of a lane's 16 quotients, those next to a rounding boundary moved to the side
+// of it (or onto it) where y / s lies with y from the formulas in pairs: so
+// close, the fp32 steps before the quotient could decide the code.  The
+// arguments one by one: they stay in registers.  x, w: the head's row and its
+// weights (or null); r: hi + lo of its 1 / rms.
+template <bool INTER>
+__device__ __noinline__ Floats<16> settle(Floats<16> q, const uint16_t* x, const float* w,
+                                          const float* trow, int half, float r_hi, float r_lo,
+                                          int c0, int c1, bool turn, float s, uint32_t near) {
+  auto value = [&](int i) -> Pair {
+    const float v = bf16_bits_to_f32(x[i]);
+    return w ? times(two_prod(v, w[i]), {r_hi, r_lo}) : Pair{v, 0.f};
+  };
+  auto side = [&](float f, Pair y) -> float {
+    if (!near_boundary(f, near) || !(fabsf(f) < 1000.f)) return f;   // (480 is the last boundary)
+    const uint32_t bits = __float_as_uint(f) & 0x7FFFFFFFu;
+    const uint32_t b = (bits + (1u << 18)) & ~kE4m3Low;   // the boundary next to |f|
+    const Pair bs = two_prod(__uint_as_float(b), s);
+    const float sign = f < 0.f ? -1.f : 1.f;
+    const float d = (sign * y.hi - bs.hi) + (sign * y.lo - bs.lo);   // (|y| - b s: hi - hi is exact)
+    const uint32_t to = d > 0.f ? b + 1 : (d < 0.f && b > 0) ? b - 1 : b;
+    return __uint_as_float(to | (__float_as_uint(f) & 0x80000000u));
+  };
+#pragma unroll 1
+  for (int k = 0; k < 8; ++k) {
+    // the lane's pair k (rotated or not)
+    const int ka = INTER ? 2 * k : k, kb = INTER ? 2 * k + 1 : 8 + k;
+    if (!near_boundary(q.v[ka], near) && !near_boundary(q.v[kb], near)) continue;
+    const int ia = 8 * (ka < 8 ? c0 : c1) + (ka & 7), ib = 8 * (kb < 8 ? c0 : c1) + (kb & 7);
+    Pair a = value(ia), b = value(ib);
+    if (turn) {
+      const int t = INTER ? ia / 2 : ia;
+      const Pair c = {trow[t], 0.f}, sn = {trow[half + t], 0.f}, nsn = {-trow[half + t], 0.f};
+      const Pair a0 = a;
+      a = plus(times(a0, c), times(b, nsn));
+      b = plus(times(b, c), times(a0, sn));
+    }
+    q.v[ka] = side(q.v[ka], a);
+    q.v[kb] = side(q.v[kb], b);
+  }
+  return q;
+}
+
 // E4M3(fl32(x / s)) of a lane's 16 elements (z = RN(1/s)): the quotients of
-// quotients_for_codes, in packed pairs.
+// quotients_for_codes, in packed pairs.  Where one lies within `near` fp32 steps
+// of a rounding boundary, `exact` settles them: by the IEEE division of what came
+// in as it is (near = 1), or by `settle` for what was computed in fp32.
+template <typename F>
 __device__ __forceinline__ void store_e4m3(const Row& x, float s, float z, uint8_t* row,
-                                           const Pieces& pc) {
+                                           const Pieces& pc, uint32_t near, F&& exact) {
   const uint64_t z2 = pack2(z, z), ns2 = pack2(-s, -s);
   Floats<16> q;
   uint32_t m = 0xFFFFFFFFu;
@@ -173,21 +275,17 @@ __device__ __forceinline__ void store_e4m3(const Row& x, float s, float z, uint8
     const float2 f = unpack2(fma2(fma2(q0, ns2, x.v[i]), z2, q0));
     q.v[2 * i] = f.x;
     q.v[2 * i + 1] = f.y;
-    m = min(m, min((__float_as_uint(f.x) + 1u) & kE4m3Low, (__float_as_uint(f.y) + 1u) & kE4m3Low));
+    m = min(m, min((__float_as_uint(f.x) + near) & kE4m3Low, (__float_as_uint(f.y) + near) & kE4m3Low));
   }
-  if (m <= 2u) {   // some quotient next to a rounding boundary
-    Floats<16> in;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = unpack2(x.v[i]);
-      in.v[2 * i] = f.x;
-      in.v[2 * i + 1] = f.y;
-    }
-    q = ieee_quotients<16>(in, s);
-  }
+  if (m <= 2 * near) q = exact(q);
   *reinterpret_cast<uint2*>(row + 8 * pc.c0) = pack_e4m3x8(q.v);
   *reinterpret_cast<uint2*>(row + 8 * pc.c1) = pack_e4m3x8(q.v + 8);
 }
+
+// Steps of a computed quotient from a boundary within which it is settled in
+// pairs: fp32's error is 2 to 3 steps as a rule, 2 u of the rotation's larger
+// product without a norm and 12.5 u with one at most.
+constexpr uint32_t kNear = 16;
 
 // One NVFP4 half block (8 elements; the neighbouring lane holds the other
 // half): codes in a word, and the block's scale code.  Every lane of the warp
@@ -274,7 +372,8 @@ __device__ __forceinline__ long rope_page(const RopeArgs& a, const Token& k, boo
 // gridDim.y blocks: a group takes every (per_token gridDim.y)-th of the token's
 // rows (queries, keys, values in one numbering), the next row's loads going
 // out before the present one's arithmetic.
-template <int D, int FMT, bool INTER>
+// QF8 (FMT 0): the queries leave as E4M3 codes.
+template <int D, int FMT, bool INTER, bool QF8>
 __global__ void __launch_bounds__(kRopeThreads, rope_ctas(FMT))
     rope_kernel(const RopeArgs a, int per_token) {
   // the append is an ordinary launch (it starts after all earlier work), the
@@ -284,6 +383,7 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(FMT))
   constexpr int kLanes = D / 16, kGroups = kRopeThreads / kLanes;
   const int p = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
   const unsigned token = blockIdx.x * (unsigned)(kGroups / per_token) + group / per_token;
+  const bool q_codes = FMT == 0 ? QF8 : a.q_fp8 != 0;
   const int nq = a.q.heads, nqk = nq + a.k.heads, H = nqk + (FMT == 0 ? 0 : a.v.heads);
   const int first = blockIdx.y * per_token + group % per_token, step = per_token * gridDim.y;
   const bool in = token < a.tokens, report = in && p == 0 && first == 0;
@@ -324,20 +424,46 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(FMT))
     // every lane of the warp takes part in the norm's butterfly when any row
     // of the call has a norm
     const float* w = isq ? a.q_norm : isv ? nullptr : a.k_norm;
+    Pair r = {1.f, 0.f};
     if (a.q_norm || a.k_norm) {
-      const float r = f.template inv_rms<kLanes>(a.eps);
-      if (w) f.norm(r, w, pc);
+      const bool coded = w && (isq ? q_codes : FMT == kFmtFp8);
+      if ((FMT != 0 || QF8) && __any_sync(0xffffffffu, coded))
+        r = inv_rms_pair<kLanes>(f, a.eps);
+      else
+        r.hi = f.template inv_rms<kLanes>(a.eps);
+      if (w) f.norm(r.hi + r.lo, w, pc);
     }
     if (turned.turn && !isv) ang.apply(f);
+
+    // E4M3 codes: values that are the input itself take the plain append's
+    // quotient, computed ones next to a rounding boundary are settled
+    const bool computed = w != nullptr || (pc.turn && !isv);
+    auto codes_to = [&](float s, float z, uint8_t* to) {
+      store_e4m3(f, s, z, to, pc, computed ? kNear : 1u, [&](const Floats<16>& q) -> Floats<16> {
+        if (computed) {
+          const RopeRows& src = isq ? a.q : a.k;
+          return settle<INTER>(q, src.data + (long)token * src.token_stride + (long)h * src.head_stride,
+                               w, a.cos_sin + tk.pos * a.rot, a.rot / 2, r.hi, r.lo, pc.c0, pc.c1,
+                               pc.turn, s, kNear);
+        }
+        Floats<16> in;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 v = unpack2(f.v[k]);
+          in.v[2 * k] = v.x;
+          in.v[2 * k + 1] = v.y;
+        }
+        return ieee_quotients<16>(in, s);
+      });
+    };
 
     if (isq || FMT == 0) {
       if (row) {
         const RopeRows& dst = isq ? a.q_out : a.k_out;
         const long at = (long)token * dst.token_stride + (long)h * dst.head_stride;
-        if (isq && a.q_fp8) {
+        if (isq && q_codes) {
           const float s = a.q_hs ? __ldg(a.q_hs + h) : a.q_scale;
-          store_e4m3(f, s, a.q_hs ? __frcp_rn(s) : a.q_recip,
-                     reinterpret_cast<uint8_t*>(dst.data) + at, pc);
+          codes_to(s, a.q_hs ? __frcp_rn(s) : a.q_recip, reinterpret_cast<uint8_t*>(dst.data) + at);
         } else {
           f.store_bf16(dst.data + at, pc);
         }
@@ -351,7 +477,7 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(FMT))
       uint8_t* codes = isv ? a.v_codes : a.k_codes;
       if constexpr (FMT == kFmtFp8) {
         if (store)
-          store_e4m3(f, s, hs ? __frcp_rn(s) : (isv ? a.v_recip : a.k_recip), codes + crow * D, pc);
+          codes_to(s, hs ? __frcp_rn(s) : (isv ? a.v_recip : a.k_recip), codes + crow * D);
       } else {   // lanes without a row stay for their neighbours' shuffles
         store_nvfp4<D>(f, s, store, codes, isv ? a.v_bscale : a.k_bscale, crow, pc);
       }
@@ -416,11 +542,14 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t st) {
   }
   const unsigned per_block = (unsigned)(kGroups / per_token);
   const dim3 grid((a.tokens + per_block - 1) / per_block, y), block(kRopeThreads);
-  if (a.fmt == 0) return launch_pdl(rope_kernel<D, 0, INTER>, grid, block, 0, st, a, per_token);
+  if (a.fmt == 0 && a.q_fp8)
+    return launch_pdl(rope_kernel<D, 0, INTER, true>, grid, block, 0, st, a, per_token);
+  if (a.fmt == 0)
+    return launch_pdl(rope_kernel<D, 0, INTER, false>, grid, block, 0, st, a, per_token);
   if (a.fmt == kFmtFp8)
-    rope_kernel<D, kFmtFp8, INTER><<<grid, block, 0, st>>>(a, per_token);
+    rope_kernel<D, kFmtFp8, INTER, false><<<grid, block, 0, st>>>(a, per_token);
   else
-    rope_kernel<D, kFmtNvfp4, INTER><<<grid, block, 0, st>>>(a, per_token);
+    rope_kernel<D, kFmtNvfp4, INTER, false><<<grid, block, 0, st>>>(a, per_token);
   return cudaGetLastError();
 }
 

@@ -386,3 +386,28 @@ def test_new_lens_beyond_the_batch_and_below_zero():
     cache.append_rope(ro, x, x, start, new_lens=torch.tensor([5, 6, 2 ** 31 - 1], device=DEV).int())
     full.append_rope(ro, x, x, start)
     assert torch.equal(cache.k_codes, full.k_codes) and torch.equal(cache.v_codes, full.v_codes)
+
+
+def test_codes_next_to_boundaries_are_decided_in_64_bits():
+    """Half a million values, the scale put so that some quotients lie on a rounding
+    boundary: the codes are the 64-bit ones.  They have to be wherever fp32's error is
+    within the 16 steps (each at least u of the value) that send a quotient to 48
+    bits: 2 u of mag without a norm, so down to |y| = mag / 7 with the quotient's own
+    step; with one 12.5 u (the squares' sum and eps 15 u, halved by the root, which is
+    within 1 u itself, two products 2 u, the rotation 2 u), so from 0.9 mag on."""
+    T, H, D = 512, 8, 128
+    for inter in (False, True):
+        for norm in (False, True):
+            ro = make_rotary(D, D, inter, norm)
+            q = rand((T, H, D), 3)
+            pos = torch.randint(0, 700, (T,), generator=gen(4), device=DEV).int()
+            y, mag = reference(q, ro.q_norm, pos.cpu().numpy(), ro, D)
+            sure = np.abs(y) >= mag * (0.9 if norm else 1 / 7)
+            for i in range(4):
+                # |y[0, 0, i]| becomes 17 x 2: a boundary (17 has five bits)
+                scale = float(np.float32(np.abs(y[0, 0, i]) / (17 * 2.0)))
+                q8, _ = runtime.norm_rope(ro, q, None, pos, q_out_type="e4m3", q_scale=scale)
+                got = R.e4m3_values(q8.cpu().numpy())
+                want = R.round_value(y / np.float64(np.float32(scale)), R.E4M3_POS)
+                assert np.array_equal(got[sure], want[sure])
+                assert (got != want).sum() <= 4    # the rest: nearly all (cancelled sums may differ)
