@@ -17,7 +17,15 @@
 // value moves between lanes (pairs side by side lie within a piece anyway).
 // Both 16-byte loads of a lane group cover whole 32-byte sectors, the row's sum
 // of squares is a butterfly over its lanes, and an NVFP4 block of 16 is the
-// pieces of two neighbouring lanes (rot is a multiple of 32).
+// pieces of two neighbouring lanes (rot is a multiple of 32).  The arithmetic
+// runs on packed fp32 pairs.
+//
+// Measured on GB300: 8192 tokens x 40 heads of 128 with norm, bf16 out (172 MB):
+// 30.3 us, 5.7 TB/s, 85% of the copy rate; one token each of 64 requests: 2.5
+// us, of which an empty launch takes most.  The append of 4 x 2048 padded tokens
+// (half of them real, 48 heads, 95 MB): 27.3 us, 52% of the copy rate, bound by
+// instruction issue (63%: conversions, quotients and their boundary checks); one
+// token each of 48 requests: 4.1 us.
 
 #include <algorithm>
 
@@ -30,11 +38,13 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 // Resident blocks per SM: four hide the most latency where rows leave as bf16
-// (chunk of 8192 tokens, 40 heads: 31.3 us against 35.1 with three); the
-// quantisers need more registers than that leaves (4 x 2048 padded tokens, 48
-// heads: 29.7 us with three, 31.3 with four).
+// (8192 tokens, 40 heads: 30.3 us against 35.9 with three); the quantisers need
+// more registers than that leaves (4 x 2048 padded tokens, 48 heads: 27.3 us with
+// three, 29.5 with four, 30.1 with two).
 constexpr int rope_ctas(int fmt) { return fmt == 0 ? 4 : 3; }
-// From this many lanes (two thousand per SM) on, groups take kRowsEach rows.
+// From this many lanes (two thousand per SM) on, groups take kRowsEach rows: the
+// chunk of 8192 tokens takes 30.3 us so against 46.7 with a group for every row
+// (three rows each: 31.2).  Fewer lanes than that fill the GPU only once.
 constexpr unsigned long long kManyThreads = 152ull * 2048;
 constexpr int kRowsEach = 6;
 

@@ -35,6 +35,19 @@
 // Sums and accumulators are fp32.
 // Every wait is bounded; a timeout sets an error bit and the partials become
 // NaN.
+//
+// What bounds it (FP8, head_dim 128, 256 rows x 8 heads over 32768 tokens in 11
+// splits: 88 CTAs): a 128-token tile of both row tiles takes some 3300 cycles,
+// of which the tensor pipe is busy 2048 (2 x 2 products of 128^3); the rest is
+// the chain scores -> maximum -> exponentials -> P V of each slot, which the
+// other slot covers but for ~300 cycles a unit, and shared memory, whose 128
+// bytes per cycle the operands of the products and the conversion share.  Some
+// 9000 cycles pass before the first scores (the queries and pages come from
+// DRAM, the code is cold) and 7500 after the last (128 KB of partials per CTA).
+// The kernel alone: 53.5 us, 47% of its SMs' tensor cycles.  Measured slower:
+// clusters that merge eight splits through distributed shared memory (+4 us),
+// the partials staged for bulk stores (+0.7 us), P handed over whole (+0.5 us),
+// one lane issuing the MMAs in a branch (84 instead of some 75 cycles each).
 
 #include <type_traits>
 
@@ -667,6 +680,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 // warp per row: every partial is one coalesced read, eight in flight per lane.
 constexpr int kMergeWarps = 8;
 
+// 64 x 32 rows of 12 partials (13 MB): about 5 us behind the kernels that wrote
+// them, 8 to 9 from DRAM; bound by the latency of its two rounds of reads.
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_rows_kernel(const CombineArgs a) {
   constexpr int kPer = D / 32;   // dims per lane
@@ -737,6 +752,9 @@ cudaError_t with_kernel(int fmt, int D, int R, int wide_p, F&& f) {
   auto by_p = [&](auto kfmt, auto kd, auto mt) {
     return wide_p ? pick(kfmt, kd, mt, std::true_type{}) : pick(kfmt, kd, mt, std::false_type{});
   };
+  // Up to 128 rows one row tile with token tiles in both slots, else two row
+  // tiles (16 x 8k, 64 rows: 17.3 us against 21.2 with two; 64 x 32k, 256 rows:
+  // 57.8 against 70.0 with one).
   auto by_rows = [&](auto kfmt, auto kd) {
     return R > kTok ? by_p(kfmt, kd, std::integral_constant<int, 2>{})
                     : by_p(kfmt, kd, std::integral_constant<int, 1>{});
