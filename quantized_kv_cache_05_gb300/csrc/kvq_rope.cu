@@ -21,11 +21,12 @@
 // runs on packed fp32 pairs.
 //
 // Measured on GB300: 8192 tokens x 40 heads of 128 with norm, bf16 out (172 MB):
-// 30.3 us, 5.7 TB/s, 85% of the copy rate; one token each of 64 requests: 2.5
-// us, of which an empty launch takes most.  The append of 4 x 2048 padded tokens
-// (half of them real, 48 heads, 95 MB): 27.3 us, 52% of the copy rate, bound by
-// instruction issue (63%: conversions, quotients and their boundary checks); one
-// token each of 48 requests: 4.1 us.
+// 30.4 us, 5.7 TB/s, 84% of the copy rate; one token each of 64 requests: 2.4
+// us, where an empty kernel takes 0.7: the latency of its loads one behind the
+// other.  The append of 4 x 2048 ragged padded tokens (48 heads, 94 MB): 27.5 us,
+// 51% of the copy rate; 62% of the issue slots while an SM is busy, 47% over the
+// kernel.  One token each of 48 requests: 4.3 us.  Settling quotients takes 0.9
+// and 0.7 us of these two.
 
 #include <algorithm>
 

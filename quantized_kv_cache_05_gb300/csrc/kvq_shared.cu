@@ -37,17 +37,16 @@
 // NaN.
 //
 // What bounds it (FP8, head_dim 128, 256 rows x 8 heads over 32768 tokens in 11
-// splits: 88 CTAs): a 128-token tile of both row tiles takes some 3300 cycles,
-// of which the tensor pipe is busy 2048 (2 x 2 products of 128^3); the rest is
-// the chain scores -> maximum -> exponentials -> P V of each slot, which the
-// other slot covers but for ~300 cycles a unit, and shared memory, whose 128
-// bytes per cycle the operands of the products and the conversion share.  Some
-// 9000 cycles pass before the first scores (the queries and pages come from
-// DRAM, the code is cold) and 7500 after the last (128 KB of partials per CTA).
-// The kernel alone: 53.5 us, 47% of its SMs' tensor cycles.  Measured slower:
-// clusters that merge eight splits through distributed shared memory (+4 us),
-// the partials staged for bulk stores (+0.7 us), P handed over whole (+0.5 us),
-// one lane issuing the MMAs in a branch (84 instead of some 75 cycles each).
+// splits: 88 CTAs): clock stamps in the kernel show a 128-token tile of both row
+// tiles every 3300 to 3500 cycles, for which the products need 2048 (2 x 2 of
+// 128^3); the rest is the chain scores -> maximum -> exponentials -> P V as far
+// as the other slot does not cover it.  Some 10000 cycles pass before the first
+// scores, most of them until the queries have come, and 8000 from the last
+// tile to the end (128 KB of partials per CTA), of 98000.  The kernel alone:
+// 52.7 us, its SMs' tensor pipes active 51% of the time.  Measured slower:
+// clusters that merge eight splits through distributed shared memory (4 requests
+// x 1k: +4 us), the partials staged for bulk stores (64 x 32k: +0.8 us), P handed
+// over whole (+0.1 to 0.4 us).
 
 #include <type_traits>
 
@@ -680,8 +679,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 // warp per row: every partial is one coalesced read, eight in flight per lane.
 constexpr int kMergeWarps = 8;
 
-// 64 x 32 rows of 12 partials (13 MB): about 5 us behind the kernels that wrote
-// them, 8 to 9 from DRAM; bound by the latency of its two rounds of reads.
+// 64 x 32 rows of 12 partials (13 MB): 8.5 to 9.1 us with cold caches, 1.5 TB/s
+// and 14% of the issue slots: bound by the latency of its two rounds of reads.
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_rows_kernel(const CombineArgs a) {
   constexpr int kPer = D / 32;   // dims per lane
