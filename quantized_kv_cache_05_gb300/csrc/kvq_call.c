@@ -158,6 +158,16 @@ static int optional_address(PyObject* t, void** out) {
   return address(t, out);
 }
 
+/* The error flag: int32 on the device (kernels write it), or its address. */
+static int flag_address(PyObject* t, long dev, void** out) {
+  long long numel;
+  if (t != Py_None && !PyLong_Check(t)) {
+    if (here(t, t_i32, dev, "error_flag") || method_long(t, s_numel, &numel)) return -1;
+    if (numel < 1) return refuse("error_flag", "expected one entry");
+  }
+  return optional_address(t, out);
+}
+
 /* One float per head, dense. */
 static int head_scales(PyObject* t, long long n, long dev, const float** out) {
   *out = NULL;
@@ -237,7 +247,7 @@ static PyObject* norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const int fp8 = PyObject_IsTrue(a[10]);
   float scale;
   if (PyErr_Occurred() || optional_address(a[1], &stream) || as_float(a[11], &scale) ||
-      optional_address(a[13], &flag))
+      flag_address(a[13], dev, &flag))
     return NULL;
   PyObject *q = a[5], *k = a[6];
   rows_t qr, qo, kr, ko;
@@ -296,7 +306,7 @@ static PyObject* rope_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const int fp8 = PyObject_IsTrue(a[14]);
   float scale;
   if (PyErr_Occurred() || !c || optional_address(a[1], &stream) || as_float(a[15], &scale) ||
-      optional_address(a[17], &flag)) {
+      flag_address(a[17], dev, &flag)) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "rope_append: no cache");
     return NULL;
   }
@@ -369,7 +379,7 @@ static PyObject* decode_shared(PyObject* self, PyObject* const* a, Py_ssize_t n)
   if (optional_address(a[1], &stream) || as_int(a[4], &len) || optional_address(a[5], &table) ||
       as_int(a[6], &splits) || optional_address(a[9], &po) || optional_address(a[10], &pl) ||
       optional_address(a[11], &cn) || optional_address(a[12], &out) ||
-      optional_address(a[13], &flag))
+      flag_address(a[13], dev, &flag))
     return NULL;
   kvq_decode_params p = *given;
   rows_t qr;

@@ -4,9 +4,10 @@ import ctypes
 import math
 
 import pytest
+import torch
 
 from quantized_kv_cache_05_gb300 import build as kbuild
-from quantized_kv_cache_05_gb300 import kvq
+from quantized_kv_cache_05_gb300 import kvq, runtime
 
 P = 1 << 20   # an aligned address that nothing dereferences
 OK, INV, UNS = kvq.KVQ_OK, kvq.KVQ_ERR_INVALID, kvq.KVQ_ERR_UNSUPPORTED
@@ -140,3 +141,21 @@ def test_append_mla_refused():
 def test_struct_sizes():
     # the C structs' layout (LP64)
     assert ctypes.sizeof(kvq.kvq_rotary) == 48 and ctypes.sizeof(kvq.kvq_heads) == 32
+
+
+@pytest.mark.parametrize("flag", [torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int64),
+                                  torch.zeros(1)])
+def test_error_flags_of_another_type_or_device_are_refused(flag):
+    """Kernels write the flag: a tensor elsewhere is refused before any launch."""
+    call, ro = runtime._calls(), kvq.kvq_rotary()
+    with pytest.raises(ValueError, match="error_flag"):
+        call.norm_rope(0, None, ctypes.addressof(ro), -1, -1, None, None, None, None, None, False, 1.0,
+                       None, flag)
+    c = kvq.kvq_cache()
+    with pytest.raises(ValueError, match="error_flag"):
+        call.rope_append(0, None, ctypes.addressof(c), 1, ctypes.addressof(ro), -1, -1, None, None, None,
+                         None, None, None, None, False, 1.0, None, flag)
+    p = kvq.kvq_decode_params()
+    with pytest.raises(ValueError, match="error_flag"):
+        call.decode_shared(0, None, ctypes.addressof(c), ctypes.addressof(p), 0, None, 1, None, None, None,
+                           None, None, None, flag)
