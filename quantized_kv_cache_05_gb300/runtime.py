@@ -103,11 +103,20 @@ class Rotary:
         return self._struct
 
 
-def _query_out(q: torch.Tensor, out: Optional[torch.Tensor], kind: str) -> torch.Tensor:
+def _rows_like(t: torch.Tensor, dtype: torch.dtype, stream) -> torch.Tensor:
+    """A dense tensor of t's shape for a kernel on `stream` to write: from that stream's
+    memory, since work that the current one has yet to do may use what it freed."""
+    if stream is not None and kvq._stream(stream) != torch.cuda.current_stream().cuda_stream:
+        with torch.cuda.stream(torch.cuda.ExternalStream(kvq._stream(stream))):
+            return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+
+
+def _query_out(q: torch.Tensor, out: Optional[torch.Tensor], kind: str, stream) -> torch.Tensor:
     if kind not in OUT_TORCH or kind == "f32":
         raise ValueError("q_out_type: bf16 or e4m3")
     if out is None:
-        return torch.empty_like(q, dtype=OUT_TORCH[kind], memory_format=torch.contiguous_format)
+        return _rows_like(q, OUT_TORCH[kind], stream)
     if out.numel() != q.numel() or out.shape[-2:] != q.shape[-2:]:
         raise ValueError("q_out: expected q's shape")
     return out
@@ -127,11 +136,12 @@ def norm_rope(rotary: Rotary, q: Optional[torch.Tensor], k: Optional[torch.Tenso
               error_flag: Optional[torch.Tensor] = None, stream=None):
     """Norm and rotation of queries and keys (kvq_norm_rope): q bf16 [T][Hq][D] and k
     bf16 [T][Hk][D], positions int32 [T].  Returns (q_out, k_out): new tensors, or the
-    given ones (bf16 outputs may be the inputs).  q_out_type "e4m3": uint8 codes."""
+    given ones (bf16 outputs may be the inputs).  q_out_type "e4m3": uint8 codes.
+    New tensors belong to the stream that is given."""
     if q is not None:
-        q_out = _query_out(q, q_out, q_out_type)
+        q_out = _query_out(q, q_out, q_out_type, stream)
     if k is not None and k_out is None:
-        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        k_out = _rows_like(k, k.dtype, stream)
     dev = _launch_device(rotary.device)
     addr, nq, nk = rotary.args
     st = (_call or _calls()).norm_rope(dev, kvq._stream(stream), addr, nq, nk,
@@ -257,7 +267,7 @@ class QuantizedKVCache:
         fp8 = False
         if q is not None:
             kind = q_out_type or ("e4m3" if q_out is not None and q_out.dtype == torch.uint8 else "bf16")
-            q_out = _query_out(q, q_out, kind)
+            q_out = _query_out(q, q_out, kind, stream)
             fp8 = kind == "e4m3"
         dev = _launch_device(rotary.device, self.k_codes.get_device())
         c = self.struct()

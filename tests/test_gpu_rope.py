@@ -411,3 +411,26 @@ def test_codes_next_to_boundaries_are_decided_in_64_bits():
                 want = R.round_value(y / np.float64(np.float32(scale)), R.E4M3_POS)
                 assert np.array_equal(got[sure], want[sure])
                 assert (got != want).sum() <= 4    # the rest: nearly all (cancelled sums may differ)
+
+
+@pytest.mark.parametrize("append", [False, True])
+def test_new_outputs_belong_to_the_stream_that_is_given(append):
+    """A freed tensor that the current stream has yet to write is not the memory of an
+    output that a kernel on another stream writes first."""
+    ro = make_rotary(128, 128, False, True)
+    x, start = rand((64, 1, 2, 128), 1), torch.zeros(64, device=DEV).int()
+    cache = make_cache("fp8", 64, 2, 16, 2, 128, 1)
+    want, _ = runtime.norm_rope(ro, x[:, 0], None, start)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    late = torch.empty_like(want)
+    torch.cuda._sleep(20_000_000)   # about ten milliseconds
+    late.fill_(7)
+    del late
+    if append:
+        got = cache.append_rope(ro, x, x, start, q=x, stream=side)[:, 0]
+    else:
+        got, _ = runtime.norm_rope(ro, x[:, 0], None, start, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
