@@ -511,8 +511,11 @@ kvq_status kvq_shared_splits(int num_sms, int batch, int num_kv_heads, int q_per
   // tile and kFixed around them (256-row tiles; 128-row ones kTile1, kFixed1);
   // the requests' own chunks take kOwn + kOwnToken per token (half the longest
   // is taken as the mean), two CTAs on each SM that the prefix leaves free,
-  // and the rest when it is done.  Merging adds kMerge, and a launch of its
-  // own kMergeLaunch where not all own chunks fit beside the prefix.
+  // and the rest when it is done.  Merging adds kMerge per partial of a row
+  // (where own chunks merge in place, more with the q_per_kv rows that a CTA
+  // merges, from four on: 96 requests x 8k with 16 rows each take 31.2 us with
+  // 16 splits merged in place, 27.0 with 18 and the merging launch), and a
+  // launch of its own kMergeLaunch where not all own chunks fit beside the prefix.
   constexpr double kTile = 1.75, kFixed = 8, kTile1 = 1.15, kFixed1 = 4.5;
   constexpr double kOwn = 5, kOwnToken = 0.01, kMerge = 0.12, kMergeLaunch = 4;
   const bool wide = (long long)batch * q_per_kv > 128;
@@ -533,7 +536,7 @@ kvq_status kvq_shared_splits(int num_sms, int batch, int num_kv_heads, int q_per
       const double room = 2.0 * (double)std::max<long long>(0, num_sms - ctas);
       double t = t_prefix + kMerge * (sp + so);
       if (own <= room) {
-        t = std::max(t_prefix, t_own) + kMerge * (sp + so);
+        t = std::max(t_prefix, t_own) + kMerge * std::max(1.0, q_per_kv / 4.0) * (sp + so);
       } else {
         const double beside = room * std::floor(t_prefix / t_own);
         t += kMergeLaunch;
