@@ -21,12 +21,12 @@
 // runs on packed fp32 pairs.
 //
 // Measured on GB300: 8192 tokens x 40 heads of 128 with norm, bf16 out (172 MB):
-// 30.4 us, 5.7 TB/s, 84% of the copy rate; one token each of 64 requests: 2.4
+// 30.2 us, 5.7 TB/s, 85% of the copy rate; one token each of 64 requests: 2.3
 // us, where an empty kernel takes 0.7: the latency of its loads one behind the
-// other.  The append of 4 x 2048 ragged padded tokens (48 heads, 94 MB): 27.5 us,
-// 51% of the copy rate; 62% of the issue slots while an SM is busy, 47% over the
-// kernel.  One token each of 48 requests: 4.3 us.  Settling quotients takes 0.9
-// and 0.7 us of these two.
+// other.  The append of 4 x 2048 ragged padded tokens (48 heads, 94 MB): 27.0 us,
+// 52% of the copy rate; 57 to 62% of the issue slots while an SM is busy, 46% over
+// the kernel.  One token each of 48 requests: 4.3 us.  Settling quotients takes
+// 0.8 and 0.7 us of these two.
 
 #include <algorithm>
 
@@ -37,15 +37,17 @@
 namespace kvq {
 namespace {
 
-constexpr int kRopeThreads = 256;
-// Resident blocks per SM: four hide the most latency where rows leave as bf16
-// (8192 tokens, 40 heads: 30.3 us against 35.9 with three); the quantisers need
-// more registers than that leaves (4 x 2048 padded tokens, 48 heads: 27.3 us with
-// three, 29.5 with four, 30.1 with two).
-constexpr int rope_ctas(int fmt) { return fmt == 0 ? 4 : 3; }
+// Small blocks, so that the last ones to run leave few SMs idle (the append of
+// 4 x 2048 padded tokens, 48 heads: 26.4 us against 27.3 with half as many of
+// 256 threads), six to an SM: with four 29.1 us, with eight, which leave 64
+// registers, 28.1.  Rows that leave as bf16 take 30 us with either (8192 tokens,
+// 40 heads).
+constexpr int kRopeThreads = 128;
+constexpr int kRopeCtas = 6;
 // From this many lanes (two thousand per SM) on, groups take kRowsEach rows: the
-// chunk of 8192 tokens takes 30.3 us so against 46.7 with a group for every row
-// (three rows each: 31.2).  Fewer lanes than that fill the GPU only once.
+// append of 4 x 2048 padded tokens takes 26.5 us so against 47.0 with a group for
+// every row (three rows each: 29.4, twelve: 27.0).  Fewer lanes than that fill the
+// GPU only once.
 constexpr unsigned long long kManyThreads = 152ull * 2048;
 constexpr int kRowsEach = 6;
 
@@ -385,7 +387,7 @@ __device__ __forceinline__ long rope_page(const RopeArgs& a, const Token& k, boo
 // out before the present one's arithmetic.
 // QF8 (FMT 0): the queries leave as E4M3 codes.
 template <int D, int FMT, bool INTER, bool QF8>
-__global__ void __launch_bounds__(kRopeThreads, rope_ctas(FMT))
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     rope_kernel(const RopeArgs a, int per_token) {
   // the append is an ordinary launch (it starts after all earlier work), the
   // other a programmatic one
