@@ -48,6 +48,7 @@
 // writes NaN for its partial instead of hanging.
 
 #include <cfloat>
+#include <climits>
 #include <cmath>
 
 #pragma once
@@ -147,12 +148,13 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
-  // Behind the shared prefix's kernel (a.late_merge) it reads nothing of that
-  // kernel's before the merge, and that kernel let it start only after its
-  // own wait for everything earlier.
-  if (a.fresh == 0 && !a.late_merge) griddep_wait();
+  // Behind the shared prefix's kernel it reads nothing of that kernel's before
+  // the merge, and that kernel let it start only after its own wait for
+  // everything earlier.  (Quantised probabilities have no shared prefix.)
+  const bool late = !PROBQ && a.late_merge;
+  if (a.fresh == 0 && !late) griddep_wait();
   // partials only: the merging kernel may take its place now, it waits
-  if (a.late_merge && !a.counters) griddep_launch_dependents();
+  if (late && !a.counters) griddep_launch_dependents();
 
   // one-page requests: the page index does not depend on the length, so its
   // load overlaps the length's
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     L = L < 0 ? 0 : cap;
   }
   // a shared prefix is not this kernel's (a.skip is a whole number of pages)
-  if (a.skip > 0 && L >= a.skip) {
+  if (!PROBQ && a.skip > 0 && L >= a.skip) {
     L -= a.skip;
     bt += a.skip / a.ps;
   }
@@ -176,11 +178,12 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
   const int cstart = (int)min((long)split * c, (long)L);
   const int cend = (int)min((long)cstart + c, (long)L);
   const int nboxes = (cend - cstart + kBoxTokens - 1) / kBoxTokens;
-  // first box of the chunk that holds an appended position (overlap mode)
-  const int fresh_box = a.fresh == 0 ? 0 : (max(L - a.fresh, cstart) - cstart) / kBoxTokens;
-  // this thread has waited for the preceding kernel (no load has to, behind
-  // the shared prefix's)
-  bool dep_done = a.fresh == 0 && !a.late_merge;
+  // first box of the chunk that holds an appended position (overlap mode); no
+  // load has to wait behind the shared prefix's kernel
+  const int fresh_box = late ? INT_MAX
+                        : a.fresh == 0 ? 0
+                                       : (max(L - a.fresh, cstart) - cstart) / kBoxTokens;
+  bool dep_done = a.fresh == 0 && !late;   // this thread has waited for the preceding kernel
   // this warp's boxes: warp, warp + NW, ...
   const int nw = nboxes > warp ? (nboxes - warp + NW - 1) / NW : 0;
   const int total = kSweeps * nw;
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
       }
     }
     const long row = ((long)page * a.Hkv + h) * a.ps + off;
-    if (!dep_done && !a.late_merge && box >= fresh_box) {
+    if (!dep_done && box >= fresh_box) {
       griddep_wait();
       dep_done = true;
     }
@@ -628,7 +631,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
   // prefix's kernel, with a merge of its own to come, one CTA's wait will do,
   // so that the others leave their SM to the next ones
   if (!dep_done && threadIdx.x == 0 &&
-      (!a.late_merge || a.counters ||
+      (!late || a.counters ||
        (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)))
     griddep_wait();
   if (threadIdx.x < a.G) {
