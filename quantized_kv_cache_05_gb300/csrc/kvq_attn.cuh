@@ -462,9 +462,9 @@ __device__ __forceinline__ void store_item(const PartialArgs& a, size_t row0, in
 // step.
 template <int DT>
 __device__ __forceinline__ void merge_staged(const PartialArgs& a, size_t row0, int rows,
-                                             const float* staged, const float* w,
+                                             int s, const float* staged, const float* w,
                                              const float* winv, bool ok) {
-  const int s = a.part_splits, nq = a.Dv / 4;
+  const int nq = a.Dv / 4;
   const float4* po = reinterpret_cast<const float4*>(staged);
 #pragma unroll 1
   for (int i = threadIdx.x; i < rows * nq; i += blockDim.x) {
@@ -483,11 +483,12 @@ __device__ __forceinline__ void merge_staged(const PartialArgs& a, size_t row0, 
 // the row pieces are separate bulk copies, each a full round trip.)  The
 // async-proxy read follows the acquire, behind a proxy fence.  bar: an
 // mbarrier initialized with one arrival and unused so far; wbuf: kMaxGroup *
-// (kMaxFusedSplits + 1) floats outside the stage.
+// (kMaxFusedSplits + 1) floats outside the stage; s: the partials of a row.
 template <int DEPTH = 32, int NI = 1>
 __device__ __forceinline__ void fused_combine_staged(const PartialArgs& a, int bh, size_t part_row,
-                                                     int rows, uint32_t stage, const float* stage_p,
-                                                     uint32_t cap, float* wbuf, uint32_t bar) {
+                                                     int rows, int s, uint32_t stage,
+                                                     const float* stage_p, uint32_t cap,
+                                                     float* wbuf, uint32_t bar) {
   __shared__ int is_last;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -501,7 +502,6 @@ __device__ __forceinline__ void fused_combine_staged(const PartialArgs& a, int b
   }
   __syncthreads();
   if (!is_last) return;
-  const int s = a.part_splits;
   float* winv = wbuf + kMaxGroup * kMaxFusedSplits;
   const uint64_t bytes = (uint64_t)rows * s * a.Dv * 4;
   if (bytes > cap) {
@@ -517,11 +517,11 @@ __device__ __forceinline__ void fused_combine_staged(const PartialArgs& a, int b
   merge_weights(a.part_lse, part_row, rows, s, wbuf, winv);
   const bool ok = __syncthreads_and(mbar_wait(bar, 0) ? 1 : 0) != 0;
   if (a.out_dtype == 0)
-    merge_staged<0>(a, part_row, rows, stage_p, wbuf, winv, ok);
+    merge_staged<0>(a, part_row, rows, s, stage_p, wbuf, winv, ok);
   else if (a.out_dtype == 1)
-    merge_staged<1>(a, part_row, rows, stage_p, wbuf, winv, ok);
+    merge_staged<1>(a, part_row, rows, s, stage_p, wbuf, winv, ok);
   else
-    merge_staged<2>(a, part_row, rows, stage_p, wbuf, winv, ok);
+    merge_staged<2>(a, part_row, rows, s, stage_p, wbuf, winv, ok);
   if (!ok && threadIdx.x == 0) record_error(a.error_flag, 1);
 }
 

@@ -106,7 +106,10 @@ constexpr int ctas_per_sm() {
 // NH = number of 8-head groups (1: up to 8 query heads per kv head, 2: up to
 // 16); QF8: the query is E4M3 codes (FP8 query), and with an FP8 cache the
 // scores run on the E4M3 x E4M3 MMA straight from the cached code bytes.
-template <int FMT, int D, bool PROBQ, int NH, bool QF8, int NW>
+// BEHIND: the requests' own tokens behind a shared prefix's kernel (a variant, as
+// the ordinary decode of 32768 tokens takes 32.5 us without these terms and 32.7
+// with them decided at run time).
+template <int FMT, int D, bool PROBQ, int NH, bool QF8, int NW, bool BEHIND>
 __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     partial_kernel(const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const PartialArgs a) {
@@ -150,11 +153,10 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
   }
   // Behind the shared prefix's kernel it reads nothing of that kernel's before
   // the merge, and that kernel let it start only after its own wait for
-  // everything earlier.  (Quantised probabilities have no shared prefix.)
-  const bool late = !PROBQ && a.late_merge;
-  if (a.fresh == 0 && !late) griddep_wait();
+  // everything earlier.
+  if (!BEHIND && a.fresh == 0) griddep_wait();
   // partials only: the merging kernel may take its place now, it waits
-  if (late && !a.counters) griddep_launch_dependents();
+  if (BEHIND && !a.counters) griddep_launch_dependents();
 
   // one-page requests: the page index does not depend on the length, so its
   // load overlaps the length's
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     L = L < 0 ? 0 : cap;
   }
   // a shared prefix is not this kernel's (a.skip is a whole number of pages)
-  if (!PROBQ && a.skip > 0 && L >= a.skip) {
+  if (BEHIND && L >= a.skip) {
     L -= a.skip;
     bt += a.skip / a.ps;
   }
@@ -180,10 +182,10 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
   const int nboxes = (cend - cstart + kBoxTokens - 1) / kBoxTokens;
   // first box of the chunk that holds an appended position (overlap mode); no
   // load has to wait behind the shared prefix's kernel
-  const int fresh_box = late ? INT_MAX
+  const int fresh_box = BEHIND ? INT_MAX
                         : a.fresh == 0 ? 0
                                        : (max(L - a.fresh, cstart) - cstart) / kBoxTokens;
-  bool dep_done = a.fresh == 0 && !late;   // this thread has waited for the preceding kernel
+  bool dep_done = !BEHIND && a.fresh == 0;   // this thread has waited for the preceding kernel
   // this warp's boxes: warp, warp + NW, ...
   const int nw = nboxes > warp ? (nboxes - warp + NW - 1) / NW : 0;
   const int total = kSweeps * nw;
@@ -627,11 +629,12 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
       ofrag[((warp * MT + i) * NH + hh) * 32 + lane] =
           make_float4(o[i][hh][0], o[i][hh][1], o[i][hh][2], o[i][hh][3]);
   const size_t part_row = ((size_t)b * a.Hq + (size_t)h * a.G);   // first query head
+  const int psplits = BEHIND ? a.part_splits : a.num_splits;      // partials of a row
   // the grid ends after the preceding kernel in every mode; behind the shared
   // prefix's kernel, with a merge of its own to come, one CTA's wait will do,
   // so that the others leave their SM to the next ones
   if (!dep_done && threadIdx.x == 0 &&
-      (!late || a.counters ||
+      (!BEHIND || a.counters ||
        (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)))
     griddep_wait();
   if (threadIdx.x < a.G) {
@@ -647,7 +650,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
                            : ex2(sm.m[w][row] - M) / Ltot * out_mult;
     float lse = (M == -INFINITY || Ltot == 0.f) ? -INFINITY : (M + log2f(Ltot)) * kLn2;
     if (bad) lse = NAN;
-    a.part_lse[(part_row + row) * a.part_splits + split] = lse;
+    a.part_lse[(part_row + row) * psplits + split] = lse;
   }
   __syncthreads();
 
@@ -669,9 +672,9 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     }
     if (bad) acc = make_float4(NAN, NAN, NAN, NAN);
     const int d0 = (D / 8) * (ln >> 2) + 2 * i;
-    float* r0 = a.part_o + ((part_row + h0) * a.part_splits + split) * D + d0;
+    float* r0 = a.part_o + ((part_row + h0) * psplits + split) * D + d0;
     *reinterpret_cast<float2*>(r0) = make_float2(acc.x, acc.z);
-    if (h0 + 1 < a.G) *reinterpret_cast<float2*>(r0 + (size_t)a.part_splits * D) =
+    if (h0 + 1 < a.G) *reinterpret_cast<float2*>(r0 + (size_t)psplits * D) =
         make_float2(acc.y, acc.w);
   }
   // fused combine: the G rows' partials staged at the ring base (the O
@@ -685,14 +688,17 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn_bytes));
     const uint32_t usable = dyn_bytes - (ring - smem_u32(dyn_smem));
     fused_combine_staged<ctas_per_sm<FMT, D, PROBQ, NH, NW>() == 4 ? 16 : 32>(
-        a, bh, part_row, a.G, ring, reinterpret_cast<const float*>(ofrag), usable - kWbuf,
+        a, bh, part_row, a.G, psplits, ring, reinterpret_cast<const float*>(ofrag), usable - kWbuf,
         reinterpret_cast<float*>(dyn_smem + (ring - smem_u32(dyn_smem)) + usable - kWbuf),
         smem_u32(&sm.comb_full));
   }
 }
 
-template <int FMT, int D, bool PROBQ, int NH, bool QF8, int NW>
+template <int FMT, int D, bool PROBQ, int NH, bool QF8, int NW, bool BEHIND = false>
 cudaError_t launch_partial_t(const TensorMaps& m, const PartialArgs& a, cudaStream_t st) {
+  // quantised probabilities and head_dim 256 have no shared prefix
+  if constexpr (!BEHIND && !PROBQ && D <= 128)
+    if (a.late_merge) return launch_partial_t<FMT, D, PROBQ, NH, QF8, NW, true>(m, a, st);
   using Rg = Ring<FMT, D, PROBQ, NH, NW>;
   static_assert(Rg::kBytes >= Rg::kEpilogue && Rg::kBytes >= Rg::kStream, "ring too small");
   size_t smem = 1024 + (size_t)Rg::kBytes + (PROBQ ? (size_t)a.score_floats * 4 : 0);
@@ -707,7 +713,7 @@ cudaError_t launch_partial_t(const TensorMaps& m, const PartialArgs& a, cudaStre
     smem = std::max(smem, std::min(need, kPerCta));
   }
   smem = (smem + 15) / 16 * 16;
-  auto kern = partial_kernel<FMT, D, PROBQ, NH, QF8, NW>;
+  auto kern = partial_kernel<FMT, D, PROBQ, NH, QF8, NW, BEHIND>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;

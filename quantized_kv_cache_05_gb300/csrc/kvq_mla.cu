@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           base + kOffTile + kMlaHeads * kMlaLat * 4,
                           reinterpret_cast<float*>(gbase + kOffRaw));
   else if (a.counters)
-    fused_combine_staged<32, 4>(a, b, part_row, kMlaHeads, base + kOffTile,
+    fused_combine_staged<32, 4>(a, b, part_row, kMlaHeads, a.num_splits, base + kOffTile,
                                 reinterpret_cast<const float*>(gbase + kOffTile), kTileBytes,
                                 reinterpret_cast<float*>(gbase + kOffRaw), smem_u32(&sm.comb_full));
 }
