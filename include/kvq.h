@@ -173,6 +173,14 @@ typedef struct kvq_decode_params {
   int32_t q_fp8;
   float q_scale;             /* q_fp8 without q_head_scale: finite > 0 */
   const float* q_head_scale; /* (device, optional) [num_q_heads] */
+  /*
+   * kvq_decode_shared only (the other calls ignore it).  0: the prefix's
+   * probabilities enter the products with V in two f16 parts, as kvq_decode's
+   * do.  1: in one, rounded by up to 2^-11 of a weight where kvq_decode keeps
+   * 2^-22; a bf16 output, whose own rounding is 2^-8, then differs here and
+   * there by one step, and the products take half the tensor-core time.
+   */
+  int32_t prefix_p_f16;
 } kvq_decode_params;
 
 /* Human-readable name of a status code (static string). */
@@ -411,8 +419,8 @@ kvq_status kvq_decode(const kvq_cache* c, const kvq_decode_params* p, const void
  * cores over 128 rows, and kvq_decode reads a prefix that only one or two
  * requests share (or that is shorter than what each adds) in less time.
  * fresh_tokens is taken as 0 where prefix_len is positive.  The prefix's
- * probabilities are rounded to 11 bits for the products with V where the
- * output is bf16 (8 bits itself), and kept to 22 for fp32 and E4M3 outputs.
+ * probabilities keep 22 bits in the products with V, as kvq_decode's do, or 11
+ * where p->prefix_p_f16 asks for that.
  * Two or three launches on `stream` (three where not all own chunks fit on the
  * SMs beside the prefix); calls that share partials or counters must not
  * overlap on the GPU.
@@ -431,6 +439,8 @@ kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int
  * SMs that it leaves free.  own_splits is a power of two up to 16 with at
  * least 128 tokens of max_own_len, the longest own part, per chunk;
  * prefix_splits has at least one 128-token tile per chunk; together at most 64.
+ * The model's times are those of an FP8 cache with head_dim 128; fmt is checked
+ * and changes nothing so far.
  */
 kvq_status kvq_shared_splits(int num_sms, int batch, int num_kv_heads, int q_per_kv,
                              int prefix_len, int max_own_len, int fmt,

@@ -110,6 +110,7 @@ kvq_status check_params(const kvq_decode_params* p) {
   if (p->fresh_tokens < 0) return KVQ_ERR_INVALID;
   if (p->q_fp8 != 0 && p->q_fp8 != 1) return KVQ_ERR_INVALID;
   if (p->q_fp8 && !p->q_head_scale && !finite_pos(p->q_scale)) return KVQ_ERR_INVALID;
+  if (p->prefix_p_f16 != 0 && p->prefix_p_f16 != 1) return KVQ_ERR_INVALID;
   return KVQ_OK;
 }
 
@@ -507,7 +508,8 @@ kvq_status kvq_shared_splits(int num_sms, int batch, int num_kv_heads, int q_per
       (fmt != KVQ_FP8_E4M3 && fmt != KVQ_NVFP4))
     return KVQ_ERR_INVALID;
   // A model of the step in microseconds, from measurements on GB300 (FP8,
-  // head_dim 128): the prefix's kernel runs one CTA per SM, kTile per token
+  // head_dim 128, probabilities in two parts; other formats, head dims and one
+  // part are taken for the same): the prefix's kernel runs one CTA per SM, kTile per token
   // tile and kFixed around them (256-row tiles; 128-row ones kTile1, kFixed1);
   // the requests' own chunks take kOwn + kOwnToken per token (half the longest
   // is taken as the mean), two CTAs on each SM that the prefix leaves free,
@@ -516,7 +518,7 @@ kvq_status kvq_shared_splits(int num_sms, int batch, int num_kv_heads, int q_per
   // merges, from four on: 96 requests x 8k with 16 rows each take 31.2 us with
   // 16 splits merged in place, 27.0 with 18 and the merging launch), and a
   // launch of its own kMergeLaunch where not all own chunks fit beside the prefix.
-  constexpr double kTile = 1.75, kFixed = 8, kTile1 = 1.15, kFixed1 = 4.5;
+  constexpr double kTile = 2.2, kFixed = 6, kTile1 = 1.5, kFixed1 = 5.5;
   constexpr double kOwn = 5, kOwnToken = 0.01, kMerge = 0.12, kMergeLaunch = 4;
   const bool wide = (long long)batch * q_per_kv > 128;
   const long long base = num_kv_heads * shared_row_tiles(batch, q_per_kv);
@@ -740,7 +742,7 @@ kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int
   a.splits = prefix_splits;
   a.box = 16;   // TMA boxes: the largest power of two up to a tile that divides the pages
   while (a.box < 128 && c->page_size % (2 * a.box) == 0) a.box *= 2;
-  a.wide_p = p->out_dtype != KVQ_OUT_BF16;
+  a.wide_p = p->prefix_p_f16 == 0;
   a.sm_scale = p->sm_scale;
   a.k_scale = c->k_scale;
   a.v_scale = c->v_scale;

@@ -110,7 +110,7 @@ struct SharedArgs {
   int R, G, Hq, Hkv, ps, num_pages;   // R = batch * G rows per kv head
   int prefix, splits, box;            // tokens, splits of this kernel, TMA box rows
   int split0, part_splits;            // first partial's index among a row's, their number
-  int wide_p;                         // 1: P as high part and residual (fp32 and E4M3 outputs)
+  int wide_p;                         // 1: P as high part and residual, 0: one f16 (prefix_p_f16)
   float sm_scale, k_scale, v_scale;
   const float* k_hs;
   const float* v_hs;

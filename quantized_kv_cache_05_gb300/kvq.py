@@ -51,6 +51,7 @@ class kvq_decode_params(ctypes.Structure):
         ("num_splits", _i32), ("seq_lens", _P), ("max_kv_len", _i32), ("sm_scale", _f),
         ("prob_scale", _f), ("out_dtype", _i32), ("out_scale", _f), ("error_flag", _P),
         ("fresh_tokens", _i32), ("q_fp8", _i32), ("q_scale", _f), ("q_head_scale", _P),
+        ("prefix_p_f16", _i32),
     ]
 
 

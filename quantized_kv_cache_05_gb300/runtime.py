@@ -301,6 +301,9 @@ class DecodeConfig:
     q_fp8: bool = False
     q_scale: float = 1.0
     q_head_scale: Optional[torch.Tensor] = None
+    # SharedDecode: the prefix's probabilities in one f16 instead of two
+    # (kvq_decode_params)
+    prefix_p_f16: bool = False
 
     def params(self, seq_lens: Optional[torch.Tensor], error_flag: Optional[torch.Tensor] = None
                ) -> kvq.kvq_decode_params:
@@ -310,7 +313,7 @@ class DecodeConfig:
             self.batch, self.num_q_heads, self.qk_dim, self.v_dim, self.num_splits,
             ptr(seq_lens), self.max_kv_len, self.sm_scale, self.prob_scale, OUT[self.out],
             self.out_scale, ptr(error_flag), self.fresh_tokens, 1 if self.q_fp8 else 0, self.q_scale,
-            ptr(self.q_head_scale))
+            ptr(self.q_head_scale), 1 if self.prefix_p_f16 else 0)
 
 
 class DecodeWorkspace:
@@ -391,9 +394,11 @@ class SharedDecode:
                  q_fp8: bool = False, q_scale: float = 1.0,
                  q_head_scale: Optional[torch.Tensor] = None,
                  prefix_table: Optional[torch.Tensor] = None,
-                 splits: Optional[tuple[int, int]] = None):
+                 splits: Optional[tuple[int, int]] = None, prefix_p_f16: bool = False):
         """prefix_table: the shared pages (int32; default: the first row of the cache's
-        block table); splits: (prefix, own) chunks, by default kvq_shared_splits'."""
+        block table); splits: (prefix, own) chunks, by default kvq_shared_splits';
+        prefix_p_f16: the prefix's probabilities with 11 bits instead of 22, for bf16
+        outputs that need not be kvq_decode's to the last step."""
         _check(0 <= prefix_len <= max_kv_len, "prefix_len: expected 0 .. max_kv_len")
         _check(batch <= cache.block_table.shape[0], "more requests than the block table has")
         _check(num_q_heads % cache.Hkv == 0, "num_q_heads: a multiple of the kv heads")
@@ -415,7 +420,8 @@ class SharedDecode:
             cache, prefix_len, prefix_table, sp)
         cfg = self.cfg = DecodeConfig(batch, num_q_heads, cache.D, cache.D, so, max_kv_len, sm_scale,
                                       out=out, out_scale=out_scale, q_fp8=q_fp8, q_scale=q_scale,
-                                      q_head_scale=_head_scale(q_head_scale, num_q_heads))
+                                      q_head_scale=_head_scale(q_head_scale, num_q_heads),
+                                      prefix_p_f16=prefix_p_f16)
         self.ws = FusedWorkspace(dataclasses.replace(cfg, num_splits=so + sp), cache.Hkv, device)
         self._params = cfg.params(None)   # the lengths and the flag come with each step
 

@@ -414,3 +414,49 @@ def test_runtime_refuses():
             plan(*args)
     with pytest.raises(kvq.KvqError):
         runtime.SharedDecode(B.cache, 2, 4, 150, B.cap, 0.1)(B.q, B.lens_t)
+
+
+def round_bf16(x):
+    """The nearest bf16 value (8 significant bits) of each 64-bit number."""
+    m, e = np.frexp(x)
+    return np.ldexp(np.rint(m * 256) / 256, e)
+
+
+def check_rounded(B, got, out, ref, what=""):
+    """Rounding is monotone: the output lies between the rounded ends of the interval
+    of the fp32 result, whose bound holds P's two f16 parts: 2^-22 of a weight, and for
+    each shared token 2^-32 of the row's largest weight."""
+    o, tol, mag = ref
+    vmax = float(B.val[1].abs().max())
+    # + the last fp32 steps (normalisation, the quotient by the output's scale)
+    tol = tol + 2.0 ** -22 * mag + 2.0 ** -32 * B.prefix * vmax + 2.0 ** -21 * np.abs(o)
+    if out == "bf16":
+        g, lo, hi = got.double().cpu().numpy(), round_bf16(o - tol), round_bf16(o + tol)
+    else:
+        s = float(np.float32(0.004))
+        g = R.e4m3_values(got.cpu().numpy())
+        lo, hi = R.round_value((o - tol) / s, R.E4M3_POS), R.round_value((o + tol) / s, R.E4M3_POS)
+    bad = ~((g >= lo) & (g <= hi))
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size}, at {np.argwhere(bad)[0]}"
+
+
+@pytest.mark.parametrize("out", ["bf16", "e4m3"])
+@pytest.mark.parametrize("fmt,D,n", [("fp8", 64, 12), ("fp8", 128, 40), ("nvfp4", 64, 40), ("nvfp4", 128, 12)])
+def test_weights_keep_two_f16_parts(out, fmt, D, n):
+    """A few large weights decide each row here: one f16 part (some 2^-12 of a weight)
+    puts bf16 outputs on the other side of a rounding boundary, 3 to 55 of these cases'
+    12288 to 81920 beyond the bound."""
+    B = Batch(fmt, D, 16, 2, 16, 656, [(5 * b) % 7 for b in range(n)], 11, q_std=4.0)
+    check_rounded(B, run(B, out), out, B.reference())
+
+
+def test_one_f16_part_where_the_caller_asks_for_it():
+    """prefix_p_f16: within 2^-11 of a weight for every output type, and not the default."""
+    for n, D in ((5, 128), (40, 64)):
+        B = Batch("fp8", D, 16, 2, 16, 656, [(5 * b) % 7 for b in range(n)], 11, q_std=4.0)
+        ref = B.reference()
+        for out in ("f32", "bf16", "e4m3"):
+            o, tol, mag = ref
+            narrow = run(B, out, prefix_p_f16=True)
+            B.check(narrow, out, (o, tol + 2.0 ** -11 * mag, mag))
+            assert not torch.equal(narrow, run(B, out))

@@ -84,3 +84,9 @@ def test_splits():
     assert 8 * f(152, 8, 8, 4, 65536, 0, 1)[1] in range(128, 153)
     assert f(0, 4, 8, 4, 1024, 60, 1)[0] == INV and f(152, 4, 8, 0, 1024, 60, 1)[0] == INV
     assert f(152, 4, 8, 4, -1, 60, 1)[0] == INV and f(152, 4, 8, 4, 16, -1, 1)[0] == INV
+
+
+@pytest.mark.parametrize("v", [-1, 2])
+def test_prefix_p_f16_is_0_or_1(v):
+    assert call(p=params(batch=0, prefix_p_f16=v)) == INV
+    assert call(p=params(batch=0, prefix_p_f16=1)) == OK
