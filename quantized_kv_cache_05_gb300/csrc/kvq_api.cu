@@ -570,7 +570,8 @@ namespace {
 // in too.
 kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const void* q,
                        float* part_o, float* part_lse, uint32_t* counters, void* out,
-                       cudaStream_t stream, int prefix_len = 0, int prefix_splits = 0) {
+                       cudaStream_t stream, int prefix_len = 0, int prefix_splits = 0,
+                       uint32_t* ready = nullptr) {
   kvq_status s = check_cache(c);
   if (s != KVQ_OK) return s;
   s = check_params(p);
@@ -633,6 +634,7 @@ kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const voi
     a.part_splits = p->num_splits + prefix_splits;
     a.skip = prefix_len;
     a.late_merge = 1;
+    a.ready = ready;
   }
   a.counters = counters;
   a.out = out;
@@ -748,6 +750,8 @@ kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int
   a.v_scale = c->v_scale;
   a.k_hs = c->k_head_scale;
   a.v_hs = c->v_head_scale;
+  a.ready = counters;
+  a.ready_n = p->batch * c->num_kv_heads;   // < 2^31, as partials are
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -770,7 +774,7 @@ kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int
   s = cuda_status(launch_shared_prefix(c->fmt, D, maps, a, as_stream(stream)));
   if (s != KVQ_OK) return s;
   s = decode_impl(c, p, q, part_o, part_lse, fused ? counters : nullptr, out, as_stream(stream),
-                  prefix_len, prefix_splits);
+                  prefix_len, prefix_splits, counters);
   if (s != KVQ_OK || fused) return s;
   CombineArgs m{};
   m.part_o = part_o;

@@ -483,12 +483,14 @@ __device__ __forceinline__ void merge_staged(const PartialArgs& a, size_t row0, 
 // the row pieces are separate bulk copies, each a full round trip.)  The
 // async-proxy read follows the acquire, behind a proxy fence.  bar: an
 // mbarrier initialized with one arrival and unused so far; wbuf: kMaxGroup *
-// (kMaxFusedSplits + 1) floats outside the stage; s: the partials of a row.
+// (kMaxFusedSplits + 1) floats outside the stage; s: the partials of a row; base:
+// what the counter holds before the first arrival.
 template <int DEPTH = 32, int NI = 1>
 __device__ __forceinline__ void fused_combine_staged(const PartialArgs& a, int bh, size_t part_row,
                                                      int rows, int s, uint32_t stage,
                                                      const float* stage_p, uint32_t cap,
-                                                     float* wbuf, uint32_t bar) {
+                                                     float* wbuf, uint32_t bar,
+                                                     unsigned base = 0u) {
   __shared__ int is_last;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -497,7 +499,7 @@ __device__ __forceinline__ void fused_combine_staged(const PartialArgs& a, int b
                  : "=r"(prev)
                  : "l"(a.counters + bh)
                  : "memory");
-    is_last = prev == (unsigned)(a.num_splits - 1);
+    is_last = prev == base + (unsigned)(a.num_splits - 1);
     if (is_last) a.counters[bh] = 0u;
   }
   __syncthreads();

@@ -367,6 +367,30 @@ __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Hand-over between kernels of one stream that does not go through
+// griddepcontrol.wait: being allowed to start (launch_dependents of the kernel
+// before) says nothing about what is visible.  A thread that has waited for
+// everything earlier publishes words in global memory, and a kernel that started
+// early acquires one: what was complete for the publisher then is for the
+// acquiring thread, and past a barrier for its CTA.
+constexpr uint32_t kReady = 0x10000u;   // above any count of arrivals in the same word
+__device__ __forceinline__ void publish_ready(uint32_t* words, int n, int lane) {
+  asm volatile("fence.acq_rel.gpu;" ::: "memory");
+  for (int i = lane; i < n; i += 32)
+    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(words + i), "r"(kReady) : "memory");
+}
+// Bounded like mbar_wait.
+__device__ __forceinline__ bool acquire_ready(const uint32_t* word) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 0; i < (1u << 28); ++i) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(word) : "memory");
+    if (v >= kReady) return true;
+    if ((i & 63) == 63 && globaltimer_ns() - t0 > 250000000ull) return false;
+  }
+  return false;
+}
+
 // fl32(p / y) for the FP8 probabilities, with y = prob_scale known per call.
 // fast: z = RN(1/y) precomputed; q0 = RN(p z) has a relative error of at most
 // about 2^-23, the remainder r = RN(p - q0 y) is then accurate to 2^-24, and

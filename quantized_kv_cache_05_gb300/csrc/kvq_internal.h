@@ -89,9 +89,12 @@ struct PartialArgs {
   int part_splits;
   // shared-prefix decode: requests of at least `skip` tokens (whole pages)
   // start there, and the preceding kernel in the stream writes the partials
-  // num_splits .. part_splits - 1: only the merge waits for it
+  // num_splits .. part_splits - 1: only the merge waits for it.  `ready`
+  // [B * Hkv] (the counters, also where `counters` is null) is what that kernel
+  // publishes when it has waited for everything earlier
   int skip;
   int late_merge;
+  uint32_t* ready;
 };
 
 // The shared prefix's partials (kvq_shared.cu).
@@ -114,6 +117,8 @@ struct SharedArgs {
   float sm_scale, k_scale, v_scale;
   const float* k_hs;
   const float* v_hs;
+  uint32_t* ready;                    // published for the own chunks' kernel (PartialArgs)
+  int ready_n;
 };
 
 // Rows of heads: head h of token t starts at data + t * token_stride + h *
@@ -164,7 +169,8 @@ struct CombineArgs {
 };
 
 // Launch with programmatic stream serialization (the kernel calls
-// griddep_wait() before reading its inputs).
+// griddep_wait() before reading its inputs; the decode behind a shared prefix
+// acquires them from the prefix's kernel instead, which has waited).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t st, Args&&... args) {

@@ -63,7 +63,7 @@ constexpr int kTok = 128;                 // tokens per tile
 constexpr int kCol = kTok * 128;          // bytes of 64 f16 columns of 128 rows
 constexpr int kConvWarp = 8;              // warps 0-7 softmax (slots 0, 1)
 constexpr int kConvWarps = 4;
-constexpr int kMmaWarp = kConvWarp + kConvWarps, kTmaWarp = kMmaWarp + 1;
+constexpr int kMmaWarp = kConvWarp + kConvWarps, kTmaWarp = kMmaWarp + 1, kReadyWarp = kTmaWarp + 1;
 constexpr int kSharedThreads = 512;       // four warpgroups: softmax x 2, convert, MMA and TMA
 // Registers per thread of the warpgroups (the launch gives each thread 128, 512
 // for the four): a softmax thread holds its row's 128 scores at once.
@@ -160,8 +160,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // Every thread waits for the earlier work before any of them lets the decode
-  // kernel start: it reads its inputs without a wait of its own.
+  // Every thread waits for the earlier work; the decode kernel, which may start
+  // from here on and does not wait for this one, acquires that from the words
+  // that the first CTA's spare warp publishes.
   griddep_wait();
   griddep_launch_dependents();
 
@@ -220,6 +221,10 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       copy_tile(j, 0, row);
       copy_tile(j, 1, row);
     }
+  } else if (warp == kReadyWarp) {   // needs nothing of the CTA's set-up either
+    asm volatile("bar.arrive 3, %0;" ::"n"(kSharedThreads) : "memory");
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+      publish_ready(a.ready, a.ready_n, lane);
   }
   // Queries.  Two row tiles: their 16-byte pieces go straight to the places of
   // the operand tile that their f16 values take, piece c of a row there, FP8
@@ -264,7 +269,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     len = live ? __ldg(a.seq_lens + b) : -1;
   }
   tc_fence_before();
-  if (warp != kTmaWarp) asm volatile("bar.sync 3, %0;" ::"n"(kSharedThreads) : "memory");
+  if (warp != kTmaWarp && warp != kReadyWarp) asm volatile("bar.sync 3, %0;" ::"n"(kSharedThreads) : "memory");
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   if (warp == kMmaWarp && tmem != 0) *abort_flag = 1;   // (never: all of it is ours)

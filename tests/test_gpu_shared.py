@@ -460,3 +460,49 @@ def test_one_f16_part_where_the_caller_asks_for_it():
             narrow = run(B, out, prefix_p_f16=True)
             B.check(narrow, out, (o, tol + 2.0 ** -11 * mag, mag))
             assert not torch.equal(narrow, run(B, out))
+
+
+@pytest.mark.parametrize("splits", [(4, 2), (9, 16), (17, 4)])
+def test_inputs_written_right_before_the_call(splits):
+    """Queries, lengths, block table and own pages written by the kernels right before
+    the call in one graph, other values at every replay: the own chunks run on all SMs
+    beside the prefix and have to see them (compared with the same call on its own)."""
+    own = [200 + (29 * b) % 300 for b in range(24)]
+    B = Batch("fp8", 128, 32, 8, 16, 2176, own, 21)
+    plan = B.plan("bf16", splits)
+    names = ("q", "lens", "bt", "v")
+    live = dict(q=B.q, lens=B.lens_t, bt=B.bt, v=B.codes[1])
+    sets = []
+    for k in range(4):
+        lens = torch.tensor([2176 + (v * (k + 3) + 11 * b) % 500 for b, v in enumerate(own)], device=DEV).int()
+        lens = lens.clamp(max=B.cap)
+        perm = torch.arange(B.B, device=DEV).roll(k)     # another request's pages behind the prefix
+        # (every row long enough: entries past a request's own pages are page 0)
+        bt, q, v = B.bt[perm].contiguous(), B.q.roll(k, 0).contiguous(), B.codes[1].roll(k, 0).contiguous()
+        sets.append(dict(q=q, lens=torch.minimum(lens, B.lens_t[perm]).int(), bt=bt, v=v))
+    want = []
+    for s in sets:
+        for n in names:
+            live[n].copy_(s[n])
+        torch.cuda.synchronize()
+        want.append(plan(B.q, B.lens_t).clone())
+        torch.cuda.synchronize()
+    assert not torch.equal(want[0], want[1])
+    src = {n: torch.empty_like(sets[0][n]) for n in names}
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        # element kernels, not copies: their writes stay in the caches
+        live["v"].copy_(src["v"] ^ 0)
+        live["bt"].copy_(src["bt"] + 0)
+        live["lens"].copy_(src["lens"] + 0)
+        live["q"].copy_(src["q"] * 1)
+        out = plan(B.q, B.lens_t)
+    for k in range(300):
+        for n in names:
+            src[n].copy_(sets[k % 4][n])
+        g.replay()
+        got = out.clone()
+        if k % 50 < 8:
+            assert torch.equal(got, want[k % 4]), k
+    torch.cuda.synchronize()
+    assert int(plan.ws.counters.abs().sum()) == 0
