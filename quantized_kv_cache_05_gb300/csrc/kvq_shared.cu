@@ -51,6 +51,7 @@
 // x 1k: +4 us), the partials staged for bulk stores (64 x 32k: +0.8 us), P handed
 // over whole (+0.1 to 0.4 us).
 
+#include <cfloat>
 #include <type_traits>
 
 #include "kvq_attn.cuh"
@@ -445,12 +446,22 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     const uint32_t sS = lane_addr + slot * 128, sO = lane_addr + 256 + slot * 128;
 
     // ---- the row's query, into its operand tile
-    float qsc;   // score scale, log2 domain
+    // Score scale, log2 domain: positive, so that the row's largest score is that of
+    // its largest product and the -inf past the prefix stays one.  A scale below
+    // zero (a query head's) turns the query's sign instead; one of zero, also by
+    // underflow (|q| below 2^-113), counts as the smallest normal number, whose
+    // products with scores below 2^31 are nothing beside an exponent.
+    float qsc;
     {
       // the largest magnitudes of a piece's even and odd bf16 values
       auto largest = [](const uint4& v) -> uint32_t {
         return __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
                         __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+      };
+      uint32_t flip = 0u;   // sign bits of a pair, where the query's sign turns
+      auto settle_scale = [&](float s) {
+        if (s < 0.f) flip = 0x80008000u;
+        qsc = s == 0.f ? FLT_MIN : fabsf(s);   // (NaN stays)
       };
       // bf16 piece c, prescaled by a power of two, as f16
       auto scale_piece = [&](const uint4& v, float f, int c) {
@@ -459,7 +470,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           o[k] = pack_f16x2(__uint_as_float(w[k] << 16) * f,
-                            __uint_as_float(w[k] & 0xFFFF0000u) * f);
+                            __uint_as_float(w[k] & 0xFFFF0000u) * f) ^ flip;
         sts128(q_at(r, c), o[0], o[1], o[2], o[3]);
       };
       // 16 FP8 codes as the f16 pieces 2c and 2c + 1
@@ -469,12 +480,14 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         e4m3x4_to_f16x2x2(v.y, o[2], o[3]);
         e4m3x4_to_f16x2x2(v.z, o[4], o[5]);
         e4m3x4_to_f16x2x2(v.w, o[6], o[7]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] ^= flip;
         sts128(q_at(r, 2 * c), o[0], o[1], o[2], o[3]);
         sts128(q_at(r, 2 * c + 1), o[4], o[5], o[6], o[7]);
       };
       const float k_log2 =
           (a.k_hs ? a.sm_scale * __ldg(a.k_hs + h) : a.sm_scale * a.k_scale) * 1.4426950408889634f;
-      qsc = a.q_fp8 ? k_log2 * (a.q_hs ? __ldg(a.q_hs + hq) : a.q_scale) : 0.f;
+      if (a.q_fp8) settle_scale(k_log2 * (a.q_hs ? __ldg(a.q_hs + hq) : a.q_scale));
       if constexpr (MT == 2) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();   // the warp's rows are here
@@ -486,7 +499,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 #pragma unroll 8
           for (int c = 0; c < D / 8; ++c) m2 = __vmaxu2(m2, largest(lds128(q_at(r, c))));
           const int e = q_prescale_exp(max(m2 & 0xFFFFu, m2 >> 16));
-          qsc = scale_pow2(k_log2, -e);
+          settle_scale(scale_pow2(k_log2, -e));
 #pragma unroll 4
           for (int c = 0; c < D / 8; ++c) scale_piece(lds128(q_at(r, c)), exp2i(e), c);
         }
@@ -506,7 +519,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 #pragma unroll
           for (int c = 0; c < D / 8; ++c) m2 = __vmaxu2(m2, largest(v[c]));
           const int e = q_prescale_exp(max(m2 & 0xFFFFu, m2 >> 16));
-          qsc = scale_pow2(k_log2, -e);
+          settle_scale(scale_pow2(k_log2, -e));
           if (slot == 0) {   // (both slots have the same rows)
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) scale_piece(v[c], exp2i(e), c);

@@ -506,3 +506,28 @@ def test_inputs_written_right_before_the_call(splits):
             assert torch.equal(got, want[k % 4]), k
     torch.cuda.synchronize()
     assert int(plan.ws.counters.abs().sum()) == 0
+
+
+@pytest.mark.parametrize("n", [5, 40])
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+def test_head_scales_of_zero_and_below(n, fmt):
+    """A scale of zero gives every token the same weight, one below zero turns the
+    order round; the prefix ends inside a 128-token tile."""
+    B = Batch(fmt, 64, 8, 2, 16, 400, [(7 * b) % 30 for b in range(n)], 4, q_fp8=True)
+    hs = torch.tensor([0.0, 0.017, -0.017, -0.0, 0.03, 0.0, -0.03, 0.01], device=DEV)
+    B.q64 = B.q.view(torch.float8_e4m3fn).double() * hs.double()[:, None]
+    ref = B.reference()
+    o = run(B, "f32", q_head_scale=hs)
+    B.check(o, "f32", ref)
+    cfg = runtime.DecodeConfig(B.B, 8, 64, 64, 2, B.cap, B.sm, out="f32", q_fp8=True, q_head_scale=hs)
+    B.check(runtime.decode_fused(B.cache, B.q, B.lens_t, cfg), "f32", ref)
+
+
+@pytest.mark.parametrize("n", [5, 40])
+def test_queries_whose_scale_underflows(n):
+    """|q| below 2^-113 and a small score scale: their product falls out of fp32's range,
+    and every token has the same weight."""
+    B = Batch("fp8", 64, 8, 2, 16, 400, [(7 * b) % 30 for b in range(n)], 4)
+    B.q = (torch.randn(B.q.shape, generator=B.g, device=DEV) * 2.0 ** -118).bfloat16()
+    B.q64, B.sm = B.q.double(), 2.0 ** -25
+    B.check(run(B, "f32"), "f32")
