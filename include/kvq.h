@@ -406,8 +406,8 @@ kvq_status kvq_decode(const kvq_cache* c, const kvq_decode_params* p, const void
  *   prefix_len (host) a multiple of page_size, at most p->max_kv_len; 0 is
  *              kvq_decode.
  *   prefix_table (device int32, optional) [prefix_len / page_size] the shared
- *              pages; NULL: the first entries of the first row of the block
- *              table, whose request then has to be one that shares them.
+ *              pages; NULL: the first entries of the block table's row of the
+ *              first request that is at least prefix_len long.
  *   prefix_splits, p->num_splits: chunks of the prefix (at least one 128-token
  *              tile each: more are lowered) and of each request's own tokens;
  *              kvq_shared_splits picks both.  Together at most 64.

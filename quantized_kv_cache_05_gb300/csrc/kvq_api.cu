@@ -729,7 +729,10 @@ kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int
   a.q_hs = p->q_fp8 ? p->q_head_scale : nullptr;
   a.k_bscale = static_cast<const uint8_t*>(c->k_bscale);
   a.v_bscale = static_cast<const uint8_t*>(c->v_bscale);
-  a.prefix_table = prefix_table ? prefix_table : c->block_table;
+  a.prefix_table = prefix_table;
+  a.block_table = c->block_table;
+  a.batch = p->batch;
+  a.max_pages = c->max_pages_per_seq;
   a.seq_lens = p->seq_lens;
   a.part_o = part_o;
   a.part_lse = part_lse;

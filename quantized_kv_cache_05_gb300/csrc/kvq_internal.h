@@ -105,7 +105,9 @@ struct SharedArgs {
   const float* q_hs;
   const uint8_t* k_bscale;
   const uint8_t* v_bscale;
-  const int32_t* prefix_table;
+  const int32_t* prefix_table;        // null: the block table's row of a request that shares
+  const int32_t* block_table;
+  int batch, max_pages;
   const int32_t* seq_lens;
   float* part_o;
   float* part_lse;

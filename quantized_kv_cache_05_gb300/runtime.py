@@ -395,8 +395,8 @@ class SharedDecode:
                  q_head_scale: Optional[torch.Tensor] = None,
                  prefix_table: Optional[torch.Tensor] = None,
                  splits: Optional[tuple[int, int]] = None, prefix_p_f16: bool = False):
-        """prefix_table: the shared pages (int32; default: the first row of the cache's
-        block table); splits: (prefix, own) chunks, by default kvq_shared_splits';
+        """prefix_table: the shared pages (int32; default: the first entries of the first
+        request that is at least prefix_len long); splits: (prefix, own) chunks, by default kvq_shared_splits';
         prefix_p_f16: the prefix's probabilities with 11 bits instead of 22, for bf16
         outputs that need not be kvq_decode's to the last step."""
         _check(0 <= prefix_len <= max_kv_len, "prefix_len: expected 0 .. max_kv_len")

@@ -531,3 +531,20 @@ def test_queries_whose_scale_underflows(n):
     B.q = (torch.randn(B.q.shape, generator=B.g, device=DEV) * 2.0 ** -118).bfloat16()
     B.q64, B.sm = B.q.double(), 2.0 ** -25
     B.check(run(B, "f32"), "f32")
+
+
+@pytest.mark.parametrize("n", [6, 40, 70])
+def test_the_prefix_comes_from_a_request_that_shares_it(n):
+    """Without a table of its own: idle and shorter requests come first, with entries
+    of no meaning (out of range, or other pages) in their rows of the block table."""
+    for lead in ([None], [-40, None, -1], [None] * (n - 1)):
+        own = lead + [(13 * b) % 50 for b in range(n - len(lead))]
+        B = Batch("fp8", 128, 8, 2, 16, 320, own, n)
+        for b, v in enumerate(own):
+            if v is None:
+                B.bt[b] = -1 if b % 2 == 0 else 2 ** 30
+        for out in ("f32", "bf16"):
+            B.check(run(B, out), out, what=f"{lead}")
+    B = Batch("fp8", 128, 8, 2, 16, 320, [None, -5] * (n // 2))
+    B.bt[0] = -1
+    B.check(run(B, "f32"), "f32", what="nobody shares")
