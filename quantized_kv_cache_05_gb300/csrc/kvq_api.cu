@@ -34,37 +34,48 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+// Encodes a map of bytes with dense boxes (the arguments of
+// cuTensorMapEncodeTiled).  The driver's call wants a current context, which a
+// thread that has made no runtime call with one has not: it gets the device's.
+bool encode_map(CUtensorMap* m, cuuint32_t rank, const void* base, const cuuint64_t* dims,
+                const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle sw) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  auto encode = [&] {
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  int dev = 0;
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess &&
+      cudaSetDevice(dev) == cudaSuccess)
+    r = encode();
+  return r == CUDA_SUCCESS;
+}
+
 // 2-D byte view [rows][row_bytes] of a cache tensor, box_rows-row boxes, with the
 // widest hardware swizzle the row allows.
 bool make_row_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows,
                   uint32_t box_rows = kBoxTokens) {
-  auto fn = encode_fn();
-  if (!fn) return false;
   cuuint64_t dims[2] = {row_bytes, rows};
   cuuint64_t strides[1] = {row_bytes};
   cuuint32_t box[2] = {(cuuint32_t)row_bytes, box_rows};
-  cuuint32_t estr[2] = {1, 1};
   CUtensorMapSwizzle sw = row_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                           : row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                             : CU_TENSOR_MAP_SWIZZLE_NONE;
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(m, 2, base, dims, strides, box, sw);
 }
 
 // 3-D byte view [rows][n_slices][slice_bytes] of a row-major tensor whose rows
 // are n_slices * slice_bytes wide; boxes of one slice x box_rows rows.
 bool make_slice_map(CUtensorMap* m, const void* base, uint64_t slice_bytes, uint64_t n_slices,
                     uint64_t rows, CUtensorMapSwizzle sw, uint32_t box_rows = kBoxTokens) {
-  auto fn = encode_fn();
-  if (!fn) return false;
   cuuint64_t dims[3] = {slice_bytes, n_slices, rows};
   cuuint64_t strides[2] = {slice_bytes, slice_bytes * n_slices};
   cuuint32_t box[3] = {(cuuint32_t)slice_bytes, 1, box_rows};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(m, 3, base, dims, strides, box, sw);
 }
 
 bool is_mla(const kvq_cache* c) { return c->rope_dim > 0; }

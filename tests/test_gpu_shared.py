@@ -548,3 +548,32 @@ def test_the_prefix_comes_from_a_request_that_shares_it(n):
     B = Batch("fp8", 128, 8, 2, 16, 320, [None, -5] * (n // 2))
     B.bt[0] = -1
     B.check(run(B, "f32"), "f32", what="nobody shares")
+
+
+def test_first_call_of_a_thread():
+    """Each entry point as the first CUDA call that a thread makes."""
+    import threading
+    B = Batch("fp8", 128, 16, 2, 16, 320, [30] * 4)
+    plan = B.plan("f32")
+    cfg = runtime.DecodeConfig(4, 16, 128, 128, 2, B.cap, B.sm, out="f32")
+    ws = runtime.FusedWorkspace(cfg, 2)
+    q = B.q.reshape(4, 1, 16, 128)
+    calls = [lambda: plan(B.q, B.lens_t), lambda: runtime.decode_fused(B.cache, B.q, B.lens_t, cfg, ws),
+             lambda: runtime.prefill(B.cache, q, B.lens_t, cfg, 1, want[2])]
+    want = [None, None, torch.zeros(4, 1, 16, 128, device=DEV)]
+    for i, c in enumerate(calls):
+        want[i] = c().clone()
+    torch.cuda.synchronize()
+    for c, w in zip(calls, want):
+        got = []
+
+        def work():
+            try:
+                got.append(c())
+            except Exception as e:   # noqa: BLE001 - shown by the assertion
+                got.append(e)
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert isinstance(got[0], torch.Tensor) and torch.equal(got[0], w), got
