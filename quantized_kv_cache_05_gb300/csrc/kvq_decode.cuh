@@ -720,21 +720,28 @@ cudaError_t launch_partial_t(const TensorMaps& m, const PartialArgs& a, cudaStre
     if (a.late_merge) return launch_partial_t<FMT, D, PROBQ, NH, QF8, NW, true>(m, a, st);
   using Rg = Ring<FMT, D, PROBQ, NH, NW>;
   static_assert(Rg::kBytes >= Rg::kEpilogue && Rg::kBytes >= Rg::kStream, "ring too small");
-  size_t smem = 1024 + (size_t)Rg::kBytes + (PROBQ ? (size_t)a.score_floats * 4 : 0);
+  constexpr size_t kBase = 1024 + (size_t)Rg::kBytes;
+  // the shared memory that keeps ctas_per_sm CTAs resident (228 KB per SM, 1 KB
+  // reserved per CTA, the static part under 4 KB, the alignment slack)
+  constexpr size_t kPerCta = 233472 / ctas_per_sm<FMT, D, PROBQ, NH, NW>() - 1024 - 4096 - 1024;
+  size_t smem = kBase + (PROBQ ? (size_t)a.score_floats * 4 : 0);
   if (a.counters) {
     // room for the fused merge to stage its partials (G rows x s splits x Dv
-    // floats, and the weights) in one bulk copy, within the shared memory
-    // that keeps ctas_per_sm CTAs resident (228 KB per SM, 1 KB reserved per
-    // CTA, the static part under 4 KB, the alignment slack)
-    constexpr size_t kPerCta = 233472 / ctas_per_sm<FMT, D, PROBQ, NH, NW>() - 1024 - 4096 - 1024;
+    // floats, and the weights) in one bulk copy, where that fits
     const size_t need = 1024 + (size_t)a.G * a.part_splits * a.Dv * 4 +
                         (kMaxGroup * kMaxFusedSplits + kMaxGroup) * 4;
     smem = std::max(smem, std::min(need, kPerCta));
   }
   smem = (smem + 15) / 16 * 16;
   auto kern = partial_kernel<FMT, D, PROBQ, NH, QF8, NW, BEHIND>;
+  // The kernel's limit is the same for all calls, the most that any of them takes:
+  // set to each call's own size, a call of another thread could lower it between
+  // here and the launch, which then fails.
+  constexpr size_t kMost =
+      (std::max(kBase + (PROBQ ? (size_t)kScoreCapacity * 4 : 0), kPerCta) + 15) / 16 * 16;
+  static_assert(kMost + 4096 <= 232448, "shared memory of one CTA");
   cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                            (int)cudaSharedmemCarveoutMaxShared);

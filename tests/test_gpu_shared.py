@@ -577,3 +577,41 @@ def test_first_call_of_a_thread():
         t.join()
         torch.cuda.synchronize()
         assert isinstance(got[0], torch.Tensor) and torch.equal(got[0], w), got
+
+
+def test_two_threads_with_different_splits():
+    """Calls of one kernel with different scratch sizes from two threads at once."""
+    import threading
+    B = Batch("fp8", 128, 16, 2, 16, 8192, [30] * 4)
+    plans = [B.plan("f32", s) for s in ((1, 1), (60, 4))]
+    cfgs = [runtime.DecodeConfig(4, 16, 128, 128, s, B.cap, B.sm, out="f32") for s in (1, 64)]
+    calls = []
+    for plan, cfg in zip(plans, cfgs):
+        ws = runtime.FusedWorkspace(cfg, 2)
+        calls.append((lambda plan=plan: plan(B.q, B.lens_t),
+                      lambda cfg=cfg, ws=ws: runtime.decode_fused(B.cache, B.q, B.lens_t, cfg, ws)))
+    want = [[c().clone() for c in pair] for pair in calls]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                torch.zeros(1, device=DEV)   # (a call that the thread's context comes from)
+                for _ in range(400):
+                    for c in calls[i]:
+                        c()
+                for c, w in zip(calls[i], want[i]):
+                    got = c()
+                    torch.cuda.current_stream().synchronize()
+                    if not torch.equal(got, w):
+                        wrong.append(i)
+        except Exception as e:   # noqa: BLE001 - shown by the assertion
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
