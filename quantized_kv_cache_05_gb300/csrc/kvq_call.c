@@ -396,12 +396,34 @@ static PyObject* decode_shared(PyObject* self, PyObject* const* a, Py_ssize_t n)
   return PyLong_FromLong(st);
 }
 
+/* block_table(device, table, requests): refuses a table that is not a dense int32
+ * [at least requests][pages] there. */
+static PyObject* block_table(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 3) {
+    PyErr_SetString(PyExc_TypeError, "block_table: three arguments");
+    return NULL;
+  }
+  const long dev = PyLong_AsLong(a[0]);
+  const long long requests = PyLong_AsLongLong(a[2]);
+  long long size[4], stride[4];
+  if (PyErr_Occurred() || here(a[1], t_i32, dev, "block_table")) return NULL;
+  const int d = layout(a[1], size, stride, "block_table");
+  if (d < 0) return NULL;
+  if (d != 2 || (size[1] > 1 && stride[1] != 1) || (size[0] > 1 && stride[0] != size[1]))
+    return refuse("block_table", "expected a contiguous [batch][pages]"), NULL;
+  if (size[0] < requests) return refuse("block_table", "fewer rows than requests"), NULL;
+  Py_RETURN_NONE;
+}
+
 static PyMethodDef methods[] = {
     {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, "The library's functions."},
     {"norm_rope", (PyCFunction)(void (*)(void))norm_rope, METH_FASTCALL, "kvq_norm_rope"},
     {"rope_append", (PyCFunction)(void (*)(void))rope_append, METH_FASTCALL, "kvq_rope_append"},
     {"decode_shared", (PyCFunction)(void (*)(void))decode_shared, METH_FASTCALL,
      "kvq_decode_shared"},
+    {"block_table", (PyCFunction)(void (*)(void))block_table, METH_FASTCALL,
+     "The check of a call's block table."},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kvq_call",

@@ -182,7 +182,6 @@ class QuantizedKVCache:
         self.k_pe = (torch.zeros((num_pages, page_size, rope_dim), dtype=torch.bfloat16,
                                  device=device) if rope_dim else None)
         self.block_table = block_table.to(device=device, dtype=torch.int32).contiguous()
-        self.max_pages_per_seq = self.block_table.shape[1]
         # per-kv-head scales (float32 [Hkv] on the device), replacing k_scale / v_scale
         def _hs(t):
             if t is None:
@@ -226,13 +225,17 @@ class QuantizedKVCache:
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         self.k_codes, self.v_codes, self.k_pe = k_codes, v_codes, None
         self.k_bscale, self.v_bscale = k_bscale, v_bscale
-        self.block_table, self.max_pages_per_seq = block_table, block_table.shape[1]
+        self.block_table = block_table
         self.k_head_scale, self.v_head_scale = k_head_scale, v_head_scale
         return self
 
     @property
     def mla(self) -> bool:
         return self.rope > 0
+
+    @property
+    def max_pages_per_seq(self) -> int:
+        return self.block_table.shape[1]
 
     def struct(self) -> kvq.kvq_cache:
         # in the order of kvq_cache's fields
@@ -270,9 +273,11 @@ class QuantizedKVCache:
             q_out = _query_out(q, q_out, kind, stream)
             fp8 = kind == "e4m3"
         dev = _launch_device(rotary.device, self.k_codes.get_device())
+        call = _call or _calls()
+        call.block_table(dev, self.block_table, 0)   # (it may be another one than at the start)
         c = self.struct()
         addr, nq, nk = rotary.args
-        st = (_call or _calls()).rope_append(
+        st = call.rope_append(
             dev, kvq._stream(stream), ctypes.addressof(c),
             self.block_table.shape[0], addr, nq, nk, k_new, v_new, kpe_new, start_pos, new_lens, q,
             q_out, fp8, q_scale, q_head_scale, error_flag)
@@ -431,8 +436,10 @@ class SharedDecode:
         -> the output buffer [batch][Hq][D], overwritten by the next step."""
         ws = self.ws
         dev = _launch_device(self.cache.k_codes.get_device())
+        call = _call or _calls()
+        call.block_table(dev, self.cache.block_table, self.cfg.batch)   # (as in append_rope)
         c = self.cache.struct()
-        st = (_call or _calls()).decode_shared(
+        st = call.decode_shared(
             dev, kvq._stream(stream), ctypes.addressof(c),
             ctypes.addressof(self._params), self.prefix_len, self.prefix_table, self.prefix_splits, q,
             seq_lens, ws.part_o, ws.part_lse, ws.counters, ws.out, error_flag)

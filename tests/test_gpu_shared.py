@@ -615,3 +615,22 @@ def test_two_threads_with_different_splits():
     for t in threads:
         t.join()
     assert not wrong, wrong
+
+
+def test_block_tables_put_in_later():
+    """The cache's table may be replaced between calls: by one as large it is used, a
+    smaller one is refused before any launch."""
+    B = Batch("fp8", 64, 4, 2, 16, 160, [4, 20])
+    plan, x = B.plan("f32"), torch.zeros(2, 1, 2, 64, device=DEV).bfloat16()
+    want = plan(B.q, B.lens_t).clone()
+    old = B.cache.block_table
+    B.cache.block_table = torch.cat([old, old])
+    assert torch.equal(plan(B.q, B.lens_t), want)
+    for bad, error in ((old[:1], ValueError), (old.long(), ValueError), (old[:, 1:], ValueError),
+                       (old.cpu(), ValueError), (old[:, :4].contiguous(), kvq.KvqError)):
+        B.cache.block_table = bad
+        with pytest.raises(error):
+            plan(B.q, B.lens_t)
+        if error is ValueError:
+            with pytest.raises(ValueError):
+                B.cache.append_rope(runtime.Rotary(None), x, x, B.lens_t)

@@ -3,9 +3,10 @@ call (the addresses are never touched) and the split rule."""
 import math
 
 import pytest
+import torch
 
 from quantized_kv_cache_05_gb300 import build as kbuild
-from quantized_kv_cache_05_gb300 import kvq
+from quantized_kv_cache_05_gb300 import kvq, runtime
 
 P = 1 << 20
 OK, INV, UNS = kvq.KVQ_OK, kvq.KVQ_ERR_INVALID, kvq.KVQ_ERR_UNSUPPORTED
@@ -90,3 +91,20 @@ def test_splits():
 def test_prefix_p_f16_is_0_or_1(v):
     assert call(p=params(batch=0, prefix_p_f16=v)) == INV
     assert call(p=params(batch=0, prefix_p_f16=1)) == OK
+
+
+def test_block_table_of_a_call():
+    """The table as it is at the call: fewer rows, another type or strides, refused."""
+    check = runtime._calls().block_table
+    t = torch.zeros(3, 4, dtype=torch.int32)      # (device -1: host memory)
+    for ok in ((t, 0), (t, 3), (t[:1], 1), (t[:0], 0), (torch.zeros(3, 1, dtype=torch.int32), 3)):
+        check(-1, *ok)
+    for bad in ((t, 4), (t[:2], 3), (t.long(), 0), (t.t(), 0), (t[:, :2], 0), (t[0], 0), (t[None], 0)):
+        with pytest.raises(ValueError, match="block_table"):
+            check(-1, *bad)
+    with pytest.raises(ValueError, match="block_table"):
+        check(0, t, 0)                            # of another device
+    c = runtime.QuantizedKVCache("fp8", 8, 16, 2, 64, t, 1.0, 1.0, device="cpu")
+    assert c.struct().max_pages_per_seq == 4
+    c.block_table = t[:, :2].contiguous()         # a narrower table: its own width
+    assert c.max_pages_per_seq == 2 and c.struct().max_pages_per_seq == 2
