@@ -74,7 +74,8 @@ def _launch_device(*held: int) -> int:
 class Rotary:
     """The norm and rotation of a layer's queries and keys (``kvq_rotary``): the
     table of ``rope_table`` (None: no rotation) and the norms' weights (float32
-    [head_dim] each; None: no norm)."""
+    [head_dim] each; None: no norm).  It keeps these tensors, whose addresses its
+    struct holds; others need a Rotary of their own."""
 
     def __init__(self, table: Optional[torch.Tensor], interleaved: bool = False,
                  q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None,
@@ -84,7 +85,7 @@ class Rotary:
                 _here(t, torch.float32, what)
                 _check(t.is_contiguous(), f"{what}: expected a contiguous tensor")
         _check(table is None or table.dim() == 2, "table: expected [positions][rot_dim]")
-        self.table, self.q_norm, self.k_norm = table, q_norm, k_norm
+        self._tensors = table, q_norm, k_norm
         r = self._struct = kvq.kvq_rotary()
         if table is not None:
             r.cos_sin, r.num_positions, r.rot_dim = table.data_ptr(), *table.shape
@@ -94,10 +95,16 @@ class Rotary:
         r.eps = eps
         # for the calls: the struct's address, the norms' lengths (-1: none); the
         # device that the tensors are on
-        self.args = (ctypes.addressof(r), -1 if q_norm is None else q_norm.numel(),
-                     -1 if k_norm is None else k_norm.numel())
+        self._args = (ctypes.addressof(r), -1 if q_norm is None else q_norm.numel(),
+                      -1 if k_norm is None else k_norm.numel())
         held = [t for t in (table, q_norm, k_norm) if t is not None]
         self.device = held[0].get_device() if held else -1
+
+    # read-only: a tensor put in their place would leave the struct with the address of
+    # one that is gone
+    table = property(lambda self: self._tensors[0])
+    q_norm = property(lambda self: self._tensors[1])
+    k_norm = property(lambda self: self._tensors[2])
 
     def struct(self) -> kvq.kvq_rotary:
         return self._struct
@@ -143,7 +150,7 @@ def norm_rope(rotary: Rotary, q: Optional[torch.Tensor], k: Optional[torch.Tenso
     if k is not None and k_out is None:
         k_out = _rows_like(k, k.dtype, stream)
     dev = _launch_device(rotary.device)
-    addr, nq, nk = rotary.args
+    addr, nq, nk = rotary._args
     st = (_call or _calls()).norm_rope(dev, kvq._stream(stream), addr, nq, nk,
                                        q, k, positions, q_out, k_out, q_out_type == "e4m3", q_scale,
                                        q_head_scale, error_flag)
@@ -276,7 +283,7 @@ class QuantizedKVCache:
         call = _call or _calls()
         call.block_table(dev, self.block_table, 0)   # (it may be another one than at the start)
         c = self.struct()
-        addr, nq, nk = rotary.args
+        addr, nq, nk = rotary._args
         st = call.rope_append(
             dev, kvq._stream(stream), ctypes.addressof(c),
             self.block_table.shape[0], addr, nq, nk, k_new, v_new, kpe_new, start_pos, new_lens, q,

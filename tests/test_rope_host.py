@@ -159,3 +159,19 @@ def test_error_flags_of_another_type_or_device_are_refused(flag):
     with pytest.raises(ValueError, match="error_flag"):
         call.decode_shared(0, None, ctypes.addressof(c), ctypes.addressof(p), 0, None, 1, None, None, None,
                            None, None, None, flag)
+
+
+def test_a_rotary_keeps_its_tensors(monkeypatch):
+    """Its struct holds their addresses: they cannot be replaced."""
+    monkeypatch.setattr(runtime, "_here", lambda *a: None)      # host tensors do here
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    table, w, v = torch.zeros(10, 64), torch.ones(64), torch.ones(64)
+    ro = runtime.Rotary(table, False, w, v)
+    for name, t in (("table", table), ("q_norm", w), ("k_norm", v)):
+        assert getattr(ro, name) is t
+        with pytest.raises(AttributeError):
+            setattr(ro, name, torch.zeros(20, 64))
+        with pytest.raises(AttributeError):
+            delattr(ro, name)
+    assert ro.struct().cos_sin == table.data_ptr() and ro.struct().q_norm == w.data_ptr()
+    assert runtime.Rotary(None).table is None
