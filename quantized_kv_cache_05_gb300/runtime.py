@@ -399,7 +399,8 @@ def prefill(cache: QuantizedKVCache, q: torch.Tensor, seq_lens: torch.Tensor, cf
 class SharedDecode:
     """Decode steps of a batch whose requests share their first prefix_len tokens
     (kvq_decode_shared): the configuration and its scratch, kept between steps.
-    Steps of one object must not overlap on the GPU (they share the scratch)."""
+    Steps of one object must not overlap on the GPU (they share the scratch).  What it
+    is made with stays as it is: another configuration needs an object of its own."""
 
     def __init__(self, cache: QuantizedKVCache, batch: int, num_q_heads: int, prefix_len: int,
                  max_kv_len: int, sm_scale: float, out: str = "bf16", out_scale: float = 1.0,
@@ -428,27 +429,36 @@ class SharedDecode:
             kvq.check(st, "kvq_shared_splits")
         else:
             sp, so = splits
-        self.cache, self.prefix_len, self.prefix_table, self.prefix_splits = (
-            cache, prefix_len, prefix_table, sp)
-        cfg = self.cfg = DecodeConfig(batch, num_q_heads, cache.D, cache.D, so, max_kv_len, sm_scale,
+        self._cache, self._prefix = cache, (prefix_len, prefix_table, sp)
+        cfg = self._cfg = DecodeConfig(batch, num_q_heads, cache.D, cache.D, so, max_kv_len, sm_scale,
                                       out=out, out_scale=out_scale, q_fp8=q_fp8, q_scale=q_scale,
                                       q_head_scale=_head_scale(q_head_scale, num_q_heads),
                                       prefix_p_f16=prefix_p_f16)
-        self.ws = FusedWorkspace(dataclasses.replace(cfg, num_splits=so + sp), cache.Hkv, device)
+        self._ws = FusedWorkspace(dataclasses.replace(cfg, num_splits=so + sp), cache.Hkv, device)
         self._params = cfg.params(None)   # the lengths and the flag come with each step
+
+    # read-only, and the configuration as a copy: the parameters and the scratch were
+    # made for these
+    cache = property(lambda self: self._cache)
+    prefix_len = property(lambda self: self._prefix[0])
+    prefix_table = property(lambda self: self._prefix[1])
+    prefix_splits = property(lambda self: self._prefix[2])
+    ws = property(lambda self: self._ws)
+    cfg = property(lambda self: dataclasses.replace(self._cfg))
 
     def __call__(self, q: torch.Tensor, seq_lens: torch.Tensor,
                  error_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """q bf16 (FP8 query: uint8) [batch][Hq][D], seq_lens int32 [batch] (whole lengths)
         -> the output buffer [batch][Hq][D], overwritten by the next step."""
-        ws = self.ws
-        dev = _launch_device(self.cache.k_codes.get_device())
+        ws, cache = self._ws, self._cache
+        prefix_len, prefix_table, prefix_splits = self._prefix
+        dev = _launch_device(cache.k_codes.get_device())
         call = _call or _calls()
-        call.block_table(dev, self.cache.block_table, self.cfg.batch)   # (as in append_rope)
-        c = self.cache.struct()
+        call.block_table(dev, cache.block_table, self._cfg.batch)   # (as in append_rope)
+        c = cache.struct()
         st = call.decode_shared(
             dev, kvq._stream(stream), ctypes.addressof(c),
-            ctypes.addressof(self._params), self.prefix_len, self.prefix_table, self.prefix_splits, q,
+            ctypes.addressof(self._params), prefix_len, prefix_table, prefix_splits, q,
             seq_lens, ws.part_o, ws.part_lse, ws.counters, ws.out, error_flag)
         if st:
             kvq.check(st, "kvq_decode_shared")

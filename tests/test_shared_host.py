@@ -1,6 +1,7 @@
 """kvq_decode_shared and kvq_shared_splits on the host: refusals before any CUDA
 call (the addresses are never touched) and the split rule."""
 import math
+import weakref
 
 import pytest
 import torch
@@ -108,3 +109,21 @@ def test_block_table_of_a_call():
     assert c.struct().max_pages_per_seq == 4
     c.block_table = t[:, :2].contiguous()         # a narrower table: its own width
     assert c.max_pages_per_seq == 2 and c.struct().max_pages_per_seq == 2
+
+
+def test_a_shared_decode_keeps_what_it_is_made_with(monkeypatch):
+    """Its parameters hold addresses, its scratch a size: neither can be replaced."""
+    monkeypatch.setattr(runtime, "_here", lambda *a: None)      # host tensors do here
+    c = runtime.QuantizedKVCache("fp8", 8, 16, 2, 64, torch.zeros(3, 4, dtype=torch.int32), 1.0, 1.0,
+                                 device="cpu")
+    scale, table = torch.ones(4), torch.zeros(2, dtype=torch.int32)
+    plan = runtime.SharedDecode(c, 3, 4, 32, 64, 0.1, q_fp8=True, q_head_scale=scale, prefix_table=table,
+                                splits=(1, 1))
+    assert plan.cache is c and plan.prefix_table is table and plan.prefix_len == 32
+    for name in ("cache", "prefix_len", "prefix_table", "prefix_splits", "ws", "cfg"):
+        with pytest.raises(AttributeError):
+            setattr(plan, name, getattr(plan, name))
+    address, kept = scale.data_ptr(), weakref.ref(scale)
+    plan.cfg.q_head_scale = None                                # a copy's
+    del scale
+    assert kept() is plan.cfg.q_head_scale and plan._params.q_head_scale == address
