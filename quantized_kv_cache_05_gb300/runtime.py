@@ -429,6 +429,7 @@ class SharedDecode:
             kvq.check(st, "kvq_shared_splits")
         else:
             sp, so = splits
+            _check(sp >= 1 and so >= 1, "splits: at least one of the prefix and one of the own tokens")
         self._cache, self._prefix = cache, (prefix_len, prefix_table, sp)
         cfg = self._cfg = DecodeConfig(batch, num_q_heads, cache.D, cache.D, so, max_kv_len, sm_scale,
                                       out=out, out_scale=out_scale, q_fp8=q_fp8, q_scale=q_scale,

@@ -127,3 +127,18 @@ def test_a_shared_decode_keeps_what_it_is_made_with(monkeypatch):
     plan.cfg.q_head_scale = None                                # a copy's
     del scale
     assert kept() is plan.cfg.q_head_scale and plan._params.q_head_scale == address
+
+
+def host_cache(rows=3, **kw):
+    """A cache in host memory, for what is refused before any CUDA call."""
+    args = dict(fmt="fp8", num_pages=8, page_size=16, num_kv_heads=2, head_dim=64, k_scale=1.0, v_scale=1.0,
+                block_table=torch.zeros(rows, 4, dtype=torch.int32), device="cpu")
+    return runtime.QuantizedKVCache(**{**args, **kw})
+
+
+@pytest.mark.parametrize("splits", [(0, 1), (1, 0), (-1, 8), (8, -1), (-7, 8)])
+@pytest.mark.parametrize("prefix", [0, 32])
+def test_splits_below_one_are_refused(splits, prefix):
+    """The scratch holds the sum of both: one below zero would make it too small."""
+    with pytest.raises(ValueError, match="splits"):
+        runtime.SharedDecode(host_cache(), 3, 4, prefix, 64, 0.1, splits=splits)
