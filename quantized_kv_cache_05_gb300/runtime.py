@@ -129,9 +129,16 @@ def _query_out(q: torch.Tensor, out: Optional[torch.Tensor], kind: str, stream) 
     return out
 
 
-def _head_scale(t: Optional[torch.Tensor], heads: int) -> Optional[torch.Tensor]:
+def _with(t: torch.Tensor, dtype: torch.dtype, device: torch.device, what: str) -> None:
+    """A tensor of this type on the device of the object that keeps it."""
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{what}: expected {dtype} on {device}, got {t.dtype} on {t.device}")
+
+
+def _head_scale(t: Optional[torch.Tensor], heads: int,
+                device: torch.device) -> Optional[torch.Tensor]:
     if t is not None:
-        _here(t, torch.float32, "q_head_scale")
+        _with(t, torch.float32, device, "q_head_scale")
         _check(t.numel() == heads and t.is_contiguous(), "q_head_scale: one scale per query head")
     return t
 
@@ -417,7 +424,7 @@ class SharedDecode:
         _check(num_q_heads % cache.Hkv == 0, "num_q_heads: a multiple of the kv heads")
         device = cache.k_codes.device
         if prefix_table is not None:
-            _here(prefix_table, torch.int32, "prefix_table")
+            _with(prefix_table, torch.int32, device, "prefix_table")
             _check(prefix_table.is_contiguous() and
                    prefix_table.numel() * cache.page_size >= prefix_len,
                    "prefix_table: one page per page_size shared tokens")
@@ -433,7 +440,7 @@ class SharedDecode:
         self._cache, self._prefix = cache, (prefix_len, prefix_table, sp)
         cfg = self._cfg = DecodeConfig(batch, num_q_heads, cache.D, cache.D, so, max_kv_len, sm_scale,
                                       out=out, out_scale=out_scale, q_fp8=q_fp8, q_scale=q_scale,
-                                      q_head_scale=_head_scale(q_head_scale, num_q_heads),
+                                      q_head_scale=_head_scale(q_head_scale, num_q_heads, device),
                                       prefix_p_f16=prefix_p_f16)
         self._ws = FusedWorkspace(dataclasses.replace(cfg, num_splits=so + sp), cache.Hkv, device)
         self._params = cfg.params(None)   # the lengths and the flag come with each step

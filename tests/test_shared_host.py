@@ -142,3 +142,15 @@ def test_splits_below_one_are_refused(splits, prefix):
     """The scratch holds the sum of both: one below zero would make it too small."""
     with pytest.raises(ValueError, match="splits"):
         runtime.SharedDecode(host_cache(), 3, 4, prefix, 64, 0.1, splits=splits)
+
+
+def test_tensors_of_another_device_than_the_cache_are_refused():
+    """Whatever device is current when the object is made."""
+    c = host_cache()
+    away = [dict(prefix_table=torch.zeros(2, dtype=torch.int32, device="meta")),
+            dict(q_fp8=True, q_head_scale=torch.ones(4, device="meta"))]
+    for kw in away:
+        with pytest.raises(ValueError, match="expected .* on cpu"):
+            runtime.SharedDecode(c, 3, 4, 32, 64, 0.1, splits=(1, 1), **kw)
+    runtime.SharedDecode(c, 3, 4, 32, 64, 0.1, splits=(1, 1), q_fp8=True, q_head_scale=torch.ones(4),
+                         prefix_table=torch.zeros(2, dtype=torch.int32))
