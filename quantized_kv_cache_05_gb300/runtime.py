@@ -16,6 +16,7 @@ from . import kvq
 
 FMT = {"fp8": kvq.KVQ_FP8_E4M3, "nvfp4": kvq.KVQ_NVFP4}
 OUT = {"f32": kvq.KVQ_OUT_F32, "bf16": kvq.KVQ_OUT_BF16, "e4m3": kvq.KVQ_OUT_E4M3}
+MAX_SPLITS = 64   # partials of a row that a call joins (kvq_decode_params)
 OUT_TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.uint8}
 
 
@@ -416,8 +417,8 @@ class SharedDecode:
                  prefix_table: Optional[torch.Tensor] = None,
                  splits: Optional[tuple[int, int]] = None, prefix_p_f16: bool = False):
         """prefix_table: the shared pages (int32; default: the first entries of the first
-        request that is at least prefix_len long); splits: (prefix, own) chunks, by default kvq_shared_splits';
-        prefix_p_f16: the prefix's probabilities with 11 bits instead of 22, for bf16
+        request that is at least prefix_len long); splits: (prefix, own) chunks, by
+        default kvq_shared_splits'; prefix_p_f16: the prefix's probabilities with 11 bits instead of 22, for bf16
         outputs that need not be kvq_decode's to the last step."""
         _check(0 <= prefix_len <= max_kv_len, "prefix_len: expected 0 .. max_kv_len")
         _check(batch <= cache.block_table.shape[0], "more requests than the block table has")
@@ -437,11 +438,19 @@ class SharedDecode:
         else:
             sp, so = splits
             _check(sp >= 1 and so >= 1, "splits: at least one of the prefix and one of the own tokens")
+            if prefix_len > 0:   # as the call lowers them
+                sp = min(sp, (prefix_len + 127) // 128)
+                if sp + so > MAX_SPLITS:
+                    raise kvq.KvqError(kvq.KVQ_ERR_UNSUPPORTED, "SharedDecode: splits")
         self._cache, self._prefix = cache, (prefix_len, prefix_table, sp)
         cfg = self._cfg = DecodeConfig(batch, num_q_heads, cache.D, cache.D, so, max_kv_len, sm_scale,
                                       out=out, out_scale=out_scale, q_fp8=q_fp8, q_scale=q_scale,
                                       q_head_scale=_head_scale(q_head_scale, num_q_heads, device),
                                       prefix_p_f16=prefix_p_f16)
+        # the call's own checks, without requests: what no step could do is refused here
+        kvq.check(kvq.kvq_decode_shared(cache.struct(), dataclasses.replace(cfg, batch=0).params(None),
+                                        prefix_len, None, sp, None, None, None, None, None, 0),
+                  "SharedDecode")
         self._ws = FusedWorkspace(dataclasses.replace(cfg, num_splits=so + sp), cache.Hkv, device)
         self._params = cfg.params(None)   # the lengths and the flag come with each step
 

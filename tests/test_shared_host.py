@@ -154,3 +154,22 @@ def test_tensors_of_another_device_than_the_cache_are_refused():
             runtime.SharedDecode(c, 3, 4, 32, 64, 0.1, splits=(1, 1), **kw)
     runtime.SharedDecode(c, 3, 4, 32, 64, 0.1, splits=(1, 1), q_fp8=True, q_head_scale=torch.ones(4),
                          prefix_table=torch.zeros(2, dtype=torch.int32))
+
+
+def test_refused_at_the_making():
+    """What no step of the object could do raises before its scratch is made."""
+    def make(c, hq=4, prefix=32, cap=64, splits=(1, 1), **kw):
+        return runtime.SharedDecode(c, 3, hq, prefix, cap, 0.1, splits=splits, **kw)
+
+    mla = host_cache(fmt="nvfp4", num_kv_heads=1, head_dim=512, rope_dim=64)
+    wide = host_cache(fmt="nvfp4", head_dim=256)
+    for want, kw in ((UNS, dict(c=mla, hq=16)), (UNS, dict(c=wide)), (INV, dict(c=host_cache(), prefix=24)),
+                     (UNS, dict(c=host_cache(), hq=34)), (INV, dict(c=host_cache(), cap=80)),
+                     (UNS, dict(c=host_cache(), splits=(1, 64))), (UNS, dict(c=host_cache(), splits=(1, 65))),
+                     (INV, dict(c=host_cache(k_scale=0.0))), (INV, dict(c=host_cache(), q_fp8=True, q_scale=0.0)),
+                     (INV, dict(c=host_cache(), out="e4m3", out_scale=0.0))):
+        with pytest.raises(kvq.KvqError) as e:
+            make(**kw)
+        assert e.value.status == want, kw
+    # more prefix splits than tiles are lowered, and the scratch holds what is left
+    assert make(host_cache(), splits=(200, 63)).ws.part_lse.numel() == 3 * 4 * 64
