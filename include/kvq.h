@@ -403,8 +403,8 @@ kvq_status kvq_decode(const kvq_cache* c, const kvq_decode_params* p, const void
  *              length: tokens prefix_len .. seq_lens[b] - 1 are its own.  A
  *              request shorter than prefix_len (0 for a padded row) takes no
  *              part in the sharing and reads its own table only.
- *   prefix_len (host) a multiple of page_size, at most p->max_kv_len; 0 is
- *              kvq_decode.
+ *   prefix_len (host) a multiple of page_size, at most p->max_kv_len and
+ *              2^31 - 4097; 0 is kvq_decode.
  *   prefix_table (device int32, optional) [prefix_len / page_size] the shared
  *              pages; NULL: the first entries of the block table's row of the
  *              first request that is at least prefix_len long.

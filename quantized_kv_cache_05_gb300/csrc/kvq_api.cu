@@ -2,6 +2,7 @@
 // any launch), TMA descriptor setup and kernel dispatch.  Host code only.
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -716,6 +717,9 @@ kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int
   if (reinterpret_cast<uintptr_t>(part_o) & 31u) return KVQ_ERR_INVALID;
   if (p->num_q_heads % c->num_kv_heads != 0) return KVQ_ERR_INVALID;
   if (is_mla(c) || p->prob_scale > 0.f) return KVQ_ERR_UNSUPPORTED;
+  // token numbers are 32-bit, and each lane's (32 boxes of up to 128 tokens) is formed
+  // before it is compared
+  if (prefix_len > INT_MAX - 4096) return KVQ_ERR_UNSUPPORTED;
   const int D = c->head_dim;
   if (p->qk_dim != D || p->v_dim != D) return KVQ_ERR_INVALID;
   if (D != 64 && D != 128) return KVQ_ERR_UNSUPPORTED;

@@ -173,3 +173,11 @@ def test_refused_at_the_making():
         assert e.value.status == want, kw
     # more prefix splits than tiles are lowered, and the scratch holds what is left
     assert make(host_cache(), splits=(200, 63)).ws.part_lse.numel() == 3 * 4 * 64
+
+
+def test_prefixes_next_to_2_to_the_31_are_refused():
+    """Token numbers past the prefix's last tile have to fit 32 bits."""
+    c = cache(max_pages_per_seq=1 << 27)
+    for prefix, want in ((2 ** 31 - 16, UNS), (2 ** 31 - 4096, UNS), (2 ** 31 - 4112, OK)):
+        p = params(batch=0 if want == OK else 4, max_kv_len=prefix)
+        assert call(c=c, p=p, prefix=prefix) == want
