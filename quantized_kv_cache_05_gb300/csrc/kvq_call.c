@@ -56,11 +56,10 @@ static int address(PyObject* t, void** out) {
 static int here(PyObject* t, PyObject* dtype, long dev, const char* what) {
   PyObject* d = PyObject_GetAttr(t, s_dtype);
   if (!d) return -1;
-  Py_DECREF(d);   /* the type object lives on */
-  if (d != dtype) {
-    PyErr_Format(PyExc_ValueError, "%s: expected %R, got %R", what, dtype, d);
-    return -1;
-  }
+  const int same = d == dtype;
+  if (!same) PyErr_Format(PyExc_ValueError, "%s: expected %R, got %R", what, dtype, d);
+  Py_DECREF(d);
+  if (!same) return -1;
   long long at;
   if (method_long(t, s_get_device, &at)) return -1;
   if (at != dev) {

@@ -2,6 +2,9 @@
 (the addresses here are never touched)."""
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -175,3 +178,28 @@ def test_a_rotary_keeps_its_tensors(monkeypatch):
             delattr(ro, name)
     assert ro.struct().cos_sin == table.data_ptr() and ro.struct().q_norm == w.data_ptr()
     assert runtime.Rotary(None).table is None
+
+
+def test_a_refused_type_is_named_while_it_lives():
+    """A type object that only the attribute's reader holds: it is still there when the
+    refusal names it (freed memory is overwritten under this allocator)."""
+    code = """
+from quantized_kv_cache_05_gb300 import runtime
+
+class Type:
+    def __repr__(self):
+        return "a type of its own"
+
+class Flag:
+    dtype = property(lambda self: Type())
+
+try:
+    runtime._calls().block_table(0, Flag(), 0)
+except ValueError as e:
+    assert "a type of its own" in str(e), e
+    print("refused")
+"""
+    r = subprocess.run([sys.executable, "-c", code], env={**os.environ, "PYTHONMALLOC": "debug"},
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "refused" in r.stdout, (r.returncode, r.stderr[-500:])
