@@ -434,3 +434,99 @@ def test_new_outputs_belong_to_the_stream_that_is_given(append):
     side.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------------------
+# chunks: more lanes than fill the GPU, so that a lane group walks several rows
+# of its token with the next row's loads in flight
+# ---------------------------------------------------------------------------
+
+def chunk_tokens(dim, heads, extra):
+    """Tokens just past the launcher's change of geometry (152 x 2048 lanes), an odd count."""
+    return (152 * 2048 // (dim // 16) // heads + extra) | 1
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("dim,rot,inter,norm,hq,hk", [
+    (64, 64, False, True, 10, 3), (64, 32, True, False, 7, 2), (128, 128, True, True, 10, 3),
+    (128, 64, False, False, 72, 9), (256, 256, False, True, 10, 3), (256, 96, True, False, 5, 2)])
+def test_norm_rope_chunk(dim, rot, inter, norm, hq, hk, q8):
+    T = chunk_tokens(dim, hq + hk, 40)
+    assert T * (dim // 16) * (hq + hk) >= 152 * 2048
+    x = rand((T, (hq + hk) * dim), 7 * dim + rot + q8)
+    q, k = x[:, :hq * dim].unflatten(1, (hq, dim)), x[:, hq * dim:].unflatten(1, (hk, dim))
+    ro = make_rotary(dim, rot, inter, norm)
+    pos = torch.randint(0, 700, (T,), generator=gen(6), device=DEV).int()
+    pos[3::17] = -1      # padding among the tokens
+    fill = torch.uint8 if q8 else torch.bfloat16
+    qo, ko = (torch.full((T, h, dim), 3, device=DEV, dtype=t) for h, t in ((hq, fill), (hk, torch.bfloat16)))
+    runtime.norm_rope(ro, q, k, pos, q_out=qo, k_out=ko, q_out_type="e4m3" if q8 else "bf16", q_scale=0.021)
+    live = pos >= 0
+    assert (qo[~live] == 3).all() and (ko[~live] == 3).all()
+    p = pos[live].cpu().numpy()
+    R.check_bf16(f64(ko[live]), *reference(k[live], ro.k_norm, p, ro, dim), "k")
+    y = reference(q[live], ro.q_norm, p, ro, dim)
+    if q8:
+        R.check_grid(R.e4m3_values(qo[live].cpu().numpy()), *y, np.float64(np.float32(0.021)), R.E4M3_POS, "q8")
+    else:
+        R.check_bf16(f64(qo[live]), *y, "q")
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("dim,rot,inter,norm,hq,hkv,q8,hs", [
+    (64, 64, False, True, 7, 3, False, False), (64, 32, True, False, 7, 3, True, True),
+    (128, 128, True, True, 7, 3, False, True), (128, 64, False, False, 55, 5, True, False),
+    (256, 96, False, True, 7, 3, True, False), (256, 256, True, False, 0, 1, False, False)])
+def test_append_chunk(fmt, dim, rot, inter, norm, hq, hkv, q8, hs):
+    B, ps = 5, 48
+    H = hq + 2 * hkv
+    T = chunk_tokens(dim, H, 3) // B + 2
+    assert B * T * (dim // 16) * H >= 152 * 2048
+    per = (T + 90) // ps + 1
+    cache = make_cache(fmt, B, per, ps, hkv, dim, 3, hs)
+    plain = make_cache(fmt, B, per, ps, hkv, dim, 3, hs)
+    ro = make_rotary(dim, rot, inter, norm, rows=T + 100)
+    x = rand((B, T, H * dim), dim + T)
+    cut = lambda a, n: x[..., a * dim:(a + n) * dim].unflatten(2, (n, dim))
+    k, v = cut(hq, hkv), cut(hq + hkv, hkv)
+    q = cut(0, hq) if hq else None
+    start = torch.randint(0, 90, (B,), generator=gen(9), device=DEV).int()
+    lens = torch.tensor([T, 0, T - 1, T // 3, 1], device=DEV).int()
+    old = {n: getattr(cache, n).clone() for n in ("k_codes", "v_codes", "k_bscale", "v_bscale")
+           if getattr(cache, n) is not None}
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    qo = torch.full((B, T, hq, dim), 3, device=DEV, dtype=torch.uint8 if q8 else torch.bfloat16) if hq else None
+    cache.append_rope(ro, k, v, start, new_lens=lens, q=q, q_out=qo, q_scale=0.019, error_flag=flag)
+    plain.append(k.contiguous(), v.contiguous(), start)
+    torch.cuda.synchronize()
+    assert int(flag) == 0
+    kg = f64(cache.k_head_scale)[None, :, None] if hs else np.float64(np.float32(0.0213))
+    for b in range(B):
+        n = int(lens[b])
+        pos = int(start[b]) + torch.arange(n, device=DEV)
+        p = pos.cpu().numpy()
+        for name in ("v_codes", "v_bscale"):
+            if name in old:
+                assert torch.equal(rows_of(cache, getattr(cache, name), pos, b),
+                                   rows_of(plain, getattr(plain, name), pos, b)), name
+        if n:
+            yk = reference(k[b, :n], ro.k_norm, p, ro, dim)
+            codes = rows_of(cache, cache.k_codes, pos, b).cpu().numpy()
+            if fmt == "fp8":
+                R.check_grid(R.e4m3_values(codes), *yk, kg, R.E4M3_POS, "K")
+            else:
+                R.check_nvfp4(codes, rows_of(cache, cache.k_bscale, pos, b).cpu().numpy(), *yk, kg, "K")
+        if hq:
+            if n:
+                yq = reference(q[b, :n], ro.q_norm, p, ro, dim)
+                if q8:
+                    R.check_grid(R.e4m3_values(qo[b, :n].cpu().numpy()), *yq, np.float64(np.float32(0.019)),
+                                 R.E4M3_POS, "q")
+                else:
+                    R.check_bf16(f64(qo[b, :n]), *yq, "q")
+            assert (qo[b, n:] == 3).all()
+        rest = torch.ones(per * ps, dtype=torch.bool, device=DEV)
+        rest[pos] = False
+        at = rest.nonzero()[:, 0]
+        for name, t in old.items():
+            assert torch.equal(rows_of(cache, getattr(cache, name), at, b), rows_of(cache, t, at, b)), name
