@@ -419,8 +419,10 @@ kvq_status kvq_decode(const kvq_cache* c, const kvq_decode_params* p, const void
  * cores over 128 rows, and kvq_decode reads a prefix that only one or two
  * requests share (or that is shorter than what each adds) in less time.
  * fresh_tokens is taken as 0 where prefix_len is positive.  The prefix's
- * probabilities keep 22 bits in the products with V, as kvq_decode's do, or 11
- * where p->prefix_p_f16 asks for that.
+ * probabilities enter the products with V in two f16 parts, as kvq_decode's do, or
+ * in one where p->prefix_p_f16 asks for that: each off by at most 2^-22 (2^-11) of
+ * itself, or by 2^-32 of the row's largest one where that is more, so that a token
+ * below 2^-32 of the largest counts in the sum alone.
  * Two or three launches on `stream` (three where not all own chunks fit on the
  * SMs beside the prefix); calls that share partials or counters must not
  * overlap on the GPU.

@@ -418,8 +418,8 @@ class SharedDecode:
                  splits: Optional[tuple[int, int]] = None, prefix_p_f16: bool = False):
         """prefix_table: the shared pages (int32; default: the first entries of the first
         request that is at least prefix_len long); splits: (prefix, own) chunks, by
-        default kvq_shared_splits'; prefix_p_f16: the prefix's probabilities with 11 bits instead of 22, for bf16
-        outputs that need not be kvq_decode's to the last step."""
+        default kvq_shared_splits'; prefix_p_f16: the prefix's probabilities with 11 bits
+        instead of 22, for bf16 outputs that need not be kvq_decode's to the last step."""
         _check(0 <= prefix_len <= max_kv_len, "prefix_len: expected 0 .. max_kv_len")
         _check(batch <= cache.block_table.shape[0], "more requests than the block table has")
         _check(num_q_heads % cache.Hkv == 0, "num_q_heads: a multiple of the kv heads")

@@ -634,3 +634,30 @@ def test_block_tables_put_in_later():
         if error is ValueError:
             with pytest.raises(ValueError):
                 B.cache.append_rope(runtime.Rotary(None), x, x, B.lens_t)
+
+
+@pytest.mark.parametrize("gap", [12.0, 16.0, 19.0, 23.0])
+@pytest.mark.parametrize("out", ["f32", "bf16", "e4m3"])
+def test_a_long_flat_tail_behind_one_large_weight(gap, out):
+    """One token far above 32767 equal ones, all in one split.  Bound: an absolute
+    2^-32 of the largest weight for each token (the residual's step), 2048 steps of
+    16 tokens that each add at most 2^-23 of the accumulator, and the exponents'."""
+    B = Batch("fp8", 64, 2, 1, 128, 32768, [0, 0, 0], 3)
+    q, k_scale = 1.0, float(np.float32(0.0137))
+    B.q = torch.full_like(B.q, q)
+    B.q64 = B.q.double()
+    # scores: 64 dims of q k: the codes 0.5 everywhere and 8 at the large token
+    B.codes[0].copy_(torch.tensor(0.5).to(torch.float8_e4m3fn).view(torch.uint8).to(DEV))
+    first = int(B.shared_pages[0])
+    B.codes[0][first, :, 5] = torch.tensor(8.0).to(torch.float8_e4m3fn).view(torch.uint8).to(DEV)
+    B.codes[1].copy_(B.codes[1] & 0x7F)    # values of one sign: the tail adds up
+    B.val = [c.view(torch.float8_e4m3fn).double() * float(np.float32(s)) for c, s in zip(B.codes, (0.0137, 0.0119))]
+    B.sm = gap / (64 * q * 7.5 * k_scale)
+    o, tol, mag = B.reference()
+    vmax = float(B.val[1].abs().max())
+    ref = (o, tol + 2.0 ** -12 * mag + 2.0 ** -32 * B.prefix * vmax, mag)
+    o1 = run(B, out, (1, 1))
+    if out == "f32":
+        assert (np.abs(o1.double().cpu().numpy() - o) <= ref[1]).all()
+    else:
+        check_rounded(B, o1, out, ref)
