@@ -239,7 +239,7 @@ kvq_status kvq_quantize_append(const kvq_cache* c, const void* k_new, const void
  *             (interleaved = 1), i < rot_dim/2; the rest passes unrotated.
  * All of it runs in fp32 on the bf16 input; a result is rounded once, to its
  * output type.  E4M3 codes whose fp32 quotient lies within 16 steps of a
- * rounding boundary are decided with 48 bits (values that neither norm nor
+ * rounding boundary are decided with some 48 bits, 43 where a norm is given (values that neither norm nor
  * rotation changes keep kvq_quantize_fp8's quotient).  A row's sum of squares
  * has to stay in the range of fp32.
  */
