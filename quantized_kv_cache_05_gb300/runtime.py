@@ -3,6 +3,13 @@ torch tensors, and one decode step (partial + combine).
 
 Marshalling only -- torch allocates memory and supplies streams; every
 computation is a libkvq.so kernel.  Nothing here falls back to torch math.
+
+A call's ``stream`` (default: the current one) is where its kernels run, and nothing
+more: what another stream still writes of the inputs, the cache or the scratch has to
+be waited for first (``wait_stream``), and a tensor of another stream's memory has to
+be kept, or marked with ``record_stream``, until the given one is done with it.  That
+holds for the scratch too, which its object zeroes on the stream that is current when
+it is made.
 """
 from __future__ import annotations
 
@@ -152,7 +159,7 @@ def norm_rope(rotary: Rotary, q: Optional[torch.Tensor], k: Optional[torch.Tenso
     """Norm and rotation of queries and keys (kvq_norm_rope): q bf16 [T][Hq][D] and k
     bf16 [T][Hk][D], positions int32 [T].  Returns (q_out, k_out): new tensors, or the
     given ones (bf16 outputs may be the inputs).  q_out_type "e4m3": uint8 codes.
-    New tensors belong to the stream that is given."""
+    New tensors belong to the stream that is given; inputs do not (see the top)."""
     if q is not None:
         q_out = _query_out(q, q_out, q_out_type, stream)
     if k is not None and k_out is None:
@@ -281,7 +288,8 @@ class QuantizedKVCache:
         them strided as a packed projection's slices are; start_pos int32 [B]; new_lens
         int32 [B] or None (all T).  MLA: k_new the latents [B][T][1][512], kpe_new
         [B][T][1][64].  Returns q_out (q_out_type "bf16", or "e4m3": uint8 codes; by
-        default q_out's own type, bf16 without one)."""
+        default q_out's own type, bf16 without one).  On a given stream: the result belongs
+        to it, the inputs do not (see the top)."""
         fp8 = False
         if q is not None:
             kind = q_out_type or ("e4m3" if q_out is not None and q_out.dtype == torch.uint8 else "bf16")
@@ -466,7 +474,8 @@ class SharedDecode:
     def __call__(self, q: torch.Tensor, seq_lens: torch.Tensor,
                  error_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """q bf16 (FP8 query: uint8) [batch][Hq][D], seq_lens int32 [batch] (whole lengths)
-        -> the output buffer [batch][Hq][D], overwritten by the next step."""
+        -> the output buffer [batch][Hq][D], overwritten by the next step.  On a given
+        stream: ordered behind the object's making and kept as said at the top."""
         ws, cache = self._ws, self._cache
         prefix_len, prefix_table, prefix_splits = self._prefix
         dev = _launch_device(cache.k_codes.get_device())
