@@ -530,3 +530,39 @@ def test_append_chunk(fmt, dim, rot, inter, norm, hq, hkv, q8, hs):
         at = rest.nonzero()[:, 0]
         for name, t in old.items():
             assert torch.equal(rows_of(cache, getattr(cache, name), at, b), rows_of(cache, t, at, b)), name
+
+
+@pytest.mark.parametrize("kind", ["fp8", "nvfp4", "mla"])
+def test_append_in_the_plain_ones_place_before_an_overlapping_decode(kind):
+    """Without queries the call stands where kvq_quantize_append does in the contract of
+    fresh_tokens: the decode right behind it starts early and still reads the new rows
+    (other ones at every step), bit for bit what it reads after a wait."""
+    B, T, ps, per = 24, 3, 16, 40
+    mla = kind == "mla"
+    hq, hkv, D, qk = (16, 1, 512, 576) if mla else (8, 2, 128, 128)
+    cache = make_cache("fp8" if kind == "fp8" else "nvfp4", B, per, ps, hkv, D, 3, rope=64 if mla else 0)
+    ro = runtime.Rotary(runtime.rope_table(700, 64), False, None, weights(D, 1), EPS)
+    start = torch.tensor([(37 * b) % 600 if b % 3 else b % 13 for b in range(B)], device=DEV).int()
+    lens = start + T
+    q = rand((B, hq, qk), 5)
+    new = [(rand((B, T, hkv, D), 10 + k, 1 + k), None if mla else rand((B, T, hkv, D), 20 + k),
+            rand((B, T, 1, 64), 30 + k) if mla else None) for k in range(3)]
+    for splits in (1, 4):
+        cfg = runtime.DecodeConfig(B, hq, qk, D, splits, per * ps, qk ** -0.5, out="f32")
+        ws = runtime.FusedWorkspace(cfg, hkv)
+        want = []
+        for k, v, e in new:
+            cache.append_rope(ro, k, v, start, kpe_new=e)
+            torch.cuda.synchronize()
+            want.append(runtime.decode_fused(cache, q, lens, cfg, ws).clone())
+            torch.cuda.synchronize()
+        assert not torch.equal(want[0], want[1])
+        cfg.fresh_tokens = T
+        got = []
+        for i in range(30):
+            k, v, e = new[i % 3]
+            cache.append_rope(ro, k, v, start, kpe_new=e)
+            got.append(runtime.decode_fused(cache, q, lens, cfg, ws).clone())
+        torch.cuda.synchronize()
+        for i, g in enumerate(got):
+            assert torch.equal(g, want[i % 3]), i

@@ -661,3 +661,13 @@ def test_a_long_flat_tail_behind_one_large_weight(gap, out):
         assert (np.abs(o1.double().cpu().numpy() - o) <= ref[1]).all()
     else:
         check_rounded(B, o1, out, ref)
+
+
+@pytest.mark.parametrize("out", ["bf16", "e4m3"])
+def test_the_rounded_bound_tells_one_part_from_two(out):
+    """What check_rounded has to see: the same call with one f16 part fails it."""
+    B = Batch("fp8", 64, 16, 2, 16, 656, [(5 * b) % 7 for b in range(40)], 11, q_std=4.0)
+    ref = B.reference()
+    check_rounded(B, run(B, out), out, ref)
+    with pytest.raises(AssertionError):
+        check_rounded(B, run(B, out, prefix_p_f16=True), out, ref)
