@@ -178,7 +178,7 @@ typedef struct kvq_decode_params {
    * probabilities enter the products with V in two f16 parts, as kvq_decode's
    * do.  1: in one, rounded by up to 2^-11 of a weight where kvq_decode keeps
    * 2^-22; a bf16 output, whose own rounding is 2^-8, then differs here and
-   * there by one step, and the products take half the tensor-core time.
+   * there by one step, and the products with V take half the tensor-core time.
    */
   int32_t prefix_p_f16;
 } kvq_decode_params;

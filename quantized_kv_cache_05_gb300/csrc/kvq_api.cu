@@ -527,9 +527,10 @@ kvq_status kvq_shared_splits(int num_sms, int batch, int num_kv_heads, int q_per
   // is taken as the mean), two CTAs on each SM that the prefix leaves free,
   // and the rest when it is done.  Merging adds kMerge per partial of a row
   // (where own chunks merge in place, more with the q_per_kv rows that a CTA
-  // merges, from four on: 96 requests x 8k with 16 rows each take 31.2 us with
-  // 16 splits merged in place, 27.0 with 18 and the merging launch), and a
-  // launch of its own kMergeLaunch where not all own chunks fit beside the prefix.
+  // merges, from four on: 96 requests x 8k with 16 rows each, probabilities in one
+  // part, take 31.2 us with 16 splits merged in place, 27.0 with 18 and the merging
+  // launch), and a launch of its own kMergeLaunch where not all own chunks fit
+  // beside the prefix.
   constexpr double kTile = 2.2, kFixed = 6, kTile1 = 1.5, kFixed1 = 5.5;
   constexpr double kOwn = 5, kOwnToken = 0.01, kMerge = 0.12, kMergeLaunch = 4;
   const bool wide = (long long)batch * q_per_kv > 128;

@@ -33,21 +33,22 @@
 // counts, 2^-32 of the row's largest weight for each token (a weight below that
 // is in the sum and not in the products).  A caller that asks for it gets one
 // part: 2^-11 of a weight from 2^-21 of the reference on, the same 2^-32 below
-// (64 requests x 32k tokens, FP8: 57.1 us a call against 65.6 with two; NVFP4, 48 x
-// 16k: 36.5 against 39.9; 4 x 1k: 10.6 against 11.6).  Sums and accumulators are
+// (64 requests x 32k tokens, FP8: 60.2 us against 66.7 with two; NVFP4, 48 x 16k:
+// 36.6 against 41.2; 4 x 1k: 11.1 against 12.2).  Sums and accumulators are
 // fp32.
 // Every wait is bounded; a timeout sets an error bit and the partials become
 // NaN.
 //
-// What bounds it (FP8, head_dim 128, 256 rows x 8 heads over 32768 tokens in 11
-// splits: 88 CTAs): clock stamps in the kernel show a 128-token tile of both row
-// tiles every 3300 to 3500 cycles, for which the products need 2048 (2 x 2 of
-// 128^3); the rest is the chain scores -> maximum -> exponentials -> P V as far
-// as the other slot does not cover it.  Some 10000 cycles pass before the first
-// scores, most of them until the queries have come, and 8000 from the last
-// tile to the end (128 KB of partials per CTA), of 98000.  The kernel alone:
-// 52.7 us, its SMs' tensor pipes active 51% of the time.  Measured slower:
-// clusters that merge eight splits through distributed shared memory (4 requests
+// What bounds it (FP8, head_dim 128, 256 rows x 8 heads over 32768 tokens in 12
+// splits: 96 CTAs): a 128-token tile of both row tiles takes 2.2 us (the slope of
+// the time from 4 to 8 splits), for which the products need 3072 cycles (2 x 3 of
+// 128^3: 1.5 us at 2070 MHz); the rest is the chain scores -> maximum ->
+// exponentials -> P V as far as the other slot does not cover it.  The kernel
+// alone: 61.1 us, its SMs' tensor pipes active 60% of the time.  With one part and
+// 11 splits clock stamps showed a tile every 3300 to 3500 cycles against 2048 of
+// products, some 10000 cycles before the first scores, most of them until the
+// queries have come, and 8000 from the last tile to the end (128 KB of partials per
+// CTA), of 98000.  Measured slower (with one part): clusters that merge eight splits through distributed shared memory (4 requests
 // x 1k: +4 us), the partials staged for bulk stores (64 x 32k: +0.8 us), P handed
 // over whole (+0.1 to 0.4 us).
 
@@ -256,10 +257,10 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   // the operand tile that their f16 values take, piece c of a row there, FP8
   // codes at 2c (they widen to 2c and 2c + 1); consecutive lanes copy
   // consecutive pieces, and rows past the last are zeros (64 requests x 32k
-  // tokens, 256 rows: 57.1 us against 59.0 with a row per thread, whose loads
-  // touch 32 lines each).  One row tile: a row per thread in registers, which
-  // is less code for the few rows (4 requests x 1k: 10.2 us against 10.9
-  // staged).  (Plain copies and loads: queries may lie in pinned host memory.)
+  // tokens, 256 rows, P in one part: 57.1 us against 59.0 with a row per thread,
+  // whose loads touch 32 lines each).  One row tile: a row per thread in registers,
+  // which is less code for the few rows (4 requests x 1k, one part: 10.2 us against
+  // 10.9 staged).  (Plain copies and loads: queries may lie in pinned host memory.)
   const uint32_t qtile = base + (MT == 2 ? slot * Sg::kTile : 0);
   auto q_at = [&](int trow, int piece) -> uint32_t {
     return qtile + (piece >> 3) * kCol + (trow >> 3) * 1024 + (trow & 7) * 128 +
@@ -725,8 +726,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 // warp per row: every partial is one coalesced read, eight in flight per lane.
 constexpr int kMergeWarps = 8;
 
-// 64 x 32 rows of 12 partials (13 MB): 8.5 to 9.1 us with cold caches, 1.5 TB/s
-// and 14% of the issue slots: bound by the latency of its two rounds of reads.
+// 64 x 32 rows of 13 partials (14 MB): 9.2 us with cold caches, 1.5 TB/s and 12%
+// of the issue slots: bound by the latency of its two rounds of reads.
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_rows_kernel(const CombineArgs a) {
   constexpr int kPer = D / 32;   // dims per lane
@@ -798,8 +799,8 @@ cudaError_t with_kernel(int fmt, int D, int R, int wide_p, F&& f) {
     return wide_p ? pick(kfmt, kd, mt, std::true_type{}) : pick(kfmt, kd, mt, std::false_type{});
   };
   // Up to 128 rows one row tile with token tiles in both slots, else two row
-  // tiles (16 x 8k, 64 rows: 17.3 us against 21.2 with two; 64 x 32k, 256 rows:
-  // 57.8 against 70.0 with one).
+  // tiles (16 x 8k, 64 rows: 20.5 us against 25.3 with two; 64 x 32k, 256 rows:
+  // 67.3 against 83.7 with one).
   auto by_rows = [&](auto kfmt, auto kd) {
     return R > kTok ? by_p(kfmt, kd, std::integral_constant<int, 2>{})
                     : by_p(kfmt, kd, std::integral_constant<int, 1>{});
