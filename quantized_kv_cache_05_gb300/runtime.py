@@ -456,9 +456,11 @@ class SharedDecode:
                                       q_head_scale=_head_scale(q_head_scale, num_q_heads, device),
                                       prefix_p_f16=prefix_p_f16)
         # the call's own checks, without requests: what no step could do is refused here
-        kvq.check(kvq.kvq_decode_shared(cache.struct(), dataclasses.replace(cfg, batch=0).params(None),
-                                        prefix_len, None, sp, None, None, None, None, None, 0),
-                  "SharedDecode")
+        # (without any request a step does nothing)
+        if batch > 0:
+            none = dataclasses.replace(cfg, batch=0).params(None)
+            kvq.check(kvq.kvq_decode_shared(cache.struct(), none, prefix_len, None, sp, None, None, None,
+                                            None, None, 0), "SharedDecode")
         self._ws = FusedWorkspace(dataclasses.replace(cfg, num_splits=so + sp), cache.Hkv, device)
         self._params = cfg.params(None)   # the lengths and the flag come with each step
 

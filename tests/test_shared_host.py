@@ -181,3 +181,9 @@ def test_prefixes_next_to_2_to_the_31_are_refused():
     for prefix, want in ((2 ** 31 - 16, UNS), (2 ** 31 - 4096, UNS), (2 ** 31 - 4112, OK)):
         p = params(batch=0 if want == OK else 4, max_kv_len=prefix)
         assert call(c=c, p=p, prefix=prefix) == want
+
+
+def test_no_requests_and_an_empty_table():
+    """A step of no requests does nothing, so nothing of it is refused."""
+    plan = runtime.SharedDecode(host_cache(rows=0), 0, 4, 32, 64, 0.1, splits=(1, 1))
+    assert plan.ws.out.shape == (0, 4, 64)
