@@ -41,8 +41,8 @@
 //
 // What bounds it (FP8, head_dim 128, 256 rows x 8 heads over 32768 tokens in 12
 // splits: 96 CTAs): a 128-token tile of both row tiles takes 2.2 us (the slope of
-// the time from 4 to 8 splits), for which the products need 3072 cycles (2 x 3 of
-// 128^3: 1.5 us at 2070 MHz); the rest is the chain scores -> maximum ->
+// the time from 4 to 8 splits), for which the products (2 x 3 of 128^3) need 1.5
+// us at 2070 MHz; the rest is the chain scores -> maximum ->
 // exponentials -> P V as far as the other slot does not cover it.  The kernel
 // alone: 61.1 us, its SMs' tensor pipes active 60% of the time.  With one part and
 // 11 splits clock stamps showed a tile every 3300 to 3500 cycles against 2048 of
