@@ -42,15 +42,15 @@
 // What bounds it (FP8, head_dim 128, 256 rows x 8 heads over 32768 tokens in 12
 // splits: 96 CTAs): a 128-token tile of both row tiles takes 2.2 us (the slope of
 // the time from 4 to 8 splits), for which the products (2 x 3 of 128^3) need 1.5
-// us at 2070 MHz; the rest is the chain scores -> maximum ->
-// exponentials -> P V as far as the other slot does not cover it.  The kernel
-// alone: 61.1 us, its SMs' tensor pipes active 60% of the time.  With one part and
+// us at 2070 MHz; the rest is the chain scores -> maximum -> exponentials -> P V as
+// far as the other slot does not cover it.  The kernel alone: 61.1 us, its SMs'
+// tensor pipes active 60% of the time.  With one part and
 // 11 splits clock stamps showed a tile every 3300 to 3500 cycles against 2048 of
 // products, some 10000 cycles before the first scores, most of them until the
 // queries have come, and 8000 from the last tile to the end (128 KB of partials per
-// CTA), of 98000.  Measured slower (with one part): clusters that merge eight splits through distributed shared memory (4 requests
-// x 1k: +4 us), the partials staged for bulk stores (64 x 32k: +0.8 us), P handed
-// over whole (+0.1 to 0.4 us).
+// CTA), of 98000.  Measured slower (with one part): clusters that merge eight splits
+// through distributed shared memory (4 requests x 1k: +4 us), the partials staged
+// for bulk stores (64 x 32k: +0.8 us), P handed over whole (+0.1 to 0.4 us).
 
 #include <cfloat>
 #include <type_traits>
