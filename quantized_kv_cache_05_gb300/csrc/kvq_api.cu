@@ -122,7 +122,6 @@ kvq_status check_params(const kvq_decode_params* p) {
   if (p->fresh_tokens < 0) return KVQ_ERR_INVALID;
   if (p->q_fp8 != 0 && p->q_fp8 != 1) return KVQ_ERR_INVALID;
   if (p->q_fp8 && !p->q_head_scale && !finite_pos(p->q_scale)) return KVQ_ERR_INVALID;
-  if (p->prefix_p_f16 != 0 && p->prefix_p_f16 != 1) return KVQ_ERR_INVALID;
   return KVQ_OK;
 }
 
@@ -521,8 +520,8 @@ kvq_status kvq_shared_splits(int num_sms, int batch, int num_kv_heads, int q_per
     return KVQ_ERR_INVALID;
   // A model of the step in microseconds, from measurements on GB300 (FP8,
   // head_dim 128, probabilities in two parts; other formats, head dims and one
-  // part are taken for the same): the prefix's kernel runs one CTA per SM, kTile per token
-  // tile and kFixed around them (256-row tiles; 128-row ones kTile1, kFixed1);
+  // part are taken for the same): the prefix's kernel runs one CTA per SM, kTile
+  // per token tile and kFixed around them (256-row tiles; 128-row ones kTile1, kFixed1);
   // the requests' own chunks take kOwn + kOwnToken per token (half the longest
   // is taken as the mean), two CTAs on each SM that the prefix leaves free,
   // and the rest when it is done.  Merging adds kMerge per partial of a row
@@ -713,6 +712,7 @@ kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int
   if (prefix_len < 0 || prefix_len % c->page_size != 0 || prefix_len > p->max_kv_len)
     return KVQ_ERR_INVALID;
   if (prefix_len > 0 && prefix_splits < 1) return KVQ_ERR_INVALID;
+  if (p->prefix_p_f16 != 0 && p->prefix_p_f16 != 1) return KVQ_ERR_INVALID;
   if (p->batch > 0 && (!q || !aligned16(q) || !part_o || !part_lse || !counters || !out))
     return KVQ_ERR_INVALID;
   if (reinterpret_cast<uintptr_t>(part_o) & 31u) return KVQ_ERR_INVALID;

@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     len = live ? __ldg(a.seq_lens + b) : -1;
   }
   tc_fence_before();
-  if (warp != kTmaWarp && warp != kReadyWarp) asm volatile("bar.sync 3, %0;" ::"n"(kSharedThreads) : "memory");
+  if (warp != kTmaWarp && warp != kReadyWarp)
+    asm volatile("bar.sync 3, %0;" ::"n"(kSharedThreads) : "memory");
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   if (warp == kMmaWarp && tmem != 0) *abort_flag = 1;   // (never: all of it is ours)

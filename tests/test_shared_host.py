@@ -187,3 +187,10 @@ def test_no_requests_and_an_empty_table():
     """A step of no requests does nothing, so nothing of it is refused."""
     plan = runtime.SharedDecode(host_cache(rows=0), 0, 4, 32, 64, 0.1, splits=(1, 1))
     assert plan.ws.out.shape == (0, 4, 64)
+
+
+def test_prefix_p_f16_is_nothing_to_the_other_calls():
+    """They neither read nor check it."""
+    p = params(batch=0, prefix_p_f16=7)
+    assert kvq.kvq_decode(cache(), p, P, P, P, P, P, 0) == OK
+    assert kvq.kvq_decode_partial(cache(), p, P, P, P, 0) == OK
