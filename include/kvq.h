@@ -72,6 +72,8 @@ typedef int kvq_status;
                                        (kvq_rope_append: the token's rows are not written) */
 #define KVQ_DEVERR_BAD_POSITION 8   /* a position past the rotation table; its rows are
                                        not written */
+#define KVQ_DEVERR_REFUSED 16       /* kvq_plan_step: a request was not served */
+#define KVQ_DEVERR_BAD_POOL 32      /* kvq_plan_step: the free pages' count is out of range */
 
 /*
  * A paged quantized KV cache.  Caller-owned plain struct; the library only
@@ -322,6 +324,85 @@ kvq_status kvq_rope_append(const kvq_cache* c, const kvq_rotary* r, int batch, i
                            const float* q_head_scale, int32_t* error_flag, void* stream);
 
 /*
+ * A step's paging on the GPU: what the appends, kvq_chunk_attention and the
+ * decodes take -- block table, lengths, start positions, packed offsets, slots and
+ * positions of the new tokens -- from the requests' lengths and their changes.
+ *
+ * Request b holds seq_lens[b] tokens in the first ceil(length / page_size) pages of
+ * its block-table row.  add_lens[b] > 0 adds that many tokens; below zero takes the
+ * last ones off again (all of them where there are fewer), so INT32_MIN ends a
+ * request; 0 leaves it.  The free pages are a stack, free_pages[0 .. *free_count - 1]:
+ *  - first the pages that are no longer needed go on it, in the order of the
+ *    requests and, within one, of its block-table entries (those entries stay);
+ *  - then the requests that grow take theirs from its top in the same order, each
+ *    page into the next entry of the request's row.  A request is served whole or not
+ *    at all: where the pages are not all there, it and every later request that needs
+ *    a page get none; nor does one that would pass its block-table row, or whose
+ *    tokens would pass max_tokens.  Such a request keeps its length and sets
+ *    KVQ_DEVERR_REFUSED.
+ * Lengths outside [0, max_pages_per_seq page_size] are clamped (KVQ_DEVERR_SEQ_CLAMPED),
+ * a count outside [0, num_pages] too, and pages past num_pages that come back are
+ * dropped (both KVQ_DEVERR_BAD_POOL).
+ *
+ * Outputs (the last four may be NULL):
+ *   seq_lens_out   [batch] the new lengths (may be seq_lens)
+ *   free_count_out [1] the new count (may be free_count); free_pages at and above it
+ *                  holds what was popped
+ *   start_pos      [batch] the lengths before: where the new tokens go
+ *   q_offsets      [batch + 1] request b's new tokens are rows q_offsets[b] ..
+ *                  q_offsets[b + 1] - 1 of the packed step, whether it is served or
+ *                  not; at most max_tokens
+ *   slots          [max_tokens] of each new token, page * page_size + row; -1 for the
+ *                  tokens of refused requests and rows past the last token, and (with
+ *                  KVQ_DEVERR_BAD_PAGE) where the page is out of range
+ *   positions      [max_tokens] of each new token; -1 as above, except for bad pages
+ * counter is one word that is zero before the first call and left so.  No other two
+ * of these arrays may overlap.  All of it runs on the GPU, in one launch: a captured
+ * step replays with lengths that change.  batch <= 8192 (else KVQ_ERR_UNSUPPORTED).
+ * Calls that share the free pages or the counter must not overlap on the GPU.
+ */
+typedef struct kvq_page_plan {
+  int32_t batch;             /* >= 0 (0: nothing is written but the rows past the last token,
+                                the first offset and the count) */
+  int32_t page_size;         /* >= 1 */
+  int32_t num_pages;         /* >= 1, of the cache and of free_pages */
+  int32_t max_pages_per_seq; /* >= 1, with page_size below 2^31 tokens */
+  int32_t max_tokens;        /* >= 0, rows of the packed step */
+  int32_t* block_table;      /* (device) [batch][max_pages_per_seq], updated */
+  const int32_t* seq_lens;   /* (device) [batch] */
+  int32_t* seq_lens_out;     /* (device) [batch] */
+  const int32_t* add_lens;   /* (device) [batch] */
+  int32_t* free_pages;       /* (device) [num_pages], updated */
+  const int32_t* free_count; /* (device) [1] */
+  int32_t* free_count_out;   /* (device) [1] */
+  uint32_t* counter;         /* (device) [1] */
+  int32_t* start_pos;        /* (device, optional) */
+  int32_t* q_offsets;        /* (device, optional) */
+  int64_t* slots;            /* (device, optional) */
+  int32_t* positions;        /* (device, optional) */
+  int32_t* error_flag;       /* (device, optional) KVQ_DEVERR_* bits OR-ed in */
+} kvq_page_plan;
+
+kvq_status kvq_plan_step(const kvq_page_plan* p, void* stream);
+
+/*
+ * kvq_rope_append for a packed step: row t of k, v, kpe, q and q_out is a token of
+ * some request, at positions[t] (device int32; NULL where nothing is rotated), and its
+ * cache row is slots[t] (device int64): row slots[t] % page_size of page slots[t] /
+ * page_size.  The block table is not read.  Tokens at negative positions are skipped,
+ * as are those past the rotation table (KVQ_DEVERR_BAD_POSITION); a token with a
+ * negative slot, or with one past the cache (KVQ_DEVERR_BAD_PAGE), gets no cache row,
+ * but its q_out row is written.  No two tokens may share a slot.  All else is
+ * kvq_rope_append's, the codes too.
+ */
+kvq_status kvq_rope_append_slots(const kvq_cache* c, const kvq_rotary* r, int num_tokens,
+                                 const int32_t* positions, const int64_t* slots,
+                                 const kvq_heads* k, const kvq_heads* v, const kvq_heads* kpe,
+                                 const kvq_heads* q, const kvq_heads* q_out, int q_fp8,
+                                 float q_scale, const float* q_head_scale, int32_t* error_flag,
+                                 void* stream);
+
+/*
  * Split-count heuristic (host only, deterministic).  base = batch *
  * num_kv_heads (MLA: batch) CTAs per split; the partial kernel keeps
  * ctas_per_sm CTAs resident per SM (2: six-warp CTAs, or four-warp CTAs
@@ -447,6 +528,74 @@ kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int
 kvq_status kvq_shared_splits(int num_sms, int batch, int num_kv_heads, int q_per_kv,
                              int prefix_len, int max_own_len, int fmt,
                              int* prefix_splits /* host */, int* own_splits /* host */);
+
+/*
+ * Differential attention: the difference of two softmax maps.  A head of head_dim D
+ * has two queries and two keys of D / 2 elements, side by side in its row -- q = [q1
+ * q2], and in the cache k = [k1 k2] -- and values of D:
+ *   S1_i = sm_scale q1 . k1_i,  S2_i = sm_scale q2 . k2_i
+ *   o = sum_i softmax_i(S1) v_i - lambda[hq] sum_i softmax_i(S2) v_i
+ *   out = gain o                                             (norm NULL)
+ *   out = gain norm o / sqrt(sum_j o_j^2 / D + eps)          (elementwise)
+ * sm_scale is usually 1/sqrt(D / 2), and gain 1 - lambda_init.  Everything before the
+ * output's rounding is fp32; an o of zeros gives zeros, whatever eps.  The two sums of
+ * a request without tokens are zeros.
+ */
+typedef struct kvq_diff {
+  const float* lambda;       /* (device) [num_q_heads] */
+  const float* norm;         /* (device, optional) [head_dim], 16-byte aligned */
+  float eps;                 /* finite >= 0 (read where norm is given) */
+  float gain;                /* finite */
+} kvq_diff;
+
+/*
+ * kvq_decode with differential heads: a single token of each request, in one launch.
+ * As for kvq_decode, with these differences: q, out and num_q_heads count
+ * differential heads; part_o and part_lse hold two rows for each, so they are sized
+ * for 2 * num_q_heads heads; num_q_heads / num_kv_heads is at most 8 and prob_scale is
+ * 0 (else KVQ_ERR_UNSUPPORTED); not MLA.  kvq_auto_splits with twice the query heads
+ * per kv head picks num_splits.
+ */
+kvq_status kvq_decode_diff(const kvq_cache* c, const kvq_decode_params* p, const kvq_diff* d,
+                           const void* q, float* part_o, float* part_lse, uint32_t* counters,
+                           void* out, void* stream);
+
+/*
+ * Causal attention of a packed step over the cache: prompt chunks, single tokens and
+ * idle requests in any mixture.  Request b's new tokens are rows q_offsets[b] ..
+ * q_offsets[b + 1] - 1 of q and out (kvq_plan_step gives the offsets), and its
+ * seq_lens[b] = L tokens, the new ones among them, are in the cache: with n new ones,
+ * the i-th attends to tokens 0 .. L - n + i,
+ *   out[t][hq][:] = sum_j softmax_j(sm_scale q . k_j) v_j
+ * in p->out_dtype, or with d (optional) the differential attention above.  Tokens
+ * before position 0 (n > L) attend to nothing and give 0.  Rows of q and out past
+ * the last offset are neither read nor written.  Offsets are taken within [0,
+ * num_tokens] and lengths within the block table (KVQ_DEVERR_SEQ_CLAMPED); a pair of
+ * offsets that falls counts as no tokens, and no two requests may share a row.
+ *   q   (device) bf16, or E4M3 codes (p->q_fp8), [num_tokens][Hq][head_dim], 16-byte
+ *       aligned
+ *   out (device) [num_tokens][Hq][head_dim], 16-byte aligned
+ *   workspace (device) kvq_chunk_workspace_bytes of the device's SMs, p->batch and
+ *       head_dim, 32-byte aligned; nothing in it has to be kept or cleared between calls.
+ * Uses batch, num_q_heads, qk_dim = v_dim = head_dim, seq_lens, max_kv_len, sm_scale,
+ * out_dtype, out_scale, error_flag and the FP8 query of p (num_splits and fresh_tokens
+ * are ignored; prob_scale must be 0).  FP8 and NVFP4 caches with head_dim 64 or 128 and
+ * any number of query heads per kv head, per-head scales; not MLA, batch <= 8192.
+ * The work is cut by its size, over the keys too, so that all SMs get the same share of
+ * it, whatever the lengths; three launches on `stream`.
+ * The probabilities enter the products with V as f16 numbers: rounded to 2^-11 of
+ * themselves for bf16 and E4M3 outputs, in two parts (2^-22) for fp32 outputs and for
+ * differential heads; weights below 2^-32 of a row's largest count in the sum alone.
+ * A NaN among a token's keys or values reaches the rows that attend to it and no others;
+ * all dims of such a row may become NaN.
+ * Calls that share a workspace must not overlap on the GPU.
+ */
+kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_decode_params* p, const kvq_diff* d,
+                               int num_tokens, const int32_t* q_offsets, const void* q,
+                               void* workspace, size_t workspace_bytes, void* out, void* stream);
+
+/* Bytes of kvq_chunk_attention's workspace (0 for arguments below 1; batch 0 counts as 1). */
+size_t kvq_chunk_workspace_bytes(int num_sms, int batch, int head_dim);
 
 /*
  * Prefill attention over the cache (Model-Optimizer PR 1832: the prefill

@@ -125,6 +125,26 @@ kvq_status check_params(const kvq_decode_params* p) {
   return KVQ_OK;
 }
 
+kvq_status check_diff(const kvq_diff* d) {
+  if (!d || !d->lambda || !std::isfinite(d->gain)) return KVQ_ERR_INVALID;
+  if (d->norm && (!aligned16(d->norm) || !(std::isfinite(d->eps) && d->eps >= 0.f)))
+    return KVQ_ERR_INVALID;
+  return KVQ_OK;
+}
+
+// Heads, dims and lengths of an attention call against the cache (not MLA); what
+// else its kernels need, the caller checks.
+kvq_status check_heads_of(const kvq_cache* c, const kvq_decode_params* p, bool wide) {
+  const int D = c->head_dim;
+  if (p->num_q_heads % c->num_kv_heads != 0 || p->qk_dim != D || p->v_dim != D)
+    return KVQ_ERR_INVALID;
+  if ((long long)p->max_kv_len > (long long)c->max_pages_per_seq * c->page_size)
+    return KVQ_ERR_INVALID;
+  if (D != 64 && D != 128 && !(wide && D == 256 && c->fmt == KVQ_NVFP4))
+    return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
 // Rows of heads, `tokens` of them: 16-byte loads need the base and the strides
 // aligned; outputs may not overlap themselves.
 kvq_status check_heads(const kvq_heads* h, int dim, long long tokens, bool out) {
@@ -190,7 +210,82 @@ long long shared_row_tiles(long long batch, int q_per_kv) {
   return rows > 128 ? (rows + 255) / 256 : 1;
 }
 
+// TMA boxes of a 128-token tile: the largest power of two up to it that divides the pages.
+int box_rows(int page_size) {
+  int box = 16;
+  while (box < 128 && page_size % (2 * box) == 0) box *= 2;
+  return box;
+}
+
 kvq_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
+
+// kvq_rope_append and kvq_rope_append_slots: `where` says where the tokens go.
+kvq_status rope_append(const kvq_cache* c, const kvq_rotary* r, long long tokens, const kvq_heads* k,
+                       const kvq_heads* v, const kvq_heads* kpe, const kvq_heads* q,
+                       const kvq_heads* q_out, int q_fp8, float q_scale, const float* q_head_scale,
+                       int32_t* error_flag, const RopeArgs& where, cudaStream_t stream) {
+  kvq_status s = check_cache(c);
+  if (s != KVQ_OK) return s;
+  if (tokens < 0) return KVQ_ERR_INVALID;
+  const bool mla = is_mla(c);
+  const int D = c->head_dim;
+  s = check_rotary(r, mla ? c->rope_dim : D);
+  if (s != KVQ_OK) return s;
+  if (mla) {
+    if (v || !kpe) return KVQ_ERR_INVALID;
+    if (D != 512 || c->rope_dim != 64 || q) return KVQ_ERR_UNSUPPORTED;
+  } else {
+    if (!v || kpe) return KVQ_ERR_INVALID;
+    if (D != 64 && D != 128 && D != 256) return KVQ_ERR_UNSUPPORTED;
+  }
+  if (tokens == 0) return KVQ_OK;
+  if (!where.start_pos && !where.slots) return KVQ_ERR_INVALID;
+  if (where.slots && r->rot_dim > 0 && !where.positions) return KVQ_ERR_INVALID;
+  s = check_heads(k, D, tokens, false);
+  if (s == KVQ_OK) s = mla ? check_heads(kpe, c->rope_dim, tokens, false)
+                           : check_heads(v, D, tokens, false);
+  if (s != KVQ_OK) return s;
+  if (k->num_heads != c->num_kv_heads || (mla ? kpe : v)->num_heads != c->num_kv_heads)
+    return KVQ_ERR_INVALID;
+  if (q) {
+    s = check_query_rows(q, q_out, D, tokens, q_fp8, q_scale, q_head_scale);
+    if (s != KVQ_OK) return s;
+  }
+  const long long heads = mla ? 1 : 2LL * c->num_kv_heads + (q ? q->num_heads : 0);
+  if (tokens >= (1LL << 31) || tokens * heads >= (1LL << 31)) return KVQ_ERR_UNSUPPORTED;
+  RopeArgs a = where;
+  a.fmt = c->fmt;
+  rotary_args(a, r);
+  a.q = rope_rows(q);
+  a.k = rope_rows(k);
+  a.v = rope_rows(mla ? kpe : v);
+  a.q_out = rope_rows(q ? q_out : nullptr);
+  a.q_norm = q ? r->q_norm : nullptr;
+  a.k_norm = r->k_norm;
+  a.tokens = (unsigned)tokens;
+  a.q_fp8 = q ? q_fp8 : 0;
+  a.q_scale = q_scale;
+  a.q_recip = a.q_fp8 && !q_head_scale ? (float)(1.0 / (double)q_scale) : 0.f;
+  a.q_hs = q_head_scale;
+  a.error_flag = error_flag;
+  a.Hkv = c->num_kv_heads;
+  a.ps = c->page_size;
+  a.max_pages = c->max_pages_per_seq;
+  a.num_pages = c->num_pages;
+  a.block_table = c->block_table;
+  a.k_codes = static_cast<uint8_t*>(c->k_codes);
+  a.v_codes = static_cast<uint8_t*>(c->v_codes);
+  a.k_bscale = static_cast<uint8_t*>(c->k_bscale);
+  a.v_bscale = static_cast<uint8_t*>(c->v_bscale);
+  a.k_pe = static_cast<uint16_t*>(c->k_pe);
+  a.k_scale = c->k_scale;
+  a.v_scale = c->v_scale;
+  a.k_recip = (float)(1.0 / (double)c->k_scale);
+  a.v_recip = mla ? a.k_recip : (float)(1.0 / (double)c->v_scale);
+  a.k_hs = c->k_head_scale;
+  a.v_hs = c->v_head_scale;
+  return cuda_status(launch_rope(D, mla, a, stream));
+}
 
 // ---------------------------------------------------------------------------
 // Division by the prob scale (FP8 probabilities, vLLM PR 15734: softmax(QK^T)
@@ -409,70 +504,57 @@ kvq_status kvq_rope_append(const kvq_cache* c, const kvq_rotary* r, int batch, i
                            const kvq_heads* v, const kvq_heads* kpe, const kvq_heads* q,
                            const kvq_heads* q_out, int q_fp8, float q_scale,
                            const float* q_head_scale, int32_t* error_flag, void* stream) {
-  kvq_status s = check_cache(c);
-  if (s != KVQ_OK) return s;
-  if (batch < 0 || n_tokens < 0) return KVQ_ERR_INVALID;
-  const bool mla = is_mla(c);
-  const int D = c->head_dim;
-  s = check_rotary(r, mla ? c->rope_dim : D);
-  if (s != KVQ_OK) return s;
-  if (mla) {
-    if (v || !kpe) return KVQ_ERR_INVALID;
-    if (D != 512 || c->rope_dim != 64 || q) return KVQ_ERR_UNSUPPORTED;
-  } else {
-    if (!v || kpe) return KVQ_ERR_INVALID;
-    if (D != 64 && D != 128 && D != 256) return KVQ_ERR_UNSUPPORTED;
-  }
-  const long long tokens = (long long)batch * n_tokens;
-  if (tokens == 0) return KVQ_OK;
-  if (!start_pos) return KVQ_ERR_INVALID;
-  s = check_heads(k, D, tokens, false);
-  if (s == KVQ_OK) s = mla ? check_heads(kpe, c->rope_dim, tokens, false)
-                           : check_heads(v, D, tokens, false);
-  if (s != KVQ_OK) return s;
-  if (k->num_heads != c->num_kv_heads || (mla ? kpe : v)->num_heads != c->num_kv_heads)
+  RopeArgs where{};
+  where.start_pos = start_pos;
+  where.new_lens = new_lens;
+  where.T = n_tokens;
+  const long long tokens = batch < 0 || n_tokens < 0 ? -1 : (long long)batch * n_tokens;
+  return rope_append(c, r, tokens, k, v, kpe, q, q_out, q_fp8, q_scale,
+                     q_head_scale, error_flag, where, as_stream(stream));
+}
+
+kvq_status kvq_rope_append_slots(const kvq_cache* c, const kvq_rotary* r, int num_tokens,
+                                 const int32_t* positions, const int64_t* slots,
+                                 const kvq_heads* k, const kvq_heads* v, const kvq_heads* kpe,
+                                 const kvq_heads* q, const kvq_heads* q_out, int q_fp8,
+                                 float q_scale, const float* q_head_scale, int32_t* error_flag,
+                                 void* stream) {
+  RopeArgs where{};
+  where.positions = positions;
+  where.slots = reinterpret_cast<const long*>(slots);
+  return rope_append(c, r, num_tokens, k, v, kpe, q, q_out, q_fp8, q_scale, q_head_scale,
+                     error_flag, where, as_stream(stream));
+}
+
+kvq_status kvq_plan_step(const kvq_page_plan* p, void* stream) {
+  if (!p || p->batch < 0 || p->page_size < 1 || p->num_pages < 1 || p->max_pages_per_seq < 1 ||
+      p->max_tokens < 0)
     return KVQ_ERR_INVALID;
-  if (q) {
-    s = check_query_rows(q, q_out, D, tokens, q_fp8, q_scale, q_head_scale);
-    if (s != KVQ_OK) return s;
-  }
-  const long long heads = mla ? 1 : 2LL * c->num_kv_heads + (q ? q->num_heads : 0);
-  if (tokens >= (1LL << 31) || tokens * heads >= (1LL << 31)) return KVQ_ERR_UNSUPPORTED;
-  RopeArgs a{};
-  a.fmt = c->fmt;
-  rotary_args(a, r);
-  a.q = rope_rows(q);
-  a.k = rope_rows(k);
-  a.v = rope_rows(mla ? kpe : v);
-  a.q_out = rope_rows(q ? q_out : nullptr);
-  a.q_norm = q ? r->q_norm : nullptr;
-  a.k_norm = r->k_norm;
-  a.tokens = (unsigned)tokens;
-  a.start_pos = start_pos;
-  a.new_lens = new_lens;
-  a.T = n_tokens;
-  a.q_fp8 = q ? q_fp8 : 0;
-  a.q_scale = q_scale;
-  a.q_recip = a.q_fp8 && !q_head_scale ? (float)(1.0 / (double)q_scale) : 0.f;
-  a.q_hs = q_head_scale;
-  a.error_flag = error_flag;
-  a.Hkv = c->num_kv_heads;
-  a.ps = c->page_size;
-  a.max_pages = c->max_pages_per_seq;
-  a.num_pages = c->num_pages;
-  a.block_table = c->block_table;
-  a.k_codes = static_cast<uint8_t*>(c->k_codes);
-  a.v_codes = static_cast<uint8_t*>(c->v_codes);
-  a.k_bscale = static_cast<uint8_t*>(c->k_bscale);
-  a.v_bscale = static_cast<uint8_t*>(c->v_bscale);
-  a.k_pe = static_cast<uint16_t*>(c->k_pe);
-  a.k_scale = c->k_scale;
-  a.v_scale = c->v_scale;
-  a.k_recip = (float)(1.0 / (double)c->k_scale);
-  a.v_recip = mla ? a.k_recip : (float)(1.0 / (double)c->v_scale);
-  a.k_hs = c->k_head_scale;
-  a.v_hs = c->v_head_scale;
-  return cuda_status(launch_rope(D, mla, a, as_stream(stream)));
+  if (!p->free_pages || !p->free_count || !p->free_count_out || !p->counter) return KVQ_ERR_INVALID;
+  if (p->batch > 0 && (!p->block_table || !p->seq_lens || !p->seq_lens_out || !p->add_lens))
+    return KVQ_ERR_INVALID;
+  if (p->batch > kMaxPlanBatch || (long long)p->max_pages_per_seq * p->page_size >= (1LL << 31))
+    return KVQ_ERR_UNSUPPORTED;
+  PlanArgs a{};
+  a.batch = p->batch;
+  a.ps = p->page_size;
+  a.num_pages = p->num_pages;
+  a.max_pages = p->max_pages_per_seq;
+  a.max_tokens = p->max_tokens;
+  a.block_table = p->block_table;
+  a.seq_lens = p->seq_lens;
+  a.seq_lens_out = p->seq_lens_out;
+  a.add_lens = p->add_lens;
+  a.free_pages = p->free_pages;
+  a.free_count = p->free_count;
+  a.free_count_out = p->free_count_out;
+  a.counter = p->counter;
+  a.start_pos = p->start_pos;
+  a.q_offsets = p->q_offsets;
+  a.slots = reinterpret_cast<long*>(p->slots);
+  a.positions = p->positions;
+  a.error_flag = p->error_flag;
+  return cuda_status(launch_plan(a, as_stream(stream)));
 }
 
 kvq_status kvq_auto_splits(int num_sms, int batch, int num_kv_heads, int q_per_kv,
@@ -579,11 +661,11 @@ namespace {
 // Shared body of kvq_decode_partial and kvq_decode (fused when counters), and
 // of kvq_decode_shared: with prefix_splits > 0 the requests start at token
 // prefix_len, and the merge takes the preceding kernel's prefix_splits partials
-// in too.
+// in too.  And of kvq_decode_diff: with `diff`, each query head is two rows.
 kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const void* q,
                        float* part_o, float* part_lse, uint32_t* counters, void* out,
                        cudaStream_t stream, int prefix_len = 0, int prefix_splits = 0,
-                       uint32_t* ready = nullptr) {
+                       uint32_t* ready = nullptr, const kvq_diff* diff = nullptr) {
   kvq_status s = check_cache(c);
   if (s != KVQ_OK) return s;
   s = check_params(p);
@@ -593,8 +675,9 @@ kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const voi
   if (counters && !out) return KVQ_ERR_INVALID;
   if (counters && p->num_splits > kMaxFusedSplits) return KVQ_ERR_UNSUPPORTED;
   if (p->num_q_heads % c->num_kv_heads != 0) return KVQ_ERR_INVALID;
-  const int G = p->num_q_heads / c->num_kv_heads;
-  if (G > kMaxGroup) return KVQ_ERR_UNSUPPORTED;
+  const int maps = diff ? 2 : 1;
+  if (p->num_q_heads / c->num_kv_heads > kMaxGroup / maps) return KVQ_ERR_UNSUPPORTED;
+  const int G = maps * (p->num_q_heads / c->num_kv_heads);
   if ((long long)p->max_kv_len > (long long)c->max_pages_per_seq * c->page_size)
     return KVQ_ERR_INVALID;
   if ((long long)p->batch * c->num_kv_heads >= (1LL << 31)) return KVQ_ERR_UNSUPPORTED;
@@ -623,7 +706,7 @@ kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const voi
   a.part_lse = part_lse;
   a.error_flag = p->error_flag;
   a.batch = p->batch;
-  a.Hq = p->num_q_heads;
+  a.Hq = G * c->num_kv_heads;
   a.Hkv = c->num_kv_heads;
   a.G = G;
   a.ps = c->page_size;
@@ -677,11 +760,18 @@ kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const voi
   if (!ok_dims) return KVQ_ERR_UNSUPPORTED;
   a.out_mult = probq ? c->v_scale * p->prob_scale : c->v_scale;
   const uint64_t row_bytes = c->fmt == KVQ_FP8_E4M3 ? D : D / 2;
-  TensorMaps maps;
-  if (!make_row_map(&maps.k16, c->k_codes, row_bytes, rows) ||
-      !make_row_map(&maps.v16, c->v_codes, row_bytes, rows))
+  TensorMaps m;
+  if (!make_row_map(&m.k16, c->k_codes, row_bytes, rows) ||
+      !make_row_map(&m.v16, c->v_codes, row_bytes, rows))
     return KVQ_ERR_CUDA;
-  return cuda_status(launch_partial(c->fmt, D, probq, maps, a, stream));
+  if (diff) {
+    a.diff_lambda = diff->lambda;
+    a.diff_norm = diff->norm;
+    a.diff_eps = diff->eps;
+    a.diff_gain = diff->gain;
+    return cuda_status(launch_partial_diff(c->fmt, D, m, a, stream));
+  }
+  return cuda_status(launch_partial(c->fmt, D, probq, m, a, stream));
 }
 
 }  // namespace
@@ -699,6 +789,22 @@ kvq_status kvq_decode(const kvq_cache* c, const kvq_decode_params* p, const void
   if (p && p->batch > 0 && (!counters || !out)) return KVQ_ERR_INVALID;
   return decode_impl(c, p, q, part_o, part_lse, counters, out,
                      as_stream(stream));
+}
+
+kvq_status kvq_decode_diff(const kvq_cache* c, const kvq_decode_params* p, const kvq_diff* d,
+                           const void* q, float* part_o, float* part_lse, uint32_t* counters,
+                           void* out, void* stream) {
+  kvq_status s = check_cache(c);
+  if (s != KVQ_OK) return s;
+  s = check_params(p);
+  if (s == KVQ_OK) s = check_diff(d);
+  if (s != KVQ_OK) return s;
+  if (is_mla(c) || p->prob_scale > 0.f) return KVQ_ERR_UNSUPPORTED;
+  s = check_heads_of(c, p, true);
+  if (s != KVQ_OK) return s;
+  if (p->num_q_heads / c->num_kv_heads > kMaxGroup / 2) return KVQ_ERR_UNSUPPORTED;
+  if (p->batch > 0 && (!counters || !out)) return KVQ_ERR_INVALID;
+  return decode_impl(c, p, q, part_o, part_lse, counters, out, as_stream(stream), 0, 0, nullptr, d);
 }
 
 kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int prefix_len,
@@ -761,8 +867,7 @@ kvq_status kvq_decode_shared(const kvq_cache* c, const kvq_decode_params* p, int
   a.num_pages = c->num_pages;
   a.prefix = prefix_len;
   a.splits = prefix_splits;
-  a.box = 16;   // TMA boxes: the largest power of two up to a tile that divides the pages
-  while (a.box < 128 && c->page_size % (2 * a.box) == 0) a.box *= 2;
+  a.box = box_rows(c->page_size);
   a.wide_p = p->prefix_p_f16 == 0;
   a.sm_scale = p->sm_scale;
   a.k_scale = c->k_scale;
@@ -826,6 +931,81 @@ kvq_status kvq_decode_combine(const kvq_decode_params* p, const float* part_o,
   a.out_dtype = p->out_dtype;
   a.out_scale = p->out_scale;
   return cuda_status(launch_combine(a, as_stream(stream)));
+}
+
+size_t kvq_chunk_workspace_bytes(int num_sms, int batch, int head_dim) {
+  if (num_sms < 1 || batch < 0 || head_dim < 1) return 0;
+  return chunk_workspace_bytes(num_sms, std::max(batch, 1), head_dim);
+}
+
+kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_decode_params* p, const kvq_diff* d,
+                               int num_tokens, const int32_t* q_offsets, const void* q,
+                               void* workspace, size_t workspace_bytes, void* out, void* stream) {
+  kvq_status s = check_cache(c);
+  if (s != KVQ_OK) return s;
+  s = check_params(p);
+  if (s == KVQ_OK && d) s = check_diff(d);
+  if (s != KVQ_OK) return s;
+  if (num_tokens < 0) return KVQ_ERR_INVALID;
+  if (is_mla(c) || p->prob_scale > 0.f) return KVQ_ERR_UNSUPPORTED;
+  s = check_heads_of(c, p, false);
+  if (s != KVQ_OK) return s;
+  const int G = p->num_q_heads / c->num_kv_heads, D = c->head_dim;
+  if ((long long)num_tokens * G >= (1LL << 30) || p->batch > kMaxPlanBatch ||
+      p->max_kv_len > INT_MAX - 4096)
+    return KVQ_ERR_UNSUPPORTED;
+  if (p->batch == 0 || num_tokens == 0) return KVQ_OK;
+  if (!q || !aligned16(q) || !q_offsets || !out || !aligned16(out)) return KVQ_ERR_INVALID;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 31u)) return KVQ_ERR_INVALID;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  if (workspace_bytes < chunk_workspace_bytes(sms, p->batch, D)) return KVQ_ERR_WORKSPACE;
+  ChunkArgs a{};
+  a.q = q;
+  a.q_fp8 = p->q_fp8;
+  a.q_scale = p->q_scale;
+  a.q_hs = p->q_fp8 ? p->q_head_scale : nullptr;
+  a.k_bscale = static_cast<const uint8_t*>(c->k_bscale);
+  a.v_bscale = static_cast<const uint8_t*>(c->v_bscale);
+  a.block_table = c->block_table;
+  a.seq_lens = p->seq_lens;
+  a.q_offsets = q_offsets;
+  a.workspace = static_cast<uint8_t*>(workspace);
+  a.out = out;
+  a.error_flag = p->error_flag;
+  a.batch = p->batch;
+  a.num_tokens = num_tokens;
+  a.G = G;
+  a.Hq = p->num_q_heads;
+  a.Hkv = c->num_kv_heads;
+  a.D = D;
+  a.ps = c->page_size;
+  a.max_pages = c->max_pages_per_seq;
+  a.num_pages = c->num_pages;
+  a.max_kv_len = p->max_kv_len;
+  a.box = box_rows(c->page_size);
+  a.out_dtype = p->out_dtype;
+  a.out_scale = p->out_scale;
+  a.sm_scale = p->sm_scale;
+  a.k_scale = c->k_scale;
+  a.v_scale = c->v_scale;
+  a.k_hs = c->k_head_scale;
+  a.v_hs = c->v_head_scale;
+  if (d) {
+    a.diff_lambda = d->lambda;
+    a.diff_norm = d->norm;
+    a.diff_eps = d->eps;
+    a.diff_gain = d->gain;
+  }
+  const uint64_t rows = (uint64_t)c->num_pages * c->num_kv_heads * c->page_size;
+  const uint64_t row_bytes = c->fmt == KVQ_FP8_E4M3 ? D : D / 2;
+  TensorMaps maps;
+  if (!make_row_map(&maps.k16, c->k_codes, row_bytes, rows, (uint32_t)a.box) ||
+      !make_row_map(&maps.v16, c->v_codes, row_bytes, rows, (uint32_t)a.box))
+    return KVQ_ERR_CUDA;
+  return cuda_status(launch_chunk(c->fmt, D, maps, a, sms, as_stream(stream)));
 }
 
 kvq_status kvq_prefill(const kvq_cache* c, const kvq_decode_params* p, int q_len, const void* q,

@@ -276,6 +276,10 @@ __device__ __forceinline__ void store_out_t(void* out, float out_scale, size_t i
   }
 }
 
+// 1 / sqrt(x), and 0 for 0 (the norm of nothing but zeros is zeros); NaN stays.
+__device__ __forceinline__ float inv_rms_of(float x) {
+  return x > 0.f ? 1.f / sqrtf(x) : x == 0.f ? 0.f : NAN;
+}
 
 // Merge of the s split partials of `rows` consecutive query heads starting at
 // partial row `row0` (M = max lse, w_j = e^(lse_j - M), O = sum w_j o_j /
@@ -524,6 +528,125 @@ __device__ __forceinline__ void fused_combine_staged(const PartialArgs& a, int b
     merge_staged<1>(a, part_row, rows, s, stage_p, wbuf, winv, ok);
   else
     merge_staged<2>(a, part_row, rows, s, stage_p, wbuf, winv, ok);
+  if (!ok && threadIdx.x == 0) record_error(a.error_flag, 1);
+}
+
+// The merge of differential heads (rows 2i and 2i + 1 of the kv head are head i's two
+// maps): one warp per head forms both rows' sums, y = o1 - lambda o2, and its norm over
+// the D values that the warp holds.  Arrival, weights and staging are
+// fused_combine_staged's.
+template <int D, bool STAGED>
+__device__ __forceinline__ void merge_diff(const PartialArgs& a, size_t row0, int rows, int s,
+                                           const float* po, const float* w, const float* winv,
+                                           bool ok) {
+  constexpr int kQuads = D / 4;                       // float4 columns of a row
+  constexpr int NV = (kQuads + 31) / 32;              // of a lane
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+#pragma unroll 1
+  for (int i = threadIdx.x >> 5; i < rows / 2; i += warps) {
+    const size_t head = (row0 >> 1) + i;              // of all (request, query head)s
+    const int hq = (int)(head % (size_t)(a.Hq / 2));
+    const float lam = __ldg(a.diff_lambda + hq);
+    float4 y[NV];
+    float ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int q = lane + 32 * v;
+      y[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (q >= kQuads) continue;
+      float4 o[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int r = 2 * i + m;
+        const float4* p = reinterpret_cast<const float4*>(po) + (size_t)r * s * kQuads + q;
+        const float* wr = w + r * kMaxFusedSplits;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if constexpr (STAGED) {
+          acc = accum_splits(p, kQuads, wr, s, acc);
+        } else {
+#pragma unroll 1
+          for (int j0 = 0; j0 < s; j0 += 8) {
+            float4 u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              u[k] = j0 + k < s ? __ldcg(p + (size_t)(j0 + k) * kQuads)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float wk = j0 + k < s ? wr[j0 + k] : 0.f;
+              acc.x += wk * u[k].x;
+              acc.y += wk * u[k].y;
+              acc.z += wk * u[k].z;
+              acc.w += wk * u[k].w;
+            }
+          }
+        }
+        const float iv = ok ? winv[r] : NAN;
+        o[m] = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
+      }
+      y[v] = make_float4(o[0].x - lam * o[1].x, o[0].y - lam * o[1].y, o[0].z - lam * o[1].z,
+                         o[0].w - lam * o[1].w);
+      ss += y[v].x * y[v].x + y[v].y * y[v].y + y[v].z * y[v].z + y[v].w * y[v].w;
+    }
+    float r = a.diff_gain;
+    if (a.diff_norm) {
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+      r *= inv_rms_of(ss * (1.f / D) + a.diff_eps);
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int q = lane + 32 * v;
+      if (q >= kQuads) continue;
+      const float4 n = a.diff_norm ? __ldg(reinterpret_cast<const float4*>(a.diff_norm) + q)
+                                   : make_float4(1.f, 1.f, 1.f, 1.f);
+      const size_t at = head * D + 4 * q;
+      const float z[4] = {y[v].x * r * n.x, y[v].y * r * n.y, y[v].z * r * n.z, y[v].w * r * n.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (a.out_dtype == 0) store_out_t<0>(a.out, a.out_scale, at + e, z[e]);
+        else if (a.out_dtype == 1) store_out_t<1>(a.out, a.out_scale, at + e, z[e]);
+        else store_out_t<2>(a.out, a.out_scale, at + e, z[e]);
+      }
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void fused_combine_diff(const PartialArgs& a, int bh, size_t part_row,
+                                                   int rows, int s, uint32_t stage,
+                                                   const float* stage_p, uint32_t cap, float* wbuf,
+                                                   uint32_t bar) {
+  __shared__ int is_last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    unsigned prev;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                 : "=r"(prev)
+                 : "l"(a.counters + bh)
+                 : "memory");
+    is_last = prev == (unsigned)(a.num_splits - 1);
+    if (is_last) a.counters[bh] = 0u;
+  }
+  __syncthreads();
+  if (!is_last) return;
+  float* winv = wbuf + kMaxGroup * kMaxFusedSplits;
+  const uint64_t bytes = (uint64_t)rows * s * D * 4;
+  const float* part = a.part_o + part_row * s * D;
+  const bool staged = bytes <= cap;
+  if (staged && threadIdx.x == 0) {
+    asm volatile("fence.proxy.async.global;" ::: "memory");   // acquired data -> bulk copy
+    mbar_arrive_expect_tx(bar, (uint32_t)bytes);
+    bulk_load(stage, part, (uint32_t)bytes, bar);
+  }
+  merge_weights(a.part_lse, part_row, rows, s, wbuf, winv);
+  if (!staged) {
+    __syncthreads();
+    merge_diff<D, false>(a, part_row, rows, s, part, wbuf, winv, true);
+    return;
+  }
+  const bool ok = __syncthreads_and(mbar_wait(bar, 0) ? 1 : 0) != 0;
+  merge_diff<D, true>(a, part_row, rows, s, stage_p, wbuf, winv, ok);
   if (!ok && threadIdx.x == 0) record_error(a.error_flag, 1);
 }
 

@@ -22,13 +22,27 @@ typedef kvq_status (*decode_shared_fn)(const kvq_cache*, const kvq_decode_params
                                        const int32_t*, int, const void*, float*, float*, uint32_t*,
                                        void*, void*);
 
+typedef kvq_status (*plan_step_fn)(const kvq_page_plan*, void*);
+typedef kvq_status (*append_slots_fn)(const kvq_cache*, const kvq_rotary*, int, const int32_t*,
+                                      const int64_t*, const kvq_heads*, const kvq_heads*,
+                                      const kvq_heads*, const kvq_heads*, const kvq_heads*, int,
+                                      float, const float*, int32_t*, void*);
+typedef kvq_status (*decode_diff_fn)(const kvq_cache*, const kvq_decode_params*, const kvq_diff*,
+                                     const void*, float*, float*, uint32_t*, void*, void*);
+typedef kvq_status (*chunk_fn)(const kvq_cache*, const kvq_decode_params*, const kvq_diff*, int,
+                               const int32_t*, const void*, void*, size_t, void*, void*);
+
 static norm_rope_fn p_norm_rope;
 static rope_append_fn p_rope_append;
 static decode_shared_fn p_decode_shared;
+static plan_step_fn p_plan_step;
+static append_slots_fn p_append_slots;
+static decode_diff_fn p_decode_diff;
+static chunk_fn p_chunk;
 
 static PyObject *s_dtype, *s_get_device, *s_shape, *s_stride, *s_data_ptr, *s_numel,
     *s_is_contiguous;
-static PyObject *t_bf16, *t_u8, *t_i32, *t_f32;   /* torch dtypes (singletons) */
+static PyObject *t_bf16, *t_u8, *t_i32, *t_f32, *t_i64;   /* torch dtypes (singletons) */
 
 /* ------------------------------------------------------------------ helpers */
 static int refuse(const char* what, const char* why) {
@@ -129,11 +143,11 @@ static int rows(PyObject* t, PyObject* dtype, long dev, const char* what, rows_t
   return address(t, &r->h.data);
 }
 
-/* A dense int32 array of n entries. */
-static int index_array(PyObject* t, long long n, long dev, const char* what, const int32_t** out) {
+/* A dense array of n entries of the type. */
+static int dense_array(PyObject* t, PyObject* dtype, long long n, long dev, const char* what,
+                       void** out) {
   long long numel;
-  void* p;
-  if (here(t, t_i32, dev, what) || method_long(t, s_numel, &numel)) return -1;
+  if (here(t, dtype, dev, what) || method_long(t, s_numel, &numel)) return -1;
   PyObject* c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
   if (!c) return -1;
   const int dense = c == Py_True;
@@ -142,7 +156,12 @@ static int index_array(PyObject* t, long long n, long dev, const char* what, con
     PyErr_Format(PyExc_ValueError, "%s: expected %lld contiguous entries", what, n);
     return -1;
   }
-  if (address(t, &p)) return -1;
+  return address(t, out);
+}
+
+static int index_array(PyObject* t, long long n, long dev, const char* what, const int32_t** out) {
+  void* p;
+  if (dense_array(t, t_i32, n, dev, what, &p)) return -1;
   *out = (const int32_t*)p;
   return 0;
 }
@@ -211,21 +230,26 @@ static int as_float(PyObject* o, float* out) {
   } while (0)
 
 /* ------------------------------------------------------------------- calls */
-/* bind(norm_rope, rope_append, decode_shared, bfloat16, uint8, int32, float32) */
+/* bind(norm_rope, rope_append, decode_shared, plan_step, rope_append_slots,
+ *      decode_diff, chunk_attention, bfloat16, uint8, int32, float32, int64) */
 static PyObject* bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  if (n != 7) {
-    PyErr_SetString(PyExc_TypeError, "bind: seven arguments");
+  if (n != 12) {
+    PyErr_SetString(PyExc_TypeError, "bind: twelve arguments");
     return NULL;
   }
   p_norm_rope = (norm_rope_fn)PyLong_AsVoidPtr(a[0]);
   p_rope_append = (rope_append_fn)PyLong_AsVoidPtr(a[1]);
   p_decode_shared = (decode_shared_fn)PyLong_AsVoidPtr(a[2]);
+  p_plan_step = (plan_step_fn)PyLong_AsVoidPtr(a[3]);
+  p_append_slots = (append_slots_fn)PyLong_AsVoidPtr(a[4]);
+  p_decode_diff = (decode_diff_fn)PyLong_AsVoidPtr(a[5]);
+  p_chunk = (chunk_fn)PyLong_AsVoidPtr(a[6]);
   if (PyErr_Occurred()) return NULL;
-  PyObject** const types[4] = {&t_bf16, &t_u8, &t_i32, &t_f32};
-  for (int i = 0; i < 4; ++i) {
-    Py_INCREF(a[3 + i]);
-    Py_XSETREF(*types[i], a[3 + i]);
+  PyObject** const types[5] = {&t_bf16, &t_u8, &t_i32, &t_f32, &t_i64};
+  for (int i = 0; i < 5; ++i) {
+    Py_INCREF(a[7 + i]);
+    Py_XSETREF(*types[i], a[7 + i]);
   }
   Py_RETURN_NONE;
 }
@@ -395,6 +419,188 @@ static PyObject* decode_shared(PyObject* self, PyObject* const* a, Py_ssize_t n)
   return PyLong_FromLong(st);
 }
 
+/* plan_step(device, stream, plan, seq_lens, add_lens, seq_lens_out, free_count_out,
+ *           error_flag) -> status;
+ * plan is the struct's address; None leaves the lengths or the count updated in place. */
+static PyObject* plan_step(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 8 || !p_plan_step) {
+    PyErr_SetString(PyExc_TypeError, "plan_step: eight arguments, after bind");
+    return NULL;
+  }
+  const long dev = PyLong_AsLong(a[0]);
+  const kvq_page_plan* given = (const kvq_page_plan*)PyLong_AsVoidPtr(a[2]);
+  void *stream, *flag;
+  if (PyErr_Occurred() || !given) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "plan_step: no plan");
+    return NULL;
+  }
+  if (optional_address(a[1], &stream) || flag_address(a[7], dev, &flag)) return NULL;
+  kvq_page_plan p = *given;
+  const int32_t *lens_out = NULL, *count_out = NULL;
+  if (index_array(a[3], p.batch, dev, "seq_lens", &p.seq_lens) ||
+      index_array(a[4], p.batch, dev, "add_lens", &p.add_lens) ||
+      (a[5] != Py_None && index_array(a[5], p.batch, dev, "seq_lens_out", &lens_out)) ||
+      (a[6] != Py_None && index_array(a[6], 1, dev, "count_out", &count_out)))
+    return NULL;
+  p.seq_lens_out = (int32_t*)(a[5] != Py_None ? lens_out : p.seq_lens);
+  p.free_count_out = (int32_t*)(a[6] != Py_None ? count_out : p.free_count);
+  p.error_flag = (int32_t*)flag;
+  kvq_status st;
+  CALL(st, p_plan_step(&p, stream));
+  return PyLong_FromLong(st);
+}
+
+/* append_slots(device, stream, cache, rotary, q_norm len, k_norm len, k, v, kpe, slots,
+ *              positions, q, q_out, q_fp8, q_scale, q_head_scale, error_flag) -> status */
+static PyObject* append_slots(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 17 || !p_append_slots) {
+    PyErr_SetString(PyExc_TypeError, "append_slots: seventeen arguments, after bind");
+    return NULL;
+  }
+  const long dev = PyLong_AsLong(a[0]);
+  void *stream, *flag;
+  const kvq_cache* c = (const kvq_cache*)PyLong_AsVoidPtr(a[2]);
+  const kvq_rotary* rot = (const kvq_rotary*)PyLong_AsVoidPtr(a[3]);
+  const long nq = PyLong_AsLong(a[4]), nk = PyLong_AsLong(a[5]);
+  const int fp8 = PyObject_IsTrue(a[13]);
+  float scale;
+  if (PyErr_Occurred() || !c || !rot || optional_address(a[1], &stream) ||
+      as_float(a[14], &scale) || flag_address(a[16], dev, &flag)) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "append_slots: no cache or rotation");
+    return NULL;
+  }
+  const int mla = c->rope_dim > 0;
+  rows_t kr, vr, er, qr, qo;
+  void *slots = NULL, *pos = NULL;
+  const float* hs = NULL;
+  if (rows(a[6], t_bf16, dev, "k", &kr)) return NULL;
+  if (kr.n != 3 || kr.h.num_heads != c->num_kv_heads || kr.dim != c->head_dim)
+    return refuse("k", "expected [tokens][kv heads][dim] of the cache's"), NULL;
+  const long long T = kr.tokens;
+  if (T > INT32_MAX) return refuse("k", "too many tokens"), NULL;
+  if (nk >= 0 && nk != c->head_dim)
+    return refuse("k_norm", "expected one weight per element"), NULL;
+  if (mla != (a[7] == Py_None) || mla != (a[8] != Py_None))
+    return refuse("v", "expected v, or for MLA kpe"), NULL;
+  if (!mla) {
+    if (rows(a[7], t_bf16, dev, "v", &vr)) return NULL;
+    if (vr.n != 3 || vr.tokens != T || vr.h.num_heads != kr.h.num_heads || vr.dim != kr.dim)
+      return refuse("v", "expected k's shape"), NULL;
+  } else {
+    if (rows(a[8], t_bf16, dev, "kpe", &er)) return NULL;
+    if (er.n != 3 || er.tokens != T || er.h.num_heads != 1 || er.dim != c->rope_dim)
+      return refuse("kpe", "expected [tokens][1][rope]"), NULL;
+  }
+  PyObject* q = a[11];
+  if (q != Py_None) {
+    if (rows(q, t_bf16, dev, "q", &qr) || rows(a[12], fp8 ? t_u8 : t_bf16, dev, "q_out", &qo) ||
+        head_scales(a[15], qr.h.num_heads, dev, &hs))
+      return NULL;
+    if (qr.n != 3 || qr.tokens != T || qr.dim != c->head_dim)
+      return refuse("q", "expected [tokens][heads][dim]"), NULL;
+    if (qo.tokens != T || qo.dim != qr.dim || qo.h.num_heads != qr.h.num_heads)
+      return refuse("q_out", "expected q's shape"), NULL;
+    if (nq >= 0 && nq != qr.dim) return refuse("q_norm", "expected one weight per element"), NULL;
+  }
+  if (dense_array(a[9], t_i64, T, dev, "slots", &slots)) return NULL;
+  if (a[10] != Py_None && dense_array(a[10], t_i32, T, dev, "positions", &pos)) return NULL;
+  kvq_status st = KVQ_OK;
+  if (T > 0)
+    CALL(st, p_append_slots(c, rot, (int)T, (const int32_t*)pos, (const int64_t*)slots, &kr.h,
+                            mla ? NULL : &vr.h, mla ? &er.h : NULL, q != Py_None ? &qr.h : NULL,
+                            q != Py_None ? &qo.h : NULL, fp8, scale, hs, (int32_t*)flag, stream));
+  return PyLong_FromLong(st);
+}
+
+/* A dense [tokens][heads][dim] of queries that the parameters describe; its tokens. */
+static int query_rows(PyObject* t, const kvq_decode_params* p, long dev, rows_t* r) {
+  if (rows(t, p->q_fp8 ? t_u8 : t_bf16, dev, "q", r)) return -1;
+  if (r->n != 3 || r->h.num_heads != p->num_q_heads || r->dim != p->qk_dim ||
+      r->h.head_stride != r->dim ||
+      (r->tokens > 1 && r->h.token_stride != r->dim * r->h.num_heads))
+    return refuse("q", "expected a contiguous [tokens][heads][dim]");
+  return 0;
+}
+
+/* decode_diff(device, stream, cache, params, diff, q, seq_lens, part_o, part_lse,
+ *             counters, out, error_flag) -> status;
+ * cache, params and diff are the structs' addresses. */
+static PyObject* decode_diff(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 12 || !p_decode_diff) {
+    PyErr_SetString(PyExc_TypeError, "decode_diff: twelve arguments, after bind");
+    return NULL;
+  }
+  const long dev = PyLong_AsLong(a[0]);
+  const kvq_cache* c = (const kvq_cache*)PyLong_AsVoidPtr(a[2]);
+  const kvq_decode_params* given = (const kvq_decode_params*)PyLong_AsVoidPtr(a[3]);
+  const kvq_diff* d = (const kvq_diff*)PyLong_AsVoidPtr(a[4]);
+  void *stream, *flag, *po, *pl, *cn, *out;
+  if (PyErr_Occurred() || !c || !given || !d) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "decode_diff: no cache or parameters");
+    return NULL;
+  }
+  if (optional_address(a[1], &stream) || optional_address(a[7], &po) ||
+      optional_address(a[8], &pl) || optional_address(a[9], &cn) ||
+      optional_address(a[10], &out) || flag_address(a[11], dev, &flag))
+    return NULL;
+  kvq_decode_params p = *given;
+  rows_t qr;
+  if (query_rows(a[5], &p, dev, &qr)) return NULL;
+  if (qr.tokens != p.batch) return refuse("q", "expected one token per request"), NULL;
+  if (index_array(a[6], p.batch, dev, "seq_lens", &p.seq_lens)) return NULL;
+  p.error_flag = (int32_t*)flag;
+  kvq_status st = KVQ_OK;
+  if (p.batch > 0)
+    CALL(st, p_decode_diff(c, &p, d, qr.h.data, (float*)po, (float*)pl, (uint32_t*)cn, out, stream));
+  return PyLong_FromLong(st);
+}
+
+/* chunk_attention(device, stream, cache, params, diff, q, q_offsets, seq_lens,
+ *                 workspace, bytes, out, out type, error_flag) -> status;
+ * diff may be 0, out is a tensor of q's shape. */
+static PyObject* chunk_attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 13 || !p_chunk) {
+    PyErr_SetString(PyExc_TypeError, "chunk_attention: thirteen arguments, after bind");
+    return NULL;
+  }
+  const long dev = PyLong_AsLong(a[0]);
+  const kvq_cache* c = (const kvq_cache*)PyLong_AsVoidPtr(a[2]);
+  const kvq_decode_params* given = (const kvq_decode_params*)PyLong_AsVoidPtr(a[3]);
+  const kvq_diff* d = (const kvq_diff*)PyLong_AsVoidPtr(a[4]);
+  const long long bytes = PyLong_AsLongLong(a[9]);
+  void *stream, *flag, *ws;
+  if (PyErr_Occurred() || !c || !given) {
+    if (!PyErr_Occurred())
+      PyErr_SetString(PyExc_ValueError, "chunk_attention: no cache or parameters");
+    return NULL;
+  }
+  if (optional_address(a[1], &stream) || optional_address(a[8], &ws) ||
+      flag_address(a[12], dev, &flag))
+    return NULL;
+  kvq_decode_params p = *given;
+  rows_t qr, o;
+  const int32_t* offsets;
+  if (query_rows(a[5], &p, dev, &qr)) return NULL;
+  if (index_array(a[6], (long long)p.batch + 1, dev, "q_offsets", &offsets) ||
+      index_array(a[7], p.batch, dev, "seq_lens", &p.seq_lens))
+    return NULL;
+  if (rows(a[10], a[11], dev, "out", &o)) return NULL;
+  if (o.n != 3 || o.tokens != qr.tokens || o.h.num_heads != p.num_q_heads || o.dim != p.v_dim ||
+      o.h.head_stride != o.dim || (o.tokens > 1 && o.h.token_stride != o.dim * o.h.num_heads))
+    return refuse("out", "expected a contiguous [tokens][heads][dim]"), NULL;
+  if (qr.tokens > INT32_MAX) return refuse("q", "too many tokens"), NULL;
+  p.error_flag = (int32_t*)flag;
+  kvq_status st = KVQ_OK;
+  if (p.batch > 0 && qr.tokens > 0)
+    CALL(st, p_chunk(c, &p, d, (int)qr.tokens, offsets, qr.h.data, ws, (size_t)bytes, o.h.data,
+                     stream));
+  return PyLong_FromLong(st);
+}
+
 /* block_table(device, table, requests): refuses a table that is not a dense int32
  * [at least requests][pages] there. */
 static PyObject* block_table(PyObject* self, PyObject* const* a, Py_ssize_t n) {
@@ -421,6 +627,12 @@ static PyMethodDef methods[] = {
     {"rope_append", (PyCFunction)(void (*)(void))rope_append, METH_FASTCALL, "kvq_rope_append"},
     {"decode_shared", (PyCFunction)(void (*)(void))decode_shared, METH_FASTCALL,
      "kvq_decode_shared"},
+    {"plan_step", (PyCFunction)(void (*)(void))plan_step, METH_FASTCALL, "kvq_plan_step"},
+    {"append_slots", (PyCFunction)(void (*)(void))append_slots, METH_FASTCALL,
+     "kvq_rope_append_slots"},
+    {"decode_diff", (PyCFunction)(void (*)(void))decode_diff, METH_FASTCALL, "kvq_decode_diff"},
+    {"chunk_attention", (PyCFunction)(void (*)(void))chunk_attention, METH_FASTCALL,
+     "kvq_chunk_attention"},
     {"block_table", (PyCFunction)(void (*)(void))block_table, METH_FASTCALL,
      "The check of a call's block table."},
     {NULL, NULL, 0, NULL}};

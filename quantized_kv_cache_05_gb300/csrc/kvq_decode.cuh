@@ -109,7 +109,13 @@ constexpr int ctas_per_sm() {
 // BEHIND: the requests' own tokens behind a shared prefix's kernel (a variant, as
 // the ordinary decode of 32768 tokens takes 32.5 us without these terms and 32.7
 // with them decided at run time).
-template <int FMT, int D, bool PROBQ, int NH, bool QF8, int NW, bool BEHIND>
+// DIFF: differential heads.  Their halves of the head dims are two maps that share the
+// values, so each is a row of its own: query row 2i of the kv head is [q1 0] of head i,
+// row 2i + 1 is [0 q2] (a.G and a.Hq count these rows), and all that follows, the
+// partials too, is the decode of twice the heads; the cache is read once for both maps.
+// Only the merge joins a head's two.  (Half of the
+// score MMAs multiply zeros; the codes' loads and conversions bound the kernel.)
+template <int FMT, int D, bool PROBQ, int NH, bool QF8, int NW, bool BEHIND, bool DIFF>
 __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     partial_kernel(const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const PartialArgs a) {
@@ -316,8 +322,9 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
 #pragma unroll
   for (int hh = 0; hh < NH; ++hh) {
     const int head = g + 8 * hh;
-    const bool valid = head < a.G;
-    const size_t qrow = (size_t)b * a.Hq + hq0 + (valid ? head : 0);
+    // lanes t = 0, 1 hold the first half of the head dims, 2 and 3 the second
+    const bool valid = head < a.G && (!DIFF || (t >> 1) == (head & 1));
+    const size_t qrow = ((size_t)b * a.Hq + hq0 + (valid ? head : 0)) >> (DIFF ? 1 : 0);
     if constexpr (QF8) {
       const uint8_t* qp = static_cast<const uint8_t*>(a.q) + qrow * D + (D / 4) * t;
       if constexpr (kRawK) {
@@ -337,7 +344,8 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int hc = 2 * t + e + 8 * hh;   // this lane's accumulator column
-        const float qs = a.q_hs ? fetch(a.q_hs + hq0 + min(hc, a.G - 1)) : a.q_scale;
+        const float qs =
+            a.q_hs ? fetch(a.q_hs + ((hq0 + min(hc, a.G - 1)) >> (DIFF ? 1 : 0))) : a.q_scale;
         qsc[hh][e] = qk_scale_log2 * qs;
       }
     } else {
@@ -706,17 +714,23 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     uint32_t dyn_bytes;
     asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn_bytes));
     const uint32_t usable = dyn_bytes - (ring - smem_u32(dyn_smem));
-    fused_combine_staged<ctas_per_sm<FMT, D, PROBQ, NH, NW>() == 4 ? 16 : 32>(
-        a, bh, part_row, a.G, psplits, ring, reinterpret_cast<const float*>(ofrag), usable - kWbuf,
-        reinterpret_cast<float*>(dyn_smem + (ring - smem_u32(dyn_smem)) + usable - kWbuf),
-        smem_u32(&sm.comb_full), BEHIND ? kReady : 0u);
+    float* wbuf = reinterpret_cast<float*>(dyn_smem + (ring - smem_u32(dyn_smem)) + usable - kWbuf);
+    if constexpr (DIFF)
+      fused_combine_diff<D>(a, bh, part_row, a.G, psplits, ring,
+                            reinterpret_cast<const float*>(ofrag), usable - kWbuf, wbuf,
+                            smem_u32(&sm.comb_full));
+    else
+      fused_combine_staged<ctas_per_sm<FMT, D, PROBQ, NH, NW>() == 4 ? 16 : 32>(
+          a, bh, part_row, a.G, psplits, ring, reinterpret_cast<const float*>(ofrag), usable - kWbuf,
+          wbuf, smem_u32(&sm.comb_full), BEHIND ? kReady : 0u);
   }
 }
 
-template <int FMT, int D, bool PROBQ, int NH, bool QF8, int NW, bool BEHIND = false>
+template <int FMT, int D, bool PROBQ, int NH, bool QF8, int NW, bool BEHIND = false,
+          bool DIFF = false>
 cudaError_t launch_partial_t(const TensorMaps& m, const PartialArgs& a, cudaStream_t st) {
   // quantised probabilities and head_dim 256 have no shared prefix
-  if constexpr (!BEHIND && !PROBQ && D <= 128)
+  if constexpr (!BEHIND && !DIFF && !PROBQ && D <= 128)
     if (a.late_merge) return launch_partial_t<FMT, D, PROBQ, NH, QF8, NW, true>(m, a, st);
   using Rg = Ring<FMT, D, PROBQ, NH, NW>;
   static_assert(Rg::kBytes >= Rg::kEpilogue && Rg::kBytes >= Rg::kStream, "ring too small");
@@ -733,7 +747,7 @@ cudaError_t launch_partial_t(const TensorMaps& m, const PartialArgs& a, cudaStre
     smem = std::max(smem, std::min(need, kPerCta));
   }
   smem = (smem + 15) / 16 * 16;
-  auto kern = partial_kernel<FMT, D, PROBQ, NH, QF8, NW, BEHIND>;
+  auto kern = partial_kernel<FMT, D, PROBQ, NH, QF8, NW, BEHIND, DIFF>;
   // The kernel's limit is the same for all calls, the most that any of them takes:
   // set to each call's own size, a call of another thread could lower it between
   // here and the launch, which then fails.

@@ -95,6 +95,10 @@ struct PartialArgs {
   int skip;
   int late_merge;
   uint32_t* ready;
+  // differential heads (kvq_decode_diff): Hq and G count query rows, two per head
+  const float* diff_lambda;   // [Hq / 2], or null
+  const float* diff_norm;     // [Dv], or null
+  float diff_eps, diff_gain;
 };
 
 // The shared prefix's partials (kvq_shared.cu).
@@ -141,7 +145,8 @@ struct RopeArgs {
   const float* q_norm;
   const float* k_norm;
   float eps;
-  const int32_t* positions;   // kvq_norm_rope: per token
+  const int32_t* positions;   // kvq_norm_rope, kvq_rope_append_slots: per token
+  const long* slots;          // kvq_rope_append_slots: per token, else null
   const int32_t* start_pos;   // append: per request
   const int32_t* new_lens;
   int T;                      // append: tokens per request
@@ -160,6 +165,51 @@ struct RopeArgs {
   float k_scale, v_scale, k_recip, v_recip;
   const float* k_hs;
   const float* v_hs;
+};
+
+// A packed ragged step over the cache (kvq_chunk.cu).
+struct ChunkArgs {
+  const void* q;              // [num_tokens][Hq][D] bf16, or E4M3 codes when q_fp8
+  int q_fp8;
+  float q_scale;
+  const float* q_hs;
+  const uint8_t* k_bscale;
+  const uint8_t* v_bscale;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* q_offsets;
+  uint8_t* workspace;
+  void* out;
+  int32_t* error_flag;
+  int batch, num_tokens, G, Hq, Hkv, D, ps, max_pages, num_pages, max_kv_len;
+  int box;                    // TMA box rows
+  int out_dtype;
+  float out_scale, sm_scale, k_scale, v_scale;
+  const float* k_hs;
+  const float* v_hs;
+  const float* diff_lambda;   // differential heads, else null
+  const float* diff_norm;
+  float diff_eps, diff_gain;
+};
+
+// A step's paging (kvq_plan.cu).
+constexpr int kMaxPlanBatch = 8192;   // requests whose sums fit the shared memory of a CTA
+constexpr int kErrRefused = 16, kErrPool = 32;   // KVQ_DEVERR_REFUSED, KVQ_DEVERR_BAD_POOL
+struct PlanArgs {
+  int batch, ps, num_pages, max_pages, max_tokens;
+  int32_t* block_table;
+  const int32_t* seq_lens;
+  int32_t* seq_lens_out;
+  const int32_t* add_lens;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* free_count_out;
+  uint32_t* counter;
+  int32_t* start_pos;         // the last four: null where not wanted
+  int32_t* q_offsets;
+  long* slots;
+  int32_t* positions;
+  int32_t* error_flag;
 };
 
 struct CombineArgs {
@@ -228,11 +278,17 @@ struct TensorMaps {
 
 cudaError_t launch_partial(int fmt, int D, bool probq, const TensorMaps& m, const PartialArgs& a,
                            cudaStream_t st);
+cudaError_t launch_partial_diff(int fmt, int D, const TensorMaps& m, const PartialArgs& a,
+                                cudaStream_t st);
 cudaError_t launch_partial_nvfp4(int D, bool probq, const TensorMaps& m, const PartialArgs& a,
                                  cudaStream_t st);
 cudaError_t launch_mla_partial(const CUtensorMap& tcodes, const CUtensorMap& tpe,
                                const CUtensorMap& tcodes64, const CUtensorMap& tpe64,
                                const PartialArgs& a, cudaStream_t st);
+size_t chunk_workspace_bytes(int grid, int batch, int D);
+cudaError_t launch_chunk(int fmt, int D, const TensorMaps& m, const ChunkArgs& a, int grid,
+                         cudaStream_t st);
+cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st);
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st);
 cudaError_t launch_merge_rows(const CombineArgs& a, cudaStream_t st);
 cudaError_t launch_shared_prefix(int fmt, int D, const TensorMaps& m, const SharedArgs& a,

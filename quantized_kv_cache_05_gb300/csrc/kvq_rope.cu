@@ -370,8 +370,19 @@ __device__ __forceinline__ Token token_of(const RopeArgs& a, unsigned token, boo
 
 // Cache row of kv head 0 at the token's position (head h: + h page_size), or -1
 // (skipped): past the block table as in the plain append, or a page index out
-// of range.
-__device__ __forceinline__ long rope_page(const RopeArgs& a, const Token& k, bool report) {
+// of range.  With slots, the token's own: below zero, or past the cache, skipped.
+__device__ __forceinline__ long rope_page(const RopeArgs& a, const Token& k, unsigned token,
+                                          bool report) {
+  if (a.slots) {
+    const long slot = __ldg(a.slots + token);
+    if (slot < 0) return -1;
+    if (slot >= (long)a.num_pages * a.ps) {   // (below 2^31, as the cache's rows are)
+      if (report) record_error(a.error_flag, 4);
+      return -1;
+    }
+    const unsigned page = (unsigned)slot / (unsigned)a.ps;
+    return (long)page * a.Hkv * a.ps + ((unsigned)slot - page * (unsigned)a.ps);
+  }
   if (k.pos >= (long)a.max_pages * a.ps) return -1;
   const unsigned pos = (unsigned)k.pos, pi = pos / (unsigned)a.ps;
   const int page = __ldg(a.block_table + (size_t)k.b * a.max_pages + pi);
@@ -424,7 +435,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
   if (turned.turn && ok) ang.load(a.cos_sin + tk.pos * a.rot, a.rot / 2, turned);
   // cache row of kv head 0: the token's, whatever the head
   long page_row = -1;
-  if constexpr (FMT != 0) page_row = ok ? rope_page(a, tk, report) : -1;
+  if constexpr (FMT != 0) page_row = ok ? rope_page(a, tk, token, report) : -1;
 
 #pragma unroll 1
   for (int i0 = 0; i0 < H; i0 += step) {   // the same rounds for every lane of the warp
@@ -510,7 +521,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_mla_kernel(const RopeArgs a
   const unsigned token = blockIdx.x * (unsigned)(kRopeThreads / 32) + threadIdx.x / 32;
   if (token >= a.tokens) return;   // the whole warp, as below
   const Token tk = token_of(a, token, lane == 0);
-  const long crow = tk.ok ? rope_page(a, tk, lane == 0) : -1;
+  const long crow = tk.ok ? rope_page(a, tk, token, lane == 0) : -1;
   if (crow < 0) return;
 
   const Pieces pc = pieces<D>(lane, 0);

@@ -25,6 +25,7 @@ KVQ_FP8_E4M3, KVQ_NVFP4 = 1, 2
 KVQ_OUT_F32, KVQ_OUT_BF16, KVQ_OUT_E4M3 = 0, 1, 2
 KVQ_DEVERR_WAIT_TIMEOUT, KVQ_DEVERR_SEQ_CLAMPED = 1, 2
 KVQ_DEVERR_BAD_PAGE, KVQ_DEVERR_BAD_POSITION = 4, 8
+KVQ_DEVERR_REFUSED, KVQ_DEVERR_BAD_POOL = 16, 32
 KVQ_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 _i32 = ctypes.c_int32
@@ -66,6 +67,20 @@ class kvq_heads(ctypes.Structure):
     _fields_ = [("data", _P), ("token_stride", _i64), ("head_stride", _i64), ("num_heads", _i32)]
 
 
+class kvq_diff(ctypes.Structure):
+    _fields_ = [("lambda_", _P), ("norm", _P), ("eps", _f), ("gain", _f)]
+
+
+class kvq_page_plan(ctypes.Structure):
+    _fields_ = [
+        ("batch", _i32), ("page_size", _i32), ("num_pages", _i32), ("max_pages_per_seq", _i32),
+        ("max_tokens", _i32), ("block_table", _P), ("seq_lens", _P), ("seq_lens_out", _P),
+        ("add_lens", _P), ("free_pages", _P), ("free_count", _P), ("free_count_out", _P),
+        ("counter", _P), ("start_pos", _P), ("q_offsets", _P), ("slots", _P), ("positions", _P),
+        ("error_flag", _P),
+    ]
+
+
 _heads_p = ctypes.POINTER(kvq_heads)
 
 # name -> (restype, argtypes); the exported surface of include/kvq.h
@@ -98,6 +113,15 @@ SIGNATURES = {
     "kvq_rope_append": (_int, [ctypes.POINTER(kvq_cache), ctypes.POINTER(kvq_rotary), _int, _int,
                                _P, _P, _heads_p, _heads_p, _heads_p, _heads_p, _heads_p, _int, _f,
                                _P, _P, _P]),
+    "kvq_decode_diff": (_int, [ctypes.POINTER(kvq_cache), ctypes.POINTER(kvq_decode_params),
+                               ctypes.POINTER(kvq_diff), _P, _P, _P, _P, _P, _P]),
+    "kvq_chunk_attention": (_int, [ctypes.POINTER(kvq_cache), ctypes.POINTER(kvq_decode_params),
+                                   ctypes.POINTER(kvq_diff), _int, _P, _P, _P, _sz, _P, _P]),
+    "kvq_chunk_workspace_bytes": (_sz, [_int, _int, _int]),
+    "kvq_plan_step": (_int, [ctypes.POINTER(kvq_page_plan), _P]),
+    "kvq_rope_append_slots": (_int, [ctypes.POINTER(kvq_cache), ctypes.POINTER(kvq_rotary), _int,
+                                     _P, _P, _heads_p, _heads_p, _heads_p, _heads_p, _heads_p,
+                                     _int, _f, _P, _P, _P]),
 }
 
 _lock = threading.Lock()
@@ -280,12 +304,48 @@ def kvq_rope_append(cache: kvq_cache, rotary: kvq_rotary, batch: int, n_tokens: 
                                  _addr(error_flag), _stream(stream))
 
 
+def kvq_plan_step(plan: kvq_page_plan, stream=None) -> int:
+    """A step's block-table entries, lengths, offsets, slots and positions."""
+    return lib().kvq_plan_step(_ref(plan), _stream(stream))
+
+
+def kvq_rope_append_slots(cache: kvq_cache, rotary: kvq_rotary, num_tokens: int, positions, slots,
+                          k: Optional[kvq_heads], v: Optional[kvq_heads], kpe: Optional[kvq_heads],
+                          q: Optional[kvq_heads], q_out: Optional[kvq_heads], q_fp8: int,
+                          q_scale: float, q_head_scale, error_flag=None, stream=None) -> int:
+    """kvq_rope_append of a packed step's rows into their slots."""
+    return lib().kvq_rope_append_slots(_ref(cache), _ref(rotary), num_tokens, _addr(positions),
+                                       _addr(slots), _ref(k), _ref(v), _ref(kpe), _ref(q),
+                                       _ref(q_out), q_fp8, q_scale, _addr(q_head_scale),
+                                       _addr(error_flag), _stream(stream))
+
+
 def kvq_decode_shared(cache: kvq_cache, params: kvq_decode_params, prefix_len: int, prefix_table,
                       prefix_splits: int, q, part_o, part_lse, counters, out, stream=None) -> int:
     """kvq_decode with the batch's shared first prefix_len tokens computed once."""
     return lib().kvq_decode_shared(_ref(cache), _ref(params), prefix_len, _addr(prefix_table),
                                    prefix_splits, _addr(q), _addr(part_o), _addr(part_lse),
                                    _addr(counters), _addr(out), _stream(stream))
+
+
+def kvq_decode_diff(cache: kvq_cache, params: kvq_decode_params, diff: kvq_diff, q, part_o, part_lse,
+                    counters, out, stream=None) -> int:
+    """kvq_decode with differential heads (partials for twice num_q_heads)."""
+    return lib().kvq_decode_diff(_ref(cache), _ref(params), _ref(diff), _addr(q), _addr(part_o),
+                                 _addr(part_lse), _addr(counters), _addr(out), _stream(stream))
+
+
+def kvq_chunk_attention(cache: kvq_cache, params: kvq_decode_params, diff: Optional[kvq_diff],
+                        num_tokens: int, q_offsets, q, workspace, workspace_bytes: int, out,
+                        stream=None) -> int:
+    """Causal attention of a packed ragged step over the cache."""
+    return lib().kvq_chunk_attention(_ref(cache), _ref(params), _ref(diff), num_tokens,
+                                     _addr(q_offsets), _addr(q), _addr(workspace), workspace_bytes,
+                                     _addr(out), _stream(stream))
+
+
+def kvq_chunk_workspace_bytes(num_sms: int, batch: int, head_dim: int) -> int:
+    return int(lib().kvq_chunk_workspace_bytes(num_sms, batch, head_dim))
 
 
 def kvq_shared_splits(num_sms: int, batch: int, num_kv_heads: int, q_per_kv: int, prefix_len: int,

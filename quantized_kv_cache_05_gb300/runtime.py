@@ -52,7 +52,9 @@ def _calls():
                                "`python -c 'import __graft_entry__ as g; g.build()'`") from e
         ptr = lambda f: ctypes.cast(f, ctypes.c_void_p).value
         m.bind(ptr(L.kvq_norm_rope), ptr(L.kvq_rope_append), ptr(L.kvq_decode_shared),
-               torch.bfloat16, torch.uint8, torch.int32, torch.float32)
+               ptr(L.kvq_plan_step), ptr(L.kvq_rope_append_slots), ptr(L.kvq_decode_diff),
+               ptr(L.kvq_chunk_attention), torch.bfloat16, torch.uint8, torch.int32, torch.float32,
+               torch.int64)
         _call = m
     return _call
 
@@ -308,6 +310,142 @@ class QuantizedKVCache:
             kvq.check(st, "kvq_rope_append")
         return q_out
 
+    def append_slots(self, rotary: Rotary, k_new: torch.Tensor, v_new: Optional[torch.Tensor],
+                     slots: torch.Tensor, positions: Optional[torch.Tensor],
+                     kpe_new: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                     q_out: Optional[torch.Tensor] = None, q_out_type: Optional[str] = None,
+                     q_scale: float = 1.0, q_head_scale: Optional[torch.Tensor] = None,
+                     error_flag: Optional[torch.Tensor] = None,
+                     stream=None) -> Optional[torch.Tensor]:
+        """``append_rope`` of a packed step (kvq_rope_append_slots): k_new/v_new bf16
+        [T][Hkv][D], q bf16 [T][Hq][D] (strided as there), slots int64 [T] and positions
+        int32 [T] as a StepPlan gives them; MLA: k_new the latents [T][1][512], kpe_new
+        [T][1][64].  Returns q_out, as there."""
+        fp8 = False
+        if q is not None:
+            kind = q_out_type or ("e4m3" if q_out is not None and q_out.dtype == torch.uint8 else "bf16")
+            q_out = _query_out(q, q_out, kind, stream)
+            fp8 = kind == "e4m3"
+        dev = _launch_device(rotary.device, self.k_codes.get_device())
+        c = self.struct()
+        addr, nq, nk = rotary._args
+        st = (_call or _calls()).append_slots(
+            dev, kvq._stream(stream), ctypes.addressof(c), addr, nq, nk, k_new, v_new, kpe_new, slots,
+            positions, q, q_out, fp8, q_scale, q_head_scale, error_flag)
+        if st:
+            kvq.check(st, "kvq_rope_append_slots")
+        return q_out
+
+
+class PagePool:
+    """The free pages of a cache: a stack on the GPU (``kvq_page_plan``).  free int32
+    [num_pages], of which the first count[0] are free."""
+
+    def __init__(self, num_pages: int, device: str | torch.device = "cuda"):
+        _check(num_pages >= 1, "num_pages: at least one")
+        self._set(torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device),
+                  torch.tensor([num_pages], dtype=torch.int32, device=device))
+
+    @classmethod
+    def wrap(cls, free: torch.Tensor, count: torch.Tensor) -> "PagePool":
+        """A pool over tensors that the caller holds: int32 [num_pages] and [1]."""
+        for t, what in ((free, "free"), (count, "count")):
+            _here(t, torch.int32, what)
+            _check(t.dim() == 1 and t.is_contiguous(), f"{what}: expected a dense vector")
+        _check(free.numel() >= 1 and count.numel() == 1, "expected [num_pages] and one count")
+        self = cls.__new__(cls)
+        self._set(free, count)
+        return self
+
+    def _set(self, free: torch.Tensor, count: torch.Tensor) -> None:
+        self._free, self._count = free, count
+        self._counter = torch.zeros(1, dtype=torch.int32, device=free.device)
+
+    # read-only: plans keep their addresses
+    free = property(lambda self: self._free)
+    count = property(lambda self: self._count)
+    counter = property(lambda self: self._counter)
+
+
+class StepPlan:
+    """The paging of a step on the GPU (kvq_plan_step): block-table entries, lengths,
+    offsets, slots and positions from the changes of the requests' lengths.  It keeps
+    the tables and its outputs, which every call overwrites: start_pos [batch],
+    q_offsets [batch + 1], positions [max_tokens] (int32) and slots [max_tokens]
+    (int64).  Calls of the plans of one pool must not overlap on the GPU."""
+
+    def __init__(self, block_table: torch.Tensor, page_size: int, pool: PagePool, max_tokens: int):
+        """block_table int32 [batch][pages], of the cache whose free pages the pool has;
+        max_tokens: rows of the packed step."""
+        device = pool.free.device
+        _with(block_table, torch.int32, device, "block_table")
+        _check(block_table.dim() == 2 and block_table.is_contiguous(),
+               "block_table: expected a contiguous [batch][pages]")
+        _check(max_tokens >= 0, "max_tokens: expected 0 or more")
+        B = block_table.shape[0]
+        new = lambda n, dtype=torch.int32: torch.empty(n, dtype=dtype, device=device)
+        self._tensors = (block_table, pool, new(B), new(B + 1), new(max_tokens, torch.int64),
+                         new(max_tokens))
+        p = self._struct = kvq.kvq_page_plan()
+        p.batch, p.page_size, p.num_pages = B, page_size, pool.free.numel()
+        p.max_pages_per_seq, p.max_tokens = block_table.shape[1], max_tokens
+        ptr = lambda t: t.data_ptr()
+        p.block_table, p.free_pages, p.free_count = ptr(block_table), ptr(pool.free), ptr(pool.count)
+        p.counter = ptr(pool.counter)
+        p.start_pos, p.q_offsets, p.slots, p.positions = map(ptr, self._tensors[2:])
+        self._device = block_table.get_device()
+
+    # read-only: the struct holds their addresses
+    block_table = property(lambda self: self._tensors[0])
+    pool = property(lambda self: self._tensors[1])
+    start_pos = property(lambda self: self._tensors[2])
+    q_offsets = property(lambda self: self._tensors[3])
+    slots = property(lambda self: self._tensors[4])
+    positions = property(lambda self: self._tensors[5])
+
+    def __call__(self, seq_lens: torch.Tensor, add_lens: torch.Tensor,
+                 seq_lens_out: Optional[torch.Tensor] = None,
+                 count_out: Optional[torch.Tensor] = None,
+                 error_flag: Optional[torch.Tensor] = None, stream=None) -> "StepPlan":
+        """seq_lens and add_lens int32 [batch]: the lengths, and the tokens that come
+        (below zero: go).  The new lengths and the pool's count replace the old ones, or
+        go to the given tensors.  Returns itself."""
+        dev = _launch_device(self._device)
+        st = (_call or _calls()).plan_step(dev, kvq._stream(stream), ctypes.addressof(self._struct),
+                                           seq_lens, add_lens, seq_lens_out, count_out, error_flag)
+        if st:
+            kvq.check(st, "kvq_plan_step")
+        return self
+
+
+class Differential:
+    """What differential heads subtract and how they are normed (``kvq_diff``): lam
+    float32 [num_q_heads], norm float32 [head_dim] or None, gain (usually 1 -
+    lambda_init).  It keeps these tensors, whose addresses its struct holds."""
+
+    def __init__(self, lam: torch.Tensor, norm: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                 gain: float = 1.0):
+        for t, what in ((lam, "lam"), (norm, "norm")):
+            if t is not None:
+                _here(t, torch.float32, what)
+                _check(t.dim() == 1 and t.is_contiguous(), f"{what}: expected a dense vector")
+        self._tensors = lam, norm
+        self._struct = kvq.kvq_diff(lam.data_ptr(), norm.data_ptr() if norm is not None else None,
+                                    eps, gain)
+
+    lam = property(lambda self: self._tensors[0])
+    norm = property(lambda self: self._tensors[1])
+
+    def struct(self) -> kvq.kvq_diff:
+        return self._struct
+
+    def _for(self, num_q_heads: int, head_dim: int, device: torch.device) -> int:
+        """The struct's address, for heads of this kind."""
+        _with(self.lam, torch.float32, device, "lam")
+        _check(self.lam.numel() == num_q_heads, "lam: one per query head")
+        _check(self.norm is None or self.norm.numel() == head_dim, "norm: one weight per element")
+        return ctypes.addressof(self._struct)
+
 
 @dataclasses.dataclass
 class DecodeConfig:
@@ -491,3 +629,109 @@ class SharedDecode:
         if st:
             kvq.check(st, "kvq_decode_shared")
         return ws.out
+
+
+class DiffDecode:
+    """Decode steps of differential heads (kvq_decode_diff): the configuration and its
+    scratch, kept between steps.  Steps of one object must not overlap on the GPU (they
+    share the scratch)."""
+
+    def __init__(self, cache: QuantizedKVCache, batch: int, num_q_heads: int, max_kv_len: int,
+                 sm_scale: float, diff: Differential, out: str = "bf16", out_scale: float = 1.0,
+                 q_fp8: bool = False, q_scale: float = 1.0,
+                 q_head_scale: Optional[torch.Tensor] = None, splits: Optional[int] = None,
+                 fresh_tokens: int = 0):
+        """num_q_heads counts differential heads (two queries of head_dim / 2 each);
+        splits: chunks of a request's tokens, by default kvq_auto_splits'."""
+        _check(batch <= cache.block_table.shape[0], "more requests than the block table has")
+        _check(num_q_heads % cache.Hkv == 0, "num_q_heads: a multiple of the kv heads")
+        device = cache.k_codes.device
+        if splits is None:
+            sms = torch.cuda.get_device_properties(device).multi_processor_count
+            st, splits = kvq.kvq_auto_splits(sms, max(batch, 1), cache.Hkv,
+                                             2 * num_q_heads // cache.Hkv, max_kv_len,
+                                             FMT[cache.fmt])
+            kvq.check(st, "kvq_auto_splits")
+        cfg = self._cfg = DecodeConfig(batch, num_q_heads, cache.D, cache.D, splits, max_kv_len,
+                                       sm_scale, out=out, out_scale=out_scale,
+                                       fresh_tokens=fresh_tokens, q_fp8=q_fp8, q_scale=q_scale,
+                                       q_head_scale=_head_scale(q_head_scale, num_q_heads, device))
+        self._cache, self._diff = cache, (diff, diff._for(num_q_heads, cache.D, device))
+        # the call's own checks, without requests
+        none = dataclasses.replace(cfg, batch=0).params(None)
+        kvq.check(kvq.kvq_decode_diff(cache.struct(), none, diff.struct(), None, None, None, None,
+                                      None, 0), "DiffDecode")
+        two = dataclasses.replace(cfg, num_q_heads=2 * num_q_heads)
+        self._ws = FusedWorkspace(two, cache.Hkv, device)
+        self._out = torch.empty((batch, num_q_heads, cache.D), dtype=OUT_TORCH[out], device=device)
+        self._params = cfg.params(None)   # the lengths and the flag come with each step
+
+    cache = property(lambda self: self._cache)
+    diff = property(lambda self: self._diff[0])
+    cfg = property(lambda self: dataclasses.replace(self._cfg))
+
+    def __call__(self, q: torch.Tensor, seq_lens: torch.Tensor,
+                 error_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """q bf16 (FP8 query: uint8) [batch][Hq][D], seq_lens int32 [batch] -> the output
+        buffer [batch][Hq][D], overwritten by the next step (streams: as SharedDecode)."""
+        ws, cache = self._ws, self._cache
+        dev = _launch_device(cache.k_codes.get_device())
+        call = _call or _calls()
+        call.block_table(dev, cache.block_table, self._cfg.batch)
+        c = cache.struct()
+        st = call.decode_diff(dev, kvq._stream(stream), ctypes.addressof(c),
+                              ctypes.addressof(self._params), self._diff[1], q, seq_lens, ws.part_o,
+                              ws.part_lse, ws.counters, self._out, error_flag)
+        if st:
+            kvq.check(st, "kvq_decode_diff")
+        return self._out
+
+
+class ChunkAttention:
+    """Causal attention of packed steps over the cache (kvq_chunk_attention): prompt
+    chunks and single tokens together, with plain or differential heads.  It keeps the
+    configuration and the workspace; steps of one object must not overlap on the GPU."""
+
+    def __init__(self, cache: QuantizedKVCache, batch: int, num_q_heads: int, max_kv_len: int,
+                 sm_scale: float, out: str = "bf16", out_scale: float = 1.0, q_fp8: bool = False,
+                 q_scale: float = 1.0, q_head_scale: Optional[torch.Tensor] = None,
+                 diff: Optional[Differential] = None):
+        _check(batch <= cache.block_table.shape[0], "more requests than the block table has")
+        device = cache.k_codes.device
+        cfg = self._cfg = DecodeConfig(batch, num_q_heads, cache.D, cache.D, 1, max_kv_len, sm_scale,
+                                       out=out, out_scale=out_scale, q_fp8=q_fp8, q_scale=q_scale,
+                                       q_head_scale=_head_scale(q_head_scale, num_q_heads, device))
+        self._cache = cache
+        self._diff = (diff, diff._for(num_q_heads, cache.D, device) if diff is not None else 0)
+        # the call's own checks, without requests
+        none = dataclasses.replace(cfg, batch=0).params(None)
+        kvq.check(kvq.kvq_chunk_attention(cache.struct(), none, diff.struct() if diff else None, 0,
+                                          None, None, None, 0, None, 0), "ChunkAttention")
+        sms = torch.cuda.get_device_properties(device).multi_processor_count
+        self._ws = torch.empty(kvq.kvq_chunk_workspace_bytes(sms, batch, cache.D), dtype=torch.uint8,
+                               device=device)
+        self._params = cfg.params(None)
+
+    cache = property(lambda self: self._cache)
+    diff = property(lambda self: self._diff[0])
+    cfg = property(lambda self: dataclasses.replace(self._cfg))
+
+    def __call__(self, q: torch.Tensor, q_offsets: torch.Tensor, seq_lens: torch.Tensor,
+                 out: Optional[torch.Tensor] = None, error_flag: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+        """q bf16 (FP8 query: uint8) [tokens][Hq][D], q_offsets int32 [batch + 1] (a
+        StepPlan's), seq_lens int32 [batch] (with the new tokens) -> out [tokens][Hq][D],
+        a new tensor unless one is given (a new one belongs to the given stream)."""
+        cache, kind = self._cache, OUT_TORCH[self._cfg.out]
+        if out is None:
+            out = _rows_like(q, kind, stream)
+        dev = _launch_device(cache.k_codes.get_device())
+        call = _call or _calls()
+        call.block_table(dev, cache.block_table, self._cfg.batch)
+        c = cache.struct()
+        st = call.chunk_attention(dev, kvq._stream(stream), ctypes.addressof(c),
+                                  ctypes.addressof(self._params), self._diff[1], q, q_offsets,
+                                  seq_lens, self._ws, self._ws.numel(), out, kind, error_flag)
+        if st:
+            kvq.check(st, "kvq_chunk_attention")
+        return out
