@@ -584,7 +584,7 @@ kvq_status kvq_decode_diff(const kvq_cache* c, const kvq_decode_params* p, const
  * The work is cut by its size, over the keys too, so that all SMs get the same share of
  * it, whatever the lengths; three launches on `stream`.
  * The probabilities enter the products with V as f16 numbers: rounded to 2^-11 of
- * themselves for bf16 and E4M3 outputs, in two parts (2^-22) for fp32 outputs and for
+ * themselves for bf16 and E4M3 outputs, in two parts (2^-21) for fp32 outputs and for
  * differential heads; weights below 2^-32 of a row's largest count in the sum alone.
  * A NaN among a token's keys or values reaches the rows that attend to it and no others;
  * all dims of such a row may become NaN.

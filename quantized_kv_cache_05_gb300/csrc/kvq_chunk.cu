@@ -25,7 +25,7 @@
 //    become zeros, and the rows that see one of them become NaN as a whole.
 //  * Rounding.  P enters the products with V in one f16 part for 16- and 8-bit outputs
 //    (2^-11 of a weight, against 2^-8 of the value that a bf16 output's rounding takes), in
-//    two (2^-22) for fp32 outputs, and for differential heads, whose difference may be
+//    two (2^-21) for fp32 outputs, and for differential heads, whose difference may be
 //    small beside the two sums.  Sums and accumulators are fp32.
 // Every wait is bounded; a timeout sets an error bit and the rows become NaN.
 
@@ -40,9 +40,11 @@ namespace {
 
 constexpr int kTok = 128;                 // keys per tile, rows per accumulator
 constexpr int kCol = kTok * 128;          // bytes of 64 f16 columns of 128 rows
-constexpr int kConvWarp = 8;              // warps 0-7 softmax (slots 0, 1)
-constexpr int kConvWarps = 4;
-constexpr int kMmaWarp = kConvWarp + kConvWarps, kTmaWarp = kMmaWarp + 1;
+// The issuing warps come first: an SM sub-core's scheduler prefers its oldest warp, and
+// as the youngest the MMA warp took some 20 cycles an instruction, with every wait on the
+// slots' critical path.
+constexpr int kMmaWarp = 0, kTmaWarp = 1, kSoftWarp = 4, kConvWarp = 12;
+constexpr int kSoftWarps = 8, kConvWarps = 4;   // softmax: four for each of the slots 0, 1
 constexpr int kThreads = 512;             // four warpgroups: softmax x 2, convert, MMA and TMA
 // Registers per thread of the warpgroups (the launch gives each thread 128, 512
 // for the four): a softmax thread holds its row's 128 scores at once.
@@ -328,7 +330,7 @@ struct ChunkGeom {
 struct ChunkCtl {
   uint64_t raw_full[2][4], raw_empty[2][4];   // [K, V][slot]
   uint64_t op_full[2][2], op_empty[2][2];     // [K, V][operand tile]
-  uint64_t s_full[2], p_full[2][2], o_full[2];   // per softmax slot (P: per half of the keys)
+  uint64_t s_full[2], p_full[2], o_full[2];   // per softmax slot
   uint64_t q_full, mma_done;
   uint32_t tmem;
   int abort_flag;
@@ -337,6 +339,9 @@ struct ChunkCtl {
   // scales (a[0]), then their states (a: maximum, b: sum); with differential heads the
   // factors of the sums (a) and the sums of squares of the halves (b)
   float a[2][kTok], b[2][kTok];
+  // the softmax warps' places and pieces: their registers are for the scores
+  Cut at[kSoftWarps];
+  Piece piece[kSoftWarps];
 };
 
 // A row's 32 output elements from element `c` on, in the output's type.
@@ -399,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sm.op_empty[i][k]), 1);
       }
       mbar_init(smem_u32(&sm.s_full[i]), 1);
-      for (int k = 0; k < 2; ++k) mbar_init(smem_u32(&sm.p_full[i][k]), 4);
+      mbar_init(smem_u32(&sm.p_full[i]), 4);
       mbar_init(smem_u32(&sm.o_full[i]), 1);
     }
     mbar_init(smem_u32(&sm.q_full), 8);
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   Piece p;
 
-  if (warp >= kMmaWarp) {
+  if (warp < kSoftWarp) {
     regs_dec<kRegIssue>();
     if (warp == kTmaWarp) {
       // ================================================================= TMA
@@ -500,83 +505,92 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 2; ++t)
           for (int i = max(0, issued[t] - Cg::kSlots); i < issued[t]; ++i)
             mbar_wait(smem_u32(&sm.raw_full[t][i % Cg::kSlots]), (i / Cg::kSlots) & 1);
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp && elect_lane()) {
       // ================================================================= MMA
-      // The warp stays converged, its elected lane issues; tensor memory
-      // starts at column 0 (all of it is this CTA's).
+      // One thread, with as few instructions as there can be between a wait and the
+      // products: beside the softmax warps each takes many cycles, and all of them are on
+      // the slots' critical path.  Tensor memory starts at column 0 (all of it is this
+      // CTA's).  A unit is a key tile in a slot: both slots take every tile, or turns.  In
+      // its slot a unit's S follows the earlier one's P V, whose P's columns it needs, and
+      // the two are issued together, so that the slots take turns on the tensor pipe, one in
+      // its products while the other is in its softmax.  (A warp for each slot runs the
+      // slots in step instead: 290 us against 208 for 2048 rows x 32 heads behind 6144
+      // tokens.)
       constexpr uint32_t kIdS = idesc(0, 0, 0, kTok), kIdO = idesc(0, 0, 1, D);
       const uint64_t dq = sdesc(base, 16, 1024);
       const uint64_t dk = sdesc(base + Cg::kOffK, 16, 1024);
       const uint64_t dv = sdesc(base + Cg::kOffV, kCol, 1024);   // MN-major
-      auto wait_warp = [&](uint64_t& bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, wait(bar, parity));
-      };
-      bool ok = true;
-      int j0 = 0, pieces = 0;          // key tiles and pieces before this one
-      int done[2] = {0, 0};            // units of each slot whose P has been taken
-      while (ok && walk.next(p)) {
-        const bool two = two_rows(p);
-        const int nt = p.kv1 - p.kv0, units = two ? 2 * nt : nt;
-        ok = wait_warp(sm.q_full, pieces & 1);
-        ++pieces;
-        // unit u: slot u & 1; the piece's key tile u / 2 or u
-        auto issue_s = [&](int u) {
-          const int j = j0 + (two ? u >> 1 : u), slot = u & 1;
-          // the first use of a K tile waits for it
-          if (!two || slot == 0) ok = ok && wait_warp(sm.op_full[0][j & 1], (j >> 1) & 1);
-          if (!ok) return;
+      unsigned jk = 0, jv = 0;         // key tiles whose S, whose P V is issued
+      unsigned taken[2] = {0, 0};      // units of each slot whose P has been taken
+      // P V of key tile jv and S of key tile jk in a slot (either may be missing)
+      auto step = [&](auto slot_c, bool product, bool score, bool two, bool acc) -> bool {
+        constexpr int slot = decltype(slot_c)::value;
+        // (a tile's V is converted before the next one's K)
+        if (score) {
+          if (!(two && slot == 1) && !wait(sm.op_full[0][jk & 1], (jk >> 1) & 1)) return false;
+        } else if (!wait(sm.op_full[1][jv & 1], (jv >> 1) & 1)) {
+          return false;
+        }
+        if (product) {
+          const uint64_t v = dv + (jv & 1) * (unsigned)(Cg::kTile >> 4);
+          constexpr uint32_t pc = slot * 128, o = 256 + slot * 128;
+          if (!wait(sm.p_full[slot], taken[slot] & 1)) return false;
           tc_fence_after();
-          const uint64_t q = dq + (uint64_t)((two ? slot : 0) * Cg::kTile >> 4);
-          const uint64_t k = dk + (uint64_t)((j & 1) * Cg::kTile >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kTok / 16; ++kk) {
+            const uint64_t vk = v + (kk * 2048 >> 4);
+            if constexpr (P2) {   // high parts and residuals in alternating 16-column groups
+              const uint32_t pk = pc + 32 * (kk >> 1) + 8 * (kk & 1);
+              mma_ts(o, pk, vk, kIdO, kk > 0 || acc);
+              mma_ts(o, pk + 16, vk, kIdO, true);
+            } else {
+              mma_ts(o, pc + 8 * kk, vk, kIdO, kk > 0 || acc);
+            }
+          }
+          ++taken[slot];
+        }
+        if (score) {
           constexpr int kSteps = D / 16 / (DIFF ? 2 : 1);
-          const int k0 = DIFF ? slot * kSteps : 0;   // differential: the map's half of the dims
+          constexpr int k0 = DIFF ? slot * kSteps : 0;   // differential: the map's half of the dims
+          const uint64_t k = dk + (jk & 1) * (unsigned)(Cg::kTile >> 4);
+          const uint64_t q = dq + (two ? slot * Cg::kTile >> 4 : 0);
 #pragma unroll
           for (int s = 0; s < kSteps; ++s) {
             const int kk = k0 + s;
-            const uint64_t off = (uint64_t)(((kk >> 2) * kCol + (kk & 3) * 32) >> 4);
-            mma_ss_elect(slot * 128, q + off, k + off, kIdS, s > 0);
+            const uint64_t off = ((kk >> 2) * kCol + (kk & 3) * 32) >> 4;
+            mma(slot * 128, q + off, k + off, kIdS, s > 0);
           }
-          mma_commit_elect(smem_u32(&sm.s_full[slot]));
-          if (!two || slot == 1) mma_commit_elect(smem_u32(&sm.op_empty[0][j & 1]));
-        };
-        for (int u = 0; u < min(2, units) && ok; ++u) issue_s(u);
-        for (int u = 0; u < units && ok; ++u) {
-          const int j = j0 + (two ? u >> 1 : u), slot = u & 1;
-          const bool acc = u > 1;      // not the slot's first unit of the piece
-          const uint64_t v = dv + (uint64_t)((j & 1) * Cg::kTile >> 4);
-          const uint32_t pc = slot * 128, o = 256 + slot * 128;
-          if (!two || slot == 0) ok = wait_warp(sm.op_full[1][j & 1], (j >> 1) & 1);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {   // the halves of P, as they are written
-            ok = ok && wait_warp(sm.p_full[slot][half], done[slot] & 1);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int k4 = 0; k4 < kTok / 32; ++k4) {
-              const int kk = half * (kTok / 32) + k4;
-              const uint64_t vk = v + (uint64_t)(kk * 2048 >> 4);
-              if constexpr (P2) {   // high parts and residuals in alternating 16-column groups
-                const uint32_t pk = pc + 32 * (kk >> 1) + 8 * (kk & 1);
-                mma_ts_elect(o, pk, vk, kIdO, acc || kk > 0);
-                mma_ts_elect(o, pk + 16, vk, kIdO, true);
-              } else {
-                mma_ts_elect(o, pc + 8 * kk, vk, kIdO, acc || kk > 0);
-              }
-            }
-          }
-          if (!ok) break;
-          ++done[slot];
-          mma_commit_elect(smem_u32(&sm.o_full[slot]));
-          if (!two || slot == 1) mma_commit_elect(smem_u32(&sm.op_empty[1][j & 1]));
-          if (u + 2 < units) issue_s(u + 2);
+          mma_commit(smem_u32(&sm.s_full[slot]));
+        } else {                       // the slot's last of the piece
+          mma_commit(smem_u32(&sm.o_full[slot]));
         }
-        j0 += nt;
+        if (!two || slot == 1) {       // the tiles are free
+          if (score) mma_commit(smem_u32(&sm.op_empty[0][jk++ & 1]));
+          if (product) mma_commit(smem_u32(&sm.op_empty[1][jv++ & 1]));
+        }
+        return true;
+      };
+      using Zero = std::integral_constant<int, 0>;
+      using One = std::integral_constant<int, 1>;
+      unsigned pieces = 0;
+      bool ok = true;
+      while (ok && walk.next(p)) {
+        const bool two = two_rows(p);
+        const int nt = p.kv1 - p.kv0, units = two ? 2 * nt : nt;
+        ok = wait(sm.q_full, pieces++ & 1);
+        tc_fence_after();
+#pragma unroll 1
+        for (int u = 0; u < units + 2 && ok; u += 2) {
+          if (u < units || u - 2 < units) ok = step(Zero{}, u >= 2, u < units, two, u > 2);
+          if (ok && (u + 1 < units || (u >= 2 && u - 1 < units)))
+            ok = step(One{}, u >= 2, u + 1 < units, two, u > 2);
+        }
       }
       // every MMA has completed at exit (bounded wait)
-      mma_commit_elect(smem_u32(&sm.mma_done));
+      mma_commit(smem_u32(&sm.mma_done));
       mbar_wait(smem_u32(&sm.mma_done), 0);
-      __syncwarp();
     }
+    __syncwarp();
   } else if (warp >= kConvWarp) {
     regs_dec<kRegConv>();
     // ============================================================= convert
@@ -682,13 +696,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     regs_inc<kRegSoft>();
     // ============================================================= softmax
-    const int slot = (warp >> 2) & 1, r = threadIdx.x & (kTok - 1);
+    const int sw = warp - kSoftWarp, slot = sw >> 2, r = threadIdx.x & (kTok - 1);
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t sS = lane_addr + slot * 128, sO = lane_addr + 256 + slot * 128;
-    int j0 = 0;        // key tiles before the piece
-    int units = 0;     // of this slot, before the piece
-    bool ok = true;    // (after a timeout the pieces' barriers are still met)
-    while (walk.next(p)) {
+    unsigned j0 = 0;      // key tiles before the piece
+    unsigned units = 0;   // of this slot, before the piece
+    unsigned ends = 0;    // pieces before in which this slot had units
+    bool ok = true;       // (after a timeout the pieces' barriers are still met)
+    if (lane == 0) sm.at[sw] = walk.at;
+    __syncwarp();
+    while (true) {
+      {
+        Walk w = walk;
+        w.at = sm.at[sw];
+        if ((int)blockIdx.x < head.shares) w.end = cuts[blockIdx.x + 1];
+        if (!w.next(p)) break;
+        __syncwarp();
+        if (lane == 0) {
+          sm.at[sw] = w.at;
+          sm.piece[sw] = p;
+        }
+        __syncwarp();
+      }
       const bool two = two_rows(p);
       const int nt = p.kv1 - p.kv0;
       const int R = p.r.n * a.G;                                    // the request's rows
@@ -806,11 +835,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cnt = two ? nt : (nt + 1 - slot) / 2;
       float m = -INFINITY, l = 0.f;   // reference max (log2), sum of 2^(x - m + 7)
       bool poison = false;            // sees a token whose values are NaN
-      const int all = p.r.L - p.r.n + p.tile * kRt / a.G + 1;   // keys that every row sees
+      // keys from the piece's first on that this row sees, and that every row does
+      const int mine = seen - p.kv0 * kTok;
+      const int every = p.r.L - p.r.n + p.tile * kRt / a.G + 1 - p.kv0 * kTok;
+      asm volatile("" ::: "memory");   // (what follows reads the piece from shared memory)
       for (int i = 0; i < cnt && ok; ++i) {
         const int jj = two ? i : 2 * i + slot;         // key tile of the piece
-        const int kt = p.kv0 + jj;
-        const int nvalid = seen - kt * kTok;           // keys of this tile that the row sees
+        const int nvalid = mine - jj * kTok;           // keys of this tile that the row sees
         ok = __all_sync(0xffffffffu, wait(sm.s_full[slot], (units + i) & 1));
         if (!ok) break;
         tc_fence_after();
@@ -819,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32(sS + 32 * c, s[c]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_wait_ld32(s[c]);
-        if ((kt + 1) * kTok > all) {   // some row does not see all of it
+        if ((jj + 1) * kTok > every) {   // some row does not see all of it
           if (__any_sync(0xffffffffu, nvalid < kTok)) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -828,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (32 * c + k >= nvalid) s[c][k] = 0xFF800000u;   // -inf
           }
           // the V operand tile of the same number: converted, with its NaN rows listed
-          const int j = j0 + jj;
+          const unsigned j = j0 + jj;
           ok = __all_sync(0xffffffffu, wait(sm.op_full[1][j & 1], (j >> 1) & 1));
           if (!ok) break;
 #pragma unroll
@@ -879,29 +910,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pack2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), q2, r2));
             const float p0 = ex2(x.x), p1 = ex2(x.y);
             sum2 = add2(sum2, pack2(p0, p1));
-            hi[k] = pack_f16x2(p0, p1);
-            if constexpr (P2) {
-              const float2 f = unpack_f16x2(hi[k]);
-              lo[k] = pack_f16x2(p0 - f.x, p1 - f.y);
+            if constexpr (P2) {   // the leading 11 bits, and what is left
+              const float h0 = __uint_as_float(__float_as_uint(p0) & 0xFFFFE000u);
+              const float h1 = __uint_as_float(__float_as_uint(p1) & 0xFFFFE000u);
+              hi[k] = pack_f16x2(h0, h1);
+              const float2 r = unpack2(fma2(pack2(h0, h1), pack2(-1.f, -1.f), pack2(p0, p1)));
+              lo[k] = pack_f16x2(r.x, r.y);
+            } else {
+              hi[k] = pack_f16x2(p0, p1);
             }
           }
           tmem_st16(sS + (P2 ? 32 * c : 16 * c), hi);
           if constexpr (P2) tmem_st16(sS + 32 * c + 16, lo);
-          if (c & 1) {   // half of P is written (and O rescaled): its MMAs may go
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[slot][c >> 1]));
-          }
         }
+        // P is written (and O rescaled): its products may go.  (Handed over in halves, each
+        // with a wait of its own: 722 us against 685 for 4096 rows x 32 heads behind 12288
+        // tokens.)
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[slot]));
         const float2 sum = unpack2(sum2);
         l += sum.x + sum.y;
       }
       if (poison) l = NAN;
       j0 += nt;
       units += cnt;
+      __syncwarp();
+      p = *const_cast<const Piece*>(&sm.piece[sw]);
 
       // ---- the rows' results
+      asm volatile("" ::: "memory");
       // f[s] is the factor of slot s's accumulator, lse the row's.  Joined (one
       // accumulator's rows, or differential heads written whole): each slot does half of
       // the dims of both accumulators.
@@ -933,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.a[slot][r] = two ? own : m;
         if (!two) sm.b[slot][r] = l;
       }
-      if (cnt > 0) ok = ok && wait(sm.o_full[slot], (units - 1) & 1);
+      if (cnt > 0) ok = ok && wait(sm.o_full[slot], ends++ & 1);
       tc_fence_before();
       if (join) asm volatile("bar.sync 1, 256;" ::: "memory");   // both accumulators are done
       const bool bad = __any_sync(0xffffffffu, !ok || *abort_flag != 0);
