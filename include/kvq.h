@@ -575,15 +575,17 @@ kvq_status kvq_decode_diff(const kvq_cache* c, const kvq_decode_params* p, const
  *   q   (device) bf16, or E4M3 codes (p->q_fp8), [num_tokens][Hq][head_dim], 16-byte
  *       aligned
  *   out (device) [num_tokens][Hq][head_dim], 16-byte aligned
- *   workspace (device) kvq_chunk_workspace_bytes of the device's SMs, p->batch and
- *       head_dim, 32-byte aligned; nothing in it has to be kept or cleared between calls.
+ *   workspace (device) kvq_chunk_workspace_bytes for the device's SMs, 32-byte aligned;
+ *       nothing in it has to be kept or cleared between calls.
  * Uses batch, num_q_heads, qk_dim = v_dim = head_dim, seq_lens, max_kv_len, sm_scale,
  * out_dtype, out_scale, error_flag and the FP8 query of p (num_splits and fresh_tokens
  * are ignored; prob_scale must be 0).  FP8 and NVFP4 caches with head_dim 64 or 128 and
  * any number of query heads per kv head, per-head scales; not MLA, batch <= 8192.
- * The work is cut by its size, over the keys too, so that all SMs get the same share of
- * it, whatever the lengths; three launches on `stream`.
- * The probabilities enter the products with V as f16 numbers: rounded to 2^-11 of
+ * The chunks' work is cut by its size, over the keys too, so that all SMs get the same
+ * share of it, whatever the lengths.  In a batch of more than one, requests with a single
+ * new token are the split-KV decode's (at most 16 query rows per kv head, 8 differential
+ * ones; with more they count as chunks).  Three or four launches on `stream`.
+ * The chunks' probabilities enter the products with V as f16 numbers: rounded to 2^-11 of
  * themselves for bf16 and E4M3 outputs, in two parts (2^-21) for fp32 outputs and for
  * differential heads; weights below 2^-32 of a row's largest count in the sum alone.
  * A NaN among a token's keys or values reaches the rows that attend to it and no others;
@@ -594,8 +596,10 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_decode_params* p, c
                                int num_tokens, const int32_t* q_offsets, const void* q,
                                void* workspace, size_t workspace_bytes, void* out, void* stream);
 
-/* Bytes of kvq_chunk_attention's workspace (0 for arguments below 1; batch 0 counts as 1). */
-size_t kvq_chunk_workspace_bytes(int num_sms, int batch, int head_dim);
+/* Bytes of kvq_chunk_attention's workspace, for these heads, batch and max_kv_len (0 for
+ * arguments below their range); d as in the call. */
+size_t kvq_chunk_workspace_bytes(int num_sms, const kvq_cache* c, const kvq_decode_params* p,
+                                 const kvq_diff* d);
 
 /*
  * Prefill attention over the cache (Model-Optimizer PR 1832: the prefill

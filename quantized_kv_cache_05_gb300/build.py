@@ -16,7 +16,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkvq.so")
 CALL = os.path.join(HERE, "_kvq_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["kvq_api.cu", "kvq_append.cu", "kvq_chunk.cu", "kvq_decode.cu", "kvq_decode_diff.cu",
-           "kvq_decode_nvfp4.cu", "kvq_mla.cu", "kvq_plan.cu", "kvq_prefill.cu", "kvq_rope.cu", "kvq_shared.cu"]
+           "kvq_decode_nvfp4.cu", "kvq_decode_packed.cu", "kvq_mla.cu", "kvq_plan.cu",
+           "kvq_prefill.cu", "kvq_rope.cu", "kvq_shared.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # host code: no FP contraction (the host-side checks emulate device fp32
 # operations one by one)

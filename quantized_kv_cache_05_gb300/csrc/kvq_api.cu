@@ -217,6 +217,32 @@ int box_rows(int page_size) {
   return box;
 }
 
+// Workspace of kvq_chunk_attention: that of the chunks' kernels, then the counters and
+// partials of the decode that takes the requests with a single new token (splits 0: there
+// is none).  The decode reads a request's keys once for up to 16 query rows, in one
+// launch with its own split; as row tiles of 128 those few rows cost as much as full
+// ones (28 single tokens beside 4 chunks, NVFP4: 268 us, YYY with it).  A lone
+// request is never worth its launch.
+struct ChunkParts {
+  int splits;
+  size_t counters, lse, o, bytes;
+};
+ChunkParts chunk_parts(int sms, const kvq_cache* c, const kvq_decode_params* p, const kvq_diff* d) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  ChunkParts w{};
+  const int D = c->head_dim, rows = (d ? 2 : 1) * (p->num_q_heads / c->num_kv_heads);
+  w.counters = up(chunk_workspace_bytes(sms, std::max(p->batch, 1), D));
+  w.bytes = w.counters;
+  if (p->batch < 2 || rows > kMaxGroup ||
+      kvq_auto_splits(sms, p->batch, c->num_kv_heads, rows, p->max_kv_len, c->fmt, &w.splits) != KVQ_OK)
+    return w;
+  const size_t groups = (size_t)p->batch * c->num_kv_heads, parts = groups * rows * w.splits;
+  w.lse = w.counters + up(groups * sizeof(uint32_t));
+  w.o = w.lse + up(parts * sizeof(float));
+  w.bytes = w.o + parts * D * sizeof(float);
+  return w;
+}
+
 kvq_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
 
 // kvq_rope_append and kvq_rope_append_slots: `where` says where the tokens go.
@@ -661,11 +687,13 @@ namespace {
 // Shared body of kvq_decode_partial and kvq_decode (fused when counters), and
 // of kvq_decode_shared: with prefix_splits > 0 the requests start at token
 // prefix_len, and the merge takes the preceding kernel's prefix_splits partials
-// in too.  And of kvq_decode_diff: with `diff`, each query head is two rows.
+// in too.  Of kvq_decode_diff: with `diff`, each query head is two rows.  And of
+// kvq_chunk_attention: with q_offsets, for the requests that have one of num_tokens rows.
 kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const void* q,
                        float* part_o, float* part_lse, uint32_t* counters, void* out,
                        cudaStream_t stream, int prefix_len = 0, int prefix_splits = 0,
-                       uint32_t* ready = nullptr, const kvq_diff* diff = nullptr) {
+                       uint32_t* ready = nullptr, const kvq_diff* diff = nullptr,
+                       const int32_t* q_offsets = nullptr, int num_tokens = 0) {
   kvq_status s = check_cache(c);
   if (s != KVQ_OK) return s;
   s = check_params(p);
@@ -764,6 +792,8 @@ kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const voi
   if (!make_row_map(&m.k16, c->k_codes, row_bytes, rows) ||
       !make_row_map(&m.v16, c->v_codes, row_bytes, rows))
     return KVQ_ERR_CUDA;
+  a.q_offsets = q_offsets;
+  a.num_tokens = num_tokens;
   if (diff) {
     a.diff_lambda = diff->lambda;
     a.diff_norm = diff->norm;
@@ -771,6 +801,7 @@ kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const voi
     a.diff_gain = diff->gain;
     return cuda_status(launch_partial_diff(c->fmt, D, m, a, stream));
   }
+  if (q_offsets) return cuda_status(launch_partial_packed(c->fmt, D, m, a, stream));
   return cuda_status(launch_partial(c->fmt, D, probq, m, a, stream));
 }
 
@@ -933,9 +964,12 @@ kvq_status kvq_decode_combine(const kvq_decode_params* p, const float* part_o,
   return cuda_status(launch_combine(a, as_stream(stream)));
 }
 
-size_t kvq_chunk_workspace_bytes(int num_sms, int batch, int head_dim) {
-  if (num_sms < 1 || batch < 0 || head_dim < 1) return 0;
-  return chunk_workspace_bytes(num_sms, std::max(batch, 1), head_dim);
+size_t kvq_chunk_workspace_bytes(int num_sms, const kvq_cache* c, const kvq_decode_params* p,
+                                 const kvq_diff* d) {
+  if (num_sms < 1 || !c || !p || c->num_kv_heads < 1 || c->head_dim < 1 || p->batch < 0 ||
+      p->num_q_heads < 1 || p->max_kv_len < 0)
+    return 0;
+  return chunk_parts(num_sms, c, p, d).bytes;
 }
 
 kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_decode_params* p, const kvq_diff* d,
@@ -961,7 +995,8 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_decode_params* p, c
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return KVQ_ERR_CUDA;
-  if (workspace_bytes < chunk_workspace_bytes(sms, p->batch, D)) return KVQ_ERR_WORKSPACE;
+  const ChunkParts parts = chunk_parts(sms, c, p, d);
+  if (workspace_bytes < parts.bytes) return KVQ_ERR_WORKSPACE;
   ChunkArgs a{};
   a.q = q;
   a.q_fp8 = p->q_fp8;
@@ -1005,6 +1040,19 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_decode_params* p, c
   if (!make_row_map(&maps.k16, c->k_codes, row_bytes, rows, (uint32_t)a.box) ||
       !make_row_map(&maps.v16, c->v_codes, row_bytes, rows, (uint32_t)a.box))
     return KVQ_ERR_CUDA;
+  uint8_t* const w = a.workspace;
+  if (parts.splits > 0) a.counters = reinterpret_cast<uint32_t*>(w + parts.counters);
+  s = cuda_status(launch_shares(a, sms, as_stream(stream)));
+  if (s != KVQ_OK) return s;
+  if (parts.splits > 0) {
+    kvq_decode_params one = *p;
+    one.num_splits = parts.splits;
+    one.fresh_tokens = 0;
+    s = decode_impl(c, &one, q, reinterpret_cast<float*>(w + parts.o),
+                    reinterpret_cast<float*>(w + parts.lse), a.counters, out, as_stream(stream), 0,
+                    0, nullptr, d, q_offsets, num_tokens);
+    if (s != KVQ_OK) return s;
+  }
   return cuda_status(launch_chunk(c->fmt, D, maps, a, sms, as_stream(stream)));
 }
 

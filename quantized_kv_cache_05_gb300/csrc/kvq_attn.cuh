@@ -531,22 +531,20 @@ __device__ __forceinline__ void fused_combine_staged(const PartialArgs& a, int b
   if (!ok && threadIdx.x == 0) record_error(a.error_flag, 1);
 }
 
-// The merge of differential heads (rows 2i and 2i + 1 of the kv head are head i's two
-// maps): one warp per head forms both rows' sums, y = o1 - lambda o2, and its norm over
-// the D values that the warp holds.  Arrival, weights and staging are
-// fused_combine_staged's.
-template <int D, bool STAGED>
-__device__ __forceinline__ void merge_diff(const PartialArgs& a, size_t row0, int rows, int s,
-                                           const float* po, const float* w, const float* winv,
-                                           bool ok) {
+// The merge of whole heads, one warp for each, MAPS of the kv head's rows to a head (row
+// `row` of all requests' is the first one's, query head hq0's, whose output row is out0):
+// with two maps y = o1 - lambda o2, and its norm over the D values that the warp holds.
+// Arrival, weights and staging are fused_combine_staged's.
+template <int D, bool STAGED, int MAPS>
+__device__ __forceinline__ void merge_heads(const PartialArgs& a, int rows, int s, const float* po,
+                                            const float* w, const float* winv, bool ok,
+                                            size_t out0, int hq0) {
   constexpr int kQuads = D / 4;                       // float4 columns of a row
   constexpr int NV = (kQuads + 31) / 32;              // of a lane
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
 #pragma unroll 1
-  for (int i = threadIdx.x >> 5; i < rows / 2; i += warps) {
-    const size_t head = (row0 >> 1) + i;              // of all (request, query head)s
-    const int hq = (int)(head % (size_t)(a.Hq / 2));
-    const float lam = __ldg(a.diff_lambda + hq);
+  for (int i = threadIdx.x >> 5; i < rows / MAPS; i += warps) {
+    const float lam = MAPS == 2 ? __ldg(a.diff_lambda + hq0 / MAPS + i) : 0.f;
     float4 y[NV];
     float ss = 0.f;
 #pragma unroll
@@ -554,10 +552,10 @@ __device__ __forceinline__ void merge_diff(const PartialArgs& a, size_t row0, in
       const int q = lane + 32 * v;
       y[v] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (q >= kQuads) continue;
-      float4 o[2];
+      float4 o[MAPS];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int r = 2 * i + m;
+      for (int m = 0; m < MAPS; ++m) {
+        const int r = MAPS * i + m;
         const float4* p = reinterpret_cast<const float4*>(po) + (size_t)r * s * kQuads + q;
         const float* wr = w + r * kMaxFusedSplits;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -584,24 +582,36 @@ __device__ __forceinline__ void merge_diff(const PartialArgs& a, size_t row0, in
         const float iv = ok ? winv[r] : NAN;
         o[m] = make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
       }
-      y[v] = make_float4(o[0].x - lam * o[1].x, o[0].y - lam * o[1].y, o[0].z - lam * o[1].z,
-                         o[0].w - lam * o[1].w);
-      ss += y[v].x * y[v].x + y[v].y * y[v].y + y[v].z * y[v].z + y[v].w * y[v].w;
+      y[v] = o[0];
+      if constexpr (MAPS == 2) {
+        y[v] = make_float4(o[0].x - lam * o[1].x, o[0].y - lam * o[1].y, o[0].z - lam * o[1].z,
+                           o[0].w - lam * o[1].w);
+        ss += y[v].x * y[v].x + y[v].y * y[v].y + y[v].z * y[v].z + y[v].w * y[v].w;
+      }
     }
-    float r = a.diff_gain;
-    if (a.diff_norm) {
+    float r = 1.f;
+    if constexpr (MAPS == 2) {
+      r = a.diff_gain;
+      if (a.diff_norm) {
 #pragma unroll
-      for (int k = 16; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
-      r *= inv_rms_of(ss * (1.f / D) + a.diff_eps);
+        for (int k = 16; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+        r *= inv_rms_of(ss * (1.f / D) + a.diff_eps);
+      }
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int q = lane + 32 * v;
       if (q >= kQuads) continue;
-      const float4 n = a.diff_norm ? __ldg(reinterpret_cast<const float4*>(a.diff_norm) + q)
-                                   : make_float4(1.f, 1.f, 1.f, 1.f);
-      const size_t at = head * D + 4 * q;
-      const float z[4] = {y[v].x * r * n.x, y[v].y * r * n.y, y[v].z * r * n.z, y[v].w * r * n.w};
+      float4 n = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (MAPS == 2 && a.diff_norm) n = __ldg(reinterpret_cast<const float4*>(a.diff_norm) + q);
+      const size_t at = (out0 / MAPS + i) * D + 4 * q;
+      float z[4] = {y[v].x, y[v].y, y[v].z, y[v].w};
+      if constexpr (MAPS == 2) {
+        z[0] *= r * n.x;
+        z[1] *= r * n.y;
+        z[2] *= r * n.z;
+        z[3] *= r * n.w;
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (a.out_dtype == 0) store_out_t<0>(a.out, a.out_scale, at + e, z[e]);
@@ -612,11 +622,12 @@ __device__ __forceinline__ void merge_diff(const PartialArgs& a, size_t row0, in
   }
 }
 
-template <int D>
-__device__ __forceinline__ void fused_combine_diff(const PartialArgs& a, int bh, size_t part_row,
-                                                   int rows, int s, uint32_t stage,
-                                                   const float* stage_p, uint32_t cap, float* wbuf,
-                                                   uint32_t bar) {
+template <int D, int MAPS>
+__device__ __forceinline__ void fused_combine_heads(const PartialArgs& a, int bh, size_t part_row,
+                                                    int rows, int s, uint32_t stage,
+                                                    const float* stage_p, uint32_t cap,
+                                                    float* wbuf, uint32_t bar, size_t out0,
+                                                    int hq0) {
   __shared__ int is_last;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -642,11 +653,11 @@ __device__ __forceinline__ void fused_combine_diff(const PartialArgs& a, int bh,
   merge_weights(a.part_lse, part_row, rows, s, wbuf, winv);
   if (!staged) {
     __syncthreads();
-    merge_diff<D, false>(a, part_row, rows, s, part, wbuf, winv, true);
+    merge_heads<D, false, MAPS>(a, rows, s, part, wbuf, winv, true, out0, hq0);
     return;
   }
   const bool ok = __syncthreads_and(mbar_wait(bar, 0) ? 1 : 0) != 0;
-  merge_diff<D, true>(a, part_row, rows, s, stage_p, wbuf, winv, ok);
+  merge_heads<D, true, MAPS>(a, rows, s, stage_p, wbuf, winv, ok, out0, hq0);
   if (!ok && threadIdx.x == 0) record_error(a.error_flag, 1);
 }
 

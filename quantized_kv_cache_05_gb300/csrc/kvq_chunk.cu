@@ -161,6 +161,8 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const ChunkArgs a,
   griddep_launch_dependents();
   const int tid = threadIdx.x;
   const ChunkSpace sp = chunk_space(grid, a.batch, a.D);
+  if (a.counters)   // of the decode that takes the single tokens
+    for (long i = tid; i < (long)a.batch * a.Hkv; i += kShareThreads) a.counters[i] = 0u;
   Cut* cuts = reinterpret_cast<Cut*>(a.workspace + sp.cuts);
   Request* requests = reinterpret_cast<Request*>(a.workspace + sp.requests);
 
@@ -171,6 +173,7 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const ChunkArgs a,
     Request r;
     r.q0 = min(max(a.q_offsets[b], 0), a.num_tokens);
     r.n = max(min(max(a.q_offsets[b + 1], 0), a.num_tokens) - r.q0, 0);
+    if (a.counters && r.n == 1) r.n = 0;   // the decode's
     const int len = a.seq_lens[b];
     r.L = min(max(len, 0), a.max_kv_len);
     if (r.L != len && r.n > 0) record_error(a.error_flag, 2);
@@ -1203,23 +1206,14 @@ cudaError_t launch_t(const TensorMaps& m, const ChunkArgs& a, int grid, cudaStre
   using Cg = ChunkGeom<FMT, D>;
   constexpr size_t smem = Cg::kOffCtl + sizeof(ChunkCtl);
   static_assert(smem <= 232448, "shared memory of one CTA");
-  constexpr size_t kMostFirst = (size_t)kMaxPlanBatch * sizeof(int);
-  static_assert(kMostFirst + sizeof(ShareSmem) <= 232448, "shared memory of one CTA");
-  constexpr int kRt = DIFF ? kTok : kRows;
   auto kern = chunk_kernel<FMT, D, P2, DIFF>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(share_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)kMostFirst);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(share_kernel, dim3(1), dim3(kShareThreads), (size_t)a.batch * sizeof(int), st, a,
-                 grid, kRt, DIFF);
-  if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, m.k16, m.v16, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(merge_kernel<D, DIFF>, dim3(kRt / kMergeWarps, grid), dim3(32 * kMergeWarps), 0,
-                    st, a, grid);
+  return launch_pdl(merge_kernel<D, DIFF>, dim3((DIFF ? kTok : kRows) / kMergeWarps, grid),
+                    dim3(32 * kMergeWarps), 0, st, a, grid);
 }
 
 template <int FMT, int D>
@@ -1230,6 +1224,17 @@ cudaError_t by_kind(const TensorMaps& m, const ChunkArgs& a, int grid, cudaStrea
 }
 
 }  // namespace
+
+cudaError_t launch_shares(const ChunkArgs& a, int grid, cudaStream_t st) {
+  constexpr size_t kMost = (size_t)kMaxPlanBatch * sizeof(int);
+  static_assert(kMost + sizeof(ShareSmem) <= 232448, "shared memory of one CTA");
+  cudaError_t e =
+      cudaFuncSetAttribute(share_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+  if (e != cudaSuccess) return e;
+  const bool diff = a.diff_lambda != nullptr;
+  return launch_pdl(share_kernel, dim3(1), dim3(kShareThreads), (size_t)a.batch * sizeof(int), st,
+                    a, grid, diff ? kTok : kRows, diff);
+}
 
 size_t chunk_workspace_bytes(int grid, int batch, int D) { return chunk_space(grid, batch, D).bytes; }
 

@@ -109,13 +109,16 @@ constexpr int ctas_per_sm() {
 // BEHIND: the requests' own tokens behind a shared prefix's kernel (a variant, as
 // the ordinary decode of 32768 tokens takes 32.5 us without these terms and 32.7
 // with them decided at run time).
-// DIFF: differential heads.  Their halves of the head dims are two maps that share the
+// MODE 0: the decode.  1 and 2: the merge writes whole heads, a warp for each, and the
+// requests' tokens may be rows of a packed step (a.q_offsets: those with one new token take
+// part, the others' CTAs end at once); 1, differential heads, 2, plain ones.
+// Differential heads: their halves of the head dims are two maps that share the
 // values, so each is a row of its own: query row 2i of the kv head is [q1 0] of head i,
 // row 2i + 1 is [0 q2] (a.G and a.Hq count these rows), and all that follows, the
 // partials too, is the decode of twice the heads; the cache is read once for both maps.
 // Only the merge joins a head's two.  (Half of the
 // score MMAs multiply zeros; the codes' loads and conversions bound the kernel.)
-template <int FMT, int D, bool PROBQ, int NH, bool QF8, int NW, bool BEHIND, bool DIFF>
+template <int FMT, int D, bool PROBQ, int NH, bool QF8, int NW, bool BEHIND, int MODE>
 __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     partial_kernel(const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const PartialArgs a) {
@@ -126,6 +129,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
   constexpr int KS8 = D / 32;                      // its k-steps
   constexpr int MT = Gm::kMT;
   constexpr int kSweeps = PROBQ ? 2 : 1;
+  constexpr bool DIFF = MODE == 1;
 
   extern __shared__ uint8_t dyn_smem[];
   __shared__ Smem<NW> sm;
@@ -164,6 +168,14 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
   // to the copies that its threads issue (13 x 4080, one tile per prefix CTA: 11.85
   // -> 12.0 us; no difference from 4 x 1k to 64 x 32k).
   if (!BEHIND && a.fresh == 0) griddep_wait();
+  size_t token = b;   // row of q and out
+  if constexpr (MODE != 0) {
+    if (a.q_offsets) {
+      const int q0 = min(max(__ldg(a.q_offsets + b), 0), a.num_tokens);
+      if (min(max(__ldg(a.q_offsets + b + 1), 0), a.num_tokens) - q0 != 1) return;
+      token = q0;
+    }
+  }
   if constexpr (BEHIND) {
     // partials only: the merging kernel may take its place now, it waits
     if (!a.counters) griddep_launch_dependents();
@@ -324,7 +336,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     const int head = g + 8 * hh;
     // lanes t = 0, 1 hold the first half of the head dims, 2 and 3 the second
     const bool valid = head < a.G && (!DIFF || (t >> 1) == (head & 1));
-    const size_t qrow = ((size_t)b * a.Hq + hq0 + (valid ? head : 0)) >> (DIFF ? 1 : 0);
+    const size_t qrow = (token * a.Hq + hq0 + (valid ? head : 0)) >> (DIFF ? 1 : 0);
     if constexpr (QF8) {
       const uint8_t* qp = static_cast<const uint8_t*>(a.q) + qrow * D + (D / 4) * t;
       if constexpr (kRawK) {
@@ -715,10 +727,10 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn_bytes));
     const uint32_t usable = dyn_bytes - (ring - smem_u32(dyn_smem));
     float* wbuf = reinterpret_cast<float*>(dyn_smem + (ring - smem_u32(dyn_smem)) + usable - kWbuf);
-    if constexpr (DIFF)
-      fused_combine_diff<D>(a, bh, part_row, a.G, psplits, ring,
-                            reinterpret_cast<const float*>(ofrag), usable - kWbuf, wbuf,
-                            smem_u32(&sm.comb_full));
+    if constexpr (MODE != 0)
+      fused_combine_heads<D, DIFF ? 2 : 1>(
+          a, bh, part_row, a.G, psplits, ring, reinterpret_cast<const float*>(ofrag),
+          usable - kWbuf, wbuf, smem_u32(&sm.comb_full), token * a.Hq + hq0, hq0);
     else
       fused_combine_staged<ctas_per_sm<FMT, D, PROBQ, NH, NW>() == 4 ? 16 : 32>(
           a, bh, part_row, a.G, psplits, ring, reinterpret_cast<const float*>(ofrag), usable - kWbuf,
@@ -727,10 +739,10 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
 }
 
 template <int FMT, int D, bool PROBQ, int NH, bool QF8, int NW, bool BEHIND = false,
-          bool DIFF = false>
+          int MODE = 0>
 cudaError_t launch_partial_t(const TensorMaps& m, const PartialArgs& a, cudaStream_t st) {
   // quantised probabilities and head_dim 256 have no shared prefix
-  if constexpr (!BEHIND && !DIFF && !PROBQ && D <= 128)
+  if constexpr (!BEHIND && MODE == 0 && !PROBQ && D <= 128)
     if (a.late_merge) return launch_partial_t<FMT, D, PROBQ, NH, QF8, NW, true>(m, a, st);
   using Rg = Ring<FMT, D, PROBQ, NH, NW>;
   static_assert(Rg::kBytes >= Rg::kEpilogue && Rg::kBytes >= Rg::kStream, "ring too small");
@@ -747,7 +759,7 @@ cudaError_t launch_partial_t(const TensorMaps& m, const PartialArgs& a, cudaStre
     smem = std::max(smem, std::min(need, kPerCta));
   }
   smem = (smem + 15) / 16 * 16;
-  auto kern = partial_kernel<FMT, D, PROBQ, NH, QF8, NW, BEHIND, DIFF>;
+  auto kern = partial_kernel<FMT, D, PROBQ, NH, QF8, NW, BEHIND, MODE>;
   // The kernel's limit is the same for all calls, the most that any of them takes:
   // set to each call's own size, a call of another thread could lower it between
   // here and the launch, which then fails.

@@ -1,5 +1,5 @@
-// Split-KV decode of differential heads: instantiations of the partial kernel's DIFF
-// variant (sm_103a).  The kernel is in kvq_decode.cuh, the merge in kvq_attn.cuh.
+// Split-KV decode of differential heads: instantiations of the partial kernel's mode 1
+// (sm_103a).  The kernel is in kvq_decode.cuh, the merge in kvq_attn.cuh.
 
 #include "kvq_decode.cuh"
 
@@ -9,9 +9,9 @@ namespace {
 
 template <int FMT, int D, bool QF8>
 cudaError_t by_rows(const TensorMaps& m, const PartialArgs& a, cudaStream_t st) {
-  if (a.G > 8) return launch_partial_t<FMT, D, false, 2, QF8, kDecodeWarps, false, true>(m, a, st);
+  if (a.G > 8) return launch_partial_t<FMT, D, false, 2, QF8, kDecodeWarps, false, 1>(m, a, st);
   constexpr int NW = D <= 128 && kWideCta ? kWideWarps : kDecodeWarps;   // (wide_cta)
-  return launch_partial_t<FMT, D, false, 1, QF8, NW, false, true>(m, a, st);
+  return launch_partial_t<FMT, D, false, 1, QF8, NW, false, 1>(m, a, st);
 }
 
 template <int FMT, int D>

@@ -99,6 +99,8 @@ struct PartialArgs {
   const float* diff_lambda;   // [Hq / 2], or null
   const float* diff_norm;     // [Dv], or null
   float diff_eps, diff_gain;
+  const int32_t* q_offsets;   // rows of a packed step [batch + 1], or null: row b is request b's
+  int num_tokens;
 };
 
 // The shared prefix's partials (kvq_shared.cu).
@@ -179,6 +181,7 @@ struct ChunkArgs {
   const int32_t* seq_lens;
   const int32_t* q_offsets;
   uint8_t* workspace;
+  uint32_t* counters;         // [batch][Hkv] to clear where the decode takes the single tokens, or null
   void* out;
   int32_t* error_flag;
   int batch, num_tokens, G, Hq, Hkv, D, ps, max_pages, num_pages, max_kv_len;
@@ -280,12 +283,15 @@ cudaError_t launch_partial(int fmt, int D, bool probq, const TensorMaps& m, cons
                            cudaStream_t st);
 cudaError_t launch_partial_diff(int fmt, int D, const TensorMaps& m, const PartialArgs& a,
                                 cudaStream_t st);
+cudaError_t launch_partial_packed(int fmt, int D, const TensorMaps& m, const PartialArgs& a,
+                                  cudaStream_t st);
 cudaError_t launch_partial_nvfp4(int D, bool probq, const TensorMaps& m, const PartialArgs& a,
                                  cudaStream_t st);
 cudaError_t launch_mla_partial(const CUtensorMap& tcodes, const CUtensorMap& tpe,
                                const CUtensorMap& tcodes64, const CUtensorMap& tpe64,
                                const PartialArgs& a, cudaStream_t st);
 size_t chunk_workspace_bytes(int grid, int batch, int D);
+cudaError_t launch_shares(const ChunkArgs& a, int grid, cudaStream_t st);
 cudaError_t launch_chunk(int fmt, int D, const TensorMaps& m, const ChunkArgs& a, int grid,
                          cudaStream_t st);
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st);

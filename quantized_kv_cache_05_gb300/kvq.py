@@ -117,7 +117,9 @@ SIGNATURES = {
                                ctypes.POINTER(kvq_diff), _P, _P, _P, _P, _P, _P]),
     "kvq_chunk_attention": (_int, [ctypes.POINTER(kvq_cache), ctypes.POINTER(kvq_decode_params),
                                    ctypes.POINTER(kvq_diff), _int, _P, _P, _P, _sz, _P, _P]),
-    "kvq_chunk_workspace_bytes": (_sz, [_int, _int, _int]),
+    "kvq_chunk_workspace_bytes": (_sz, [_int, ctypes.POINTER(kvq_cache),
+                                        ctypes.POINTER(kvq_decode_params),
+                                        ctypes.POINTER(kvq_diff)]),
     "kvq_plan_step": (_int, [ctypes.POINTER(kvq_page_plan), _P]),
     "kvq_rope_append_slots": (_int, [ctypes.POINTER(kvq_cache), ctypes.POINTER(kvq_rotary), _int,
                                      _P, _P, _heads_p, _heads_p, _heads_p, _heads_p, _heads_p,
@@ -344,8 +346,9 @@ def kvq_chunk_attention(cache: kvq_cache, params: kvq_decode_params, diff: Optio
                                      _addr(out), _stream(stream))
 
 
-def kvq_chunk_workspace_bytes(num_sms: int, batch: int, head_dim: int) -> int:
-    return int(lib().kvq_chunk_workspace_bytes(num_sms, batch, head_dim))
+def kvq_chunk_workspace_bytes(num_sms: int, cache: kvq_cache, params: kvq_decode_params,
+                              diff: Optional[kvq_diff]) -> int:
+    return int(lib().kvq_chunk_workspace_bytes(num_sms, _ref(cache), _ref(params), _ref(diff)))
 
 
 def kvq_shared_splits(num_sms: int, batch: int, num_kv_heads: int, q_per_kv: int, prefix_len: int,

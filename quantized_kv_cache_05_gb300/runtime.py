@@ -708,9 +708,10 @@ class ChunkAttention:
         kvq.check(kvq.kvq_chunk_attention(cache.struct(), none, diff.struct() if diff else None, 0,
                                           None, None, None, 0, None, 0), "ChunkAttention")
         sms = torch.cuda.get_device_properties(device).multi_processor_count
-        self._ws = torch.empty(kvq.kvq_chunk_workspace_bytes(sms, batch, cache.D), dtype=torch.uint8,
-                               device=device)
         self._params = cfg.params(None)
+        size = kvq.kvq_chunk_workspace_bytes(sms, cache.struct(), self._params,
+                                             diff.struct() if diff else None)
+        self._ws = torch.empty(size, dtype=torch.uint8, device=device)
 
     cache = property(lambda self: self._cache)
     diff = property(lambda self: self._diff[0])

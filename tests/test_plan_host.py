@@ -153,10 +153,16 @@ def test_norm_options_are_read_with_a_norm_alone():
 
 
 def test_workspace_bytes():
-    f = kvq.kvq_chunk_workspace_bytes
-    assert f(0, 1, 128) == 0 and f(152, -1, 128) == 0 and f(152, 1, 0) == 0
-    assert f(152, 0, 128) == f(152, 1, 128) > 152 * 2 * 256 * 129 * 4
-    assert f(152, 5000, 64) < f(152, 5000, 128)
+    f = lambda sms=152, c=None, d=None, **kw: kvq.kvq_chunk_workspace_bytes(sms, c or cache(), params(**kw), d)
+    assert f(0) == 0 and f(batch=-1) == 0 and f(num_q_heads=0) == 0 and f(max_kv_len=-1) == 0
+    assert kvq.kvq_chunk_workspace_bytes(152, None, params(), None) == 0
+    base = 152 * 2 * 256 * 129 * 4
+    assert f(batch=0) == f(batch=1) >= base
+    # the decode's counters and partials: 4 x 2 groups of 4 rows (8 differential ones)
+    one = f(batch=4, max_kv_len=512)
+    assert one > f(batch=1) + 4 * 8 * 129 * 4 and f(batch=4, max_kv_len=512, d=diff()) > one
+    # rows that the decode does not take
+    assert f(batch=4, num_q_heads=34) < one
 
 
 # ---------------------------------------------------------------------- binding
