@@ -106,15 +106,15 @@ __device__ __forceinline__ int tile_cost(const Request& r, int G, int rt, bool d
 // Shares: one CTA lists the requests with new tokens, sums the costs of the row tiles
 // (consecutive ones per thread) and finds the cuts, a thread per cut.
 // ---------------------------------------------------------------------------
-constexpr int kShareThreads = 1024;
+constexpr int kShareThreads = 256;
 
 struct ShareSmem {
-  long warp_a[32], warp_b[32];
-  long total_a, total_b;
+  long warp_a[kShareThreads / 32], warp_b[kShareThreads / 32];
   long start[kShareThreads];   // cost before each thread's tiles
 };
 
-__device__ __forceinline__ void scan2(long& a, long& b, ShareSmem& sm) {
+__device__ __forceinline__ void scan2(long& a, long& b, long& total_a, long& total_b,
+                                      ShareSmem& sm) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long a0 = a, b0 = b;
 #pragma unroll
@@ -130,27 +130,21 @@ __device__ __forceinline__ void scan2(long& a, long& b, ShareSmem& sm) {
     sm.warp_b[warp] = b;
   }
   __syncthreads();
-  if (warp == 0) {
-    long x = sm.warp_a[lane], y = sm.warp_b[lane];
-    const long x0 = x, y0 = y;
+  long ta = 0, tb = 0;
+  a -= a0;
+  b -= b0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) {
-        x += u;
-        y += v;
-      }
+  for (int i = 0; i < kShareThreads / 32; ++i) {
+    if (i == warp) {
+      a += ta;
+      b += tb;
     }
-    sm.warp_a[lane] = x - x0;
-    sm.warp_b[lane] = y - y0;
-    if (lane == 31) {
-      sm.total_a = x;
-      sm.total_b = y;
-    }
+    ta += sm.warp_a[i];
+    tb += sm.warp_b[i];
   }
-  __syncthreads();
-  a += sm.warp_a[warp] - a0;
-  b += sm.warp_b[warp] - b0;
+  total_a = ta;
+  total_b = tb;
+  __syncthreads();   // (the sums' places may be written again)
 }
 
 __global__ void __launch_bounds__(kShareThreads) share_kernel(const ChunkArgs a, int grid, int rt,
@@ -186,9 +180,9 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const ChunkArgs a,
     active += r.n > 0;
     tiles += row_tiles(r.n, a.G, rt);
   }
-  scan2(active, tiles, sm);
-  const int A = (int)sm.total_a;
-  const long T = sm.total_b;
+  long all_active, T;
+  scan2(active, tiles, all_active, T, sm);
+  const int A = (int)all_active;
   for (int b = b0; b < b1; ++b) {
     const Request r = request(b);
     if (r.n == 0) continue;
@@ -220,8 +214,8 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const ChunkArgs a,
       cost += tile_cost(r, a.G, rt, diff, (int)(t - first[i]));
     }
   }
-  scan2(cost, none, sm);
-  const long W = sm.total_a;   // of one kv head
+  long W, unused;   // of one kv head
+  scan2(cost, none, W, unused, sm);
   sm.start[tid] = cost;
   __syncthreads();
 
@@ -230,9 +224,10 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const ChunkArgs a,
   const int shares = (int)min((long)grid, (whole + kCostShare - 1) / kCostShare);
   if (tid == 0) *reinterpret_cast<ChunkHead*>(a.workspace) = ChunkHead{shares, A};
   for (int c = tid; c <= shares && shares > 0; c += kShareThreads) {
-    const long x = (long)(((unsigned __int128)whole * (unsigned)c) / (unsigned)shares);
-    const long rem = x % W;
-    Cut cut{0, 0, (int)(x / W), 0};
+    const long x = whole / shares * c + min((long)c, whole % shares);
+    const int h = (int)(x / W);
+    const long rem = x - h * W;
+    Cut cut{0, 0, h, 0};
     if (rem > 0) {
       int lo = 0, hi = kShareThreads;   // the thread whose tiles hold it
       while (hi - lo > 1) {
@@ -1052,8 +1047,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // a partial: where the piece begins the row tile it is the share's last
         const int at = 2 * blockIdx.x + (p.kv0 == 0 ? 1 : 0);
-        const size_t prow = (size_t)at * kRows + (two ? slot * kTok : 0) + r;
-        if (live && (two || slot == 0)) part_lse[prow] = bad ? NAN : lse;
+        const int prow = (two ? slot * kTok : 0) + r;
+        if (live && (two || slot == 0)) part_lse[(size_t)at * kRows + prow] = bad ? NAN : lse;
+        // [8-dim column][row][8]: neighbouring lanes' rows lie side by side
+        float* po = part_o + (size_t)at * kRows * D + prow * 8;
 #pragma unroll 1
         for (int c = c0; c < c0 + nc; ++c) {
           float o[32];
@@ -1064,7 +1061,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float v[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[e] = o[8 * k + e];
-              st_v8(part_o + prow * D + 32 * c + 8 * k, v);
+              st_v8(po + (size_t)(4 * c + k) * kRows * 8, v);
             }
           }
         }
@@ -1097,16 +1094,18 @@ __device__ __forceinline__ float nan_max(float a, float b) {
 
 // ---------------------------------------------------------------------------
 // Merge of the row tiles that cuts divide (M = max lse, w_j = e^(lse_j - M), O = sum w_j
-// o_j / sum w_j, 0 when all are empty), a warp per row.  Block (x, y): rows of the tile
-// that begins in share y and goes on in the next.
+// o_j / sum w_j, 0 when all are empty), a warp for a few rows at once.  Blocks (x, y): the
+// tile that begins in share y and goes on in the next.
 // ---------------------------------------------------------------------------
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 8, kMergeRows = 4;   // rows of a warp: their loads overlap
 
 template <int D, bool DIFF>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     merge_kernel(const ChunkArgs a, int grid) {
   constexpr int kRt = DIFF ? kTok : kRows;
-  constexpr int kPer = D / 32;   // dims per lane
+  constexpr int kMaps = DIFF ? 2 : 1;
+  constexpr int NR = kMergeRows / kMaps;   // rows in one go, with their maps
+  constexpr int kPer = D / 32;             // dims per lane
   using Vec = std::conditional_t<kPer == 4, float4, float2>;
   griddep_wait();
   griddep_launch_dependents();
@@ -1119,85 +1118,116 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   // a cut inside a row tile that begins in this share
   if (cut.kv == 0 || (begin.tile_of(cut) && begin.kv > 0)) return;
   const Request q = reinterpret_cast<const Request*>(a.workspace + sp.requests)[cut.i];
-  const int r = blockIdx.x * kMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int row = cut.tile * kRt + r;
-  if (r >= kRt || row >= q.n * a.G) return;   // the whole warp
+  const int lane = threadIdx.x & 31;
+  const int rows = min(kRt, q.n * a.G - cut.tile * kRt);   // of the tile
   const float* part_lse = reinterpret_cast<const float*>(a.workspace + sp.lse);
-  const float* part_o = reinterpret_cast<const float*>(a.workspace + sp.o);
+  const float* part_o = reinterpret_cast<const float*>(a.workspace + sp.o) +
+                        (size_t)(lane * kPer / 8) * kRows * 8 + lane * kPer % 8;
   // pieces: this share's last, then the first ones of the following shares up to the one
   // that ends the row tile (shares without any key tile have none)
   int last = share + 1;
   while (last < head.shares && cuts[last + 1].tile_of(cut) && cuts[last + 1].kv > 0) ++last;
   const int pieces = last - share + 1;
-  auto slot_of = [&](int j) -> int { return j == 0 ? 2 * share + 1 : 2 * (share + j); };
+  auto slot_of = [&](int j) -> size_t { return j == 0 ? 2 * share + 1 : 2 * (share + j); };
   auto empty = [&](int j) -> bool {
     return j > 0 && cuts[share + j].tile_of(cuts[share + j + 1]) &&
            cuts[share + j].kv == cuts[share + j + 1].kv;
   };
 
-  float o[DIFF ? 2 : 1][kPer];
+  const int warps = gridDim.x * kMergeWarps;
+  for (int r0 = NR * (blockIdx.x * kMergeWarps + (threadIdx.x >> 5)); r0 < rows; r0 += NR * warps) {
+    // row i of the partials: rows r0 .., the maps of one after the other
+    auto prow = [&](int i) -> int { return min(r0 + i / kMaps, rows - 1) + (i % kMaps) * kTok; };
+    float M[kMergeRows], sum[kMergeRows], o[kMergeRows][kPer];
 #pragma unroll
-  for (int m = 0; m < (DIFF ? 2 : 1); ++m) {
-    const int pr = m * kTok + r;   // row of the partials
-    float M = -INFINITY;
-    for (int j = lane; j < pieces; j += 32)
-      if (!empty(j)) M = nan_max(M, part_lse[(size_t)slot_of(j) * kRows + pr]);
+    for (int i = 0; i < kMergeRows; ++i) {
+      M[i] = -INFINITY;
+      sum[i] = 0.f;
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) M = nan_max(M, __shfl_xor_sync(0xffffffffu, M, k));
-    float sum = 0.f;
+      for (int e = 0; e < kPer; ++e) o[i][e] = 0.f;
+    }
+    for (int j = lane; j < pieces; j += 32) {
+      const bool none = empty(j);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) o[m][i] = 0.f;
+      for (int i = 0; i < kMergeRows; ++i)
+        if (!none) M[i] = nan_max(M[i], part_lse[slot_of(j) * kRows + prow(i)]);
+    }
+#pragma unroll
+    for (int i = 0; i < kMergeRows; ++i)
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1)
+        M[i] = nan_max(M[i], __shfl_xor_sync(0xffffffffu, M[i], k));
     for (int j0 = 0; j0 < pieces; j0 += 32) {
-      const int mine = j0 + lane;
-      float w = 0.f;
-      if (mine < pieces && !empty(mine)) {
-        const float x = part_lse[(size_t)slot_of(mine) * kRows + pr];
-        w = x == -INFINITY ? 0.f : expf(x - M);
+      const bool some = j0 + lane < pieces && !empty(j0 + lane);
+      float w[kMergeRows];
+#pragma unroll
+      for (int i = 0; i < kMergeRows; ++i) {
+        const float x = some ? part_lse[slot_of(j0 + lane) * kRows + prow(i)] : -INFINITY;
+        w[i] = x == -INFINITY ? 0.f : expf(x - M[i]);
+        sum[i] += w[i];
       }
-      sum += w;
       const int n = min(32, pieces - j0);
-#pragma unroll 4
+#pragma unroll 2
       for (int j = 0; j < n; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, w, j);
-        if (wj == 0.f) continue;   // (empty pieces and rows are not read; NaN is not 0)
-        const Vec v = *(reinterpret_cast<const Vec*>(
-                            part_o + ((size_t)slot_of(j0 + j) * kRows + pr) * D) + lane);
-        const float* f = reinterpret_cast<const float*>(&v);
+        // (a share without a piece leaves nothing to read)
+        const bool here = __shfl_sync(0xffffffffu, (int)some, j) != 0;
+        Vec v[kMergeRows];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) o[m][i] += wj * f[i];
+        for (int i = 0; i < kMergeRows; ++i)
+          if (here)
+            v[i] = *reinterpret_cast<const Vec*>(part_o + slot_of(j0 + j) * kRows * D +
+                                                 (size_t)prow(i) * 8);
+#pragma unroll
+        for (int i = 0; i < kMergeRows; ++i) {
+          const float wj = __shfl_sync(0xffffffffu, w[i], j);
+          const float* f = reinterpret_cast<const float*>(&v[i]);
+          if (here && wj != 0.f) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) o[i][e] += wj * f[e];
+          }
+        }
       }
     }
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    for (int i = 0; i < kMergeRows; ++i) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) o[m][i] *= inv;
-  }
-  const int ti = row / a.G, hq = cut.h * a.G + (row - ti * a.G);
-  if constexpr (DIFF) {
-    const float lam = __ldg(a.diff_lambda + hq);
-    float ss = 0.f;
+      for (int k = 16; k > 0; k >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], k);
+      const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      o[0][i] -= lam * o[1][i];
-      ss += o[0][i] * o[0][i];
-    }
-    float rr = a.diff_gain;
-    if (a.diff_norm) {
-#pragma unroll
-      for (int k = 16; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
-      rr *= inv_rms_of(ss * (1.f / D) + a.diff_eps);
+      for (int e = 0; e < kPer; ++e) o[i][e] *= inv;
     }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      o[0][i] *= rr * (a.diff_norm ? __ldg(a.diff_norm + lane * kPer + i) : 1.f);
-  }
-  const size_t at = ((size_t)(q.q0 + ti) * a.Hq + hq) * D + lane * kPer;
+    for (int n = 0; n < NR; ++n) {
+      const int row = cut.tile * kRt + r0 + n;
+      if (r0 + n >= rows) break;
+      float* y = o[kMaps * n];
+      const int ti = row / a.G, hq = cut.h * a.G + (row - ti * a.G);
+      if constexpr (DIFF) {
+        const float lam = __ldg(a.diff_lambda + hq);
+        float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (a.out_dtype == 0) store_out_t<0>(a.out, a.out_scale, at + i, o[0][i]);
-    else if (a.out_dtype == 1) store_out_t<1>(a.out, a.out_scale, at + i, o[0][i]);
-    else store_out_t<2>(a.out, a.out_scale, at + i, o[0][i]);
+        for (int e = 0; e < kPer; ++e) {
+          y[e] -= lam * o[kMaps * n + 1][e];
+          ss += y[e] * y[e];
+        }
+        float rr = a.diff_gain;
+        if (a.diff_norm) {
+#pragma unroll
+          for (int k = 16; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+          rr *= inv_rms_of(ss * (1.f / D) + a.diff_eps);
+        }
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+          y[e] *= rr * (a.diff_norm ? __ldg(a.diff_norm + lane * kPer + e) : 1.f);
+      }
+      const size_t at = ((size_t)(q.q0 + ti) * a.Hq + hq) * D + lane * kPer;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        if (a.out_dtype == 0) store_out_t<0>(a.out, a.out_scale, at + e, y[e]);
+        else if (a.out_dtype == 1) store_out_t<1>(a.out, a.out_scale, at + e, y[e]);
+        else store_out_t<2>(a.out, a.out_scale, at + e, y[e]);
+      }
+    }
   }
 }
 
@@ -1212,8 +1242,8 @@ cudaError_t launch_t(const TensorMaps& m, const ChunkArgs& a, int grid, cudaStre
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, m.k16, m.v16, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(merge_kernel<D, DIFF>, dim3((DIFF ? kTok : kRows) / kMergeWarps, grid),
-                    dim3(32 * kMergeWarps), 0, st, a, grid);
+  // (eight blocks for a divided tile: all of them run at once)
+  return launch_pdl(merge_kernel<D, DIFF>, dim3(8, grid), dim3(32 * kMergeWarps), 0, st, a, grid);
 }
 
 template <int FMT, int D>
