@@ -1020,6 +1020,11 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_decode_params* p, c
   a.max_pages = c->max_pages_per_seq;
   a.num_pages = c->num_pages;
   a.max_kv_len = p->max_kv_len;
+  // x / G for x < 2^31: with 2^(k-1) < G <= 2^k and M = floor(2^32 (2^k - G) / G) + 1 the
+  // quotient is (floor(x M / 2^32) + x) >> k (the multiplier 2^32 + M is within 2^k of
+  // 2^(32+k) / G, so the product's error stays below x 2^k / 2^(32+k) < 1/2 of a step of 1/G)
+  while ((1u << a.g_shift) < (unsigned)G) ++a.g_shift;
+  a.g_mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << a.g_shift) - G)) / G + 1);
   a.box = box_rows(c->page_size);
   a.out_dtype = p->out_dtype;
   a.out_scale = p->out_scale;
@@ -1042,7 +1047,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_decode_params* p, c
     return KVQ_ERR_CUDA;
   uint8_t* const w = a.workspace;
   if (parts.splits > 0) a.counters = reinterpret_cast<uint32_t*>(w + parts.counters);
-  s = cuda_status(launch_shares(a, sms, as_stream(stream)));
+  s = cuda_status(launch_shares(c->fmt, a, sms, as_stream(stream)));
   if (s != KVQ_OK) return s;
   if (parts.splits > 0) {
     kvq_decode_params one = *p;

@@ -54,10 +54,12 @@ constexpr float kPShift = 7.0f;           // log2 scale of P
 constexpr int kTmem = 512;                // S0 | S1 | O0 | O1, 128 columns each
 constexpr int kRows = 2 * kTok;           // rows of a partial in the workspace
 
-// Cost of a row tile: kCostOne or kCostTwo (one accumulator's rows or two) for each key
-// tile, and kCostFixed for its queries and its output.  A share is at least kCostShare,
-// a piece kMinPiece key tiles.
-constexpr int kCostOne = 2, kCostTwo = 3, kCostFixed = 6, kCostShare = 18, kMinPiece = 2;
+// Cost of a row tile, in twelfths of a key tile with both accumulators' rows (1.9 us): for
+// each key tile 12, or with one accumulator's rows what its conversion takes (NVFP4: 1.74
+// us; FP8: half of it, as two key tiles are on their way), and kCostFixed for its queries
+// and its output (7 us).  A share is at least kCostShare, a piece kMinPiece key tiles.
+constexpr int kCostTwo = 12, kCostOneFp8 = 7, kCostOneNvfp4 = 11;
+constexpr int kCostFixed = 40, kCostShare = 64, kMinPiece = 3;
 
 // ---------------------------------------------------------------------------
 // Workspace: [head][cuts: grid + 1][requests: batch][lse: grid x 2 x kRows][o]
@@ -89,6 +91,12 @@ __host__ __device__ inline ChunkSpace chunk_space(int grid, int batch, int D) {
   return s;
 }
 
+// x / G for 0 <= x < 2^31, with the call's multiplier and shift (ChunkArgs): a division by
+// a runtime number takes some twenty instructions, many times a piece.
+__device__ __forceinline__ int over_g(const ChunkArgs& a, int x) {
+  return (int)((__umulhi((unsigned)x, a.g_mul) + (unsigned)x) >> a.g_shift);
+}
+
 // Row tiles of a request with n new tokens, rt rows in each; the keys that the last
 // row of tile j sees, and their tiles (at least one: rows that see nothing are written).
 __device__ __forceinline__ int row_tiles(int n, int G, int rt) { return (n * G + rt - 1) / rt; }
@@ -97,9 +105,9 @@ __device__ __forceinline__ int keys_of(const Request& r, int G, int rt, int j) {
   return max(0, min(r.L, r.L - r.n + e));
 }
 __device__ __forceinline__ int key_tiles(int keys) { return max(1, (keys + kTok - 1) / kTok); }
-__device__ __forceinline__ int tile_cost(const Request& r, int G, int rt, bool diff, int j) {
-  const bool two = diff || r.n * G - j * rt > kTok;
-  return kCostFixed + (two ? kCostTwo : kCostOne) * key_tiles(keys_of(r, G, rt, j));
+__device__ __forceinline__ int tile_cost(const Request& r, int G, int rt, int one, int j) {
+  const bool two = r.n * G - j * rt > kTok;   // (one: the cost with one accumulator's rows)
+  return kCostFixed + (two ? kCostTwo : one) * key_tiles(keys_of(r, G, rt, j));
 }
 
 // ---------------------------------------------------------------------------
@@ -148,7 +156,7 @@ __device__ __forceinline__ void scan2(long& a, long& b, long& total_a, long& tot
 }
 
 __global__ void __launch_bounds__(kShareThreads) share_kernel(const ChunkArgs a, int grid, int rt,
-                                                              bool diff) {
+                                                              int one) {
   extern __shared__ int first[];   // row tiles before each active request
   __shared__ ShareSmem sm;
   griddep_wait();
@@ -211,7 +219,7 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const ChunkArgs a,
     Request r = requests[i];
     for (long t = t0; t < t1; ++t) {
       if (i + 1 < A && t >= first[i + 1]) r = requests[++i];
-      cost += tile_cost(r, a.G, rt, diff, (int)(t - first[i]));
+      cost += tile_cost(r, a.G, rt, one, (int)(t - first[i]));
     }
   }
   long W, unused;   // of one kv head
@@ -239,12 +247,12 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const ChunkArgs a,
       long t = min(lo * each, T - 1), at = sm.start[lo];
       int i = owner(t);
       Request r = requests[i];
-      int tc = tile_cost(r, a.G, rt, diff, (int)(t - first[i]));
+      int tc = tile_cost(r, a.G, rt, one, (int)(t - first[i]));
       while (at + tc <= rem && t + 1 < T) {
         at += tc;
         ++t;
         if (i + 1 < A && t >= first[i + 1]) r = requests[++i];
-        tc = tile_cost(r, a.G, rt, diff, (int)(t - first[i]));
+        tc = tile_cost(r, a.G, rt, one, (int)(t - first[i]));
       }
       cut.i = i;
       cut.tile = (int)(t - first[i]);
@@ -338,7 +346,7 @@ struct ChunkCtl {
   // factors of the sums (a) and the sums of squares of the halves (b)
   float a[2][kTok], b[2][kTok];
   // the softmax warps' places and pieces: their registers are for the scores
-  Cut at[kSoftWarps];
+  Cut at[kSoftWarps], end;
   Piece piece[kSoftWarps];
 };
 
@@ -598,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok && walk.next(p)) {
       // keys that every row of the row tile sees
-      const int all = p.r.L - p.r.n + p.tile * kRt / a.G + 1;
+      const int all = p.r.L - p.r.n + over_g(a, p.tile * kRt) + 1;
       for (int kt = p.kv0; kt < p.kv1 && ok; ++kt, ++j) {
         const int rs = j % Cg::kSlots;
         const int nvalid = p.keys - kt * kTok;
@@ -702,12 +710,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned ends = 0;    // pieces before in which this slot had units
     bool ok = true;       // (after a timeout the pieces' barriers are still met)
     if (lane == 0) sm.at[sw] = walk.at;
-    __syncwarp();
+    if (threadIdx.x == 32 * kSoftWarp) sm.end = walk.end;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
     while (true) {
       {
         Walk w = walk;
         w.at = sm.at[sw];
-        if ((int)blockIdx.x < head.shares) w.end = cuts[blockIdx.x + 1];
+        w.end = sm.end;
         if (!w.next(p)) break;
         __syncwarp();
         if (lane == 0) {
@@ -721,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int R = p.r.n * a.G;                                    // the request's rows
       const int row = p.tile * kRt + (two && !DIFF ? slot * kTok : 0) + r;
       const bool live = row < R;
-      const int ti = live ? row / a.G : 0, g = live ? row - ti * a.G : 0;
+      const int ti = live ? over_g(a, row) : 0, g = live ? row - ti * a.G : 0;
       const int hq = p.h * a.G + g;
       const int seen = live ? p.r.L - p.r.n + ti + 1 : INT_MAX;    // keys of this row
 
@@ -748,8 +757,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int first = p.tile * kRt + (two && !DIFF ? slot * kTok : 0) + 32 * (warp & 3) +
                             lane / lp;
           // row first + k per: token qt, head qg of the group, without a division each
-          int qt = first / a.G, qg = first - qt * a.G;
-          const int dt = per / a.G, dg = per - dt * a.G;
+          int qt = over_g(a, first), qg = first - qt * a.G;
+          const int dt = over_g(a, per), dg = per - dt * a.G;
           const long row_bytes = a.q_fp8 ? D : 2 * D;
           const uint8_t* q0 = static_cast<const uint8_t*>(a.q) +
                               ((long)p.r.q0 * a.Hq + (long)p.h * a.G) * row_bytes + 16 * c +
@@ -781,36 +790,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (a.q_fp8) settle_scale(k_log2 * (a.q_hs ? __ldg(a.q_hs + hq) : a.q_scale));
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();   // the warp's rows are here
+        constexpr int kQ = D / 8 / kHalf;   // f16 pieces of the row
+        uint4 v[kQ];                         // (all loads at once; the scores are not here yet)
+#pragma unroll
+        for (int c = 0; c < kQ; ++c)
+          if (!(a.q_fp8 && (c & 1))) v[c] = lds128(q_at(r, dp0 + c));
         if (a.q_fp8) {
-#pragma unroll 2
-          for (int c = 0; c < D / 16 / kHalf; ++c) {   // 16 codes as two f16 pieces
-            const uint4 v = lds128(q_at(r, dp0 + 2 * c));
+#pragma unroll
+          for (int c = 0; c < kQ; c += 2) {   // 16 codes as two f16 pieces
             uint32_t o[8];
-            e4m3x4_to_f16x2x2(v.x, o[0], o[1]);
-            e4m3x4_to_f16x2x2(v.y, o[2], o[3]);
-            e4m3x4_to_f16x2x2(v.z, o[4], o[5]);
-            e4m3x4_to_f16x2x2(v.w, o[6], o[7]);
+            e4m3x4_to_f16x2x2(v[c].x, o[0], o[1]);
+            e4m3x4_to_f16x2x2(v[c].y, o[2], o[3]);
+            e4m3x4_to_f16x2x2(v[c].z, o[4], o[5]);
+            e4m3x4_to_f16x2x2(v[c].w, o[6], o[7]);
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[k] ^= flip;
-            sts128(q_at(r, dp0 + 2 * c), o[0], o[1], o[2], o[3]);
-            sts128(q_at(r, dp0 + 2 * c + 1), o[4], o[5], o[6], o[7]);
+            sts128(q_at(r, dp0 + c), o[0], o[1], o[2], o[3]);
+            sts128(q_at(r, dp0 + c + 1), o[4], o[5], o[6], o[7]);
           }
         } else {
           // prescaled by a power of two, so that the f16 values are exact
           uint32_t m2 = 0;   // the largest magnitudes of the even and odd elements
-#pragma unroll 8
-          for (int c = 0; c < D / 8 / kHalf; ++c) {
-            const uint4 v = lds128(q_at(r, dp0 + c));
-            m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                       __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-          }
+#pragma unroll
+          for (int c = 0; c < kQ; ++c)
+            m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v[c].x & 0x7FFF7FFFu, v[c].y & 0x7FFF7FFFu),
+                                       __vmaxu2(v[c].z & 0x7FFF7FFFu, v[c].w & 0x7FFF7FFFu)));
           const int e = q_prescale_exp(max(m2 & 0xFFFFu, m2 >> 16));
           settle_scale(scale_pow2(k_log2, -e));
           const float f = exp2i(e);
-#pragma unroll 4
-          for (int c = 0; c < D / 8 / kHalf; ++c) {
-            const uint4 v = lds128(q_at(r, dp0 + c));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int c = 0; c < kQ; ++c) {
+            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
             uint32_t o[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -835,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool poison = false;            // sees a token whose values are NaN
       // keys from the piece's first on that this row sees, and that every row does
       const int mine = seen - p.kv0 * kTok;
-      const int every = p.r.L - p.r.n + p.tile * kRt / a.G + 1 - p.kv0 * kTok;
+      const int every = p.r.L - p.r.n + over_g(a, p.tile * kRt) + 1 - p.kv0 * kTok;
       asm volatile("" ::: "memory");   // (what follows reads the piece from shared memory)
       for (int i = 0; i < cnt && ok; ++i) {
         const int jj = two ? i : 2 * i + slot;         // key tile of the piece
@@ -1201,7 +1211,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       const int row = cut.tile * kRt + r0 + n;
       if (r0 + n >= rows) break;
       float* y = o[kMaps * n];
-      const int ti = row / a.G, hq = cut.h * a.G + (row - ti * a.G);
+      const int ti = over_g(a, row), hq = cut.h * a.G + (row - ti * a.G);
       if constexpr (DIFF) {
         const float lam = __ldg(a.diff_lambda + hq);
         float ss = 0.f;
@@ -1255,15 +1265,16 @@ cudaError_t by_kind(const TensorMaps& m, const ChunkArgs& a, int grid, cudaStrea
 
 }  // namespace
 
-cudaError_t launch_shares(const ChunkArgs& a, int grid, cudaStream_t st) {
+cudaError_t launch_shares(int fmt, const ChunkArgs& a, int grid, cudaStream_t st) {
   constexpr size_t kMost = (size_t)kMaxPlanBatch * sizeof(int);
   static_assert(kMost + sizeof(ShareSmem) <= 232448, "shared memory of one CTA");
   cudaError_t e =
       cudaFuncSetAttribute(share_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
   if (e != cudaSuccess) return e;
   const bool diff = a.diff_lambda != nullptr;
+  const int one = diff ? kCostTwo : fmt == kFmtFp8 ? kCostOneFp8 : kCostOneNvfp4;
   return launch_pdl(share_kernel, dim3(1), dim3(kShareThreads), (size_t)a.batch * sizeof(int), st,
-                    a, grid, diff ? kTok : kRows, diff);
+                    a, grid, diff ? kTok : kRows, one);
 }
 
 size_t chunk_workspace_bytes(int grid, int batch, int D) { return chunk_space(grid, batch, D).bytes; }

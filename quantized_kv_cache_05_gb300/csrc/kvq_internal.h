@@ -186,6 +186,7 @@ struct ChunkArgs {
   int32_t* error_flag;
   int batch, num_tokens, G, Hq, Hkv, D, ps, max_pages, num_pages, max_kv_len;
   int box;                    // TMA box rows
+  uint32_t g_mul, g_shift;    // x / G = (umulhi(x, g_mul) + x) >> g_shift for x < 2^31
   int out_dtype;
   float out_scale, sm_scale, k_scale, v_scale;
   const float* k_hs;
@@ -291,7 +292,7 @@ cudaError_t launch_mla_partial(const CUtensorMap& tcodes, const CUtensorMap& tpe
                                const CUtensorMap& tcodes64, const CUtensorMap& tpe64,
                                const PartialArgs& a, cudaStream_t st);
 size_t chunk_workspace_bytes(int grid, int batch, int D);
-cudaError_t launch_shares(const ChunkArgs& a, int grid, cudaStream_t st);
+cudaError_t launch_shares(int fmt, const ChunkArgs& a, int grid, cudaStream_t st);
 cudaError_t launch_chunk(int fmt, int D, const TensorMaps& m, const ChunkArgs& a, int grid,
                          cudaStream_t st);
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st);
