@@ -210,6 +210,16 @@ long long shared_row_tiles(long long batch, int q_per_kv) {
   return rows > 128 ? (rows + 255) / 256 : 1;
 }
 
+// x / d for 0 <= x < 2^31 as (umulhi(x, mul) + x) >> shift: with 2^(k-1) < d <= 2^k and
+// mul = floor(2^32 (2^k - d) / d) + 1, the multiplier 2^32 + mul is above 2^(32+k) / d by at
+// most one, so that the quotient's excess, x / 2^(32+k), stays below 1 / d.
+void divisor(int d, uint32_t* mul, uint32_t* shift) {
+  uint32_t k = 0;
+  while ((1u << k) < (unsigned)d) ++k;
+  *shift = k;
+  *mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << k) - d)) / d + 1);
+}
+
 // TMA boxes of a 128-token tile: the largest power of two up to it that divides the pages.
 int box_rows(int page_size) {
   int box = 16;
@@ -567,6 +577,7 @@ kvq_status kvq_plan_step(const kvq_page_plan* p, void* stream) {
   a.num_pages = p->num_pages;
   a.max_pages = p->max_pages_per_seq;
   a.max_tokens = p->max_tokens;
+  divisor(p->page_size, &a.ps_mul, &a.ps_shift);
   a.block_table = p->block_table;
   a.seq_lens = p->seq_lens;
   a.seq_lens_out = p->seq_lens_out;
@@ -1020,11 +1031,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_decode_params* p, c
   a.max_pages = c->max_pages_per_seq;
   a.num_pages = c->num_pages;
   a.max_kv_len = p->max_kv_len;
-  // x / G for x < 2^31: with 2^(k-1) < G <= 2^k and M = floor(2^32 (2^k - G) / G) + 1 the
-  // quotient is (floor(x M / 2^32) + x) >> k (the multiplier 2^32 + M is within 2^k of
-  // 2^(32+k) / G, so the product's error stays below x 2^k / 2^(32+k) < 1/2 of a step of 1/G)
-  while ((1u << a.g_shift) < (unsigned)G) ++a.g_shift;
-  a.g_mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << a.g_shift) - G)) / G + 1);
+  divisor(G, &a.g_mul, &a.g_shift);
   a.box = box_rows(c->page_size);
   a.out_dtype = p->out_dtype;
   a.out_scale = p->out_scale;

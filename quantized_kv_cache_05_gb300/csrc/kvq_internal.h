@@ -201,6 +201,7 @@ constexpr int kMaxPlanBatch = 8192;   // requests whose sums fit the shared memo
 constexpr int kErrRefused = 16, kErrPool = 32;   // KVQ_DEVERR_REFUSED, KVQ_DEVERR_BAD_POOL
 struct PlanArgs {
   int batch, ps, num_pages, max_pages, max_tokens;
+  uint32_t ps_mul, ps_shift;  // x / ps = (umulhi(x, ps_mul) + x) >> ps_shift for x < 2^31
   int32_t* block_table;
   const int32_t* seq_lens;
   int32_t* seq_lens_out;

@@ -23,17 +23,21 @@
 namespace kvq {
 namespace {
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanTokens = 2 * kPlanThreads;   // tokens per CTA before another one is added
+// Threads: the requests' sums meet at fewer barriers in small blocks, and large batches
+// have several requests per thread otherwise.
+constexpr int kPlanSmall = 256, kPlanLarge = 1024;
+constexpr int kTokensEach = 2;   // per thread, before another CTA is added
 
+template <int T>
 struct PlanSmem {
-  long warp_a[32], warp_b[32];
-  long total_a, total_b;
+  long warp_a[T / 32], warp_b[T / 32];
   int pops, last;
 };
 
-// Exclusive sums of a and b over the block's threads; their totals in sm.
-__device__ __forceinline__ void scan2(long& a, long& b, PlanSmem& sm) {
+// Exclusive sums of a and b over the block's threads, and their totals.
+template <int T>
+__device__ __forceinline__ void scan2(long& a, long& b, long& total_a, long& total_b,
+                                      PlanSmem<T>& sm) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long a0 = a, b0 = b;
 #pragma unroll
@@ -49,27 +53,24 @@ __device__ __forceinline__ void scan2(long& a, long& b, PlanSmem& sm) {
     sm.warp_b[warp] = b;
   }
   __syncthreads();
-  if (warp == 0) {
-    long x = sm.warp_a[lane], y = sm.warp_b[lane];
-    const long x0 = x, y0 = y;
+  a -= a0;
+  b -= b0;
+  // the other warps' sums: a lane each
+  long x = lane < T / 32 ? sm.warp_a[lane] : 0, y = lane < T / 32 ? sm.warp_b[lane] : 0;
+  const long x0 = x, y0 = y;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) {
-        x += u;
-        y += v;
-      }
-    }
-    sm.warp_a[lane] = x - x0;
-    sm.warp_b[lane] = y - y0;
-    if (lane == 31) {
-      sm.total_a = x;
-      sm.total_b = y;
+  for (int o = 1; o < T / 32; o <<= 1) {
+    const long u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) {
+      x += u;
+      y += v;
     }
   }
-  __syncthreads();
-  a += sm.warp_a[warp] - a0;
-  b += sm.warp_b[warp] - b0;
+  total_a = __shfl_sync(0xffffffffu, x, T / 32 - 1);
+  total_b = __shfl_sync(0xffffffffu, y, T / 32 - 1);
+  a += __shfl_sync(0xffffffffu, x - x0, warp);
+  b += __shfl_sync(0xffffffffu, y - y0, warp);
+  __syncthreads();   // (the sums' places may be written again)
 }
 
 // The last of n (>= 1) non-decreasing entries that is at most x (the first is).
@@ -85,9 +86,10 @@ __device__ __forceinline__ int owner(const int* first, int n, int x) {
 
 __device__ __forceinline__ int clamp_int(long x) { return (int)min(x, (long)INT32_MAX); }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
+template <int T>
+__global__ void __launch_bounds__(T) plan_kernel(const PlanArgs a) {
   extern __shared__ int dyn[];
-  __shared__ PlanSmem sm;
+  __shared__ PlanSmem<T> sm;
   const int B = a.batch, tid = threadIdx.x;
   int* tok0 = dyn;              // first new token of each request, clipped to max_tokens
   int* take0 = tok0 + B + 1;    // pages taken by the requests before
@@ -105,8 +107,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     err |= kErrPool;
     count = count < 0 ? 0 : a.num_pages;
   }
-  const long cap = (long)a.max_pages * a.ps;
-  const int per = (B + kPlanThreads - 1) / kPlanThreads;   // consecutive requests per thread
+  const int cap = a.max_pages * a.ps;   // (< 2^31)
+  // x / page size, and the pages of x tokens, for 0 <= x < 2^31
+  auto over_ps = [&](int x) -> int {
+    return (int)((__umulhi((unsigned)x, a.ps_mul) + (unsigned)x) >> a.ps_shift);
+  };
+  auto pages = [&](int x) -> int { return x > 0 ? over_ps(x - 1) + 1 : 0; };
+  const int per = (B + T - 1) / T;   // consecutive requests per thread
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
 
   // ---- tokens and returned pages before each request
@@ -116,37 +123,37 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     const int d = a.add_lens[b];
     if (l < 0 || l > cap) {
       err |= 2;
-      l = l < 0 ? 0 : (int)cap;
+      l = l < 0 ? 0 : cap;
     }
     old[b] = l;
-    const int h = (int)(((long)l + a.ps - 1) / a.ps);
-    const long n = max((long)l + d, 0l), w = (n + a.ps - 1) / a.ps;
-    held[b] = d < 0 ? (int)w : h;
+    const int h = pages(l), w = d < 0 ? pages(d < -l ? 0 : l + d) : h;
+    held[b] = w;
     tok0[b] = max(d, 0);        // (the counts, until the sums are known)
-    back0[b] = d < 0 ? h - (int)w : 0;
+    back0[b] = h - w;
+    take0[b] = d <= 0 ? 0 : d <= cap - l ? pages(l + d) - h : -1;   // -1: past its row
     tokens += max(d, 0);
     back += back0[b];
   }
-  scan2(tokens, back, sm);
-  const long all_tokens = sm.total_a, all_back = sm.total_b;
+  long all_tokens, all_back;
+  scan2<T>(tokens, back, all_tokens, all_back, sm);
   if ((long)count + all_back > a.num_pages) err |= kErrPool;
   const int top = (int)min((long)count + all_back, (long)a.num_pages);   // after all returns
 
   // ---- pages taken before each request
-  long take = 0, unused = 0;
+  long take = 0, none = 0, all_take, unused;
   for (int b = b0; b < b1; ++b) {
     const int t = tok0[b], r = back0[b];
-    const long n = (long)old[b] + t, w = (n + a.ps - 1) / a.ps;
-    const bool fits = n <= cap && tokens + t <= a.max_tokens;
-    if (t > 0 && !fits) old[b] = -1 - old[b];
-    take0[b] = t > 0 && fits ? (int)(w - held[b]) : 0;
+    if (t > 0 && (take0[b] < 0 || tokens + t > a.max_tokens)) {
+      old[b] = -1 - old[b];
+      take0[b] = 0;
+    }
     tok0[b] = (int)min(tokens, (long)a.max_tokens);
     back0[b] = clamp_int(back);
     tokens += t;
     back += r;
     take += take0[b];
   }
-  scan2(take, unused, sm);
+  scan2<T>(take, none, all_take, unused, sm);
   int pops = 0;
   for (int b = b0; b < b1; ++b) {
     const int need = take0[b];
@@ -178,7 +185,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   }
   __syncthreads();
   if (sm.last) {
-    for (int b = tid; b < B; b += kPlanThreads) {
+    for (int b = tid; b < B; b += T) {
       const int o = old[b], d = a.add_lens[b];
       a.seq_lens_out[b] = o < 0 ? -1 - o : (int)max((long)o + d, 0l);
     }
@@ -186,13 +193,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   }
   if (blockIdx.x == 0) {
     if (a.start_pos)
-      for (int b = tid; b < B; b += kPlanThreads) a.start_pos[b] = old[b] < 0 ? -1 - old[b] : old[b];
+      for (int b = tid; b < B; b += T) a.start_pos[b] = old[b] < 0 ? -1 - old[b] : old[b];
     if (a.q_offsets)
-      for (int b = tid; b <= B; b += kPlanThreads) a.q_offsets[b] = tok0[b];
+      for (int b = tid; b <= B; b += T) a.q_offsets[b] = tok0[b];
   }
 
   // ---- this CTA's share of the items
-  const int stride = gridDim.x * kPlanThreads, first = blockIdx.x * kPlanThreads + tid;
+  const int stride = gridDim.x * T, first = blockIdx.x * T + tid;
   const int pushes = top - count;
   auto in_range = [&](int page) -> bool {
     if (page >= 0 && page < a.num_pages) return true;
@@ -225,7 +232,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       const int b = owner(tok0, B, i);
       if (old[b] >= 0) {
         pos = old[b] + (i - tok0[b]);
-        const int p = pos / a.ps;
+        const int p = over_ps(pos);
         const int page = p < held[b] ? a.block_table[(size_t)b * a.max_pages + p]
                                      : taken(take0[b] + (p - held[b]));
         if (in_range(page)) slot = (long)page * a.ps + (pos - p * a.ps);
@@ -236,18 +243,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   }
 }
 
+template <int T>
+cudaError_t launch_t(const PlanArgs& a, cudaStream_t st) {
+  constexpr size_t kMost = (5 * (size_t)kMaxPlanBatch + 1) * sizeof(int);
+  static_assert(kMost + sizeof(PlanSmem<T>) <= 232448, "shared memory of one CTA");
+  cudaError_t e = cudaFuncSetAttribute(plan_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)kMost);
+  if (e != cudaSuccess) return e;
+  const size_t smem = (5 * (size_t)a.batch + 1) * sizeof(int);
+  const long ctas = ((long)a.max_tokens + T * kTokensEach - 1) / (T * kTokensEach);
+  const dim3 grid((unsigned)(ctas < 1 ? 1 : ctas > 152 ? 152 : ctas));
+  return launch_pdl(plan_kernel<T>, grid, dim3(T), smem, st, a);
+}
+
 }  // namespace
 
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st) {
-  constexpr size_t kMost = (5 * (size_t)kMaxPlanBatch + 1) * sizeof(int);
-  static_assert(kMost + sizeof(PlanSmem) <= 232448, "shared memory of one CTA");
-  cudaError_t e =
-      cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
-  if (e != cudaSuccess) return e;
-  const size_t smem = (5 * (size_t)a.batch + 1) * sizeof(int);
-  const long ctas = ((long)a.max_tokens + kPlanTokens - 1) / kPlanTokens;
-  const dim3 grid((unsigned)(ctas < 1 ? 1 : ctas > 152 ? 152 : ctas));
-  return launch_pdl(plan_kernel, grid, dim3(kPlanThreads), smem, st, a);
+  return a.batch <= kPlanSmall ? launch_t<kPlanSmall>(a, st) : launch_t<kPlanLarge>(a, st);
 }
 
 }  // namespace kvq
