@@ -574,7 +574,7 @@ kvq_status kvq_decode_diff(const kvq_cache* c, const kvq_decode_params* p, const
  * offsets that falls counts as no tokens, and no two requests may share a row.
  *   q   (device) bf16, or E4M3 codes (p->q_fp8), [num_tokens][Hq][head_dim], 16-byte
  *       aligned
- *   out (device) [num_tokens][Hq][head_dim], 16-byte aligned
+ *   out (device) [num_tokens][Hq][head_dim], 32-byte aligned
  *   workspace (device) kvq_chunk_workspace_bytes for the device's SMs, 32-byte aligned;
  *       nothing in it has to be kept or cleared between calls.
  * Uses batch, num_q_heads, qk_dim = v_dim = head_dim, seq_lens, max_kv_len, sm_scale,

@@ -1000,7 +1000,8 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_decode_params* p, c
       p->max_kv_len > INT_MAX - 4096)
     return KVQ_ERR_UNSUPPORTED;
   if (p->batch == 0 || num_tokens == 0) return KVQ_OK;
-  if (!q || !aligned16(q) || !q_offsets || !out || !aligned16(out)) return KVQ_ERR_INVALID;
+  if (!q || !aligned16(q) || !q_offsets || !out || (reinterpret_cast<uintptr_t>(out) & 31u))
+    return KVQ_ERR_INVALID;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 31u)) return KVQ_ERR_INVALID;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||

@@ -350,40 +350,44 @@ struct ChunkCtl {
   Piece piece[kSoftWarps];
 };
 
-// A row's 32 output elements from element `c` on, in the output's type.
+// A row's 32 output elements in the output's type, 32 bytes at a time (each store touches a
+// line for every row, and their number is what it costs: half of it with 32 bytes).
 __device__ __forceinline__ void store_out32(void* out, int dtype, float scale, size_t at,
                                             const float (&v)[32]) {
   if (dtype == 0) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      p[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-  } else if (dtype == 1) {
-    uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
+    float* p = static_cast<float*>(out) + at;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      uint32_t w[4];
+      float x[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]);
-        w[e] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      p[k] = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int e = 0; e < 8; ++e) x[e] = v[8 * k + e];
+      st_v8(p + 8 * k, x);
     }
-  } else {
-    uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + at);
+    return;
+  }
+  if (dtype == 1) {
+    float* p = reinterpret_cast<float*>(static_cast<uint16_t*>(out) + at);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      uint32_t w[4];
+      float x[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 16 * k + 4 * e;
-        w[e] = f32x2_to_e4m3x2(__fdiv_rn(v[i], scale), __fdiv_rn(v[i + 1], scale)) |
-               (f32x2_to_e4m3x2(__fdiv_rn(v[i + 2], scale), __fdiv_rn(v[i + 3], scale)) << 16);
+      for (int e = 0; e < 8; ++e) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[16 * k + 2 * e], v[16 * k + 2 * e + 1]);
+        x[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
       }
-      p[k] = make_uint4(w[0], w[1], w[2], w[3]);
+      st_v8(p + 8 * k, x);
     }
+    return;
   }
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float* q = v + 4 * e;
+    x[e] = __uint_as_float(
+        f32x2_to_e4m3x2(__fdiv_rn(q[0], scale), __fdiv_rn(q[1], scale)) |
+        (f32x2_to_e4m3x2(__fdiv_rn(q[2], scale), __fdiv_rn(q[3], scale)) << 16));
+  }
+  st_v8(reinterpret_cast<float*>(static_cast<uint8_t*>(out) + at), x);
 }
 
 template <int FMT, int D, bool P2, bool DIFF>
@@ -709,6 +713,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned units = 0;   // of this slot, before the piece
     unsigned ends = 0;    // pieces before in which this slot had units
     bool ok = true;       // (after a timeout the pieces' barriers are still met)
+    // The queries of a piece, into the slot's operand tile: their 16-byte pieces go straight
+    // to the places that their f16 values take, FP8 codes at every other one (they widen to
+    // two); consecutive lanes copy consecutive pieces, and rows past the last are zeros.
+    // With one part of P the next piece's are on their way while rows are written (4096 rows
+    // behind 12288 tokens: 660 us against 676; with two parts this loses, 444 against 424 for
+    // four differential chunks of 1024: the kernels' code is larger).
+    constexpr int kHalf = DIFF ? 2 : 1;                             // of the dims in an operand
+    const int dp0 = DIFF ? slot * (D / 16) : 0;                     // its first piece (8 dims each)
+    auto q_place = [&](bool two, int trow, int piece) -> uint32_t {
+      return base + (two ? slot * Cg::kTile : 0) + (piece >> 3) * kCol + (trow >> 3) * 1024 +
+             (trow & 7) * 128 + (((piece ^ trow) & 7) << 4);
+    };
+    auto fetch_q = [&](const Piece& p) {
+      const bool two = two_rows(p);
+      if (!two && slot == 1) return;
+      const int R = p.r.n * a.G;
+      const int lp = (a.q_fp8 ? D / 16 : D / 8) / kHalf;            // pieces of a row
+      const int c = lane & (lp - 1), per = 32 / lp, trow = 32 * (warp & 3) + lane / lp;
+      const int first = p.tile * kRt + (two && !DIFF ? slot * kTok : 0) + trow;
+      // row first + k per: token qt, head qg of the group, without a division each
+      int qt = over_g(a, first), qg = first - qt * a.G;
+      const int dt = over_g(a, per), dg = per - dt * a.G;
+      const long row_bytes = a.q_fp8 ? D : 2 * D;
+      const uint8_t* q0 = static_cast<const uint8_t*>(a.q) +
+                          ((long)p.r.q0 * a.Hq + (long)p.h * a.G) * row_bytes + 16 * c +
+                          (DIFF ? slot * (row_bytes / 2) : 0);
+#pragma unroll 4
+      for (int k = 0; k < lp; ++k) {
+        const bool in = first + k * per < R;
+        const uint8_t* src = in ? q0 + ((long)qt * a.Hq + qg) * row_bytes : q0;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         q_place(two, trow + k * per, dp0 + (a.q_fp8 ? 2 * c : c))),
+                     "l"(src), "r"(in ? 16 : 0)
+                     : "memory");
+        qt += dt;
+        qg += dg;
+        if (qg >= a.G) {
+          qg -= a.G;
+          ++qt;
+        }
+      }
+    };
+    bool fetched = false;   // this piece's queries are on their way
+    auto fetch_next = [&] {
+      Walk w = walk;
+      Piece next;
+      w.at = sm.at[sw];
+      w.end = sm.end;
+      fetched = w.next(next);
+      if (fetched) fetch_q(next);
+    };
     if (lane == 0) sm.at[sw] = walk.at;
     if (threadIdx.x == 32 * kSoftWarp) sm.end = walk.end;
     asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -734,52 +789,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int hq = p.h * a.G + g;
       const int seen = live ? p.r.L - p.r.n + ti + 1 : INT_MAX;    // keys of this row
 
-      // ---- the rows' queries, into their operand tiles
-      // Their 16-byte pieces go straight to the places that their f16 values take, FP8
-      // codes at every other one (they widen to two); consecutive lanes copy consecutive
-      // pieces, and rows past the last are zeros.
-      const uint32_t qtile = base + (two ? slot * Cg::kTile : 0);
-      auto q_at = [&](int trow, int piece) -> uint32_t {
-        return qtile + (piece >> 3) * kCol + (trow >> 3) * 1024 + (trow & 7) * 128 +
-               (((piece ^ trow) & 7) << 4);
-      };
-      constexpr int kHalf = DIFF ? 2 : 1;
-      const int dp0 = DIFF ? slot * (D / 16) : 0;                   // first piece (8 dims each)
+      // ---- the rows' queries, in their operand tile
+      auto q_at = [&](int trow, int piece) -> uint32_t { return q_place(two, trow, piece); };
       // Score scale, log2 domain: positive, so that the row's largest score is that of
       // its largest product and the -inf of a key that is not seen stays one.  A scale
       // below zero (a query head's) turns the query's sign instead; one of zero, also by
       // underflow, counts as the smallest normal number.
       float qsc = 0.f;
       if (two || slot == 0) {
-        {
-          const int lp = (a.q_fp8 ? D / 16 : D / 8) / kHalf;        // pieces of a row
-          const int c = lane & (lp - 1), per = 32 / lp;
-          const int first = p.tile * kRt + (two && !DIFF ? slot * kTok : 0) + 32 * (warp & 3) +
-                            lane / lp;
-          // row first + k per: token qt, head qg of the group, without a division each
-          int qt = over_g(a, first), qg = first - qt * a.G;
-          const int dt = over_g(a, per), dg = per - dt * a.G;
-          const long row_bytes = a.q_fp8 ? D : 2 * D;
-          const uint8_t* q0 = static_cast<const uint8_t*>(a.q) +
-                              ((long)p.r.q0 * a.Hq + (long)p.h * a.G) * row_bytes + 16 * c +
-                              (DIFF ? slot * (row_bytes / 2) : 0);
-#pragma unroll 4
-          for (int k = 0; k < lp; ++k) {
-            const int trow = 32 * (warp & 3) + lane / lp + k * per;
-            const bool in = first + k * per < R;
-            const uint8_t* src = in ? q0 + ((long)qt * a.Hq + qg) * row_bytes : q0;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             q_at(trow, dp0 + (a.q_fp8 ? 2 * c : c))),
-                         "l"(src), "r"(in ? 16 : 0)
-                         : "memory");
-            qt += dt;
-            qg += dg;
-            if (qg >= a.G) {
-              qg -= a.G;
-              ++qt;
-            }
-          }
-        }
+        if (!fetched) fetch_q(p);
         const float k_log2 = (a.k_hs ? a.sm_scale * __ldg(a.k_hs + p.h) : a.sm_scale * a.k_scale) *
                              1.4426950408889634f;
         uint32_t flip = 0u;   // sign bits of a pair, where the query's sign turns
@@ -838,6 +856,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+
+      fetched = false;
 
       // ---- the slot's units
       const int cnt = two ? nt : (nt + 1 - slot) / 2;
@@ -986,6 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool bad = __any_sync(0xffffffffu, !ok || *abort_flag != 0);
       ok = !bad;
       tc_fence_after();
+      if constexpr (!P2) fetch_next();   // (before the rows are written)
       float f[2];
       if (!two) {
         factors(sm.a[0][r], sm.b[0][r], sm.a[1][r], sm.b[1][r], f[0], f[1]);

@@ -26,7 +26,7 @@ namespace {
 // Threads: the requests' sums meet at fewer barriers in small blocks, and large batches
 // have several requests per thread otherwise.
 constexpr int kPlanSmall = 256, kPlanLarge = 1024;
-constexpr int kTokensEach = 2;   // per thread, before another CTA is added
+constexpr int kTokensEach = 1;   // per thread, before another CTA is added (two: 10.7 us against 9.2 for 104000)
 
 template <int T>
 struct PlanSmem {

@@ -131,7 +131,7 @@ BOTH = [(dict(p=params(prob_scale=0.1)), UNS), (dict(p=params(num_q_heads=7)), I
 
 @pytest.mark.parametrize("kw,want", BOTH + [
     (dict(tokens=-1), INV), (dict(offs=None), INV), (dict(q=None), INV), (dict(q=P + 8), INV),
-    (dict(out=None), INV), (dict(out=P + 8), INV), (dict(ws=None), INV), (dict(ws=P + 16), INV),
+    (dict(out=None), INV), (dict(out=P + 16), INV), (dict(ws=None), INV), (dict(ws=P + 16), INV),
     (dict(tokens=1 << 30), UNS), (dict(p=params(batch=8193)), UNS),
     (dict(c=cache(head_dim=256, fmt=kvq.KVQ_NVFP4, k_bscale=P, v_bscale=P),
           p=params(qk_dim=256, v_dim=256)), UNS)])
