@@ -370,10 +370,12 @@ __device__ __forceinline__ Token token_of(const RopeArgs& a, unsigned token, boo
 
 // Cache row of kv head 0 at the token's position (head h: + h page_size), or -1
 // (skipped): past the block table as in the plain append, or a page index out
-// of range.  With slots, the token's own: below zero, or past the cache, skipped.
+// of range.  In a packed step (SLOTS) the token's slot says it: below zero, or past the
+// cache, skipped.
+template <bool SLOTS>
 __device__ __forceinline__ long rope_page(const RopeArgs& a, const Token& k, unsigned token,
                                           bool report) {
-  if (a.slots) {
+  if constexpr (SLOTS) {
     const long slot = __ldg(a.slots + token);
     if (slot < 0) return -1;
     if (slot >= (long)a.num_pages * a.ps) {   // (below 2^31, as the cache's rows are)
@@ -382,15 +384,16 @@ __device__ __forceinline__ long rope_page(const RopeArgs& a, const Token& k, uns
     }
     const unsigned page = (unsigned)slot / (unsigned)a.ps;
     return (long)page * a.Hkv * a.ps + ((unsigned)slot - page * (unsigned)a.ps);
+  } else {
+    if (k.pos >= (long)a.max_pages * a.ps) return -1;
+    const unsigned pos = (unsigned)k.pos, pi = pos / (unsigned)a.ps;
+    const int page = __ldg(a.block_table + (size_t)k.b * a.max_pages + pi);
+    if (page < 0 || page >= a.num_pages) {
+      if (report) record_error(a.error_flag, 4);
+      return -1;
+    }
+    return (long)page * a.Hkv * a.ps + (pos - pi * (unsigned)a.ps);
   }
-  if (k.pos >= (long)a.max_pages * a.ps) return -1;
-  const unsigned pos = (unsigned)k.pos, pi = pos / (unsigned)a.ps;
-  const int page = __ldg(a.block_table + (size_t)k.b * a.max_pages + pi);
-  if (page < 0 || page >= a.num_pages) {
-    if (report) record_error(a.error_flag, 4);
-    return -1;
-  }
-  return (long)page * a.Hkv * a.ps + (pos - pi * (unsigned)a.ps);
 }
 
 // FMT 0: bf16 rows out (kvq_norm_rope); otherwise K and V go to the cache.
@@ -398,8 +401,9 @@ __device__ __forceinline__ long rope_page(const RopeArgs& a, const Token& k, uns
 // gridDim.y blocks: a group takes every (per_token gridDim.y)-th of the token's
 // rows (queries, keys, values in one numbering), the next row's loads going
 // out before the present one's arithmetic.
-// QF8 (FMT 0): the queries leave as E4M3 codes.
-template <int D, int FMT, bool INTER, bool QF8>
+// QF8 (FMT 0): the queries leave as E4M3 codes.  SLOTS: see rope_page (a variant: decided at
+// run time it costs the append of 48 single tokens 0.06 us of 3.70).
+template <int D, int FMT, bool INTER, bool QF8, bool SLOTS>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     rope_kernel(const RopeArgs a, int per_token) {
   // the append is an ordinary launch (it starts after all earlier work), the
@@ -435,7 +439,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
   if (turned.turn && ok) ang.load(a.cos_sin + tk.pos * a.rot, a.rot / 2, turned);
   // cache row of kv head 0: the token's, whatever the head
   long page_row = -1;
-  if constexpr (FMT != 0) page_row = ok ? rope_page(a, tk, token, report) : -1;
+  if constexpr (FMT != 0) page_row = ok ? rope_page<SLOTS>(a, tk, token, report) : -1;
 
 #pragma unroll 1
   for (int i0 = 0; i0 < H; i0 += step) {   // the same rounds for every lane of the warp
@@ -513,7 +517,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
 
 // MLA: one warp per token, the 512-wide latent (normed, then NVFP4) on all
 // lanes, the 64 rope-key elements (rotated, bf16) on the first four.
-template <bool INTER>
+template <bool INTER, bool SLOTS>
 __global__ void __launch_bounds__(kRopeThreads) rope_mla_kernel(const RopeArgs a) {
   griddep_launch_dependents();
   constexpr int D = 512, kRope = 64;
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_mla_kernel(const RopeArgs a
   const unsigned token = blockIdx.x * (unsigned)(kRopeThreads / 32) + threadIdx.x / 32;
   if (token >= a.tokens) return;   // the whole warp, as below
   const Token tk = token_of(a, token, lane == 0);
-  const long crow = tk.ok ? rope_page(a, tk, token, lane == 0) : -1;
+  const long crow = tk.ok ? rope_page<SLOTS>(a, tk, token, lane == 0) : -1;
   if (crow < 0) return;
 
   const Pieces pc = pieces<D>(lane, 0);
@@ -569,13 +573,17 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t st) {
   const unsigned per_block = (unsigned)(kGroups / per_token);
   const dim3 grid((a.tokens + per_block - 1) / per_block, y), block(kRopeThreads);
   if (a.fmt == 0 && a.q_fp8)
-    return launch_pdl(rope_kernel<D, 0, INTER, true>, grid, block, 0, st, a, per_token);
+    return launch_pdl(rope_kernel<D, 0, INTER, true, false>, grid, block, 0, st, a, per_token);
   if (a.fmt == 0)
-    return launch_pdl(rope_kernel<D, 0, INTER, false>, grid, block, 0, st, a, per_token);
-  if (a.fmt == kFmtFp8)
-    rope_kernel<D, kFmtFp8, INTER, false><<<grid, block, 0, st>>>(a, per_token);
+    return launch_pdl(rope_kernel<D, 0, INTER, false, false>, grid, block, 0, st, a, per_token);
+  if (a.fmt == kFmtFp8 && a.slots)
+    rope_kernel<D, kFmtFp8, INTER, false, true><<<grid, block, 0, st>>>(a, per_token);
+  else if (a.fmt == kFmtFp8)
+    rope_kernel<D, kFmtFp8, INTER, false, false><<<grid, block, 0, st>>>(a, per_token);
+  else if (a.slots)
+    rope_kernel<D, kFmtNvfp4, INTER, false, true><<<grid, block, 0, st>>>(a, per_token);
   else
-    rope_kernel<D, kFmtNvfp4, INTER, false><<<grid, block, 0, st>>>(a, per_token);
+    rope_kernel<D, kFmtNvfp4, INTER, false, false><<<grid, block, 0, st>>>(a, per_token);
   return cudaGetLastError();
 }
 
@@ -583,7 +591,11 @@ template <bool INTER>
 cudaError_t dispatch_rope(int D, bool mla, const RopeArgs& a, cudaStream_t st) {
   if (mla) {
     const unsigned per = kRopeThreads / 32;
-    rope_mla_kernel<INTER><<<(a.tokens + per - 1) / per, kRopeThreads, 0, st>>>(a);
+    const unsigned grid = (a.tokens + per - 1) / per;
+    if (a.slots)
+      rope_mla_kernel<INTER, true><<<grid, kRopeThreads, 0, st>>>(a);
+    else
+      rope_mla_kernel<INTER, false><<<grid, kRopeThreads, 0, st>>>(a);
     return cudaGetLastError();
   }
   if (D == 64) return launch_rope_t<64, INTER>(a, st);

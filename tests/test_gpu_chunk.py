@@ -52,6 +52,21 @@ def test_shapes(diff, reqs):
 
 
 @pytest.mark.parametrize("diff", [False, True])
+def test_many_requests(diff):
+    """More requests, and more row tiles, than the shares' kernel has threads."""
+    reqs = [((37 * b) % 90, [0, 1, 2, 5, 40][b % 5]) for b in range(700)]
+    X = Packed("fp8", 64, 8, 4, 16, reqs, diff=diff)
+    X.check(X.run("bf16"), "bf16")
+
+
+@pytest.mark.parametrize("hq", [17, 130, 300])
+def test_many_heads_of_one_kv_head(hq):
+    """Groups larger than the decode takes, than an accumulator's rows, than a row tile."""
+    X = Packed("nvfp4", 64, hq, 1, 16, [(200, 1), (30, 3), (0, 2), (500, 1)])
+    X.check(X.run("f32"), "f32")
+
+
+@pytest.mark.parametrize("diff", [False, True])
 @pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
 @pytest.mark.parametrize("out", ["f32", "bf16", "e4m3"])
 @pytest.mark.parametrize("q_fp8,head_scales", [(False, False), (True, False), (False, True), (True, True)])
