@@ -358,7 +358,8 @@ kvq_status kvq_rope_append(const kvq_cache* c, const kvq_rotary* r, int batch, i
  *   positions      [max_tokens] of each new token; -1 as above, except for bad pages
  * counter is one word that is zero before the first call and left so.  No other two
  * of these arrays may overlap.  All of it runs on the GPU, in one launch: a captured
- * step replays with lengths that change.  batch <= 8192 (else KVQ_ERR_UNSUPPORTED).
+ * step replays with lengths that change.  batch <= 8192, max_tokens and num_pages <= 2^30
+ * (else KVQ_ERR_UNSUPPORTED).
  * Calls that share the free pages or the counter must not overlap on the GPU.
  */
 typedef struct kvq_page_plan {
@@ -554,7 +555,8 @@ typedef struct kvq_diff {
  * differential heads; part_o and part_lse hold two rows for each, so they are sized
  * for 2 * num_q_heads heads; num_q_heads / num_kv_heads is at most 8 and prob_scale is
  * 0 (else KVQ_ERR_UNSUPPORTED); not MLA.  kvq_auto_splits with twice the query heads
- * per kv head picks num_splits.
+ * per kv head picks num_splits.  With fresh_tokens lambda and norm, too, have to be
+ * complete before the append.
  */
 kvq_status kvq_decode_diff(const kvq_cache* c, const kvq_decode_params* p, const kvq_diff* d,
                            const void* q, float* part_o, float* part_lse, uint32_t* counters,
@@ -571,7 +573,9 @@ kvq_status kvq_decode_diff(const kvq_cache* c, const kvq_decode_params* p, const
  * before position 0 (n > L) attend to nothing and give 0.  Rows of q and out past
  * the last offset are neither read nor written.  Offsets are taken within [0,
  * num_tokens] and lengths within the block table (KVQ_DEVERR_SEQ_CLAMPED); a pair of
- * offsets that falls counts as no tokens, and no two requests may share a row.
+ * offsets that falls counts as no tokens.  No two requests may share a row: offsets with
+ * more of it than num_tokens rows could hold leave the chunks' rows unwritten
+ * (KVQ_DEVERR_SEQ_CLAMPED).
  *   q   (device) bf16, or E4M3 codes (p->q_fp8), [num_tokens][Hq][head_dim], 16-byte
  *       aligned
  *   out (device) [num_tokens][Hq][head_dim], 32-byte aligned
@@ -579,7 +583,7 @@ kvq_status kvq_decode_diff(const kvq_cache* c, const kvq_decode_params* p, const
  *       nothing in it has to be kept or cleared between calls.
  * Uses batch, num_q_heads, qk_dim = v_dim = head_dim, seq_lens, max_kv_len, sm_scale,
  * out_dtype, out_scale, error_flag and the FP8 query of p (num_splits and fresh_tokens
- * are ignored; prob_scale must be 0).  FP8 and NVFP4 caches with head_dim 64 or 128 and
+ * have to be in their ranges and change nothing; prob_scale must be 0).  FP8 and NVFP4 caches with head_dim 64 or 128 and
  * any number of query heads per kv head, per-head scales; not MLA, batch <= 8192.
  * The chunks' work is cut by its size, over the keys too, so that all SMs get the same
  * share of it, whatever the lengths.  In a batch of more than one, requests with a single
@@ -588,6 +592,8 @@ kvq_status kvq_decode_diff(const kvq_cache* c, const kvq_decode_params* p, const
  * The chunks' probabilities enter the products with V as f16 numbers: rounded to 2^-11 of
  * themselves for bf16 and E4M3 outputs, in two parts (2^-21) for fp32 outputs and for
  * differential heads; weights below 2^-32 of a row's largest count in the sum alone.
+ * Everything summed is fp32; long sums lose up to 1e-5 of themselves where all values have
+ * one sign (5e-5 for bf16 and E4M3 outputs): the matrix units' accumulators cut off.
  * A NaN among a token's keys or values reaches the rows that attend to it and no others;
  * all dims of such a row may become NaN.
  * Calls that share a workspace must not overlap on the GPU.

@@ -231,7 +231,7 @@ int box_rows(int page_size) {
 // partials of the decode that takes the requests with a single new token (splits 0: there
 // is none).  The decode reads a request's keys once for up to 16 query rows, in one
 // launch with its own split; as row tiles of 128 those few rows cost as much as full
-// ones (28 single tokens beside 4 chunks, NVFP4: 268 us, YYY with it).  A lone
+// ones (28 single tokens beside 4 chunks, NVFP4: 268 us, 240 with it).  A lone
 // request is never worth its launch.
 struct ChunkParts {
   int splits;
@@ -569,7 +569,8 @@ kvq_status kvq_plan_step(const kvq_page_plan* p, void* stream) {
   if (!p->free_pages || !p->free_count || !p->free_count_out || !p->counter) return KVQ_ERR_INVALID;
   if (p->batch > 0 && (!p->block_table || !p->seq_lens || !p->seq_lens_out || !p->add_lens))
     return KVQ_ERR_INVALID;
-  if (p->batch > kMaxPlanBatch || (long long)p->max_pages_per_seq * p->page_size >= (1LL << 31))
+  if (p->batch > kMaxPlanBatch || p->max_tokens > (1 << 30) || p->num_pages > (1 << 30) ||
+      (long long)p->max_pages_per_seq * p->page_size >= (1LL << 31))
     return KVQ_ERR_UNSUPPORTED;
   PlanArgs a{};
   a.batch = p->batch;

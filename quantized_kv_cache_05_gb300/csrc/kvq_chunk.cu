@@ -26,8 +26,19 @@
 //  * Rounding.  P enters the products with V in one f16 part for 16- and 8-bit outputs
 //    (2^-11 of a weight, against 2^-8 of the value that a bf16 output's rounding takes), in
 //    two (2^-21) for fp32 outputs, and for differential heads, whose difference may be
-//    small beside the two sums.  Sums and accumulators are fp32.
+//    small beside the two sums.  Sums and accumulators are fp32, long sums in chains
+//    (kChainOne).
 // Every wait is bounded; a timeout sets an error bit and the rows become NaN.
+//
+// What bounds it: 4096 rows x 32 heads (8 kv heads of 128, FP8) behind 12288 tokens take 646
+// us, 1.49 PFLOP/s or 77% of the matrix rate; 2048 rows behind 6144 197 (FP8) and 236
+// (NVFP4).  The tensor pipe is busy for 60% of the cycles and the schedulers issue in 45%:
+// a key tile of two slots takes 1.9 us where its products need 1.05, each slot being a chain
+// of scores, softmax and products, with some 200 cycles at every hand-over, and the codes of
+// NVFP4 take the converting warps 1.74 us a tile.  Beside that a piece costs 7 us (queries
+// 4, rows out 3), the shares' kernel 4, the merge 5 to 10: of a step of a few hundred
+// rows most of the 40 us.  Differential heads (four chunks of 1024, NVFP4: 446 us) spend
+// 2.3 to 3 us on 128 rows' key tile, bound by the two parts of P.
 
 #include <cfloat>
 #include <type_traits>
@@ -51,6 +62,15 @@ constexpr int kThreads = 512;             // four warpgroups: softmax x 2, conve
 constexpr int kRegSoft = 176, kRegConv = 96, kRegIssue = 64;
 static_assert(2 * kRegSoft + kRegConv + kRegIssue <= 4 * 128, "register pool of the launch");
 constexpr float kPShift = 7.0f;           // log2 scale of P
+// Units (key tiles of a slot) in a chain, whose products add up in TMEM.  The tensor cores
+// cut off what does not fit an accumulator, always towards zero: 5e-8 of the sum for each
+// product, 8 to a unit or 16 with two parts of P, so that with values of one sign 131072
+// keys in one chain lost 1e-3 of a row (with chains: 1e-5).  A longer piece is a sum of
+// chains, in fp32 rounded to nearest, kept in the workspace.  128 units with one part lose
+// 5e-5, far below its 2^-11 (no difference in time); 16 of differential heads 1.4e-5, nearly
+// the same of both maps' sums (four chunks of 1024, NVFP4: 445 us against 429 in one chain);
+// 8 of fp32 outputs 7e-6 (2048 rows behind 6144: 333 against 311).
+constexpr int kChainOne = 128, kChainDiff = 16, kChainF32 = 8;
 constexpr int kTmem = 512;                // S0 | S1 | O0 | O1, 128 columns each
 constexpr int kRows = 2 * kTok;           // rows of a partial in the workspace
 
@@ -190,8 +210,15 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const ChunkArgs a,
   }
   long all_active, T;
   scan2(active, tiles, all_active, T, sm);
-  const int A = (int)all_active;
-  for (int b = b0; b < b1; ++b) {
+  // more row tiles than all rows make: requests that share rows.  None is served (such
+  // offsets could ask for any amount of work)
+  const bool overlap = T > (long)a.num_tokens * a.G / rt + all_active;
+  if (overlap) {
+    T = 0;
+    if (tid == 0) record_error(a.error_flag, 2);
+  }
+  const int A = overlap ? 0 : (int)all_active;
+  for (int b = b0; b < b1 && !overlap; ++b) {
     const Request r = request(b);
     if (r.n == 0) continue;
     requests[active] = r;
@@ -397,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using Gm = Geom<FMT, D>;
   using Cg = ChunkGeom<FMT, D>;
   constexpr int kRt = DIFF ? kTok : kRows;   // rows of a row tile
+  constexpr int kChain = DIFF ? kChainDiff : P2 ? kChainF32 : kChainOne;
   extern __shared__ __align__(1024) uint8_t dyn_smem[];   // the swizzle period
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(dyn_smem);
@@ -591,9 +619,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
 #pragma unroll 1
         for (int u = 0; u < units + 2 && ok; u += 2) {
-          if (u < units || u - 2 < units) ok = step(Zero{}, u >= 2, u < units, two, u > 2);
+          // (the first product of a chain overwrites)
+          const bool acc = ((u >> 1) - 1) % kChain != 0;
+          if (u < units || u - 2 < units) ok = step(Zero{}, u >= 2, u < units, two, acc);
           if (ok && (u + 1 < units || (u >= 2 && u - 1 < units)))
-            ok = step(One{}, u >= 2, u + 1 < units, two, u > 2);
+            ok = step(One{}, u >= 2, u + 1 < units, two, acc);
         }
       }
       // every MMA has completed at exit (bounded wait)
@@ -867,99 +897,132 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int mine = seen - p.kv0 * kTok;
       const int every = p.r.L - p.r.n + over_g(a, p.tile * kRt) + 1 - p.kv0 * kTok;
       asm volatile("" ::: "memory");   // (what follows reads the piece from shared memory)
-      for (int i = 0; i < cnt && ok; ++i) {
-        const int jj = two ? i : 2 * i + slot;         // key tile of the piece
-        const int nvalid = mine - jj * kTok;           // keys of this tile that the row sees
+      float held = -INFINITY;         // the reference of what the chains before have left
+      // its place in the workspace, the share's last partial's: [8-dim column][row][8]
+      auto chain_at = [&](int col8) -> float* {
+        return part_o + (size_t)(2 * blockIdx.x + 1) * kRows * D + (slot * kTok + r) * 8 +
+               (size_t)col8 * kRows * 8;
+      };
+      int i = 0;
+#pragma unroll 1
+      while (true) {   // a chain at a time
+        for (const int end = min(i + kChain, cnt); i < end && ok; ++i) {
+          const int jj = two ? i : 2 * i + slot;         // key tile of the piece
+          const int nvalid = mine - jj * kTok;           // keys of this tile that the row sees
+          ok = __all_sync(0xffffffffu, wait(sm.s_full[slot], (units + i) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t s[4][32];   // the row's scores
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(sS + 32 * c, s[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_wait_ld32(s[c]);
+          if ((jj + 1) * kTok > every) {   // some row does not see all of it
+            if (__any_sync(0xffffffffu, nvalid < kTok)) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (32 * c + k >= nvalid) s[c][k] = 0xFF800000u;   // -inf
+            }
+            // the V operand tile of the same number: converted, with its NaN rows listed
+            const unsigned j = j0 + jj;
+            ok = __all_sync(0xffffffffu, wait(sm.op_full[1][j & 1], (j >> 1) & 1));
+            if (!ok) break;
+#pragma unroll
+            for (int w = 0; w < kTok / 32; ++w) {
+              const int upto = nvalid - 32 * w;   // of this word's rows, those that are seen
+              const uint32_t seen_rows =
+                  upto >= 32 ? 0xffffffffu : upto <= 0 ? 0u : (1u << upto) - 1u;
+              poison |= (*(volatile uint32_t*)&sm.nan_rows[j & 1][w] & seen_rows) != 0u;
+            }
+          }
+          float mx4[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            mx4[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+            for (int k = 1; k < 31; k += 2)
+              mx4[c] = max3(mx4[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
+            mx4[c] = fmaxf(mx4[c], __uint_as_float(s[c][31]));
+          }
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * qsc;
+          const bool move = mx > m + kLazyMax;   // also the first finite tile
+          if (__any_sync(0xffffffffu, move)) {
+            const float alpha = move ? ex2(m - mx) : 1.f;
+            m = move ? mx : m;
+            l *= alpha;
+            // O of the slot's earlier units (complete: this unit's S was committed
+            // after them)
+            if (i > 0) {
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(sO + 16 * c, o);
+                tmem_wait_ld16(o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tmem_st16(sO + 16 * c, o);
+              }
+            }
+          }
+          const float ref = (m == -INFINITY ? 0.f : m) - kPShift;
+          const uint64_t q2 = pack2(qsc, qsc), r2 = pack2(-ref, -ref);
+          uint64_t sum2 = 0ull;   // two zeros
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float2 x = unpack2(fma2(
+                  pack2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), q2, r2));
+              const float p0 = ex2(x.x), p1 = ex2(x.y);
+              sum2 = add2(sum2, pack2(p0, p1));
+              if constexpr (P2) {   // the leading 11 bits, and what is left
+                const float h0 = __uint_as_float(__float_as_uint(p0) & 0xFFFFE000u);
+                const float h1 = __uint_as_float(__float_as_uint(p1) & 0xFFFFE000u);
+                hi[k] = pack_f16x2(h0, h1);
+                const float2 r = unpack2(fma2(pack2(h0, h1), pack2(-1.f, -1.f), pack2(p0, p1)));
+                lo[k] = pack_f16x2(r.x, r.y);
+              } else {
+                hi[k] = pack_f16x2(p0, p1);
+              }
+            }
+            tmem_st16(sS + (P2 ? 32 * c : 16 * c), hi);
+            if constexpr (P2) tmem_st16(sS + 32 * c + 16, lo);
+          }
+          // P is written (and O rescaled): its products may go.  (Handed over in halves, each
+          // with a wait of its own: 722 us against 685 for 4096 rows x 32 heads behind 12288
+          // tokens.)
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[slot]));
+          const float2 sum = unpack2(sum2);
+          l += sum.x + sum.y;
+        }
+        // The chain's products are complete with the next unit's scores, whose product
+        // overwrites O.
+        if (i >= cnt || !ok) break;
         ok = __all_sync(0xffffffffu, wait(sm.s_full[slot], (units + i) & 1));
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[4][32];   // the row's scores
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(sS + 32 * c, s[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_ld32(s[c]);
-        if ((jj + 1) * kTok > every) {   // some row does not see all of it
-          if (__any_sync(0xffffffffu, nvalid < kTok)) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (32 * c + k >= nvalid) s[c][k] = 0xFF800000u;   // -inf
-          }
-          // the V operand tile of the same number: converted, with its NaN rows listed
-          const unsigned j = j0 + jj;
-          ok = __all_sync(0xffffffffu, wait(sm.op_full[1][j & 1], (j >> 1) & 1));
-          if (!ok) break;
-#pragma unroll
-          for (int w = 0; w < kTok / 32; ++w) {
-            const int upto = nvalid - 32 * w;   // of this word's rows, those that are seen
-            const uint32_t seen_rows = upto >= 32 ? 0xffffffffu : upto <= 0 ? 0u : (1u << upto) - 1u;
-            poison |= (*(volatile uint32_t*)&sm.nan_rows[j & 1][w] & seen_rows) != 0u;
-          }
-        }
-        float mx4[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx4[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-          for (int k = 1; k < 31; k += 2)
-            mx4[c] = max3(mx4[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
-          mx4[c] = fmaxf(mx4[c], __uint_as_float(s[c][31]));
-        }
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * qsc;
-        const bool move = mx > m + kLazyMax;   // also the first finite tile
-        if (__any_sync(0xffffffffu, move)) {
-          const float alpha = move ? ex2(m - mx) : 1.f;
-          m = move ? mx : m;
-          l *= alpha;
-          // O of the slot's earlier units (complete: this unit's S was committed
-          // after them)
-          if (i > 0) {
+        const float f = held == m ? 1.f : ex2(held - m);
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld16(sO + 16 * c, o);
-              tmem_wait_ld16(o);
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[16];
+          tmem_ld16(sO + 16 * c, o);
+          tmem_wait_ld16(o);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-              tmem_st16(sO + 16 * c, o);
-            }
+          for (int h = 0; h < 2; ++h) {
+            float x[8] = {};
+            if (i > kChain) ld_v8(chain_at(2 * c + h), x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = x[k] * f + __uint_as_float(o[8 * h + k]);
+            st_v8(chain_at(2 * c + h), x);
           }
         }
-        const float ref = (m == -INFINITY ? 0.f : m) - kPShift;
-        const uint64_t q2 = pack2(qsc, qsc), r2 = pack2(-ref, -ref);
-        uint64_t sum2 = 0ull;   // two zeros
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float2 x = unpack2(fma2(
-                pack2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), q2, r2));
-            const float p0 = ex2(x.x), p1 = ex2(x.y);
-            sum2 = add2(sum2, pack2(p0, p1));
-            if constexpr (P2) {   // the leading 11 bits, and what is left
-              const float h0 = __uint_as_float(__float_as_uint(p0) & 0xFFFFE000u);
-              const float h1 = __uint_as_float(__float_as_uint(p1) & 0xFFFFE000u);
-              hi[k] = pack_f16x2(h0, h1);
-              const float2 r = unpack2(fma2(pack2(h0, h1), pack2(-1.f, -1.f), pack2(p0, p1)));
-              lo[k] = pack_f16x2(r.x, r.y);
-            } else {
-              hi[k] = pack_f16x2(p0, p1);
-            }
-          }
-          tmem_st16(sS + (P2 ? 32 * c : 16 * c), hi);
-          if constexpr (P2) tmem_st16(sS + 32 * c + 16, lo);
-        }
-        // P is written (and O rescaled): its products may go.  (Handed over in halves, each
-        // with a wait of its own: 722 us against 685 for 4096 rows x 32 heads behind 12288
-        // tokens.)
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[slot]));
-        const float2 sum = unpack2(sum2);
-        l += sum.x + sum.y;
+        held = m;
       }
       if (poison) l = NAN;
       j0 += nt;
@@ -1001,6 +1064,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!two) sm.b[slot][r] = l;
       }
       if (cnt > 0) ok = ok && wait(sm.o_full[slot], ends++ & 1);
+      if (cnt > kChain) {   // the chains together
+        tc_fence_after();
+        const float f = held == m ? 1.f : ex2(held - m);
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[16];
+          tmem_ld16(sO + 16 * c, o);
+          tmem_wait_ld16(o);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x[8];
+            ld_v8(chain_at(2 * c + h), x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              o[8 * h + k] = __float_as_uint(__uint_as_float(o[8 * h + k]) + x[k] * f);
+          }
+          tmem_st16(sO + 16 * c, o);
+        }
+        tmem_wait_st();
+      }
       tc_fence_before();
       if (join) asm volatile("bar.sync 1, 256;" ::: "memory");   // both accumulators are done
       const bool bad = __any_sync(0xffffffffu, !ok || *abort_flag != 0);

@@ -155,6 +155,16 @@ def test_offsets_and_lengths_out_of_range():
     assert torch.isfinite(o[5:25]).all() and (o[25:] == 0).all()
 
 
+def test_offsets_that_overlap():
+    """Requests that share rows, more of them than the rows hold: nothing is written."""
+    X = Packed("fp8", 64, 8, 2, 16, [(200, 200), (30, 20), (200, 200), (40, 2), (200, 200)])
+    q = X.q[:200].contiguous()
+    out = torch.full(q.shape, 7.0, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    X.chunk("f32")(q, i32([0, 200, 0, 200, 0, 200]), X.lens_t, out=out, error_flag=err)
+    assert int(err) == kvq.KVQ_DEVERR_SEQ_CLAMPED and (out == 7).all()
+
+
 def test_bad_pages():
     """A page out of range is read as page 0, with its error bit."""
     X = Packed("fp8", 64, 4, 2, 16, [(200, 5), (30, 20)])
@@ -238,6 +248,23 @@ def test_flat_tail_behind_one_large_weight():
     ref = X.reference()
     for out in ("f32", "bf16"):
         X.check(X.run(out), out, ref)
+
+
+@pytest.mark.parametrize("out,diff,rows,L,norm", [
+    ("f32", False, 512, 6000, True), ("f32", True, 256, 14000, True), ("f32", True, 256, 14000, False),
+    ("bf16", False, 512, 45000, True)])
+def test_long_sums_of_one_sign(out, diff, rows, L, norm):
+    """Long pieces whose products all have one sign: an accumulator that is cut off at each
+    of its products loses more and more of it."""
+    X = Packed("fp8", 128, 32, 8, 48, [(L - rows, rows)], diff=diff, norm=norm)
+    X.codes[1] &= 0x7F
+    X.val[1] = X.val[1].abs()
+    o, tol, _ = ref = X.reference()
+    got = X.run(out)
+    X.check(got, out, ref)
+    if not diff and out == "f32":   # fp32: also on the whole
+        e = (got.double().cpu().numpy() - o) / o
+        assert abs(e.mean()) < 2.0 ** -17
 
 
 def test_is_the_decode_and_the_prefill():

@@ -70,7 +70,8 @@ def plan(**kw):
     (dict(seq_lens=None), INV), (dict(seq_lens_out=None), INV), (dict(add_lens=None), INV),
     (dict(free_pages=None), INV), (dict(free_count=None), INV), (dict(free_count_out=None), INV),
     (dict(counter=None), INV), (dict(batch=8193), UNS),
-    (dict(max_pages_per_seq=1 << 27), UNS)])
+    (dict(max_pages_per_seq=1 << 27), UNS), (dict(max_tokens=(1 << 30) + 1), UNS),
+    (dict(num_pages=(1 << 30) + 1), UNS)])
 def test_plan_refused(kw, want):
     assert plan(**kw) == want
 
