@@ -65,12 +65,12 @@ constexpr float kPShift = 7.0f;           // log2 scale of P
 // Units (key tiles of a slot) in a chain, whose products add up in TMEM.  The tensor cores
 // cut off what does not fit an accumulator, always towards zero: 5e-8 of the sum for each
 // product, 8 to a unit or 16 with two parts of P, so that with values of one sign 131072
-// keys in one chain lost 1e-3 of a row (with chains: 1e-5).  A longer piece is a sum of
+// keys in one chain lost 1e-3 of a row.  A longer piece is a sum of
 // chains, in fp32 rounded to nearest, kept in the workspace.  128 units with one part lose
 // 5e-5, far below its 2^-11 (no difference in time); 16 of differential heads 1.4e-5, nearly
 // the same of both maps' sums (four chunks of 1024, NVFP4: 445 us against 429 in one chain);
-// 8 of fp32 outputs 7e-6 (2048 rows behind 6144: 333 against 311).
-constexpr int kChainOne = 128, kChainDiff = 16, kChainF32 = 8;
+// 4 of fp32 outputs 3.5e-6 (2048 rows behind 6144: 357 against 311, and 334 with 8 units).
+constexpr int kChainOne = 128, kChainDiff = 16, kChainF32 = 4;
 constexpr int kTmem = 512;                // S0 | S1 | O0 | O1, 128 columns each
 constexpr int kRows = 2 * kTok;           // rows of a partial in the workspace
 

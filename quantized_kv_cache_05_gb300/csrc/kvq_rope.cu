@@ -26,7 +26,8 @@
 // other.  The append of 4 x 2048 ragged padded tokens (48 heads, 94 MB): 27.0 us,
 // 52% of the copy rate; 57 to 62% of the issue slots while an SM is busy, 46% over
 // the kernel.  One token each of 48 requests: 4.3 us.  Settling quotients takes
-// 0.8 and 0.7 us of these two.
+// 0.8 and 0.7 us of these two.  The packed append of 8000 tokens (48 heads, 184 MB): 45.0
+// us, 60% of the copy rate, bound as the padded one is.
 
 #include <algorithm>
 
