@@ -593,7 +593,7 @@ kvq_status kvq_decode_diff(const kvq_cache* c, const kvq_decode_params* p, const
  * themselves for bf16 and E4M3 outputs, in two parts (2^-21) for fp32 outputs and for
  * differential heads; weights below 2^-32 of a row's largest count in the sum alone.
  * Everything summed is fp32, but the matrix units' accumulators cut off: where all values
- * have one sign, long sums lose up to 5e-6 of themselves with fp32 outputs, 1.5e-5 with
+ * have one sign, long sums lose up to 6e-6 of themselves with fp32 outputs, 1.5e-5 with
  * differential heads and 5e-5 with bf16 and E4M3 outputs.
  * A NaN among a token's keys or values reaches the rows that attend to it and no others;
  * all dims of such a row may become NaN.

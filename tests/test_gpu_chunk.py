@@ -267,6 +267,14 @@ def test_long_sums_of_one_sign(out, diff, rows, L, norm):
         assert abs(e.mean()) < 2.0 ** -17
 
 
+@pytest.mark.parametrize("out,diff,past", [("f32", False, 6000), ("f32", True, 6000), ("bf16", False, 70000)])
+@pytest.mark.parametrize("ramp", [(0.2, 2.0), (2.0, 0.2)])
+def test_long_sums_of_few_rows(out, diff, past, ramp):
+    """Pieces of many key tiles with one accumulator's rows, whose maxima move."""
+    X = Packed("fp8", 64, 8, 2, 64, [(past + 13 * b, 20) for b in range(40)], diff=diff, k_ramp=ramp)
+    X.check(X.run(out), out)
+
+
 def test_is_the_decode_and_the_prefill():
     """Single tokens and equal chunks: the library's other calls agree."""
     X = Packed("nvfp4", 128, 8, 2, 16, [(400, 1), (31, 1), (0, 1)])
