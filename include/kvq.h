@@ -176,11 +176,12 @@ typedef struct kvq_decode_params {
   float q_scale;             /* q_fp8 without q_head_scale: finite > 0 */
   const float* q_head_scale; /* (device, optional) [num_q_heads] */
   /*
-   * kvq_decode_shared only (the other calls ignore it).  0: the prefix's
-   * probabilities enter the products with V in two f16 parts, as kvq_decode's
-   * do.  1: in one, rounded by up to 2^-11 of a weight where kvq_decode keeps
-   * 2^-22; a bf16 output, whose own rounding is 2^-8, then differs here and
-   * there by one step, and the products with V take half the tensor-core time.
+   * kvq_decode_shared and kvq_chunk_attention only (the other calls ignore it).
+   * 0: the probabilities of the prefix (the chunks) enter the products with V in
+   * two f16 parts, as kvq_decode's do.  1: in one, rounded by up to 2^-11 of a
+   * weight where kvq_decode keeps 2^-22; a bf16 output, whose own rounding is 2^-8,
+   * then differs here and there by one step, and the products with V take half the
+   * tensor-core time.  Differential heads have two parts either way.
    */
   int32_t prefix_p_f16;
 } kvq_decode_params;
@@ -582,19 +583,19 @@ kvq_status kvq_decode_diff(const kvq_cache* c, const kvq_decode_params* p, const
  *   workspace (device) kvq_chunk_workspace_bytes for the device's SMs, 32-byte aligned;
  *       nothing in it has to be kept or cleared between calls.
  * Uses batch, num_q_heads, qk_dim = v_dim = head_dim, seq_lens, max_kv_len, sm_scale,
- * out_dtype, out_scale, error_flag and the FP8 query of p (num_splits and fresh_tokens
+ * out_dtype, out_scale, error_flag, prefix_p_f16 and the FP8 query of p (num_splits and fresh_tokens
  * have to be in their ranges and change nothing; prob_scale must be 0).  FP8 and NVFP4 caches with head_dim 64 or 128 and
  * any number of query heads per kv head, per-head scales; not MLA, batch <= 8192.
  * The chunks' work is cut by its size, over the keys too, so that all SMs get the same
  * share of it, whatever the lengths.  In a batch of more than one, requests with a single
  * new token are the split-KV decode's (at most 16 query rows per kv head, 8 differential
  * ones; with more they count as chunks).  Three or four launches on `stream`.
- * The chunks' probabilities enter the products with V as f16 numbers: rounded to 2^-11 of
- * themselves for bf16 and E4M3 outputs, in two parts (2^-21) for fp32 outputs and for
- * differential heads; weights below 2^-32 of a row's largest count in the sum alone.
+ * The chunks' probabilities enter the products with V in two f16 parts (2^-21 of a weight),
+ * or, of plain heads and where p->prefix_p_f16 asks for it, in one (2^-11); weights below
+ * 2^-32 of a row's largest count in the sum alone.
  * Everything summed is fp32, but the matrix units' accumulators cut off: where all values
  * have one sign, long sums lose up to 6e-6 of themselves with fp32 outputs, 1.5e-5 with
- * differential heads and 5e-5 with bf16 and E4M3 outputs.
+ * differential heads and 5e-5 with bf16 and E4M3 outputs and with one part.
  * A NaN among a token's keys or values reaches the rows that attend to it and no others;
  * all dims of such a row may become NaN.
  * Calls that share a workspace must not overlap on the GPU.

@@ -992,7 +992,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_decode_params* p, c
   s = check_params(p);
   if (s == KVQ_OK && d) s = check_diff(d);
   if (s != KVQ_OK) return s;
-  if (num_tokens < 0) return KVQ_ERR_INVALID;
+  if (num_tokens < 0 || (p->prefix_p_f16 != 0 && p->prefix_p_f16 != 1)) return KVQ_ERR_INVALID;
   if (is_mla(c) || p->prob_scale > 0.f) return KVQ_ERR_UNSUPPORTED;
   s = check_heads_of(c, p, false);
   if (s != KVQ_OK) return s;
@@ -1035,6 +1035,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_decode_params* p, c
   a.max_kv_len = p->max_kv_len;
   divisor(G, &a.g_mul, &a.g_shift);
   a.box = box_rows(c->page_size);
+  a.wide_p = p->prefix_p_f16 == 0;
   a.out_dtype = p->out_dtype;
   a.out_scale = p->out_scale;
   a.sm_scale = p->sm_scale;

@@ -23,19 +23,22 @@
 //    row, by the thread that has the row.  Values of such a tile that are NaN (codes of a
 //    NaN input) would reach rows that do not see them, as 0 NaN: there the tile's NaN rows
 //    become zeros, and the rows that see one of them become NaN as a whole.
-//  * Rounding.  P enters the products with V in one f16 part for 16- and 8-bit outputs
-//    (2^-11 of a weight, against 2^-8 of the value that a bf16 output's rounding takes), in
-//    two (2^-21) for fp32 outputs, and for differential heads, whose difference may be
-//    small beside the two sums.  Sums and accumulators are fp32, long sums in chains
+//  * Rounding.  P enters the products with V in two f16 parts (2^-21 of a weight), as in the
+//    decode, so that a token has the same bits whether its request brings one or many; where
+//    the caller asks for it, plain heads have one (2^-11, against 2^-8 of the value that a
+//    bf16 output's rounding takes).  Differential heads always have two: their difference may
+//    be small beside the two sums.  Sums and accumulators are fp32, long sums in chains
 //    (kChainOne).
 // Every wait is bounded; a timeout sets an error bit and the rows become NaN.
 //
-// What bounds it: 4096 rows x 32 heads (8 kv heads of 128, FP8) behind 12288 tokens take 646
-// us, 1.49 PFLOP/s or 77% of the matrix rate; 2048 rows behind 6144 197 (FP8) and 236
-// (NVFP4).  The tensor pipe is busy for 60% of the cycles and the schedulers issue in 45%:
-// a key tile of two slots takes 1.9 us where its products need 1.05, each slot being a chain
-// of scores, softmax and products, with some 200 cycles at every hand-over, and the codes of
-// NVFP4 take the converting warps 1.74 us a tile.  Beside that a piece costs 7 us (queries
+// What bounds it: 4096 rows x 32 heads (8 kv heads of 128, FP8) behind 12288 tokens take 1108
+// us, 67% of the matrix rate with the second part's products (742 us), and 653 with one part
+// of P (495, 76%); 2048 rows behind 6144 take 312 (FP8) and 335 (NVFP4), with one part 197 and
+// 237.  With one part the tensor pipe is busy for 60% of the cycles and the schedulers issue in
+// 45%: a key tile of two slots takes 1.9 us where its products need 1.05, each slot being a
+// chain of scores, softmax and products, with some 200 cycles at every hand-over, and the codes
+// of NVFP4 take the converting warps 1.74 us a tile.  With two parts it is some 2.9 us for 1.57:
+// the softmax splits P and writes it twice.  Beside that a piece costs 7 us (queries
 // 4, rows out 3), the shares' kernel 4, the merge 5 to 10: of a step of a few hundred
 // rows most of the 40 us.  Differential heads (four chunks of 1024, NVFP4: 446 us) spend
 // 2.3 to 3 us on 128 rows' key tile, bound by the two parts of P.
@@ -66,19 +69,22 @@ constexpr float kPShift = 7.0f;           // log2 scale of P
 // cut off what does not fit an accumulator, always towards zero: 5e-8 of the sum for each
 // product, 8 to a unit or 16 with two parts of P, so that with values of one sign 131072
 // keys in one chain lost 1e-3 of a row.  A longer piece is a sum of
-// chains, in fp32 rounded to nearest, kept in the workspace.  128 units with one part lose
-// 5e-5, far below its 2^-11 (no difference in time); 16 of differential heads 1.4e-5, nearly
-// the same of both maps' sums (four chunks of 1024, NVFP4: 445 us against 429 in one chain);
-// 4 of fp32 outputs 3.5e-6 (2048 rows behind 6144: 357 against 311, and 334 with 8 units).
-constexpr int kChainOne = 128, kChainDiff = 16, kChainF32 = 4;
+// chains, in fp32 rounded to nearest, kept in the workspace.  64 units with one part lose
+// 2.5e-5 on average and up to 3.8e-5 (128: 5.6e-5 and 7.4e-5, in the same time); 32 with two
+// parts 3.3e-5 (64: 6.5e-5; 4096 rows behind 12288 tokens: 1108 us against 1076); 16 of
+// differential heads 1.4e-5, nearly the same of both maps' sums (four chunks of 1024, NVFP4:
+// 445 us against 429 in one chain); 4 of fp32 outputs 3.9e-6 (2048 rows behind 6144: 361 us
+// against 312 with 32 units, and 334 with 8).  Powers of two: a unit's place in its chain is a
+// mask.
+constexpr int kChainOne = 64, kChainTwo = 32, kChainDiff = 16, kChainF32 = 4;
 constexpr int kTmem = 512;                // S0 | S1 | O0 | O1, 128 columns each
 constexpr int kRows = 2 * kTok;           // rows of a partial in the workspace
 
 // Cost of a row tile, in twelfths of a key tile with both accumulators' rows (1.9 us): for
 // each key tile 12, or with one accumulator's rows what its conversion takes (NVFP4: 1.74
-// us; FP8: half of it, as two key tiles are on their way), and kCostFixed for its queries
-// and its output (7 us).  A share is at least kCostShare, a piece kMinPiece key tiles.
-constexpr int kCostTwo = 12, kCostOneFp8 = 7, kCostOneNvfp4 = 11;
+// us; FP8: half of it, as two key tiles are on their way; with two parts of P 1.75 to 1.9 of
+// 2.4 us), and kCostFixed for its queries and its output (7 us).  A share is at least kCostShare, a piece kMinPiece key tiles.
+constexpr int kCostTwo = 12, kCostOneFp8 = 7, kCostOneNvfp4 = 11, kCostOneWide = 9;
 constexpr int kCostFixed = 40, kCostShare = 64, kMinPiece = 3;
 
 // ---------------------------------------------------------------------------
@@ -424,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using Gm = Geom<FMT, D>;
   using Cg = ChunkGeom<FMT, D>;
   constexpr int kRt = DIFF ? kTok : kRows;   // rows of a row tile
-  constexpr int kChain = DIFF ? kChainDiff : P2 ? kChainF32 : kChainOne;
+  // units to a chain: plain heads with two parts of P know it by the output's type
+  const int chain = DIFF ? kChainDiff : !P2 ? kChainOne : a.out_dtype == 0 ? kChainF32 : kChainTwo;
   extern __shared__ __align__(1024) uint8_t dyn_smem[];   // the swizzle period
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(dyn_smem);
@@ -620,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int u = 0; u < units + 2 && ok; u += 2) {
           // (the first product of a chain overwrites)
-          const bool acc = ((u >> 1) - 1) % kChain != 0;
+          const bool acc = (((u >> 1) - 1) & (chain - 1)) != 0;
           if (u < units || u - 2 < units) ok = step(Zero{}, u >= 2, u < units, two, acc);
           if (ok && (u + 1 < units || (u >= 2 && u - 1 < units)))
             ok = step(One{}, u >= 2, u + 1 < units, two, acc);
@@ -906,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int i = 0;
 #pragma unroll 1
       while (true) {   // a chain at a time
-        for (const int end = min(i + kChain, cnt); i < end && ok; ++i) {
+        for (const int end = min(i + chain, cnt); i < end && ok; ++i) {
           const int jj = two ? i : 2 * i + slot;         // key tile of the piece
           const int nvalid = mine - jj * kTok;           // keys of this tile that the row sees
           ok = __all_sync(0xffffffffu, wait(sm.s_full[slot], (units + i) & 1));
@@ -1016,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float x[8] = {};
-            if (i > kChain) ld_v8(chain_at(2 * c + h), x);
+            if (i > chain) ld_v8(chain_at(2 * c + h), x);
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] = x[k] * f + __uint_as_float(o[8 * h + k]);
             st_v8(chain_at(2 * c + h), x);
@@ -1064,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!two) sm.b[slot][r] = l;
       }
       if (cnt > 0) ok = ok && wait(sm.o_full[slot], ends++ & 1);
-      if (cnt > kChain) {   // the chains together
+      if (cnt > chain) {   // the chains together
         tc_fence_after();
         const float f = held == m ? 1.f : ex2(held - m);
 #pragma unroll 1
@@ -1363,7 +1370,7 @@ cudaError_t launch_t(const TensorMaps& m, const ChunkArgs& a, int grid, cudaStre
 template <int FMT, int D>
 cudaError_t by_kind(const TensorMaps& m, const ChunkArgs& a, int grid, cudaStream_t st) {
   if (a.diff_lambda) return launch_t<FMT, D, true, true>(m, a, grid, st);
-  if (a.out_dtype == 0) return launch_t<FMT, D, true, false>(m, a, grid, st);
+  if (a.wide_p) return launch_t<FMT, D, true, false>(m, a, grid, st);
   return launch_t<FMT, D, false, false>(m, a, grid, st);
 }
 
@@ -1376,7 +1383,7 @@ cudaError_t launch_shares(int fmt, const ChunkArgs& a, int grid, cudaStream_t st
       cudaFuncSetAttribute(share_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
   if (e != cudaSuccess) return e;
   const bool diff = a.diff_lambda != nullptr;
-  const int one = diff ? kCostTwo : fmt == kFmtFp8 ? kCostOneFp8 : kCostOneNvfp4;
+  const int one = diff ? kCostTwo : a.wide_p ? kCostOneWide : fmt == kFmtFp8 ? kCostOneFp8 : kCostOneNvfp4;
   return launch_pdl(share_kernel, dim3(1), dim3(kShareThreads), (size_t)a.batch * sizeof(int), st,
                     a, grid, diff ? kTok : kRows, one);
 }

@@ -186,6 +186,7 @@ struct ChunkArgs {
   int32_t* error_flag;
   int batch, num_tokens, G, Hq, Hkv, D, ps, max_pages, num_pages, max_kv_len;
   int box;                    // TMA box rows
+  int wide_p;                 // 1: P as high part and residual, 0: one f16 (plain heads)
   uint32_t g_mul, g_shift;    // x / G = (umulhi(x, g_mul) + x) >> g_shift for x < 2^31
   int out_dtype;
   float out_scale, sm_scale, k_scale, v_scale;

@@ -467,8 +467,8 @@ class DecodeConfig:
     q_fp8: bool = False
     q_scale: float = 1.0
     q_head_scale: Optional[torch.Tensor] = None
-    # SharedDecode: the prefix's probabilities in one f16 instead of two
-    # (kvq_decode_params)
+    # SharedDecode: the prefix's probabilities in one f16 instead of two; ChunkAttention:
+    # those of plain heads (kvq_decode_params)
     prefix_p_f16: bool = False
 
     def params(self, seq_lens: Optional[torch.Tensor], error_flag: Optional[torch.Tensor] = None
@@ -695,12 +695,15 @@ class ChunkAttention:
     def __init__(self, cache: QuantizedKVCache, batch: int, num_q_heads: int, max_kv_len: int,
                  sm_scale: float, out: str = "bf16", out_scale: float = 1.0, q_fp8: bool = False,
                  q_scale: float = 1.0, q_head_scale: Optional[torch.Tensor] = None,
-                 diff: Optional[Differential] = None):
+                 diff: Optional[Differential] = None, p_f16: bool = False):
+        """p_f16: the probabilities of plain heads with 11 bits instead of 21, for outputs
+        that need not be the decode's to the last step (kvq_decode_params.prefix_p_f16)."""
         _check(batch <= cache.block_table.shape[0], "more requests than the block table has")
         device = cache.k_codes.device
         cfg = self._cfg = DecodeConfig(batch, num_q_heads, cache.D, cache.D, 1, max_kv_len, sm_scale,
                                        out=out, out_scale=out_scale, q_fp8=q_fp8, q_scale=q_scale,
-                                       q_head_scale=_head_scale(q_head_scale, num_q_heads, device))
+                                       q_head_scale=_head_scale(q_head_scale, num_q_heads, device),
+                                       prefix_p_f16=p_f16)
         self._cache = cache
         self._diff = (diff, diff._for(num_q_heads, cache.D, device) if diff is not None else 0)
         # the call's own checks, without requests
