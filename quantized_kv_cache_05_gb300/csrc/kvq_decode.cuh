@@ -36,7 +36,8 @@
 //    permutation.  The token-pair layout of the V^T operand is built with
 //    byte permutes (FP8) or nibble masks (E2M1).
 //  * P is split into an f16 high part and an f16 residual (two MMAs), so the
-//    probabilities keep ~22 bits; with FP8 probabilities the E4M3 code itself
+//    probabilities keep ~22 bits, down to 2^-25 of the reference weight (2^-32 in
+//    modes 1 and 2, see partial_kernel); with FP8 probabilities the E4M3 code itself
 //    is the (exact) f16 operand.
 //  * The running max moves only when a box's max exceeds it by more than
 //    2^8 (log2 domain), so O is rarely rescaled; the final normalization by
@@ -132,6 +133,11 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
   constexpr int MT = Gm::kMT;
   constexpr int kSweeps = PROBQ ? 2 : 1;
   constexpr bool DIFF = MODE == 1;
+  // log2 scale of P in modes 1 and 2 (at most 2^15 with the lazy maximum's headroom): f16's
+  // steps end at 2^-24, so that without it two parts are off by up to 2^-25 of the row's
+  // largest weight, and a long tail of weights below that is lost; with it 2^-32, as in the
+  // chunks' kernel.
+  constexpr float kShift = MODE != 0 ? 7.f : 0.f;
 
   extern __shared__ uint8_t dyn_smem[];
   __shared__ Smem<NW> sm;
@@ -563,8 +569,8 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
         uint32_t ph[NH][2], pl[NH][2];
 #pragma unroll
         for (int hh = 0; hh < NH; ++hh) {
-          const float b0 = m[hh][0] == -INFINITY ? 0.f : m[hh][0];
-          const float b1 = m[hh][1] == -INFINITY ? 0.f : m[hh][1];
+          const float b0 = (m[hh][0] == -INFINITY ? 0.f : m[hh][0]) - kShift;
+          const float b1 = (m[hh][1] == -INFINITY ? 0.f : m[hh][1]) - kShift;
           const float p0 = ex2(x[hh][0] - b0), p1 = ex2(x[hh][1] - b1);
           const float p2 = ex2(x[hh][2] - b0), p3 = ex2(x[hh][3] - b1);
           l[hh][0] += p0 + p2;
@@ -689,7 +695,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
       sm.fac[w][row] = (M == -INFINITY || sm.m[w][row] == -INFINITY || Ltot == 0.f)
                            ? 0.f
                            : ex2(sm.m[w][row] - M) / Ltot * out_mult;
-    float lse = (M == -INFINITY || Ltot == 0.f) ? -INFINITY : (M + log2f(Ltot)) * kLn2;
+    float lse = (M == -INFINITY || Ltot == 0.f) ? -INFINITY : (M - kShift + log2f(Ltot)) * kLn2;
     if (bad) lse = NAN;
     a.part_lse[(part_row + row) * psplits + split] = lse;
   }
