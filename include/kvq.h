@@ -555,7 +555,9 @@ typedef struct kvq_diff {
  * As for kvq_decode, with these differences: q, out and num_q_heads count
  * differential heads; part_o and part_lse hold two rows for each, so they are sized
  * for 2 * num_q_heads heads; num_q_heads / num_kv_heads is at most 8 and prob_scale is
- * 0 (else KVQ_ERR_UNSUPPORTED); not MLA.  kvq_auto_splits with twice the query heads
+ * 0 (else KVQ_ERR_UNSUPPORTED); not MLA.  The probabilities enter the products with V in two
+ * f16 parts: each off by at most 2^-22 of itself, or by 2^-32 of the row's largest one where
+ * that is more.  kvq_auto_splits with twice the query heads
  * per kv head picks num_splits.  With fresh_tokens lambda and norm, too, have to be
  * complete before the append.
  */

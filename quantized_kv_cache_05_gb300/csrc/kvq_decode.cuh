@@ -119,8 +119,11 @@ constexpr int ctas_per_sm() {
 // partials too, is the decode of twice the heads; the cache is read once for both maps.
 // Only the merge joins a head's two.  Half of the score MMAs multiply zeros; the codes'
 // conversions bound the kernel (48 requests of 8192 tokens, 4 differential heads on each of
-// 8 kv heads, NVFP4: 142 us, 2.5 TB/s; 49% of the issue slots with 12 warps an SM, the
-// tensor pipe 19%).
+// 8 kv heads, NVFP4: 150 us, 2.4 TB/s, with 12 warps an SM).
+// Modes 1 and 2 add a box's products with V to the row's sums outside the tensor cores, which
+// cut off what does not fit an accumulator, always towards zero: in one accumulator 100000
+// tokens of one sign in one chunk lose 8e-5 of their sum, with fp32 additions below 1e-6 (and
+// the differential step above takes 150 us instead of 143).
 template <int FMT, int D, bool PROBQ, int NH, bool QF8, int NW, bool BEHIND, int MODE>
 __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     partial_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -589,8 +592,17 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int hh = 0; hh < NH; ++hh) {
-            mma_f16(o[i][hh], va[i][0], va[i][1], va[i][2], va[i][3], ph[hh][0], ph[hh][1]);
-            mma_f16(o[i][hh], va[i][0], va[i][1], va[i][2], va[i][3], pl[hh][0], pl[hh][1]);
+            if constexpr (MODE != 0) {
+              // a box's products by themselves: see MODE
+              float d[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(d, va[i][0], va[i][1], va[i][2], va[i][3], pl[hh][0], pl[hh][1]);
+              mma_f16(d, va[i][0], va[i][1], va[i][2], va[i][3], ph[hh][0], ph[hh][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[i][hh][e] += d[e];
+            } else {
+              mma_f16(o[i][hh], va[i][0], va[i][1], va[i][2], va[i][3], ph[hh][0], ph[hh][1]);
+              mma_f16(o[i][hh], va[i][0], va[i][1], va[i][2], va[i][3], pl[hh][0], pl[hh][1]);
+            }
           }
       }
       // the box is consumed: refill its stage with this warp's load j + kRingStages
