@@ -592,9 +592,12 @@ kvq_status kvq_decode_diff(const kvq_cache* c, const kvq_decode_params* p, const
  * share of it, whatever the lengths.  In a batch of more than one, requests with a single
  * new token are the split-KV decode's (at most 16 query rows per kv head, 8 differential
  * ones; with more they count as chunks).  Three or four launches on `stream`.
- * The chunks' probabilities enter the products with V in two f16 parts (2^-21 of a weight),
- * or, of plain heads and where p->prefix_p_f16 asks for it, in one (2^-11); weights below
- * 2^-32 of a row's largest count in the sum alone.
+ * The chunks' probabilities enter the products with V in two f16 parts: each off by at most
+ * 2^-21 of itself, or by 2^-31 of the row's largest one where that is more (from 2^-10 of the
+ * largest down); of plain heads and where p->prefix_p_f16 asks for it in one: 2^-11, or 2^-32
+ * of the largest.  So a token below 2^-32 of the largest counts in the sum alone, and many
+ * small ones of one size may be off in the same direction (131072 of them: 6e-5 of a row at
+ * most).
  * Everything summed is fp32, but the matrix units' accumulators cut off: where all values
  * have one sign, long sums lose up to 6e-6 of themselves with fp32 outputs, 1.5e-5 with
  * differential heads and 5e-5 with bf16 and E4M3 outputs and with one part.

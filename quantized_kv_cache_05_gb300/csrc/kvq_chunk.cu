@@ -23,8 +23,9 @@
 //    row, by the thread that has the row.  Values of such a tile that are NaN (codes of a
 //    NaN input) would reach rows that do not see them, as 0 NaN: there the tile's NaN rows
 //    become zeros, and the rows that see one of them become NaN as a whole.
-//  * Rounding.  P enters the products with V in two f16 parts (2^-21 of a weight), as in the
-//    decode, so that a token has the same bits whether its request brings one or many; where
+//  * Rounding.  P enters the products with V in two f16 parts (2^-21 of a weight, or 2^-31 of
+//    the row's largest where that is more: f16's steps end at 2^-24, P is scaled by 2^7, and
+//    each part may be off by half a step), as in the decode, so that a token has the same bits whether its request brings one or many; where
 //    the caller asks for it, plain heads have one (2^-11, against 2^-8 of the value that a
 //    bf16 output's rounding takes).  Differential heads always have two: their difference may
 //    be small beside the two sums.  Sums and accumulators are fp32, long sums in chains

@@ -13,7 +13,7 @@ import torch
 
 from packed_ref import DEV, Packed
 from quantized_kv_cache_05_gb300 import build as kbuild
-from quantized_kv_cache_05_gb300 import kvq
+from quantized_kv_cache_05_gb300 import kvq, runtime
 
 pytestmark = pytest.mark.gpu
 
@@ -75,6 +75,23 @@ def test_tail_of_the_packed_step(reqs, diff, bits):
     ref = with_floor(X, 2.0 ** -31)
     for out in ("f32", "bf16"):
         X.check(X.run(out), out, ref, what=out)
+
+
+@pytest.mark.parametrize("bits", BITS)
+def test_tail_with_one_part(bits):
+    X = tail([(16000, 20)], bits, False)
+    o, tol, mag = with_floor(X, 2.0 ** -32)
+    att = runtime.ChunkAttention(X.cache, X.B, X.hq, X.cap, X.sm, out="f32", p_f16=True)
+    X.check(att(X.q, X.offs_t, X.lens_t), "f32", (o, tol + 2.0 ** -11 * mag, mag))
+
+
+@pytest.mark.parametrize("bits", BITS)
+def test_many_small_weights_behind_one_large_one(bits):
+    """The header's figure for 131072 of them, with the large one's values in the sum."""
+    X = tail([(131071, 20)], bits, False, lead=0.5)
+    o, tol, mag = X.reference()
+    vmax = float(X.val[1].abs().max())
+    X.check(X.run("f32"), "f32", (o, tol + 131072 * 2.0 ** -31 * vmax, mag))
 
 
 @pytest.mark.parametrize("bits", BITS)
