@@ -442,6 +442,11 @@ size_t kvq_partial_workspace_bytes(int batch, int num_q_heads, int num_splits, i
  * With prob_scale > 0 one chunk's scores must fit in on-chip memory:
  * ceil(max_kv_len / s) rounded up to 16, times Hq/Hkv, at most 16384;
  * larger chunks return KVQ_ERR_UNSUPPORTED (raise num_splits).
+ * Otherwise the weights enter the products with v^ in two f16 parts: each off
+ * by at most 2^-22 of itself, or by 2^-25 of the chunk's largest where that is
+ * more.  A chunk's products add up in the matrix units' fp32 accumulators, which
+ * cut off towards zero: where all values have one sign, 100000 tokens in one
+ * chunk lose 9e-5 of their sum, in eight chunks 7e-6.
  */
 kvq_status kvq_decode_partial(const kvq_cache* c, const kvq_decode_params* p, const void* q,
                               float* part_o, float* part_lse, void* stream);
@@ -505,7 +510,10 @@ kvq_status kvq_decode(const kvq_cache* c, const kvq_decode_params* p, const void
  * probabilities enter the products with V in two f16 parts, as kvq_decode's do, or
  * in one where p->prefix_p_f16 asks for that: each off by at most 2^-22 (2^-11) of
  * itself, or by 2^-32 of the row's largest one where that is more, so that a token
- * below 2^-32 of the largest counts in the sum alone.
+ * below 2^-32 of the largest counts in the sum alone.  A split's products add up in
+ * the matrix units' fp32 accumulators, which cut off towards zero: where all values
+ * have one sign, a prefix of 131072 tokens loses 4e-4 of its sum in one split, 2.2e-5
+ * in twelve.
  * Two or three launches on `stream` (three where not all own chunks fit on the
  * SMs beside the prefix); calls that share partials or counters must not
  * overlap on the GPU.
@@ -630,7 +638,9 @@ size_t kvq_chunk_workspace_bytes(int num_sms, const kvq_cache* c, const kvq_deco
  * fresh_tokens are ignored; prob_scale must be 0 and q_fp8 0).  FP8 or
  * NVFP4 caches with head_dim 64 or 128, per-kv-head scales allowed; not MLA.
  * Requests with L < q_len: queries before position 0 attend to nothing and
- * give 0.  q_len >= 1.
+ * give 0.  q_len >= 1.  The products add up in the matrix units' fp32 accumulators,
+ * which cut off towards zero: 60000 tokens whose values have one sign lose 3.6e-4 of
+ * their sum (kvq_chunk_attention less than 6e-6 with fp32 outputs).
  */
 kvq_status kvq_prefill(const kvq_cache* c, const kvq_decode_params* p, int q_len, const void* q,
                        void* out, void* stream);
