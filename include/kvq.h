@@ -599,7 +599,10 @@ kvq_status kvq_decode_diff(const kvq_cache* c, const kvq_decode_params* p, const
  * The chunks' work is cut by its size, over the keys too, so that all SMs get the same
  * share of it, whatever the lengths.  In a batch of more than one, requests with a single
  * new token are the split-KV decode's (at most 16 query rows per kv head, 8 differential
- * ones; with more they count as chunks).  Three or four launches on `stream`.
+ * ones; with more they count as chunks), which runs before the chunks and cuts each
+ * request's tokens into one number of chunks, made from batch and max_kv_len; those that are
+ * far longer than the others count as chunks, so that no SM waits long for one request.
+ * Three or four launches on `stream`.
  * The chunks' probabilities enter the products with V in two f16 parts: each off by at most
  * 2^-21 of itself, or by 2^-31 of the row's largest one where that is more (from 2^-10 of the
  * largest down); of plain heads and where p->prefix_p_f16 asks for it in one: 2^-11, or 2^-32

@@ -232,7 +232,12 @@ int box_rows(int page_size) {
 // is none).  The decode reads a request's keys once for up to 16 query rows, in one
 // launch with its own split; as row tiles of 128 those few rows cost as much as full
 // ones (28 single tokens beside 4 chunks, NVFP4: 268 us, 240 with it).  A lone
-// request is never worth its launch.
+// request is never worth its launch.  Where the batch fills the GPU anyway, kManyChunks
+// chunks of each request at most: how long the requests are is known on the GPU only, and
+// max_kv_len may be far more (256 requests of 1000 tokens, max_kv_len 131072, 8 kv heads: 229
+// us and 57 MB with 4 chunks, 2106 us and 311 MB with the 64 of kvq_auto_splits); far longer
+// requests than the others are not the decode's (kLongChunk).
+constexpr int kManyChunks = 4;
 struct ChunkParts {
   int splits;
   size_t counters, lse, o, bytes;
@@ -246,6 +251,7 @@ ChunkParts chunk_parts(int sms, const kvq_cache* c, const kvq_decode_params* p, 
   if (p->batch < 2 || rows > kMaxGroup ||
       kvq_auto_splits(sms, p->batch, c->num_kv_heads, rows, p->max_kv_len, c->fmt, &w.splits) != KVQ_OK)
     return w;
+  if ((long long)p->batch * c->num_kv_heads > 2 * sms) w.splits = std::min(w.splits, kManyChunks);
   const size_t groups = (size_t)p->batch * c->num_kv_heads, parts = groups * rows * w.splits;
   w.lse = w.counters + up(groups * sizeof(uint32_t));
   w.o = w.lse + up(parts * sizeof(float));
@@ -705,7 +711,8 @@ kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const voi
                        float* part_o, float* part_lse, uint32_t* counters, void* out,
                        cudaStream_t stream, int prefix_len = 0, int prefix_splits = 0,
                        uint32_t* ready = nullptr, const kvq_diff* diff = nullptr,
-                       const int32_t* q_offsets = nullptr, int num_tokens = 0) {
+                       const int32_t* q_offsets = nullptr, int num_tokens = 0,
+                       const int32_t* longest = nullptr) {
   kvq_status s = check_cache(c);
   if (s != KVQ_OK) return s;
   s = check_params(p);
@@ -806,6 +813,7 @@ kvq_status decode_impl(const kvq_cache* c, const kvq_decode_params* p, const voi
     return KVQ_ERR_CUDA;
   a.q_offsets = q_offsets;
   a.num_tokens = num_tokens;
+  a.longest = longest;
   if (diff) {
     a.diff_lambda = diff->lambda;
     a.diff_norm = diff->norm;
@@ -1057,6 +1065,7 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_decode_params* p, c
     return KVQ_ERR_CUDA;
   uint8_t* const w = a.workspace;
   if (parts.splits > 0) a.counters = reinterpret_cast<uint32_t*>(w + parts.counters);
+  a.single_splits = parts.splits;
   s = cuda_status(launch_shares(c->fmt, a, sms, as_stream(stream)));
   if (s != KVQ_OK) return s;
   if (parts.splits > 0) {
@@ -1065,7 +1074,8 @@ kvq_status kvq_chunk_attention(const kvq_cache* c, const kvq_decode_params* p, c
     one.fresh_tokens = 0;
     s = decode_impl(c, &one, q, reinterpret_cast<float*>(w + parts.o),
                     reinterpret_cast<float*>(w + parts.lse), a.counters, out, as_stream(stream), 0,
-                    0, nullptr, d, q_offsets, num_tokens);
+                    0, nullptr, d, q_offsets, num_tokens,
+                    reinterpret_cast<const int32_t*>(w) + kChunkLongest);
     if (s != KVQ_OK) return s;
   }
   return cuda_status(launch_chunk(c->fmt, D, maps, a, sms, as_stream(stream)));

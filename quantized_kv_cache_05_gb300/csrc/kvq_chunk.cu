@@ -45,6 +45,8 @@
 // 2.3 to 3 us on 128 rows' key tile, bound by the two parts of P.
 
 #include <cfloat>
+#include <climits>
+#include <cstddef>
 #include <type_traits>
 
 #include "kvq_attn.cuh"
@@ -93,7 +95,9 @@ constexpr int kCostFixed = 40, kCostShare = 64, kMinPiece = 3;
 // ---------------------------------------------------------------------------
 struct ChunkHead {
   int shares, active;     // CTAs with work; requests with new tokens
+  int longest;            // single tokens up to this many keys are the decode's (kChunkLongest)
 };
+static_assert(offsetof(ChunkHead, longest) == kChunkLongest * sizeof(int), "read by the decode");
 struct Cut {              // where a share begins: before key tile `kv` of a row tile
   int i, tile, h, kv;     // active request, row tile, kv head, key tile
   __device__ __forceinline__ bool tile_of(const Cut& o) const {
@@ -142,6 +146,14 @@ __device__ __forceinline__ int tile_cost(const Request& r, int G, int rt, int on
 // (consecutive ones per thread) and finds the cuts, a thread per cut.
 // ---------------------------------------------------------------------------
 constexpr int kShareThreads = 256;
+// The decode cuts every single token's keys into the same number of chunks, which the batch's
+// capacity gives.  One whose chunks are longer than this, and than four times the mean over
+// the decode's places (two CTAs on each SM), would keep a few SMs busy while the others, and
+// the chunks' kernel, wait: it is cut into shares with the prompt chunks instead, where a key
+// costs half as much again (batch 32 x 8 kv heads, one of 131072 keys and 31 of 1000: 148 us,
+// by the decode alone 1107; two of 32768 and 30 idle ones 82 and 281.  With twice the mean 32
+// of 1000 to 32000 keys take 413 us instead of 309).
+constexpr int kLongChunk = 4096;
 
 struct ShareSmem {
   long warp_a[kShareThreads / 32], warp_b[kShareThreads / 32];
@@ -195,16 +207,30 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const ChunkArgs a,
   Cut* cuts = reinterpret_cast<Cut*>(a.workspace + sp.cuts);
   Request* requests = reinterpret_cast<Request*>(a.workspace + sp.requests);
 
-  // ---- the active requests and their row tiles
   const int per = (a.batch + kShareThreads - 1) / kShareThreads;
   const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
+  // ---- single tokens: those that the decode takes (kLongChunk)
+  int longest = 0;
+  if (a.counters) {
+    long keys = 0, none = 0, unused;
+    for (int b = b0; b < b1; ++b)
+      if (min(max(a.q_offsets[b + 1], 0), a.num_tokens) - min(max(a.q_offsets[b], 0), a.num_tokens) == 1)
+        keys += min(max(a.seq_lens[b], 0), a.max_kv_len);
+    long all_keys;
+    scan2(keys, none, all_keys, unused, sm);
+    longest = (int)min(max((long)kLongChunk, 4 * all_keys * a.Hkv / (2 * grid)) * a.single_splits,
+                       (long)INT_MAX);
+    if (tid == 0) reinterpret_cast<ChunkHead*>(a.workspace)->longest = longest;
+  }
+
+  // ---- the active requests and their row tiles
   auto request = [&](int b) -> Request {
     Request r;
     r.q0 = min(max(a.q_offsets[b], 0), a.num_tokens);
     r.n = max(min(max(a.q_offsets[b + 1], 0), a.num_tokens) - r.q0, 0);
-    if (a.counters && r.n == 1) r.n = 0;   // the decode's
     const int len = a.seq_lens[b];
     r.L = min(max(len, 0), a.max_kv_len);
+    if (a.counters && r.n == 1 && r.L <= longest) r.n = 0;   // the decode's
     if (r.L != len && r.n > 0) record_error(a.error_flag, 2);
     r.b = b;
     return r;
@@ -264,7 +290,7 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const ChunkArgs a,
   // ---- the cuts: share c begins at c / shares of the whole
   const long whole = W * a.Hkv;
   const int shares = (int)min((long)grid, (whole + kCostShare - 1) / kCostShare);
-  if (tid == 0) *reinterpret_cast<ChunkHead*>(a.workspace) = ChunkHead{shares, A};
+  if (tid == 0) *reinterpret_cast<ChunkHead*>(a.workspace) = ChunkHead{shares, A, longest};
   for (int c = tid; c <= shares && shares > 0; c += kShareThreads) {
     const long x = whole / shares * c + min((long)c, whole % shares);
     const int h = (int)(x / W);

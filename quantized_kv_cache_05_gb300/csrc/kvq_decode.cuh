@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
     if (a.q_offsets) {
       const int q0 = min(max(__ldg(a.q_offsets + b), 0), a.num_tokens);
       if (min(max(__ldg(a.q_offsets + b + 1), 0), a.num_tokens) - q0 != 1) return;
+      if (min(max(__ldg(a.seq_lens + b), 0), cap) > *a.longest) return;   // (the chunks')
       token = q0;
     }
   }

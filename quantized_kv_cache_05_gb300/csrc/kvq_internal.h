@@ -101,6 +101,7 @@ struct PartialArgs {
   float diff_eps, diff_gain;
   const int32_t* q_offsets;   // rows of a packed step [batch + 1], or null: row b is request b's
   int num_tokens;
+  const int32_t* longest;     // with q_offsets: the most keys of a single token that takes part
 };
 
 // The shared prefix's partials (kvq_shared.cu).
@@ -170,6 +171,7 @@ struct RopeArgs {
 };
 
 // A packed ragged step over the cache (kvq_chunk.cu).
+constexpr int kChunkLongest = 2;   // word of the workspace: the decode's longest single token
 struct ChunkArgs {
   const void* q;              // [num_tokens][Hq][D] bf16, or E4M3 codes when q_fp8
   int q_fp8;
@@ -182,6 +184,7 @@ struct ChunkArgs {
   const int32_t* q_offsets;
   uint8_t* workspace;
   uint32_t* counters;         // [batch][Hkv] to clear where the decode takes the single tokens, or null
+  int single_splits;          // that decode's chunks
   void* out;
   int32_t* error_flag;
   int batch, num_tokens, G, Hq, Hkv, D, ps, max_pages, num_pages, max_kv_len;

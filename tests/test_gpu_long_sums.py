@@ -30,12 +30,12 @@ def one_sign(fmt, hq, reqs, diff):
     return X
 
 
-def check(X, got):
+def check(X, got, limit=2.0 ** -17):
     """The requests' rows: within packed_ref's bound, and on the whole."""
     o, _, _ = ref = X.reference()
     X.check(got, "f32", ref)
     rel = (got.double().cpu().numpy() - o) / o
-    assert abs(rel.mean()) < 2.0 ** -17
+    assert abs(rel.mean()) < limit
 
 
 @pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
@@ -47,6 +47,13 @@ def test_differential_decode(fmt, hq):
 
 @pytest.mark.parametrize("diff", [False, True])
 def test_single_tokens(diff):
-    """Two long single tokens in a batch so large that the split rule gives one chunk."""
-    X = one_sign("fp8", 4, [(99999, 1), (0, 0), (70000, 1)] + [(0, 0)] * 150, diff)
+    """Long single tokens in a batch so large that the split rule gives one chunk."""
+    X = one_sign("fp8", 4, [(20000 + 7 * b, 1) for b in range(100)] + [(0, 0)] * 60, diff)
     check(X, X.run("f32"))
+
+
+@pytest.mark.parametrize("diff", [False, True])
+def test_two_single_tokens(diff):
+    """Two of them alone count as chunks: what the header states for those."""
+    X = one_sign("fp8", 4, [(99999, 1), (0, 0), (70000, 1)] + [(0, 0)] * 150, diff)
+    check(X, X.run("f32"), 1.5e-5 if diff else 6e-6)
