@@ -566,7 +566,8 @@ typedef struct kvq_diff {
  * 0 (else KVQ_ERR_UNSUPPORTED); not MLA.  The probabilities enter the products with V in two
  * f16 parts: each off by at most 2^-22 of itself, or by 2^-32 of the row's largest one where
  * that is more.  kvq_auto_splits with twice the query heads
- * per kv head picks num_splits.  With fresh_tokens lambda and norm, too, have to be
+ * per kv head picks num_splits (15 instead of 16 with head_dim up to 128: NVFP4's 16 on
+ * one kv head are taken for MLA there).  With fresh_tokens lambda and norm, too, have to be
  * complete before the append.
  */
 kvq_status kvq_decode_diff(const kvq_cache* c, const kvq_decode_params* p, const kvq_diff* d,

@@ -248,8 +248,11 @@ ChunkParts chunk_parts(int sms, const kvq_cache* c, const kvq_decode_params* p, 
   const int D = c->head_dim, rows = (d ? 2 : 1) * (p->num_q_heads / c->num_kv_heads);
   w.counters = up(chunk_workspace_bytes(sms, std::max(p->batch, 1), D));
   w.bytes = w.counters;
+  // (NVFP4, one kv head and 16 rows would be taken for MLA there, whose kernel has one CTA on
+  // an SM; 15 rows are this one's as well)
   if (p->batch < 2 || rows > kMaxGroup ||
-      kvq_auto_splits(sms, p->batch, c->num_kv_heads, rows, p->max_kv_len, c->fmt, &w.splits) != KVQ_OK)
+      kvq_auto_splits(sms, p->batch, c->num_kv_heads, std::min(rows, kMaxGroup - 1), p->max_kv_len,
+                      c->fmt, &w.splits) != KVQ_OK)
     return w;
   if ((long long)p->batch * c->num_kv_heads > 2 * sms) w.splits = std::min(w.splits, kManyChunks);
   const size_t groups = (size_t)p->batch * c->num_kv_heads, parts = groups * rows * w.splits;

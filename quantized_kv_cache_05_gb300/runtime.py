@@ -648,8 +648,10 @@ class DiffDecode:
         device = cache.k_codes.device
         if splits is None:
             sms = torch.cuda.get_device_properties(device).multi_processor_count
-            st, splits = kvq.kvq_auto_splits(sms, max(batch, 1), cache.Hkv,
-                                             2 * num_q_heads // cache.Hkv, max_kv_len,
+            rows = 2 * num_q_heads // cache.Hkv
+            if rows == 16 and cache.D <= 128:
+                rows = 15   # (on one kv head NVFP4's 16 are taken for MLA, one CTA on an SM)
+            st, splits = kvq.kvq_auto_splits(sms, max(batch, 1), cache.Hkv, rows, max_kv_len,
                                              FMT[cache.fmt])
             kvq.check(st, "kvq_auto_splits")
         cfg = self._cfg = DecodeConfig(batch, num_q_heads, cache.D, cache.D, splits, max_kv_len,

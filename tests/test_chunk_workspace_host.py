@@ -24,3 +24,11 @@ def test_it_does_not_grow_with_the_longest_length(hkv):
         assert size(batch, 1 << 17) <= chunks + 4 * rows * 129 * 4 + batch * (4 * hkv + 16) + 2048
     # one that does not: as many chunks as places, in all
     assert size(2, 1 << 17) <= chunks + 304 * 4 * 129 * 4 + 4096
+
+
+def test_sixteen_rows_of_one_kv_head_are_not_mla():
+    """The formats differ in nothing that the single tokens' partials depend on."""
+    nv = dict(fmt=kvq.KVQ_NVFP4, k_bscale=1 << 20, v_bscale=1 << 20)
+    size = lambda **kw: kvq.kvq_chunk_workspace_bytes(
+        152, cache(num_kv_heads=1, **kw), params(batch=4, num_q_heads=16, max_kv_len=1 << 15), None)
+    assert size(**nv) == size()
