@@ -342,8 +342,11 @@ kvq_status kvq_rope_append(const kvq_cache* c, const kvq_rotary* r, int batch, i
  *    tokens would pass max_tokens.  Such a request keeps its length and sets
  *    KVQ_DEVERR_REFUSED.
  * Lengths outside [0, max_pages_per_seq page_size] are clamped (KVQ_DEVERR_SEQ_CLAMPED),
- * a count outside [0, num_pages] too, and pages past num_pages that come back are
- * dropped (both KVQ_DEVERR_BAD_POOL).
+ * a count outside [0, num_pages] too, and pages that come back beyond num_pages of them are
+ * dropped (both KVQ_DEVERR_BAD_POOL).  A page whose index is out of range sets
+ * KVQ_DEVERR_BAD_PAGE when it comes back and when it is taken, and is a page like any other
+ * otherwise: it goes on the stack, and the request that takes it is served, but its tokens
+ * there have no slots.  After that bit the tables and the free pages have to be made anew.
  *
  * Outputs (the last four may be NULL):
  *   seq_lens_out   [batch] the new lengths (may be seq_lens)

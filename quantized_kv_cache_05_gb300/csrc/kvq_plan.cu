@@ -221,8 +221,9 @@ __global__ void __launch_bounds__(T) plan_kernel(const PlanArgs a) {
     a.free_pages[count + r] = page;
   }
   for (int g = first; g < pops; g += stride) {
-    const int b = owner(take0, B, g);
-    a.block_table[(size_t)b * a.max_pages + held[b] + (g - take0[b])] = taken(g);
+    const int b = owner(take0, B, g), page = taken(g);
+    in_range(page);   // (where neither slots nor positions are wanted, nobody else looks)
+    a.block_table[(size_t)b * a.max_pages + held[b] + (g - take0[b])] = page;
   }
   if (!a.slots && !a.positions) return;
   const int live = tok0[B];
