@@ -553,6 +553,14 @@ kvq_status kvq_shared_splits(int num_sms, int batch, int num_kv_heads, int q_per
  * sm_scale is usually 1/sqrt(D / 2), and gain 1 - lambda_init.  Everything before the
  * output's rounding is fp32; an o of zeros gives zeros, whatever eps.  The two sums of
  * a request without tokens are zeros.
+ * Models that turn each of q1, q2, k1 and k2 over its own D / 2 elements: kvq_rotary with
+ * interleaved = 1, rot_dim = D and a table that has the D / 4 cosines of a half twice, then
+ * its sines twice, does so in the appends and in kvq_norm_rope.  Where the model pairs the
+ * elements (i, i + D/4) of a half, one permutation of its projections' rows, the same for
+ * queries and keys, makes them (2i, 2i + 1) and leaves the scores as they are.  (interleaved
+ * = 0 pairs elements of the whole head, across the two maps.)  Halves of 64 or 128 may also
+ * be turned as heads of their own, by kvq_norm_rope with head_dim D / 2, before an append
+ * with rot_dim 0; its keys are rounded to bf16 on the way.
  */
 typedef struct kvq_diff {
   const float* lambda;       /* (device) [num_q_heads] */

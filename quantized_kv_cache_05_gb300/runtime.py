@@ -421,7 +421,10 @@ class StepPlan:
 class Differential:
     """What differential heads subtract and how they are normed (``kvq_diff``): lam
     float32 [num_q_heads], norm float32 [head_dim] or None, gain (usually 1 -
-    lambda_init).  It keeps these tensors, whose addresses its struct holds."""
+    lambda_init).  It keeps these tensors, whose addresses its struct holds.  A rotation of
+    each half by itself: ``Rotary(torch.cat([c, c, s, s], 1), interleaved=True)`` of
+    ``c, s = rope_table(positions, head_dim // 2).chunk(2, 1)`` (kvq_diff says for which
+    orders of the elements)."""
 
     def __init__(self, lam: torch.Tensor, norm: Optional[torch.Tensor] = None, eps: float = 1e-5,
                  gain: float = 1.0):
