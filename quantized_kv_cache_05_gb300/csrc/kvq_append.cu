@@ -27,7 +27,7 @@ namespace {
 // Cache row of (request b, position pos, kv head h), or -1 when the position
 // is outside the request's block table.
 __device__ __forceinline__ long cache_row(const AppendArgs& a, int b, int pos, int h) {
-  if (pos < 0 || pos >= a.max_pages * a.ps) return -1;
+  if (pos < 0 || pos >= (long)a.max_pages * a.ps) return -1;
   const int page = __ldg(a.block_table + (size_t)b * a.max_pages + (unsigned)pos / (unsigned)a.ps);
   if (page < 0 || page >= a.num_pages) return -1;
   return ((long)page * a.Hkv + h) * a.ps + (unsigned)pos % (unsigned)a.ps;

@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(32 * NW, ctas_per_sm<FMT, D, PROBQ, NH, NW>())
   using Rg = Ring<FMT, D, PROBQ, NH, NW>;
   const uint32_t scores = ring + Rg::kBytes;   // FP8-prob mode only
 
-  const int cap = min(a.max_pages * a.ps, a.max_kv_len);
+  const int cap = a.max_kv_len;   // (at most what a block-table row holds: checked on the host)
   // Launched with programmatic serialization, this kernel can start before
   // the previous kernel in the stream ends, and its inputs may come from that
   // kernel.  Before the wait it only sets up its barriers -- unless the

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- chunk of this split
   int L = a.seq_lens[b];
-  const int cap = min(a.max_pages * a.ps, a.max_kv_len);
+  const int cap = a.max_kv_len;   // (at most what a block-table row holds: checked on the host)
   if (L > cap || L < 0) {
     if (tid == 0) record_error(a.error_flag, 2);
     L = L < 0 ? 0 : cap;

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kPfThreads)
   }
   griddep_wait();
 
-  const int cap = min(a.max_pages * a.ps, a.max_kv_len);
+  const int cap = a.max_kv_len;   // (at most what a block-table row holds: checked on the host)
   int L = a.seq_lens[b];
   if (L > cap || L < 0) {
     if (threadIdx.x == 0) record_error(a.error_flag, 2);
