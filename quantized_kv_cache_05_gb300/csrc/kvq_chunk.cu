@@ -40,8 +40,8 @@
 // chain of scores, softmax and products, with some 200 cycles at every hand-over, and the codes
 // of NVFP4 take the converting warps 1.74 us a tile.  With two parts it is some 2.9 us for 1.57:
 // the softmax splits P and writes it twice.  Beside that a piece costs 7 us (queries
-// 4, rows out 3), the shares' kernel 4, the merge 5 to 10: of a step of a few hundred
-// rows most of the 40 us.  Differential heads (four chunks of 1024, NVFP4: 446 us) spend
+// 4, rows out 3), the shares' kernel 5 to 6, the single tokens 10 and more, the merge 7 to 19,
+// one behind the other: of a step of a few hundred rows most of the 40 to 47 us.  Differential heads (four chunks of 1024, NVFP4: 446 us) spend
 // 2.3 to 3 us on 128 rows' key tile, bound by the two parts of P.
 
 #include <cfloat>
