@@ -25,9 +25,9 @@
 //    become zeros, and the rows that see one of them become NaN as a whole.
 //  * Rounding.  P enters the products with V in two f16 parts (2^-21 of a weight, or 2^-31 of
 //    the row's largest where that is more: f16's steps end at 2^-24, P is scaled by 2^7, and
-//    each part may be off by half a step), as in the decode, so that a token has the same bits whether its request brings one or many; where
-//    the caller asks for it, plain heads have one (2^-11, against 2^-8 of the value that a
-//    bf16 output's rounding takes).  Differential heads always have two: their difference may
+//    each part may be off by half a step), as in the decode, so that as much is kept of a token's
+//    weights whether its request brings one or many; where the caller asks for it, plain heads
+//    have one (2^-11, against 2^-8 of the value that a bf16 output's rounding takes).  Differential heads always have two: their difference may
 //    be small beside the two sums.  Sums and accumulators are fp32, long sums in chains
 //    (kChainOne).
 // Every wait is bounded; a timeout sets an error bit and the rows become NaN.
@@ -41,8 +41,9 @@
 // of NVFP4 take the converting warps 1.74 us a tile.  With two parts it is some 2.9 us for 1.57:
 // the softmax splits P and writes it twice.  Beside that a piece costs 7 us (queries
 // 4, rows out 3), the shares' kernel 5 to 6, the single tokens 10 and more, the merge 7 to 19,
-// one behind the other: of a step of a few hundred rows most of the 40 to 47 us.  Differential heads (four chunks of 1024, NVFP4: 446 us) spend
-// 2.3 to 3 us on 128 rows' key tile, bound by the two parts of P.
+// one behind the other: of a step of a few hundred rows most of the 40 to 47 us.  Differential
+// heads (four chunks of 1024, NVFP4: 441 us) spend 2.3 to 3 us on 128 rows' key tile, bound by
+// the two parts of P.
 
 #include <cfloat>
 #include <climits>
@@ -86,7 +87,8 @@ constexpr int kRows = 2 * kTok;           // rows of a partial in the workspace
 // Cost of a row tile, in twelfths of a key tile with both accumulators' rows (1.9 us): for
 // each key tile 12, or with one accumulator's rows what its conversion takes (NVFP4: 1.74
 // us; FP8: half of it, as two key tiles are on their way; with two parts of P 1.75 to 1.9 of
-// 2.4 us), and kCostFixed for its queries and its output (7 us).  A share is at least kCostShare, a piece kMinPiece key tiles.
+// 2.4 us), and kCostFixed for its queries and its output (7 us).  A share is at least
+// kCostShare, a piece kMinPiece key tiles.
 constexpr int kCostTwo = 12, kCostOneFp8 = 7, kCostOneNvfp4 = 11, kCostOneWide = 9;
 constexpr int kCostFixed = 40, kCostShare = 64, kMinPiece = 3;
 
@@ -214,7 +216,8 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const ChunkArgs a,
   if (a.counters) {
     long keys = 0, none = 0, unused;
     for (int b = b0; b < b1; ++b)
-      if (min(max(a.q_offsets[b + 1], 0), a.num_tokens) - min(max(a.q_offsets[b], 0), a.num_tokens) == 1)
+      if (min(max(a.q_offsets[b + 1], 0), a.num_tokens) -
+              min(max(a.q_offsets[b], 0), a.num_tokens) == 1)
         keys += min(max(a.seq_lens[b], 0), a.max_kv_len);
     long all_keys;
     scan2(keys, none, all_keys, unused, sm);
@@ -1410,7 +1413,10 @@ cudaError_t launch_shares(int fmt, const ChunkArgs& a, int grid, cudaStream_t st
       cudaFuncSetAttribute(share_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
   if (e != cudaSuccess) return e;
   const bool diff = a.diff_lambda != nullptr;
-  const int one = diff ? kCostTwo : a.wide_p ? kCostOneWide : fmt == kFmtFp8 ? kCostOneFp8 : kCostOneNvfp4;
+  const int one = diff                ? kCostTwo
+                  : a.wide_p          ? kCostOneWide
+                  : fmt == kFmtFp8    ? kCostOneFp8
+                                      : kCostOneNvfp4;
   return launch_pdl(share_kernel, dim3(1), dim3(kShareThreads), (size_t)a.batch * sizeof(int), st,
                     a, grid, diff ? kTok : kRows, one);
 }
