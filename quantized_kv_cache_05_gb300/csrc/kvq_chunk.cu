@@ -32,13 +32,13 @@
 //    (kChainOne).
 // Every wait is bounded; a timeout sets an error bit and the rows become NaN.
 //
-// What bounds it: 4096 rows x 32 heads (8 kv heads of 128, FP8) behind 12288 tokens take 1108
-// us, 67% of the matrix rate with the second part's products (742 us), and 653 with one part
-// of P (495, 76%); 2048 rows behind 6144 take 312 (FP8) and 335 (NVFP4), with one part 197 and
+// What bounds it: 4096 rows x 32 heads (8 kv heads of 128, FP8) behind 12288 tokens take 1047
+// us, 71% of the matrix rate with the second part's products (742 us), and 653 with one part
+// of P (495, 76%); 2048 rows behind 6144 take 299 (FP8) and 326 (NVFP4), with one part 197 and
 // 237.  With one part the tensor pipe is busy for 60% of the cycles and the schedulers issue in
 // 45%: a key tile of two slots takes 1.9 us where its products need 1.05, each slot being a
 // chain of scores, softmax and products, with some 200 cycles at every hand-over, and the codes
-// of NVFP4 take the converting warps 1.74 us a tile.  With two parts it is some 2.9 us for 1.57:
+// of NVFP4 take the converting warps 1.74 us a tile.  With two parts it is some 2.8 us for 1.57:
 // the softmax splits P and writes it twice.  Beside that a piece costs 7 us (queries
 // 4, rows out 3), the shares' kernel 5 to 6, the single tokens 10 and more, the merge 7 to 19,
 // one behind the other: of a step of a few hundred rows most of the 40 to 47 us.  Differential
@@ -75,10 +75,10 @@ constexpr float kPShift = 7.0f;           // log2 scale of P
 // keys in one chain lost 1e-3 of a row.  A longer piece is a sum of
 // chains, in fp32 rounded to nearest, kept in the workspace.  64 units with one part lose
 // 2.5e-5 on average and up to 3.8e-5 (128: 5.6e-5 and 7.4e-5, in the same time); 32 with two
-// parts 3.3e-5 (64: 6.5e-5; 4096 rows behind 12288 tokens: 1108 us against 1076); 16 of
+// parts 3.3e-5 (64: 6.5e-5; 4096 rows behind 12288 tokens: 3% less); 16 of
 // differential heads 1.4e-5, nearly the same of both maps' sums (four chunks of 1024, NVFP4:
-// 445 us against 429 in one chain); 4 of fp32 outputs 3.9e-6 (2048 rows behind 6144: 361 us
-// against 312 with 32 units, and 334 with 8).  Powers of two: a unit's place in its chain is a
+// 445 us against 429 in one chain); 4 of fp32 outputs 3.9e-6 (2048 rows behind 6144: 352 us
+// against 299 with 32 units).  Powers of two: a unit's place in its chain is a
 // mask.
 constexpr int kChainOne = 64, kChainTwo = 32, kChainDiff = 16, kChainF32 = 4;
 constexpr int kTmem = 512;                // S0 | S1 | O0 | O1, 128 columns each
@@ -783,9 +783,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The queries of a piece, into the slot's operand tile: their 16-byte pieces go straight
     // to the places that their f16 values take, FP8 codes at every other one (they widen to
     // two); consecutive lanes copy consecutive pieces, and rows past the last are zeros.
-    // With one part of P the next piece's are on their way while rows are written (4096 rows
-    // behind 12288 tokens: 660 us against 676; with two parts this loses, 444 against 424 for
-    // four differential chunks of 1024: the kernels' code is larger).
+    // Plain heads' next piece's are on their way while rows are written (4096 rows behind 12288
+    // tokens: 1047 us against 1105, with one part of P 660 against 676; with differential heads
+    // this loses, 444 against 424 for four chunks of 1024: the kernel's code is larger).
     constexpr int kHalf = DIFF ? 2 : 1;                             // of the dims in an operand
     const int dp0 = DIFF ? slot * (D / 16) : 0;                     // its first piece (8 dims each)
     auto q_place = [&](bool two, int trow, int piece) -> uint32_t {
@@ -1126,7 +1126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool bad = __any_sync(0xffffffffu, !ok || *abort_flag != 0);
       ok = !bad;
       tc_fence_after();
-      if constexpr (!P2) fetch_next();   // (before the rows are written)
+      if constexpr (!DIFF) fetch_next();   // (before the rows are written)
       float f[2];
       if (!two) {
         factors(sm.a[0][r], sm.b[0][r], sm.a[1][r], sm.b[1][r], f[0], f[1]);
