@@ -496,6 +496,7 @@ __device__ __forceinline__ void fused_combine_staged(const PartialArgs& a, int b
                                                      float* wbuf, uint32_t bar,
                                                      unsigned base = 0u) {
   __shared__ int is_last;
+  fence_proxy_async_shared();   // the fragments that stand where the bulk copy goes
   __syncthreads();
   if (threadIdx.x == 0) {
     unsigned prev;
@@ -629,6 +630,7 @@ __device__ __forceinline__ void fused_combine_heads(const PartialArgs& a, int bh
                                                     float* wbuf, uint32_t bar, size_t out0,
                                                     int hq0) {
   __shared__ int is_last;
+  fence_proxy_async_shared();   // the fragments that stand where the bulk copy goes
   __syncthreads();
   if (threadIdx.x == 0) {
     unsigned prev;
